@@ -27,7 +27,9 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibilit
 SOURCES = ["api.cu", "append.cu", "combine.cu", "decode_int8.cu", "decode_fp8.cu", "decode_int4.cu",
            "decode_tc_int8.cu", "decode_tc_fp8.cu", "decode_tc_int4.cu", "decode_tc_grp_int8.cu",
            "decode_tc_grp_fp8.cu", "decode_tc_grp_int4.cu", "decode_qt_int8.cu", "decode_qt_fp8.cu",
-           "decode_qt_int4.cu", "noalloc.cu"]
+           "decode_qt_int4.cu", "noalloc.cu", "masked.cu", "decode_mask_int8.cu", "decode_mask_fp8.cu",
+           "decode_mask_int4.cu", "qt_mask_int8.cu", "qt_mask_fp8.cu", "qt_mask_int4.cu", "key_mass_int8.cu",
+           "key_mass_fp8.cu", "key_mass_int4.cu", "evict.cu"]
 
 
 def _nvcc() -> str:
@@ -37,7 +39,8 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libkvq.so")
 
 
-HEADERS = ["kvq_internal.h", "ptx.cuh", "pipeline.cuh", "decode.cuh", "decode_tc.cuh", "decode_qt.cuh"]
+HEADERS = ["kvq_internal.h", "ptx.cuh", "pipeline.cuh", "decode.cuh", "decode_tc.cuh", "decode_qt.cuh",
+           "score_rule.cuh", "key_mass.cuh"]
 
 
 def _stamp() -> str:

@@ -189,7 +189,14 @@ size_t fixed_smem(const kvq_cache* c, int row_groups, int key_warps, int nt, int
 // wide), or -group_size for the grouped layout with per-group scales.
 int kernel_nt(const kvq_cache* c, const Plan& P) { return any_group(c) ? -c->group_size : P.nt; }
 
-cudaError_t occupancy(const kvq_cache* c, int nt, int threads, size_t smem, int* n) {
+cudaError_t occupancy(const kvq_cache* c, int nt, int threads, size_t smem, bool mask, int* n) {
+  if (mask) {
+    switch (c->dtype) {
+      case KVQ_INT8: return occupancy_decode_mask_int8(c->head_dim, nt, threads, smem, n);
+      case KVQ_FP8_E4M3: return occupancy_decode_mask_fp8(c->head_dim, nt, threads, smem, n);
+      default: return occupancy_decode_mask_int4(c->head_dim, nt, threads, smem, n);
+    }
+  }
   switch (c->dtype) {
     case KVQ_INT8: return occupancy_decode_int8(c->head_dim, nt, threads, smem, n);
     case KVQ_FP8_E4M3: return occupancy_decode_fp8(c->head_dim, nt, threads, smem, n);
@@ -264,8 +271,63 @@ kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const De
   return KVQ_OK;
 }
 
+// The key-mass kernel: K-side stages for its four 16-key warps, the query rows
+// in tiles of 8 (1, 2, 4 or 8 of them), as many CTAs per SM as leave each at
+// least three stages.
+kvq_status make_plan_mass(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, Plan* out) {
+  Plan P{};
+  P.rows = p->num_q_heads / c->num_kv_heads * p->q_tokens;
+  P.nt = P.rows <= 8 ? 1 : (P.rows <= 16 ? 2 : (P.rows <= 32 ? 4 : 8));
+  if (P.rows > 64 || (c->head_dim == 576 && P.nt > 4)) return KVQ_ERR_UNSUPPORTED;
+  P.threads = kMassThreads;
+  P.stride = stage_stride(c, true);
+  const int B = p->batch > 0 ? p->batch : 1;
+  const bool split = c->k_mode == KVQ_SCALE_PER_CHANNEL;
+  int occ = 0;
+  for (int target : {4, 3, 2, 1}) {
+    const size_t budget = (size_t)228 * 1024 / target - 1024;
+    const size_t fixed = mass_fixed_smem(c->head_dim, P.nt, split, B, 0);
+    const int min_stages = target > 1 ? 3 : 2;
+    if (fixed + (size_t)min_stages * (P.stride + 16) > budget) continue;
+    int stages = (int)((budget - fixed) / (P.stride + 16));
+    stages = stages > kMaxStages ? kMaxStages : stages;
+    const size_t smem = mass_fixed_smem(c->head_dim, P.nt, split, B, stages) + (size_t)stages * P.stride;
+    int n = 0;
+    cudaError_t e;
+    switch (c->dtype) {
+      case KVQ_INT8: e = occupancy_key_mass_int8(c->head_dim, P.nt, c->k_mode, smem, &n); break;
+      case KVQ_FP8_E4M3: e = occupancy_key_mass_fp8(c->head_dim, P.nt, c->k_mode, smem, &n); break;
+      default: e = occupancy_key_mass_int4(c->head_dim, P.nt, c->k_mode, smem, &n); break;
+    }
+    if (e != cudaSuccess) return KVQ_ERR_CUDA;
+    if (n >= target) {
+      occ = target;
+      P.stages = stages;
+      P.smem = smem;
+      break;
+    }
+  }
+  if (occ == 0) return KVQ_ERR_UNSUPPORTED;
+  const long long cap = (long long)p->max_blocks_per_seq * c->block_size;
+  const long long maxlen = (p->max_seq_len > 0 && p->max_seq_len < cap) ? p->max_seq_len : cap;
+  long long grid = (long long)dev.sms * occ;
+  const long long useful = (long long)B * c->num_kv_heads * ((maxlen + kTile - 1) / kTile + 1);
+  if (grid > useful) grid = useful;
+  P.grid = (int)(grid < 1 ? 1 : grid);
+  P.ws_plan = align256((size_t)(4 + B + 1) * 4);
+  P.ws_total = P.ws_plan;
+  *out = P;
+  return KVQ_OK;
+}
+
+// Which kernels a plan is for: the attention kernels, their masked instances
+// (no tensor-memory layout of keys as MMA rows there), the key-mass kernel.
+enum PlanKind { kPlanDecode = 0, kPlanMasked = 1, kPlanMass = 2 };
+
 kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool qt,
-                              Plan* out) {
+                              PlanKind kind, Plan* out) {
+  if (kind == kPlanMass) return make_plan_mass(c, p, dev, out);
+  const bool mask = kind == kPlanMasked;
   Plan P{};
   const int G = p->num_q_heads / c->num_kv_heads;
   P.rows = G * p->q_tokens;
@@ -281,7 +343,7 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
     *out = P;
     return KVQ_OK;
   }
-  P.tc_nr = tc_rows(c, p, P.rows);
+  P.tc_nr = mask ? 0 : tc_rows(c, p, P.rows);
   if (P.tc_nr) {
     if (kvq_status s = make_plan_tc(c, p, dev, &P)) return s;
     const int B = p->batch > 0 ? p->batch : 1;
@@ -330,7 +392,7 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
     stages = stages > kMaxStages ? kMaxStages : stages;
     const size_t smem = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, stages) + (size_t)stages * stride;
     int n = 0;
-    if (occupancy(c, kernel_nt(c, P), P.threads, smem, &n) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (occupancy(c, kernel_nt(c, P), P.threads, smem, mask, &n) != cudaSuccess) return KVQ_ERR_CUDA;
     if (n >= target) {
       occ = target;
       P.stages = stages;
@@ -358,7 +420,7 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
 // shapes reuse it (no occupancy query on the hot path).
 struct PlanKey {
   int dev, dtype, k_mode, v_mode, group_size, head_dim, num_kv_heads, block_size, batch, num_q_heads,
-      q_tokens, max_blocks_per_seq, max_seq_len, no_tc, layout, qt;
+      q_tokens, max_blocks_per_seq, max_seq_len, no_tc, layout, qt, kind;
   bool operator==(const PlanKey& o) const { return std::memcmp(this, &o, sizeof(PlanKey)) == 0; }
 };
 constexpr int kPlanCache = 64;
@@ -367,7 +429,7 @@ Plan g_plans[kPlanCache];
 int g_plan_count = 0, g_plan_next = 0;
 
 kvq_status make_plan(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, Plan* out,
-                     bool qt = false) {
+                     bool qt = false, PlanKind kind = kPlanDecode) {
   PlanKey k;
   std::memset(&k, 0, sizeof k);
   if (cudaGetDevice(&k.dev) != cudaSuccess) return KVQ_ERR_CUDA;
@@ -386,6 +448,7 @@ kvq_status make_plan(const kvq_cache* c, const kvq_decode_params* p, const Devic
   k.no_tc = (p->flags & KVQ_DECODE_NO_TCGEN05) ? 1 : 0;
   k.layout = c->layout;
   k.qt = qt ? 1 : 0;
+  k.kind = (int)kind;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     for (int i = 0; i < g_plan_count; ++i)
@@ -395,7 +458,7 @@ kvq_status make_plan(const kvq_cache* c, const kvq_decode_params* p, const Devic
       }
   }
   Plan P;
-  if (kvq_status s = make_plan_uncached(c, p, dev, qt, &P)) return s;
+  if (kvq_status s = make_plan_uncached(c, p, dev, qt, kind, &P)) return s;
   std::lock_guard<std::mutex> lk(g_mu);
   const int slot = g_plan_count < kPlanCache ? g_plan_count++ : (g_plan_next++ % kPlanCache);
   g_plan_keys[slot] = k;
@@ -498,6 +561,15 @@ kvq_status append_common(const kvq_cache* cache, const kvq_norm_rope* k_prologue
   return from_cuda(launch_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The device side of a masked call: the rule's arrays and the virtual
+// sequences of this launch.
+struct MaskCall {
+  const VSeq* vseq;
+  const float* slopes;
+  const int32_t* key_begin;
+  const int32_t* key_end;
+};
+
 // kvq_decode with the block-table row of sequence b at b / bt_div.  With
 // early_reads 1, q, the block table, seq_lens and the static scales are read
 // before the wait on the preceding grid (KVQ_DECODE_EARLY_INPUTS); with 0,
@@ -505,7 +577,8 @@ kvq_status append_common(const kvq_cache* cache, const kvq_norm_rope* k_prologue
 // sequences, whose lengths that grid writes).
 kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, const void* q,
                        const int32_t* block_table, const int32_t* seq_lens, int bt_div, int early_reads,
-                       bool qt, void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
+                       bool qt, void* workspace, size_t workspace_bytes, kvq_stream_t stream,
+                       const MaskCall* mask = nullptr) {
   kvq_cache eff_;
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
@@ -517,7 +590,7 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   Plan P;
-  if (kvq_status s = make_plan(cache, params, *dev, &P, qt)) return s;
+  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, mask ? kPlanMasked : kPlanDecode)) return s;
   if (workspace_bytes < P.ws_total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
 
   alignas(64) CUtensorMap tk, tv;
@@ -568,10 +641,29 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
   a.part_lse = reinterpret_cast<float*>(ws + P.ws_plan);
   a.part_o = reinterpret_cast<float*>(ws + P.ws_plan + P.ws_lse);
   a.err = dev->err;
+  if (mask) {
+    a.vseq = mask->vseq;
+    a.slopes = mask->slopes;
+    a.key_begin = mask->key_begin;
+    a.key_end = mask->key_end;
+  }
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (P.qt) {
+  if (mask && P.qt) {
+    switch (cache->dtype) {
+      case KVQ_INT8: e = launch_qt_mask_int8(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_qt_mask_fp8(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
+      default: e = launch_qt_mask_int4(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
+    }
+  } else if (mask) {
+    const int nt = kernel_nt(cache, P);
+    switch (cache->dtype) {
+      case KVQ_INT8: e = launch_decode_mask_int8(cache->head_dim, nt, tk, tv, a, P.grid, P.threads, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_decode_mask_fp8(cache->head_dim, nt, tk, tv, a, P.grid, P.threads, P.smem, st); break;
+      default: e = launch_decode_mask_int4(cache->head_dim, nt, tk, tv, a, P.grid, P.threads, P.smem, st); break;
+    }
+  } else if (P.qt) {
     switch (cache->dtype) {
       case KVQ_INT8: e = launch_decode_qt_int8(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
       case KVQ_FP8_E4M3: e = launch_decode_qt_fp8(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
@@ -635,7 +727,7 @@ kvq_status prefill_shape(const kvq_cache* c, const kvq_decode_params* p, kvq_dec
 // prefill's virtual sequences).
 kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params, bool qt, const void* workspace,
                         size_t workspace_bytes, const float* head_sink, void* out, float* lse_out,
-                        kvq_stream_t stream, bool warp_rows = false) {
+                        kvq_stream_t stream, bool warp_rows = false, const MaskCall* mask = nullptr) {
   kvq_cache eff_;
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
@@ -648,7 +740,7 @@ kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params,
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   Plan P;
-  if (kvq_status s = make_plan(cache, params, *dev, &P, qt)) return s;
+  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, mask ? kPlanMasked : kPlanDecode)) return s;
   if (workspace_bytes < P.ws_total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
   const char* ws = static_cast<const char*>(workspace);
   CombineArgs a{};
@@ -675,12 +767,20 @@ kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params,
   // for few rows of many pieces (one long sequence split over the GPU)
   const long long segs = (long long)params->batch * cache->num_kv_heads;
   if ((long long)P.units_max <= 16 * segs) warp_rows = true;
+  if (mask) {
+    a.vseq = mask->vseq;
+    a.slopes = mask->slopes;
+    a.key_begin = mask->key_begin;
+    a.key_end = mask->key_end;
+    a.window = params->window;
+    return from_cuda(launch_combine_masked(a, reinterpret_cast<cudaStream_t>(stream), warp_rows));
+  }
   return from_cuda(launch_combine(a, reinterpret_cast<cudaStream_t>(stream), warp_rows));
 }
 
 
 kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params* params, bool qt,
-                                 size_t* workspace_bytes) {
+                                 size_t* workspace_bytes, bool mask = false) {
   kvq_cache eff_;
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
@@ -689,8 +789,180 @@ kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   Plan P;
-  if (kvq_status s = make_plan(cache, params, *dev, &P, qt)) return s;
+  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, mask ? kPlanMasked : kPlanDecode)) return s;
   *workspace_bytes = P.ws_total;
+  return KVQ_OK;
+}
+
+// A masked call's groups: T tokens of a sequence's C at a time, n groups per
+// sequence, the last one shorter.  The query-tile kernel takes as many tokens
+// as fill its 128 rows when that gives at least 64 rows (the rule kvq_prefill
+// uses); otherwise the mma.sync kernel takes up to 8 (head_dim 576: up to its
+// 48 rows).
+struct MaskShape {
+  int T, n;
+  bool qt;
+  long long groups;  // batch * n
+};
+
+kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, MaskShape* out) {
+  if (!p || p->q_tokens < 1 || p->batch < 0 || p->num_q_heads <= 0) return KVQ_ERR_INVALID_ARG;
+  if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  const int C = p->q_tokens, G = p->num_q_heads / c->num_kv_heads;
+  if (G > 8 || p->batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)p->batch * C > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
+  MaskShape s{};
+  s.T = kQtRows / G < C ? kQtRows / G : C;
+  s.qt = qt_ok(c, p) && s.T * G >= 64;
+  if (!s.qt) {
+    const int most = c->head_dim == 576 && 48 / G < 8 ? 48 / G : 8;
+    s.T = most < C ? most : C;
+  }
+  s.n = (C + s.T - 1) / s.T;
+  s.groups = (long long)p->batch * s.n;
+  if (s.groups > (1LL << 26)) return KVQ_ERR_UNSUPPORTED;
+  *out = s;
+  return KVQ_OK;
+}
+
+// The params of a launch over `count` of the groups.
+kvq_decode_params masked_params(const kvq_decode_params* p, const MaskShape& s, long long count) {
+  kvq_decode_params v = *p;
+  v.batch = (int32_t)count;
+  v.q_tokens = s.T;
+  v.flags &= ~(KVQ_DECODE_EARLY_INPUTS | KVQ_DECODE_EARLY_CACHE);
+  return v;
+}
+
+// Launches of at most kMaxBatch groups follow one another on the stream and
+// share the split workspace behind the table of groups.
+kvq_status masked_workspace(const kvq_cache* c, const kvq_decode_params* p, const MaskShape& s, size_t* head,
+                            size_t* total) {
+  *head = align256((size_t)s.groups * sizeof(VSeq));
+  size_t most = 0;
+  const long long last = s.groups % kMaxBatch;
+  for (long long count : {s.groups >= kMaxBatch ? (long long)kMaxBatch : last, last}) {
+    const kvq_decode_params v = masked_params(p, s, count);
+    size_t ws = 0;
+    if (kvq_status st = decode_workspace_size(c, &v, s.qt, &ws, true)) return st;
+    most = ws > most ? ws : most;
+  }
+  *total = *head + most;
+  return KVQ_OK;
+}
+
+kvq_status check_mask(const kvq_score_mask* m) {
+  if (!m) return KVQ_OK;
+  if ((m->slopes && !aligned(m->slopes, 4)) || (m->key_begin && !aligned(m->key_begin, 4)) ||
+      (m->key_end && !aligned(m->key_end, 4)))
+    return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+// Enqueues the kernel that fills the table of groups.
+kvq_status prepare_groups(const kvq_cache* c, const kvq_decode_params* p, const kvq_score_mask* m,
+                          const int32_t* seq_lens, int T, int n, VSeq* table, unsigned int* err, cudaStream_t st,
+                          bool by_group = false) {
+  VSeqArgs a{};
+  a.seq_lens = seq_lens;
+  a.key_begin = m ? m->key_begin : nullptr;
+  a.key_end = m ? m->key_end : nullptr;
+  a.out = table;
+  a.batch = p->batch;
+  a.C = p->q_tokens;
+  a.T = T;
+  a.n = n;
+  a.window = p->window;
+  a.cap = p->max_blocks_per_seq * c->block_size;
+  a.max_seq_len = p->max_seq_len;
+  a.by_group = by_group ? 1 : 0;
+  a.err = err;
+  return from_cuda(launch_vseq(a, st));
+}
+
+// The key-mass kernel's groups: T tokens (at most 64 query rows) of every
+// sequence at a time, n launches of B groups each.
+struct MassShape {
+  int T, n;
+  kvq_decode_params v;  // one launch
+};
+
+kvq_status mass_shape(const kvq_cache* c, const kvq_decode_params* p, MassShape* out) {
+  if (!p || p->q_tokens < 1 || p->batch < 0 || p->num_q_heads <= 0) return KVQ_ERR_INVALID_ARG;
+  if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  const int C = p->q_tokens, G = p->num_q_heads / c->num_kv_heads;
+  if (G > 8 || p->batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)p->batch * C > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
+  MassShape s{};
+  const int most = (c->head_dim == 576 ? 32 : 64) / G;
+  s.n = (C + most - 1) / most;
+  if ((long long)p->batch * s.n > (1LL << 26)) return KVQ_ERR_UNSUPPORTED;
+  s.T = (C + s.n - 1) / s.n;
+  s.n = (C + s.T - 1) / s.T;
+  s.v = *p;
+  s.v.q_tokens = s.T;
+  s.v.flags &= ~(KVQ_DECODE_EARLY_INPUTS | KVQ_DECODE_EARLY_CACHE);
+  *out = s;
+  return KVQ_OK;
+}
+
+// check_params for a launch whose tokens may exceed a decode's eight.
+kvq_status check_mass_params(const kvq_cache* c, const kvq_decode_params* p) {
+  kvq_decode_params one = *p;
+  one.q_tokens = 1;
+  return check_params(c, &one);
+}
+
+// Host checks of an eviction's shapes.
+kvq_status check_evict(const kvq_evict_params* p) {
+  if (!p) return KVQ_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->max_blocks_per_seq <= 0 || p->max_seq_len < 0 || p->num_blocks <= 0 ||
+      p->num_kv_heads <= 0 || p->budget < 1 || p->sinks < 0 || p->recent < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (!pow2(p->block_size) || p->block_size < 16 || p->block_size > (1 << 20)) return KVQ_ERR_INVALID_ARG;
+  if ((long long)p->sinks + p->recent > p->budget) return KVQ_ERR_INVALID_ARG;
+  if ((long long)p->num_blocks * p->block_size > (1LL << 31) - 1) return KVQ_ERR_INVALID_ARG;
+  const long long cap = (long long)p->max_blocks_per_seq * p->block_size;
+  if (cap > (1LL << 30)) return KVQ_ERR_INVALID_ARG;
+  if (p->budget > cap) return KVQ_ERR_INVALID_ARG;
+  if ((long long)p->batch * p->num_kv_heads > (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+// Launch shape of kvq_evict_compact: units of up to 128 rows and about 32 KB,
+// two CTAs per SM with as many ring stages as fit.
+struct CompactPlan {
+  int rows, stages, stage_bytes, grid, units;
+  size_t smem, ws;
+};
+
+kvq_status compact_plan(const kvq_cache* c, const kvq_evict_params* p, bool mass, const DeviceInfo& dev,
+                        CompactPlan* out) {
+  if (c->num_blocks != p->num_blocks || c->block_size != p->block_size || c->num_kv_heads != p->num_kv_heads)
+    return KVQ_ERR_INVALID_ARG;
+  CompactPlan P{};
+  const int sides = c->layout == KVQ_LAYOUT_LATENT ? 1 : 2, rb = row_bytes(c);
+  const int nf = scales_per_row(c, c->k_mode) + (sides == 2 ? scales_per_row(c, c->v_mode) : 0) + (mass ? 1 : 0);
+  P.rows = kCompactRows;
+  while (P.rows > 16 && P.rows * rb * sides > 32 * 1024) P.rows >>= 1;
+  P.stage_bytes = (P.rows * (rb * sides + 4 * nf) + 127) / 128 * 128;
+  constexpr int kCtas = 2;
+  const int budget = 228 * 1024 / kCtas - 2048;
+  P.stages = budget / P.stage_bytes;
+  P.stages = P.stages > kCompactStages ? kCompactStages : P.stages;
+  if (P.stages < 2) return KVQ_ERR_UNSUPPORTED;
+  P.smem = (size_t)P.stages * P.stage_bytes;
+  const long long chunks = (p->budget + P.rows - 1) / P.rows;
+  const long long units = chunks * p->batch * p->num_kv_heads;
+  if (units > (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
+  P.units = (int)units;
+  int n = 0;
+  if (occupancy_evict_compact(P.smem, &n) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (n < 1) return KVQ_ERR_UNSUPPORTED;
+  const long long most = (long long)dev.sms * (n < kCtas ? n : kCtas);
+  P.grid = (int)(units < most ? (units > 0 ? units : 1) : most);
+  P.ws = align256((size_t)((P.units + P.grid - 1) / P.grid + 1) * 4);
+  *out = P;
   return KVQ_OK;
 }
 
@@ -812,6 +1084,287 @@ KVQ_API kvq_status kvq_prefill(const kvq_cache* cache, const kvq_decode_params* 
     return s;
   // a chunk's B x C x Hq rows have few pieces each: one warp per row
   return combine_impl(cache, &v, qt, ws, workspace_bytes - head, head_sink, out, lse_out, stream, true);
+}
+
+KVQ_API kvq_status kvq_attend_masked_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
+                                                    size_t* workspace_bytes) {
+  if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  MaskShape shape;
+  if (kvq_status s = masked_shape(&eff_, params, &shape)) return s;
+  size_t head = 0;
+  return masked_workspace(&eff_, params, shape, &head, workspace_bytes);
+}
+
+KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_params* params,
+                                     const kvq_score_mask* mask, const void* q, const int32_t* block_table,
+                                     const int32_t* seq_lens, const float* head_sink, void* out, float* lse_out,
+                                     void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  cache = &eff_;
+  MaskShape shape;
+  if (kvq_status s = masked_shape(cache, params, &shape)) return s;
+  {
+    const kvq_decode_params v = masked_params(params, shape, shape.groups < kMaxBatch ? shape.groups : kMaxBatch);
+    if (kvq_status s = check_params(cache, &v, shape.qt)) return s;
+  }
+  if (params->flags & ~(KVQ_DECODE_EARLY_INPUTS | KVQ_DECODE_NO_TCGEN05 | KVQ_DECODE_EARLY_CACHE))
+    return KVQ_ERR_INVALID_ARG;
+  if (kvq_status s = check_mask(mask)) return s;
+  if (params->batch == 0) return KVQ_OK;
+  if (!q || !block_table || !seq_lens || !workspace || !out) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256) ||
+      !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)) || (head_sink && !aligned(head_sink, 4)))
+    return KVQ_ERR_INVALID_ARG;
+  size_t head = 0, need = 0;
+  if (kvq_status s = masked_workspace(cache, params, shape, &head, &need)) return s;
+  if (workspace_bytes < need) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  VSeq* table = static_cast<VSeq*>(workspace);
+  if (kvq_status s = prepare_groups(cache, params, mask, seq_lens, shape.T, shape.n, table, dev->err,
+                                    reinterpret_cast<cudaStream_t>(stream)))
+    return s;
+  char* ws = static_cast<char*>(workspace) + head;
+  MaskCall mc{table, mask ? mask->slopes : nullptr, mask ? mask->key_begin : nullptr, mask ? mask->key_end : nullptr};
+  for (long long v0 = 0; v0 < shape.groups; v0 += kMaxBatch) {
+    const long long left = shape.groups - v0;
+    const kvq_decode_params v = masked_params(params, shape, left < kMaxBatch ? left : kMaxBatch);
+    mc.vseq = table + v0;
+    if (kvq_status s = decode_impl(cache, &v, q, block_table, seq_lens, 1, 0, shape.qt, ws, workspace_bytes - head,
+                                   stream, &mc))
+      return s;
+    if (kvq_status s = combine_impl(cache, &v, shape.qt, ws, workspace_bytes - head, head_sink, out, lse_out, stream,
+                                    shape.n > 1, &mc))
+      return s;
+  }
+  return KVQ_OK;
+}
+
+KVQ_API kvq_status kvq_key_mass_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
+                                               size_t* workspace_bytes) {
+  if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  MassShape shape;
+  if (kvq_status s = mass_shape(&eff_, params, &shape)) return s;
+  if (kvq_status s = check_mass_params(&eff_, &shape.v)) return s;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  Plan P;
+  if (kvq_status s = make_plan(&eff_, &shape.v, *dev, &P, false, kPlanMass)) return s;
+  *workspace_bytes = align256((size_t)params->batch * shape.n * sizeof(VSeq)) + P.ws_total;
+  return KVQ_OK;
+}
+
+KVQ_API kvq_status kvq_key_mass(const kvq_cache* cache, const kvq_decode_params* params, const kvq_score_mask* mask,
+                                const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                                const float* lse, float decay, int32_t fresh, float* mass, void* workspace,
+                                size_t workspace_bytes, kvq_stream_t stream) {
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  cache = &eff_;
+  MassShape shape;
+  if (kvq_status s = mass_shape(cache, params, &shape)) return s;
+  if (kvq_status s = check_mass_params(cache, &shape.v)) return s;
+  if (!(decay >= 0.0f && decay <= 1.0f) || fresh < 0) return KVQ_ERR_INVALID_ARG;
+  if (kvq_status s = check_mask(mask)) return s;
+  if (params->batch == 0) return KVQ_OK;
+  if (!q || !block_table || !seq_lens || !lse || !mass || !workspace) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+      !aligned(mass, 4) || !aligned(workspace, 256))
+    return KVQ_ERR_INVALID_ARG;
+  size_t need = 0;
+  if (kvq_status s = kvq_key_mass_workspace_size(cache, params, &need)) return s;
+  if (workspace_bytes < need) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  Plan P;
+  if (kvq_status s = make_plan(cache, &shape.v, *dev, &P, false, kPlanMass)) return s;
+  alignas(64) CUtensorMap tk;
+  if (kvq_status s = encode_codes_map(cache, cache->k_codes, &tk)) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  VSeq* table = static_cast<VSeq*>(workspace);
+  if (kvq_status s = prepare_groups(cache, params, mask, seq_lens, shape.T, shape.n, table, dev->err, st, true))
+    return s;
+
+  DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.k_scale = cache->k_scale;
+  a.k_mode = cache->k_mode;
+  a.sk_n = scales_per_row(cache, cache->k_mode);
+  a.log2_gs = cache->k_mode == KVQ_SCALE_PER_GROUP ? ilog2(cache->group_size) : 0;
+  a.num_blocks = cache->num_blocks;
+  a.block_size = cache->block_size;
+  a.log2_bs = ilog2(cache->block_size);
+  a.num_kv_heads = cache->num_kv_heads;
+  a.batch = params->batch;
+  a.num_q_heads = params->num_q_heads;
+  a.q_tokens = shape.T;
+  a.group = params->num_q_heads / cache->num_kv_heads;
+  a.rows = P.rows;
+  a.max_blocks_per_seq = params->max_blocks_per_seq;
+  a.max_seq_len = params->max_seq_len;
+  a.sm_scale = params->sm_scale > 0.0f ? params->sm_scale : 1.0f / std::sqrt((float)cache->head_dim);
+  a.softcap = params->softcap;
+  a.window = params->window;
+  a.stages = P.stages;
+  a.stage_stride = (int)P.stride;
+  a.piece_cost = kPieceCost;
+  a.bt_div = 1;
+  a.v_alias = 1;  // a stage holds the K side only
+  a.plan = reinterpret_cast<int*>(static_cast<char*>(workspace) +
+                                  align256((size_t)params->batch * shape.n * sizeof(VSeq)));
+  a.err = dev->err;
+  a.slopes = mask ? mask->slopes : nullptr;
+  a.key_begin = mask ? mask->key_begin : nullptr;
+  a.key_end = mask ? mask->key_end : nullptr;
+  MassArgs m{lse, mass, decay, fresh};
+
+  // keys that the launches below do not hold, or (several launches, each
+  // adding to the last) all of them, take their decay first
+  const long long cap = (long long)params->max_blocks_per_seq * cache->block_size;
+  const int maxlen = (int)((params->max_seq_len > 0 && params->max_seq_len < cap) ? params->max_seq_len : cap);
+  a.vseq = table;
+  const bool several = shape.n > 1;
+  if (several || params->window > 0 || a.key_begin || a.key_end) {
+    if (cudaError_t e = launch_mass_rest(a, m, several, maxlen, st)) return from_cuda(e);
+  }
+  if (several) {
+    m.decay = 1.0f;
+    m.fresh = 0;
+  }
+  for (int j = 0; j < shape.n; ++j) {
+    a.vseq = table + (size_t)j * params->batch;
+    cudaError_t e;
+    switch (cache->dtype) {
+      case KVQ_INT8: e = launch_key_mass_int8(cache->head_dim, P.nt, tk, a, m, P.grid, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_key_mass_fp8(cache->head_dim, P.nt, tk, a, m, P.grid, P.smem, st); break;
+      default: e = launch_key_mass_int4(cache->head_dim, P.nt, tk, a, m, P.grid, P.smem, st); break;
+    }
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  return KVQ_OK;
+}
+
+KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float* mass, const int32_t* block_table,
+                                    const int32_t* seq_lens, int32_t* keep, int32_t* kept_lens,
+                                    kvq_stream_t stream) {
+  if (kvq_status s = check_evict(params)) return s;
+  if (params->batch == 0) return KVQ_OK;
+  if (!mass || !block_table || !seq_lens || !keep || !kept_lens) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(mass, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(keep, 4) ||
+      !aligned(kept_lens, 4) || kept_lens == seq_lens)
+    return KVQ_ERR_INVALID_ARG;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  SelectArgs a{};
+  a.mass = mass;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.keep = keep;
+  a.kept_lens = kept_lens;
+  a.batch = params->batch;
+  a.num_kv_heads = params->num_kv_heads;
+  a.max_blocks_per_seq = params->max_blocks_per_seq;
+  a.num_blocks = params->num_blocks;
+  a.block_size = params->block_size;
+  a.log2_bs = ilog2(params->block_size);
+  const long long cap = (long long)params->max_blocks_per_seq * params->block_size;
+  a.lim = (int)((params->max_seq_len > 0 && params->max_seq_len < cap) ? params->max_seq_len : cap);
+  a.budget = params->budget;
+  a.sinks = params->sinks;
+  a.recent = params->recent;
+  a.err = dev->err;
+  // parts of at least 2048 rows, up to 16 of them, as long as more of them
+  // find free SMs; more parts when a part would not fit in shared memory
+  constexpr int kMostResident = 48 * 1024;
+  const long long segs = (long long)params->batch * params->num_kv_heads;
+  const long long rows = a.lim;
+  int cluster = 1;
+  while (cluster < 16 && rows / (2 * cluster) >= 2048 && (segs * cluster < dev->sms || rows / cluster > 16384))
+    cluster *= 2;
+  const long long part = (rows + cluster - 1) / cluster;
+  a.resident = (int)(part < kMostResident ? part : kMostResident);
+  a.resident = (a.resident + 3) & ~3;
+  if (segs * cluster > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
+  return from_cuda(launch_evict_select(a, cluster, select_smem(a.resident), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+KVQ_API kvq_status kvq_evict_compact_workspace_size(const kvq_cache* cache, const kvq_evict_params* params,
+                                                    size_t* workspace_bytes) {
+  if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  if (kvq_status s = check_evict(params)) return s;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  CompactPlan P;
+  if (kvq_status s = compact_plan(&eff_, params, true, *dev, &P)) return s;
+  *workspace_bytes = P.ws;
+  return KVQ_OK;
+}
+
+KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_params* params,
+                                     const int32_t* block_table, const int32_t* dst_table, const int32_t* keep,
+                                     const int32_t* kept_lens, float* mass, void* workspace,
+                                     size_t workspace_bytes, kvq_stream_t stream) {
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  cache = &eff_;
+  if (kvq_status s = check_evict(params)) return s;
+  if (cache->num_blocks != params->num_blocks || cache->block_size != params->block_size ||
+      cache->num_kv_heads != params->num_kv_heads)
+    return KVQ_ERR_INVALID_ARG;
+  if (params->batch == 0) return KVQ_OK;
+  if (!block_table || !keep || !kept_lens || !workspace) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || (dst_table && !aligned(dst_table, 4)) || !aligned(keep, 4) ||
+      !aligned(kept_lens, 4) || (mass && !aligned(mass, 4)) || !aligned(workspace, 256))
+    return KVQ_ERR_INVALID_ARG;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  CompactPlan P;  // (the plan with a weight array, whether or not there is one: its workspace was asked for)
+  if (kvq_status s = compact_plan(cache, params, true, *dev, &P)) return s;
+  if (workspace_bytes < P.ws) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  CompactArgs a{};
+  a.block_table = block_table;
+  a.in_place = !dst_table || dst_table == block_table;
+  a.dst_table = a.in_place ? block_table : dst_table;
+  a.keep = keep;
+  a.kept_lens = kept_lens;
+  a.sides = cache->layout == KVQ_LAYOUT_LATENT ? 1 : 2;
+  a.codes[0] = static_cast<uint8_t*>(cache->k_codes);
+  a.codes[1] = static_cast<uint8_t*>(cache->v_codes);
+  a.scale[0] = cache->k_scale;
+  a.scale[1] = cache->v_scale;
+  a.n_scale[0] = scales_per_row(cache, cache->k_mode);
+  a.n_scale[1] = a.sides == 2 ? scales_per_row(cache, cache->v_mode) : 0;
+  a.mass = mass;
+  a.row_bytes = row_bytes(cache);
+  a.batch = params->batch;
+  a.num_kv_heads = params->num_kv_heads;
+  a.max_blocks_per_seq = params->max_blocks_per_seq;
+  a.num_blocks = params->num_blocks;
+  a.block_size = params->block_size;
+  a.log2_bs = ilog2(params->block_size);
+  a.budget = params->budget;
+  a.rows = P.rows;
+  a.log2_rows = ilog2(P.rows);
+  a.stages = P.stages;
+  a.stage_bytes = P.stage_bytes;
+  a.units = P.units;
+  a.round_count = static_cast<unsigned int*>(workspace);
+  a.err = dev->err;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.in_place) {
+    const int rounds = (P.units + P.grid - 1) / P.grid;
+    if (cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)rounds * 4, st)) return from_cuda(e);
+  }
+  return from_cuda(launch_evict_compact(a, P.grid, P.smem, st));
 }
 
 KVQ_API kvq_status kvq_check_wait_timeout(uint32_t limit_us, kvq_stream_t stream) {

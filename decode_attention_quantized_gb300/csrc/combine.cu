@@ -13,24 +13,64 @@
 
 #include "kvq_internal.h"
 #include "ptx.cuh"
+#include "score_rule.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kCombineWarps = 8;
 
+// What a combine row is: its (virtual) sequence b, query head hq, kv head h,
+// row r inside the work unit, and its place `out_row` in [B, T, Hq].
+struct CombineRow {
+  int b, t, hq, h, r;
+  size_t out_row;
+  bool live;
+};
+
+template <bool MASK>
+__device__ __forceinline__ CombineRow combine_row(const CombineArgs& a, int row_id) {
+  CombineRow c;
+  c.hq = row_id % a.num_q_heads;
+  c.t = (row_id / a.num_q_heads) % a.q_tokens;
+  c.b = row_id / (a.num_q_heads * a.q_tokens);
+  c.h = c.hq / a.group;
+  c.r = c.t * a.group + (c.hq % a.group);
+  c.out_row = (size_t)row_id;
+  c.live = true;
+  if constexpr (MASK) {
+    c.live = c.t < a.vseq[c.b].ntok;
+    c.out_row = ((size_t)a.vseq[c.b].tok0 + c.t) * a.num_q_heads + c.hq;
+  }
+  return c;
+}
+
+// The bias at a masked row's anchor distance, which its partials leave out of
+// the scores (score_rule.cuh), in natural-log units.
+__device__ __forceinline__ float anchor_bias(const CombineArgs& a, const CombineRow& c) {
+  if (!a.slopes) return 0.0f;
+  const VSeq& v = a.vseq[c.b];
+  int begin, end;
+  const int pos = v.pos0 + c.t;
+  dev::row_range(a.key_begin, a.key_end, a.window, (size_t)v.tok0 + c.t, pos, v.hi, begin, end);
+  const float s = a.slopes[c.hq];
+  return -s * (float)dev::row_anchor(s, pos, begin, end);
+}
+
 // The end of one row (every lane of one warp): the merged output acc (this
 // lane's E channels) and weight sum against the row maximum m, the head sink,
 // the static V scale, the bf16 store and the natural-log LSE.
-template <int D>
-__device__ __forceinline__ void combine_finish(const CombineArgs& a, int row_id, int hq, int h, int lane,
+template <int D, bool MASK>
+__device__ __forceinline__ void combine_finish(const CombineArgs& a, const CombineRow& c, int lane,
                                                float (&acc)[D / 32], float wsum, float m) {
+  const int hq = c.hq, h = c.h;
   constexpr int E = D / 32;
   float lse_nat = -INFINITY;
   if (wsum > 0.0f) {
     const float inv = 1.0f / wsum;
     const float lse2 = m + ptx::fast_log2(wsum);
     lse_nat = lse2 * 0.69314718055994530942f;
+    if constexpr (MASK) lse_nat += anchor_bias(a, c);
     float f = inv;
     if (a.head_sink) f = inv / (1.0f + expf(a.head_sink[hq] - lse_nat));
 #pragma unroll
@@ -52,9 +92,9 @@ __device__ __forceinline__ void combine_finish(const CombineArgs& a, int row_id,
     const __nv_bfloat162 v = __floats2bfloat162_rn(acc[e], acc[e + 1]);
     packed[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  if (a.lse_out && lane == 0) a.lse_out[row_id] = lse_nat;
+  if (a.lse_out && lane == 0) a.lse_out[c.out_row] = lse_nat;
   if (lane * E >= a.out_dim) return;  // LATENT: only the leading v_head_size channels
-  uint16_t* dst = a.out + (size_t)row_id * a.out_dim + lane * E;
+  uint16_t* dst = a.out + c.out_row * a.out_dim + lane * E;
   if constexpr (E == 8) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
   } else if constexpr (E == 4) {
@@ -74,7 +114,7 @@ __device__ __forceinline__ void combine_finish(const CombineArgs& a, int row_id,
 // warp 0 adds the eight warp sums in warp order.  Every split's weight is
 // taken against the row's maximum log-sum-exp, so the result does not depend
 // on how splits are spread over warps beyond that fixed order.
-template <int D>
+template <int D, bool MASK>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineArgs a) {
   constexpr int E = D / 32;
   __shared__ float s_acc[kCombineWarps][D];
@@ -83,12 +123,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row_id = blockIdx.x;
-  const int hq = row_id % a.num_q_heads;
-  const int t = (row_id / a.num_q_heads) % a.q_tokens;
-  const int b = row_id / (a.num_q_heads * a.q_tokens);
-  const int h = hq / a.group;
-  const int r = t * a.group + (hq % a.group);  // row inside a work unit
+  const CombineRow row = combine_row<MASK>(a, (int)blockIdx.x);
+  if (MASK && !row.live) return;  // the whole CTA
+  const int b = row.b, h = row.h, r = row.r;
 
   // pieces of segment s = b * Hkv + h are the CTAs whose cost ranges [x W,
   // (x + 1) W) meet the segment's tiles, which sit at cost positions
@@ -158,7 +195,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
     for (int e = 0; e < E; ++e) acc[e] += s_acc[w][lane * E + e];
   }
 
-  combine_finish<D>(a, row_id, hq, h, lane, acc, wsum, m);
+  combine_finish<D, MASK>(a, row, lane, acc, wsum, m);
 }
 
 // One warp per output row, kCombineWarps rows a CTA: for calls with many rows
@@ -166,7 +203,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
 // batch), where a CTA per row leaves the GPU waiting on launch and latency
 // and takes room the next step's decode could use.  The row's pieces are
 // folded in slot order against the row's maximum, then combine_finish.
-template <int D>
+template <int D, bool MASK>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_rows_kernel(const CombineArgs a) {
   constexpr int E = D / 32;
   ptx::griddep_wait();
@@ -174,12 +211,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_rows_kernel(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row_ll = (long long)blockIdx.x * kCombineWarps + warp;
   if (row_ll >= (long long)a.batch * a.q_tokens * a.num_q_heads) return;
-  const int row_id = (int)row_ll;
-  const int hq = row_id % a.num_q_heads;
-  const int t = (row_id / a.num_q_heads) % a.q_tokens;
-  const int b = row_id / (a.num_q_heads * a.q_tokens);
-  const int h = hq / a.group;
-  const int r = t * a.group + (hq % a.group);
+  const CombineRow row = combine_row<MASK>(a, (int)row_ll);
+  if (MASK && !row.live) return;  // the whole warp
+  const int b = row.b, h = row.h, r = row.r;
   const int W = a.plan[0], c = a.plan[2];
   const int* pre = a.plan + 4;
   const int nb = pre[b + 1] - pre[b];
@@ -248,7 +282,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_rows_kernel(const 
       }
     }
   }
-  combine_finish<D>(a, row_id, hq, h, lane, acc, wsum, m);
+  combine_finish<D, MASK>(a, row, lane, acc, wsum, m);
 }
 
 // Sequence lengths of a prefill chunk's virtual sequences (one thread each).
@@ -287,27 +321,38 @@ cudaError_t launch_prefill_lens(const int32_t* seq_lens, int32_t* out, int batch
                     n, C, T);
 }
 
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream, bool warp_rows) {
+namespace {
+template <bool MASK>
+cudaError_t launch_combine_m(const CombineArgs& a, cudaStream_t stream, bool warp_rows) {
   const long long rows = (long long)a.batch * a.q_tokens * a.num_q_heads;
   constexpr int threads = kCombineWarps * 32;
   if (warp_rows) {
     const unsigned blocks = (unsigned)((rows + kCombineWarps - 1) / kCombineWarps);
     switch (a.head_dim) {
-      case 64: return launch_pdl(combine_rows_kernel<64>, blocks, threads, 0, stream, a);
-      case 128: return launch_pdl(combine_rows_kernel<128>, blocks, threads, 0, stream, a);
-      case 256: return launch_pdl(combine_rows_kernel<256>, blocks, threads, 0, stream, a);
-      case 576: return launch_pdl(combine_rows_kernel<576>, blocks, threads, 0, stream, a);
+      case 64: return launch_pdl(combine_rows_kernel<64, MASK>, blocks, threads, 0, stream, a);
+      case 128: return launch_pdl(combine_rows_kernel<128, MASK>, blocks, threads, 0, stream, a);
+      case 256: return launch_pdl(combine_rows_kernel<256, MASK>, blocks, threads, 0, stream, a);
+      case 576: return launch_pdl(combine_rows_kernel<576, MASK>, blocks, threads, 0, stream, a);
       default: return cudaErrorInvalidValue;
     }
   }
   const unsigned blocks = (unsigned)rows;
   switch (a.head_dim) {
-    case 64: return launch_pdl(combine_kernel<64>, blocks, threads, 0, stream, a);
-    case 128: return launch_pdl(combine_kernel<128>, blocks, threads, 0, stream, a);
-    case 256: return launch_pdl(combine_kernel<256>, blocks, threads, 0, stream, a);
-    case 576: return launch_pdl(combine_kernel<576>, blocks, threads, 0, stream, a);
+    case 64: return launch_pdl(combine_kernel<64, MASK>, blocks, threads, 0, stream, a);
+    case 128: return launch_pdl(combine_kernel<128, MASK>, blocks, threads, 0, stream, a);
+    case 256: return launch_pdl(combine_kernel<256, MASK>, blocks, threads, 0, stream, a);
+    case 576: return launch_pdl(combine_kernel<576, MASK>, blocks, threads, 0, stream, a);
     default: return cudaErrorInvalidValue;
   }
+}
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream, bool warp_rows) {
+  return launch_combine_m<false>(a, stream, warp_rows);
+}
+
+cudaError_t launch_combine_masked(const CombineArgs& a, cudaStream_t stream, bool warp_rows) {
+  return launch_combine_m<true>(a, stream, warp_rows);
 }
 
 }  // namespace kvq

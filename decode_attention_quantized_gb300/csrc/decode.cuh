@@ -39,6 +39,7 @@
 #include "kvq_internal.h"
 #include "pipeline.cuh"
 #include "ptx.cuh"
+#include "score_rule.cuh"
 
 namespace kvq {
 
@@ -66,6 +67,12 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What the f16 pair `hi` = pack_h2(a, b) leaves of a and b, as f16.
+__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return pack_h2(a - f.x, b - f.y);
 }
 
 // Exact code -> f16 conversions producing MMA operand pairs (low half first).
@@ -164,17 +171,21 @@ __device__ __forceinline__ int out_channel(int mt, int e, int g) {
 // its full mantissa.  Returns the logit factor for the row (sm_scale, tensor
 // scale, both powers of two; times log2 e when no softcap follows),
 // clamped to FLT_MAX so zero codes under a huge scale stay zero.  Rows past
-// a.rows get q = 0.  Every lane of the warp must call it.
-template <int DT, int D>
-__device__ __forceinline__ float q_prologue(const DecodeArgs& a, int rq, int b, int h, int c,
-                                            uint32_t (&qf)[D / 16][2]) {
+// `rows` get q = 0.  Every lane of the warp must call it.
+// tok0: index of the piece's first query token; rows: its query rows.  SPLIT:
+// ql gets the f16 remainders of the rounded operand values, so that qf + ql
+// carries q * s to 2^-22 (the key-mass kernel, whose fp32 result would show
+// the 2^-12 that the folded scale's rounding leaves in a logit).
+template <int DT, int D, bool SPLIT = false>
+__device__ __forceinline__ float q_prologue(const DecodeArgs& a, int rq, size_t tok0, int rows, int h, int c,
+                                            uint32_t (&qf)[D / 16][2], uint32_t (*ql)[2] = nullptr) {
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr int CPL = (DT == KVQ_INT4) ? 8 : 4;  // channels per 16-byte code chunk per lane
   constexpr int NQC = D / (4 * CPL);             // code chunks per row
-  const int G = a.group, T = a.q_tokens, Hq = a.num_q_heads;
-  const bool qvalid = rq < a.rows;
+  const int G = a.group, Hq = a.num_q_heads;
+  const bool qvalid = rq < rows;
   const int tq = qvalid ? div_small(rq, __frcp_rn((float)G)) : 0, gq = qvalid ? rq - tq * G : 0;
-  const uint16_t* qp = a.q + (((size_t)b * T + tq) * Hq + (size_t)h * G + gq) * D;
+  const uint16_t* qp = a.q + ((tok0 + tq) * Hq + (size_t)h * G + gq) * D;
   float qv[NQC][CPL];
 #pragma unroll
   for (int j = 0; j < NQC; ++j) {
@@ -230,10 +241,18 @@ __device__ __forceinline__ float q_prologue(const DecodeArgs& a, int rq, int b, 
       for (int t = 0; t < 2; ++t) {
         qf[2 * j + t][0] = pack_h2(qv[j][2 * t] * sq, qv[j][2 * t + 4] * sq);
         qf[2 * j + t][1] = pack_h2(qv[j][2 * t + 1] * sq, qv[j][2 * t + 5] * sq);
+        if constexpr (SPLIT) {
+          ql[2 * j + t][0] = rest_h2(qv[j][2 * t] * sq, qv[j][2 * t + 4] * sq, qf[2 * j + t][0]);
+          ql[2 * j + t][1] = rest_h2(qv[j][2 * t + 1] * sq, qv[j][2 * t + 5] * sq, qf[2 * j + t][1]);
+        }
       }
     } else {
       qf[j][0] = pack_h2(qv[j][0] * sq, qv[j][1] * sq);
       qf[j][1] = pack_h2(qv[j][2] * sq, qv[j][3] * sq);
+      if constexpr (SPLIT) {
+        ql[j][0] = rest_h2(qv[j][0] * sq, qv[j][1] * sq, qf[j][0]);
+        ql[j][1] = rest_h2(qv[j][2] * sq, qv[j][3] * sq, qf[j][1]);
+      }
     }
   }
   float base = a.sm_scale;
@@ -257,7 +276,10 @@ __host__ __device__ constexpr int wide_scratch_floats() {
 // GS > 0: the grouped layout with the per-group scale paths for groups of GS
 // channels compiled in (a kernel of its own per group size, so that its
 // group boundaries are compile-time and the other modes carry none of it).
-template <int DT, int D, int MINB, int NT, int GS>
+// MASK: the score rule of a masked call (distance bias, an interval of keys
+// per query token) over its virtual sequences, in kernels of its own so that
+// the unmasked ones carry none of it.
+template <int DT, int D, int MINB, int NT, int GS, bool MASK>
 __global__ void __launch_bounds__(288, MINB)
     decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const DecodeArgs a) {
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(288, MINB)
   // cache read and the consumers before their first workspace write, so the
   // plan, the first block ids and the Q prologue overlap that grid's tail.
   // Without them build_slice waits first.
-  const Slice<kTile> sp = build_slice<kTile>(a, pl_pre, pl_misc);
+  const Slice<kTile, MASK> sp = build_slice<kTile, MASK>(a, pl_pre, pl_misc);
   const int t_begin = sp.t_begin, t_end = sp.t_end;
   auto piece = [&](int gt, int& b, int& h, int& k0, int& k1, int& L, int& slot, int& next) {
     sp.piece(a, gt, b, h, k0, k1, L, slot, next);
@@ -303,7 +325,7 @@ __global__ void __launch_bounds__(288, MINB)
 
   // =============================================================== producer
   if (warp == n_cw) {
-    produce<Gm, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    produce<Gm, true, MASK>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
     return;
   }
 
@@ -354,13 +376,15 @@ __global__ void __launch_bounds__(288, MINB)
     for (int gt = t_begin, next; gt < t_end; gt = next) {
       int b, h, k0, k1, L, u;
       piece(gt, b, h, k0, k1, L, u, next);
+      const size_t tok0 = MASK ? (size_t)a.vseq[b].tok0 : (size_t)b * T;
+      const int rows = MASK ? a.vseq[b].ntok * G : a.rows;
       // Q of n-tile kq of this half (warps kq < NT), stored in k-slot order so
       // that ldmatrix yields the B fragments; the rows' logit factors beside it
       if constexpr (D <= 256) {
         if (kq < NT) {
           const int row = rh * RW + kq * 8 + g;
           uint32_t qf[Gm::NMT][2];
-          const float ag = dev::q_prologue<DT, D>(a, row, b, h, c, qf);
+          const float ag = dev::q_prologue<DT, D>(a, row, tok0, rows, h, c, qf);
 #pragma unroll
           for (int ks = 0; ks < Gm::NMT; ++ks) {
             ptx::st_shared_u32(q_base + q_off(row, ks * 16 + 2 * c), qf[ks][0]);
@@ -379,7 +403,7 @@ __global__ void __launch_bounds__(288, MINB)
         const float* ksp = a.k_scale + (size_t)h * D;
         auto row_ptr = [&](int r) {
           const int tq = dev::div_small(r, inv_g), gq = r - tq * G;
-          return a.q + (((size_t)b * T + tq) * a.num_q_heads + (size_t)h * G + gq) * D;
+          return a.q + ((tok0 + tq) * a.num_q_heads + (size_t)h * G + gq) * D;
         };
         auto load4 = [&](const uint16_t* qp, int j, float (&v)[4]) {
           const uint2 w = *reinterpret_cast<const uint2*>(qp + 16 * j + 4 * c);
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(288, MINB)
         for (int nt = 0; nt < NT; ++nt) {
           const int r = rh * RW + nt * 8 + g;
           float m = 0.0f;
-          if (r < a.rows) {
+          if (r < rows) {
             const uint16_t* qp = row_ptr(r);
 #pragma unroll 3
             for (int j = kq * KQ; j < (kq + 1) * KQ; ++j) {
@@ -435,11 +459,11 @@ __global__ void __launch_bounds__(288, MINB)
           const float qm = fmaxf(fmaxf(s_max[r], s_max[ROWS + r]), fmaxf(s_max[2 * ROWS + r], s_max[3 * ROWS + r])) * sk;
           const int eq = qm > 0.0f ? min(126, max(-126, dev::ceil_log2(qm))) : 0;
           const float sq = dev::pow2i(-eq);
-          const uint16_t* qp = row_ptr(r < a.rows ? r : 0);
+          const uint16_t* qp = row_ptr(r < rows ? r : 0);
 #pragma unroll 3
           for (int j = kq * KQ; j < (kq + 1) * KQ; ++j) {
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (r < a.rows) load4(qp, j, v);
+            if (r < rows) load4(qp, j, v);
             if (kc) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) v[i] *= ksp[16 * j + 4 * c + i] * sk;
@@ -456,13 +480,20 @@ __global__ void __launch_bounds__(288, MINB)
       ptx::named_bar_sync(1, 8 * 32);
       float al[NT][2], m[NT][2], l[NT][2];
       int pos[NT][2];
+      dev::RowRule rule[MASK ? NT : 1][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = rh * RW + nt * 8 + 2 * c + i;
           al[nt][i] = s_alpha[r];
-          pos[nt][i] = r < a.rows ? L - T + dev::div_small(r, inv_g) : -1;
+          if constexpr (MASK) {
+            const int rr = r < rows ? r : 0, t = dev::div_small(rr, inv_g);
+            rule[nt][i] = dev::row_rule(a, tok0 + t, a.vseq[b].pos0 + t, h * G + rr - t * G, L);
+            pos[nt][i] = 0;
+          } else {
+            pos[nt][i] = r < rows ? L - T + dev::div_small(r, inv_g) : -1;
+          }
           m[nt][i] = -INFINITY;
           l[nt][i] = 0.0f;
         }
@@ -582,12 +613,30 @@ __global__ void __launch_bounds__(288, MINB)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = e < 2 ? key_a : key_b, p = pos[nt][e & 1];
-              if (!(key <= p && (W == 0 || key > p - W))) x[nt][e] = -INFINITY;
+              if constexpr (MASK) {
+                const dev::RowRule& ru = rule[nt][e & 1];
+                if (a.slopes) x[nt][e] = fmaf(ru.ns, (float)(abs(ru.pos - key) - ru.d0), x[nt][e]);
+                if (!(key >= ru.begin && key < ru.end)) x[nt][e] = -INFINITY;
+              } else {
+                if (!(key <= p && (W == 0 || key > p - W))) x[nt][e] = -INFINITY;
+              }
             }
           }
           if (v_row) {
-            vpa = key_a < L ? vs_row[kq * kSub + g] : 0.0f;
-            vpb = key_b < L ? vs_row[kq * kSub + g + 8] : 0.0f;
+            bool use_a = key_a < L, use_b = key_b < L;
+            if constexpr (MASK) {
+              // a row that none of this lane's query rows sees may hold anything
+              use_a = use_b = false;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  use_a = use_a || (key_a >= rule[nt][i].begin && key_a < rule[nt][i].end);
+                  use_b = use_b || (key_b >= rule[nt][i].begin && key_b < rule[nt][i].end);
+                }
+            }
+            vpa = use_a ? vs_row[kq * kSub + g] : 0.0f;
+            vpb = use_b ? vs_row[kq * kSub + g + 8] : 0.0f;
           }
         } else {
 #pragma unroll
@@ -607,8 +656,9 @@ __global__ void __launch_bounds__(288, MINB)
         if (v_row) {
           float vm = fmaxf(vpa, vpb);
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-          if (rh == 0 && lane == 0) s_vmax[kq] = vm;
+          for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          // (unmasked: the same in both halves; masked: each half has its rows')
+          if ((MASK || rh == 0) && lane == 0) s_vmax[MASK ? warp : kq] = vm;
         }
         ptx::named_bar_sync(1, 8 * 32);
 
@@ -630,7 +680,8 @@ __global__ void __launch_bounds__(288, MINB)
         }
         float fs = 1.0f, inv = 1.0f;
         if (v_row) {
-          const float vm = fmaxf(fmaxf(s_vmax[0], s_vmax[1]), fmaxf(s_vmax[2], s_vmax[3]));
+          float vm = fmaxf(fmaxf(s_vmax[0], s_vmax[1]), fmaxf(s_vmax[2], s_vmax[3]));
+          if constexpr (MASK) vm = fmaxf(vm, fmaxf(fmaxf(s_vmax[4], s_vmax[5]), fmaxf(s_vmax[6], s_vmax[7])));
           if (vm > 0.0f) {
             const int fn = min(126, max(-126, dev::ceil_log2(vm)));
             if (fn > F) {
@@ -846,7 +897,9 @@ __global__ void __launch_bounds__(288, MINB)
 
     // ---- Q prologue: this lane's channels of query row g of the row group
     uint32_t qf[Gm::NMT][2];
-    const float alpha_g = dev::q_prologue<DT, D>(a, rg * 8 + g, b, h, c, qf);
+    const size_t tok0 = MASK ? (size_t)a.vseq[b].tok0 : (size_t)b * T;
+    const int rows = MASK ? a.vseq[b].ntok * G : a.rows;
+    const float alpha_g = dev::q_prologue<DT, D>(a, rg * 8 + g, tok0, rows, h, c, qf);
     const int r0 = rg * 8 + 2 * c, r1 = r0 + 1;
     // with a softcap the row factors also carry 1/softcap (clamped to FLT_MAX
     // like the factors themselves, so zero codes keep zero scores), and the
@@ -856,9 +909,18 @@ __global__ void __launch_bounds__(288, MINB)
     const float al1 = fminf(__shfl_sync(0xffffffffu, alpha_g, (2 * c + 1) * 4) * cf, 3.4028234e38f);
     const float cap_l2 = softcap * kLog2e;
     const float inv_g = __frcp_rn((float)G);
-    const int pos0 = r0 < a.rows ? L - T + dev::div_small(r0, inv_g) : -1;
-    const int pos1 = r1 < a.rows ? L - T + dev::div_small(r1, inv_g) : -1;
+    const int pos0 = r0 < rows ? L - T + dev::div_small(r0, inv_g) : -1;
+    const int pos1 = r1 < rows ? L - T + dev::div_small(r1, inv_g) : -1;
     const int W = a.window;
+    // (padding rows take row 0's rule: their scores only feed their own
+    // unwritten outputs)
+    dev::RowRule ru0{}, ru1{};
+    if constexpr (MASK) {
+      const int q0 = r0 < rows ? r0 : 0, q1 = r1 < rows ? r1 : 0;
+      const int t0 = dev::div_small(q0, inv_g), t1 = dev::div_small(q1, inv_g);
+      ru0 = dev::row_rule(a, tok0 + t0, a.vseq[b].pos0 + t0, h * G + q0 - t0 * G, L);
+      ru1 = dev::row_rule(a, tok0 + t1, a.vseq[b].pos0 + t1, h * G + q1 - t1 * G, L);
+    }
 
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     int F = v_sc ? -126 : 0;  // V-scale normaliser exponent (warp uniform)
@@ -959,7 +1021,28 @@ __global__ void __launch_bounds__(288, MINB)
         // a sub-tile whose keys every query position sees (below the first
         // draft, inside every row's window) needs no mask; padding rows then
         // keep finite scores, which only feed their own unwritten outputs
-        if (!(kb + kSub - 1 <= L - T && (W == 0 || kb > L - 1 - W))) {
+        bool use_a = key_a < L, use_b = key_b < L, full = true;
+        if constexpr (MASK) {
+          if (a.slopes) {
+            x[0] = fmaf(ru0.ns, (float)(abs(ru0.pos - key_a) - ru0.d0), x[0]);
+            x[1] = fmaf(ru1.ns, (float)(abs(ru1.pos - key_a) - ru1.d0), x[1]);
+            x[2] = fmaf(ru0.ns, (float)(abs(ru0.pos - key_b) - ru0.d0), x[2]);
+            x[3] = fmaf(ru1.ns, (float)(abs(ru1.pos - key_b) - ru1.d0), x[3]);
+          }
+          full = kb >= max(ru0.begin, ru1.begin) && kb + kSub <= min(ru0.end, ru1.end);
+          if (!full) {
+            const bool va0 = key_a >= ru0.begin && key_a < ru0.end, va1 = key_a >= ru1.begin && key_a < ru1.end;
+            const bool vb0 = key_b >= ru0.begin && key_b < ru0.end, vb1 = key_b >= ru1.begin && key_b < ru1.end;
+            x[0] = va0 ? x[0] : -INFINITY;
+            x[1] = va1 ? x[1] : -INFINITY;
+            x[2] = vb0 ? x[2] : -INFINITY;
+            x[3] = vb1 ? x[3] : -INFINITY;
+            // the V row of a key that neither of this lane's query rows sees
+            // may hold anything: its scales are not used
+            use_a = va0 || va1;
+            use_b = vb0 || vb1;
+          }
+        } else if (!(kb + kSub - 1 <= L - T && (W == 0 || kb > L - 1 - W))) {
           const bool va0 = key_a <= pos0 && (W == 0 || key_a > pos0 - W);
           const bool va1 = key_a <= pos1 && (W == 0 || key_a > pos1 - W);
           const bool vb0 = key_b <= pos0 && (W == 0 || key_b > pos0 - W);
@@ -1004,16 +1087,16 @@ __global__ void __launch_bounds__(288, MINB)
           if (GRP && v_grp) {
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-              if (key_a < L) ua = fmaxf(ua, vs_row[(sub * kSub + g) * NG + gi]);
-              if (key_b < L) ub = fmaxf(ub, vs_row[(sub * kSub + g + 8) * NG + gi]);
+              if (use_a) ua = fmaxf(ua, vs_row[(sub * kSub + g) * NG + gi]);
+              if (use_b) ub = fmaxf(ub, vs_row[(sub * kSub + g + 8) * NG + gi]);
             }
           } else {
-            ua = key_a < L ? vs_row[sub * kSub + g] : 0.0f;
-            ub = key_b < L ? vs_row[sub * kSub + g + 8] : 0.0f;
+            ua = use_a ? vs_row[sub * kSub + g] : 0.0f;
+            ub = use_b ? vs_row[sub * kSub + g + 8] : 0.0f;
           }
           float vm = fmaxf(ua, ub);
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
           if (vm > 0.0f) {
             const int fn = min(126, max(-126, dev::ceil_log2(vm)));
             if (fn > F) {
@@ -1058,8 +1141,8 @@ __global__ void __launch_bounds__(288, MINB)
               const uint32_t wl = R[2 * h2], wh = R[2 * h2 + 1];
               if (v_grp && ((j * CH) & gmask) == 0) {
                 const int grp = j * CH / (GRP ? GS : 1);
-                const float ga = key_a < L ? vs_row[(sub * kSub + g) * NG + grp] * vinv : 0.0f;
-                const float gb = key_b < L ? vs_row[(sub * kSub + g + 8) * NG + grp] * vinv : 0.0f;
+                const float ga = use_a ? vs_row[(sub * kSub + g) * NG + grp] * vinv : 0.0f;
+                const float gb = use_b ? vs_row[(sub * kSub + g + 8) * NG + grp] * vinv : 0.0f;
                 qb0 = ptx::movmatrix_trans(dev::pack_h2(p0 * ga, p1 * ga));
                 qb1 = ptx::movmatrix_trans(dev::pack_h2(p2 * gb, p3 * gb));
               }
@@ -1092,7 +1175,8 @@ __global__ void __launch_bounds__(288, MINB)
           }
         };
         if constexpr (DT == KVQ_FP8_E4M3) {
-          if (kb + kSub <= L) pv(dev::Flag<false>{}); else pv(dev::Flag<true>{});
+          const bool plain = MASK ? __all_sync(0xffffffffu, full) : kb + kSub <= L;
+          if (plain) pv(dev::Flag<false>{}); else pv(dev::Flag<true>{});
         } else {
           pv(dev::Flag<false>{});
         }
@@ -1171,7 +1255,7 @@ __global__ void __launch_bounds__(288, MINB)
 // Raises (never lowers) the kernel's dynamic shared-memory limit on the
 // current device; shared by the occupancy query and the launch so that a
 // query for a small plan cannot undercut a larger plan launched later.
-template <int DT, int D, int MINB, int NT, int GS>
+template <int DT, int D, int MINB, int NT, int GS, bool MASK>
 cudaError_t ensure_smem(size_t smem) {
   static int smem_set[64] = {};
   int dev = 0;
@@ -1179,7 +1263,7 @@ cudaError_t ensure_smem(size_t smem) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(decode_kernel<DT, D, MINB, NT, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_kernel<DT, D, MINB, NT, GS, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem);
     if (e != cudaSuccess) return e;
     smem_set[dev] = (int)smem;
@@ -1187,19 +1271,19 @@ cudaError_t ensure_smem(size_t smem) {
   return cudaSuccess;
 }
 
-template <int DT, int D, int MINB, int NT, int GS>
+template <int DT, int D, int MINB, int NT, int GS, bool MASK>
 cudaError_t launch_decode_d(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid,
                             int threads, size_t smem, cudaStream_t stream) {
-  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS>(smem);
+  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS, MASK>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_kernel<DT, D, MINB, NT, GS>, grid, threads, smem, stream, tk, tv, a);
+  return launch_pdl(decode_kernel<DT, D, MINB, NT, GS, MASK>, grid, threads, smem, stream, tk, tv, a);
 }
 
-template <int DT, int D, int MINB, int NT, int GS>
+template <int DT, int D, int MINB, int NT, int GS, bool MASK>
 cudaError_t occupancy_decode_d(int threads, size_t smem, int* blocks_per_sm) {
-  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS>(smem);
+  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS, MASK>(smem);
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, decode_kernel<DT, D, MINB, NT, GS>,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, decode_kernel<DT, D, MINB, NT, GS, MASK>,
                                                        threads, smem);
 }
 
@@ -1215,15 +1299,15 @@ struct KernelCfg {
 // Dispatch on head_dim and on nt (0: grouped layout; -32, -64, -128: grouped
 // layout with per-group scales of that many channels; 2, 3: wide layout; head
 // dim 576, 8-bit codes only: the wide layout with nt = 1, 2 or 3).
-template <int DT, bool Query>
+template <int DT, bool Query, bool MASK = false>
 cudaError_t dispatch_decode(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv, const DecodeArgs* a,
                             int grid, int threads, size_t smem, cudaStream_t stream, int* blocks_per_sm) {
   auto go = [&](auto cfg) -> cudaError_t {
     using K = decltype(cfg);
     if constexpr (Query)
-      return occupancy_decode_d<DT, K::d, K::minb, K::nt, K::gs>(threads, smem, blocks_per_sm);
+      return occupancy_decode_d<DT, K::d, K::minb, K::nt, K::gs, MASK>(threads, smem, blocks_per_sm);
     else
-      return launch_decode_d<DT, K::d, K::minb, K::nt, K::gs>(*tk, *tv, *a, grid, threads, smem, stream);
+      return launch_decode_d<DT, K::d, K::minb, K::nt, K::gs, MASK>(*tk, *tv, *a, grid, threads, smem, stream);
   };
   auto by_nt = [&](auto dtag) -> cudaError_t {
     constexpr int d = decltype(dtag)::value;
@@ -1245,7 +1329,7 @@ cudaError_t dispatch_decode(int head_dim, int nt, const CUtensorMap* tk, const C
     case 256: return by_nt(std::integral_constant<int, 256>{});
     case 576:
       if constexpr (DT != KVQ_INT4) {
-        if (nt == 1) return go(KernelCfg<576, 2, 1>{});  // two CTAs per SM (96 registers)
+        if (nt == 1) return go(KernelCfg<576, MASK ? 1 : 2, 1>{});  // two CTAs per SM (96 registers)
         if (nt == 2) return go(KernelCfg<576, 1, 2>{});
         if (nt == 3) return go(KernelCfg<576, 1, 3>{});
       }

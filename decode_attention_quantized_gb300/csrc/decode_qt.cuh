@@ -89,7 +89,9 @@ __device__ __forceinline__ uint32_t qt_chunk(uint32_t tile, int kk, int c) {
 
 }  // namespace dev
 
-template <int DT, int D>
+// MASK: the score rule of a masked call over its virtual sequences, in a
+// kernel of its own.
+template <int DT, int D, bool MASK>
 __global__ void __launch_bounds__(kQtWarps * 32, 1)
     decode_qt_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const DecodeArgs a) {
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     ptx::tmem_alloc(tmem_slot, C::TMEM_COLS);
     ptx::tc_fence_before();
   }
-  const Slice<KT> sp = build_slice<KT>(a, pl_pre, pl_misc);
+  const Slice<KT, MASK> sp = build_slice<KT, MASK>(a, pl_pre, pl_misc);
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
   if (warp == kProducer) {
     // ============================================================ producer
-    produce<Gm, false>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    produce<Gm, false, MASK>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
   } else if (warp >= kDqK && warp < kDqV + 4) {
     // ==================================================== K and V dequant
     // thread: key kk of the tile, channel half hf; its code chunks are read
@@ -186,6 +188,21 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
       int b, h, k0, k1, L, u;
       sp.piece(a, gt, b, h, k0, k1, L, u, next);
       int F = -126;  // V-scale normaliser exponent of the piece
+      // masked: a key that no token of the group sees (below the hull of their
+      // intervals, or in a gap between them) may hold any V scale
+      VSeq vs{};
+      if constexpr (MASK) vs = a.vseq[b];
+      auto seen = [&](int key) -> bool {
+        if constexpr (!MASK) return key < L;
+        if (key < vs.lo || key >= L) return false;
+        if (!vs.gaps) return true;
+        for (int i = 0; i < vs.ntok; ++i) {
+          int begin, end;
+          dev::row_range(a.key_begin, a.key_end, a.window, (size_t)vs.tok0 + i, vs.pos0 + i, L, begin, end);
+          if (key >= begin && key < end) return true;
+        }
+        return false;
+      };
       for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(a.stages)) {
         const uint32_t stage = rp.stage;
         const uint32_t buf = it & 1;
@@ -205,8 +222,8 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           const float* scp = reinterpret_cast<const float*>(st + 2 * Gm::CODE_BYTES + (is_v ? KT * 4 : 0));
           sc = scp[kk];
           if (is_v) {
-            if (key0 + lane < L) vm = scp[lane];
-            if (key0 + 32 + lane < L) vm = fmaxf(vm, scp[32 + lane]);
+            if (seen(key0 + lane)) vm = scp[lane];
+            if (seen(key0 + 32 + lane)) vm = fmaxf(vm, scp[32 + lane]);
           }
         }
         __syncwarp();
@@ -215,7 +232,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         if (is_v && v_row) {
           vm = ptx::redux_max(vm);
           if (vm > 0.0f) F = max(F, min(126, max(-126, dev::ceil_log2(vm))));
-          const float s = key0 + kk < L ? sc * dev::pow2i(-F) : 0.0f;
+          const float s = seen(key0 + kk) ? sc * dev::pow2i(-F) : 0.0f;
           s2 = dev::pack_h2(s, s);
           // F of this tile for the softmax warps, before the conversion and
           // the wait for the V tile: the softmax needs the normaliser, not
@@ -324,13 +341,17 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     const int G = a.group, T = a.q_tokens, Hq = a.num_q_heads, W = a.window, rows = a.rows;
     const float softcap = a.softcap;
     const float inv_cap = softcap > 0.0f ? 1.0f / softcap : 0.0f;
-    const bool valid = r < rows;
+    // (a masked call's last group of a chunk may hold fewer tokens: its rows
+    // past them are set aside per piece)
+    bool valid = r < rows;
     const bool pad_warp = 32 * q >= rows;  // every row of this warp is padding
     const int t_row = valid ? dev::div_small(r, __frcp_rn((float)G)) : 0;
+    const bool in_rows = valid;
+    dev::RowRule ru{};
 
     // Epilogue of a piece: O out of TMEM 16 columns at a time, normalized,
     // to the workspace with the base-2 log-sum-exp.
-    auto epilogue = [&](int u, uint32_t last, float mu, float l, int F) {
+    auto epilogue = [&](int u, uint32_t last, float mu, float l, int F, bool valid) {
       wait(&b_pv[last & 1], (last >> 1) & 1);
       if (pad_warp) return;
       ptx::tc_fence_after();
@@ -368,6 +389,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     uint32_t it = 0;
     int pc = 0;
     int e_u = 0, e_F = 0;  // the previous piece, for its epilogue
+    bool e_valid = false;
     uint32_t e_last = 0;
     float e_mu = 0.0f, e_l = 0.0f;
     float alpha = 1.0f;
@@ -376,6 +398,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
       const bool more = gt < sp.t_end;
       int b = 0, h = 0, k0 = 0, k1 = 0, L = 0, u = 0;
       if (more) sp.piece(a, gt, b, h, k0, k1, L, u, next);
+      if (MASK && more) valid = in_rows && t_row < a.vseq[b].ntok;
 
       // ---- Q of this piece (every QK^T of the previous piece has completed:
       // this thread waited for its last S): the per-channel K scale folded in
@@ -383,7 +406,8 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
       // two at or above its maximum, f16 pairs in the K order of the K tile.
       if (more && !pad_warp) {
         const bool kc = a.k_mode == KVQ_SCALE_PER_CHANNEL;
-        const uint16_t* src = a.q + (((size_t)b * T + t_row) * Hq + (size_t)h * G + (r - t_row * G)) * D;
+        const size_t tok0 = MASK ? (size_t)a.vseq[b].tok0 : (size_t)b * T;
+        const uint16_t* src = a.q + ((tok0 + t_row) * Hq + (size_t)h * G + (r - t_row * G)) * D;
         const float* ksp = a.k_scale + (size_t)h * D;
         int ek = 0;
         if (kc) {
@@ -464,7 +488,14 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         // and > 0 (so that alpha * -inf stays -inf)
         const int e = ek + eq, e1 = e / 2;
         alpha = valid ? fmaxf(fminf(base * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1e-30f) : 1.0f;
-        pos = valid ? L - T + t_row : -1;
+        if constexpr (MASK) {
+          // a row with no token sees the piece's keys with no bias: finite
+          // scores that feed only its own unwritten output
+          ru = dev::RowRule{0, L, 0, 0, 0.0f};
+          if (valid) ru = dev::row_rule(a, tok0 + t_row, a.vseq[b].pos0 + t_row, h * G + (r - t_row * G), L);
+        } else {
+          pos = valid ? L - T + t_row : -1;
+        }
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(b_qfull);
@@ -476,7 +507,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         // the previous piece's tiles may have run while the preceding grid
         // finished; the workspace is written only after it
         ptx::griddep_wait();
-        epilogue(e_u, e_last, e_mu, e_l, e_F);
+        epilogue(e_u, e_last, e_mu, e_l, e_F, e_valid);
       }
       if (!more) break;
 
@@ -540,12 +571,35 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
             F = fn;
           }
         }
-        const bool full = key0 + KT - 1 <= pos && (W == 0 || key0 > pos - W);
-        if (!full) {
+        if constexpr (MASK) {
+          if (a.slopes) {
+            // |pos - key| - d0 of the tile's keys: one integer base per tile,
+            // then exact small steps (the tile that holds pos folds at it)
+            if (key0 + KT - 1 <= ru.pos || key0 >= ru.pos) {
+              const float sg = key0 >= ru.pos ? ru.ns : -ru.ns;
+              const float b0 = ru.ns * (float)(abs(ru.pos - key0) - ru.d0);
 #pragma unroll
-          for (int k = 0; k < KT; ++k) {
-            const int key = key0 + k;
-            if (!(key <= pos && (W == 0 || key > pos - W))) y[k] = -INFINITY;
+              for (int k = 0; k < KT; ++k) y[k] += fmaf(sg, (float)k, b0);
+            } else {
+              const float off = (float)(ru.pos - key0), fd = (float)ru.d0;
+#pragma unroll
+              for (int k = 0; k < KT; ++k) y[k] = fmaf(ru.ns, fabsf(off - (float)k) - fd, y[k]);
+            }
+          }
+          if (!(key0 >= ru.begin && key0 + KT <= ru.end)) {
+            const int lo = min(KT, max(0, ru.begin - key0)), hi = min(KT, max(0, ru.end - key0));
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+              if (!(k >= lo && k < hi)) y[k] = -INFINITY;
+          }
+        } else {
+          const bool full = key0 + KT - 1 <= pos && (W == 0 || key0 > pos - W);
+          if (!full) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+              const int key = key0 + k;
+              if (!(key <= pos && (W == 0 || key > pos - W))) y[k] = -INFINITY;
+            }
           }
         }
         float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -605,6 +659,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         if (lane == 0) ptx::mbar_arrive(&b_pfull[buf]);
       }
       e_u = u;
+      e_valid = valid;
       e_last = it - 1;
       e_mu = mu;
       e_l = l0 + l1;
@@ -623,7 +678,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
 // Raises (never lowers) the kernel's dynamic shared-memory limit on the
 // current device, then launches one CTA per grid slot.
-template <int DT, int D>
+template <int DT, int D, bool MASK>
 cudaError_t launch_decode_qt_d(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid,
                                size_t smem, cudaStream_t stream) {
   static int smem_set[64] = {};
@@ -632,18 +687,18 @@ cudaError_t launch_decode_qt_d(const CUtensorMap& tk, const CUtensorMap& tv, con
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(decode_qt_kernel<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(decode_qt_kernel<DT, D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     smem_set[dev] = (int)smem;
   }
-  return launch_pdl(decode_qt_kernel<DT, D>, grid, kQtWarps * 32, smem, stream, tk, tv, a);
+  return launch_pdl(decode_qt_kernel<DT, D, MASK>, grid, kQtWarps * 32, smem, stream, tk, tv, a);
 }
 
-template <int DT>
+template <int DT, bool MASK = false>
 cudaError_t dispatch_decode_qt(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                int grid, size_t smem, cudaStream_t stream) {
-  if (head_dim == 256) return launch_decode_qt_d<DT, 256>(tk, tv, a, grid, smem, stream);
-  if (head_dim == 128) return launch_decode_qt_d<DT, 128>(tk, tv, a, grid, smem, stream);
+  if (head_dim == 256) return launch_decode_qt_d<DT, 256, MASK>(tk, tv, a, grid, smem, stream);
+  if (head_dim == 128) return launch_decode_qt_d<DT, 128, MASK>(tk, tv, a, grid, smem, stream);
   return cudaErrorInvalidValue;
 }
 

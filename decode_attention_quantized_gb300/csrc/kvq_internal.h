@@ -57,6 +57,20 @@ struct NormRopeArgs {
   NormRope pro;
 };
 
+// One virtual sequence of a masked call (kvq_attend_masked, kvq_key_mass): a
+// group of `ntok` consecutive query tokens of one sequence, written by the
+// preparation kernel.  Token tok0 + i sits at position pos0 + i; the group
+// together sees keys of [lo, hi) only (hi <= lo: none), hi <= the sequence's
+// length clamped to its capacity.
+struct VSeq {
+  int len;   // keys the sequence holds (clamped seq_len)
+  int lo, hi;
+  int pos0, tok0, ntok;
+  int brow;  // row of the block table
+  int gaps;  // 1: some key of [lo, hi) may be seen by no token of the group, and
+             // its cache row may then hold anything (0: every key is seen)
+};
+
 struct DecodeArgs {
   const uint16_t* q;            // bf16 bits [B, T, Hq, D]
   const int32_t* block_table;   // [B, max_blocks_per_seq]
@@ -84,6 +98,11 @@ struct DecodeArgs {
   float* part_lse;  // [units_max, rows]   base-2 log-sum-exp of each piece
   float* part_o;    // [units_max, rows, D] normalized piece output
   unsigned int* err;
+  // masked kernels only (kvq_score_mask)
+  const VSeq* vseq;           // [batch]
+  const float* slopes;        // [Hq] or null
+  const int32_t* key_begin;   // [tokens] or null
+  const int32_t* key_end;     // [tokens] or null
 };
 
 struct CombineArgs {
@@ -97,6 +116,24 @@ struct CombineArgs {
   float* lse_out;          // [B, T, Hq] or null
   int batch, q_tokens, num_q_heads, num_kv_heads, group, rows, head_dim;
   int out_dim;             // channels written per row: head_dim, or v_head_size (LATENT)
+  // masked calls only: rows are (virtual sequence, token, head)
+  const VSeq* vseq;
+  const float* slopes;
+  const int32_t* key_begin;
+  const int32_t* key_end;
+  int window;
+};
+
+// Writes the virtual sequences of a masked call: sequence b's tokens in groups
+// of T (the last one shorter), n groups per sequence.
+struct VSeqArgs {
+  const int32_t* seq_lens;   // [B]
+  const int32_t* key_begin;  // [B, C] or null
+  const int32_t* key_end;    // [B, C] or null
+  VSeq* out;                 // [B * n]
+  int batch, C, T, n, window, cap, max_seq_len;
+  int by_group;              // 1: group j of sequence b at out[j * batch + b], else at out[b * n + j]
+  unsigned int* err;
 };
 
 // The tensor-memory decode kernel (many query rows per kv head): 128 keys per
@@ -190,6 +227,88 @@ cudaError_t launch_wait_probe(unsigned int* err, unsigned long long limit_ns, cu
 // warp_rows: one warp per output row (many rows of few pieces: a prefill
 // chunk, a ragged decode batch) instead of one CTA per row.
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream, bool warp_rows = false);
+cudaError_t launch_combine_masked(const CombineArgs& a, cudaStream_t stream, bool warp_rows);
+// kvq_key_mass: the split-plan fields of DecodeArgs (K side only) and these.
+struct MassArgs {
+  const float* lse;  // [tokens, Hq]
+  float* mass;       // [num_blocks, Hkv, block_size]
+  float decay;       // factor of the weight held before (0: it is not read)
+  int fresh;         // the last `fresh` rows of a sequence held none before
+};
+constexpr int kMassWarps = 4;  // consumer warps: one 16-key sub-tile of a stage each
+constexpr int kMassThreads = 32 * (kMassWarps + 1);
+
+// What a consumer needs of a query row, in shared memory.
+struct __align__(16) MassRow {
+  float alpha;  // logit factor (with 1 / softcap folded in when there is one)
+  float c;      // log-sum-exp in log2 units, without the anchor's bias
+  float ns;     // RowRule
+  int begin;
+  int end, pos, d0, pad;
+};
+
+// Shared bytes beside the ring: alignment slack, Q, rows, split plan, barriers.
+__host__ __device__ constexpr size_t mass_fixed_smem(int head_dim, int nt, bool split, int batch, int stages) {
+  const bool qs = nt > 1 || head_dim > 256;
+  return 1024 + (qs ? (size_t)8 * nt * head_dim * 2 * (split ? 2 : 1) : 0) + (size_t)8 * nt * sizeof(MassRow) +
+         ((size_t)batch + 5 + ((batch + 5) & 1)) * 4 + (size_t)stages * 2 * 8;
+}
+
+// Keys outside the group's [lo, hi) (all of them when `all`): decay only.
+cudaError_t launch_mass_rest(const DecodeArgs& a, const MassArgs& m, bool all, int max_keys, cudaStream_t stream);
+// nt: 8-row tiles of query rows (1, 2, 4, 8).
+cudaError_t launch_key_mass_int8(int head_dim, int nt, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
+                                 int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_key_mass_fp8(int head_dim, int nt, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
+                                int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_key_mass_int4(int head_dim, int nt, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
+                                 int grid, size_t smem, cudaStream_t stream);
+cudaError_t occupancy_key_mass_int8(int head_dim, int nt, int k_mode, size_t smem, int* blocks_per_sm);
+cudaError_t occupancy_key_mass_fp8(int head_dim, int nt, int k_mode, size_t smem, int* blocks_per_sm);
+cudaError_t occupancy_key_mass_int4(int head_dim, int nt, int k_mode, size_t smem, int* blocks_per_sm);
+// kvq_evict_select: a cluster of CTAs per (sequence, kv head).
+struct SelectArgs {
+  const float* mass;           // [num_blocks, Hkv, block_size]
+  const int32_t* block_table;  // [B, max_blocks_per_seq]
+  const int32_t* seq_lens;     // [B]
+  int32_t* keep;               // [B, Hkv, budget]
+  int32_t* kept_lens;          // [B]
+  int batch, num_kv_heads, max_blocks_per_seq, num_blocks, block_size, log2_bs, lim;
+  int budget, sinks, recent;
+  int resident;                // rows whose keys a CTA keeps in shared memory
+  unsigned int* err;
+};
+constexpr int kSelThreads = 512;
+constexpr int kSelBins = 2048;
+// Shared bytes of a CTA that keeps `resident` keys: them, two histograms, scratch.
+__host__ __device__ constexpr size_t select_smem(int resident) {
+  return (size_t)resident * 4 + 2 * kSelBins * 4 + (2 * (kSelThreads / 32) + 16) * 4;
+}
+cudaError_t launch_evict_select(const SelectArgs& a, int cluster, size_t smem, cudaStream_t stream);
+
+// kvq_evict_compact.
+struct CompactArgs {
+  const int32_t* block_table;  // [B, max_blocks_per_seq] source pages
+  const int32_t* dst_table;    // the same array: in place
+  const int32_t* keep;         // [B, Hkv, budget]
+  const int32_t* kept_lens;    // [B]
+  uint8_t* codes[2];           // K, V
+  float* scale[2];
+  float* mass;                 // or null
+  int n_scale[2];              // fp32 scales per row of a side
+  int sides, row_bytes;
+  int batch, num_kv_heads, max_blocks_per_seq, num_blocks, block_size, log2_bs, budget;
+  int rows, log2_rows, stages, stage_bytes;  // rows per unit (a power of two); bytes between ring stages
+  int units, in_place;
+  unsigned int* round_count;   // [ceil(units / grid)], zero (in place)
+  unsigned int* err;
+};
+constexpr int kCompactThreads = 128;
+constexpr int kCompactRows = 128;    // most rows of a unit
+constexpr int kCompactStages = 8;    // most ring stages
+cudaError_t launch_evict_compact(const CompactArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t occupancy_evict_compact(size_t smem, int* blocks_per_sm);
+cudaError_t launch_vseq(const VSeqArgs& a, cudaStream_t stream);
 // out[b * n + j] = max(0, seq_lens[b] - C + T (j + 1)) for the n = C / T groups
 // of a prefill chunk (virtual sequences of T tokens).
 cudaError_t launch_prefill_lens(const int32_t* seq_lens, int32_t* out, int batch, int n, int C, int T,
@@ -223,6 +342,23 @@ cudaError_t launch_decode_qt_fp8(int head_dim, const CUtensorMap& tk, const CUte
                                  int grid, size_t smem, cudaStream_t stream);
 cudaError_t launch_decode_qt_int4(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                   int grid, size_t smem, cudaStream_t stream);
+
+// The same kernels with the score rule of a masked call (kvq_score_mask).
+cudaError_t launch_decode_mask_int8(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream);
+cudaError_t launch_decode_mask_fp8(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream);
+cudaError_t launch_decode_mask_int4(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream);
+cudaError_t occupancy_decode_mask_int8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
+cudaError_t occupancy_decode_mask_fp8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
+cudaError_t occupancy_decode_mask_int4(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
+cudaError_t launch_qt_mask_int8(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
+                                int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_qt_mask_fp8(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
+                               int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_qt_mask_int4(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
+                                int grid, size_t smem, cudaStream_t stream);
 
 cudaError_t occupancy_decode_int8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
 cudaError_t occupancy_decode_fp8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);

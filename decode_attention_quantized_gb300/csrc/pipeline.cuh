@@ -73,7 +73,11 @@ struct RingPos {
 // the plain equal-tiles split.  The piece of segment s in CTA x writes its
 // partial to slot s + x: distinct for every piece and contiguous over the
 // pieces of one segment (the combine walks them in that order).
-template <int KT>
+//
+// MASK (the masked kernels): `sequences` are the call's virtual sequences, and
+// the key range of each is the [lo, hi) that the preparation kernel found its
+// tokens to see together; L is then hi everywhere.
+template <int KT, bool MASK = false>
 struct Slice {
   const int* pre;  // shared [B + 1]: tile prefix over sequences
   int lim, t_begin, t_end;
@@ -81,6 +85,11 @@ struct Slice {
   // key range [lo, L) of sequence b: L clamped to the capacity bound, lo the
   // first key any query row sees (window) rounded down to the tile
   __device__ __forceinline__ void seq_range(const DecodeArgs& a, int b, int& L, int& lo) const {
+    if constexpr (MASK) {
+      L = a.vseq[b].hi;
+      lo = a.vseq[b].lo & ~(KT - 1);
+      return;
+    }
     L = a.seq_lens[b];
     L = L < 0 ? 0 : (L > lim ? lim : L);
     lo = 0;
@@ -117,18 +126,20 @@ struct Slice {
 // (KVQ_DECODE_EARLY_INPUTS) before the wait on the preceding grid, else after
 // it; the producer publishes the plan to the workspace after that wait
 // (publish_slice).  Flags seq_lens outside [0, capacity].
-template <int KT>
-__device__ Slice<KT> build_slice(const DecodeArgs& a, int* pl_pre, int* pl_misc) {
+template <int KT, bool MASK = false>
+__device__ Slice<KT, MASK> build_slice(const DecodeArgs& a, int* pl_pre, int* pl_misc) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.batch, Hkv = a.num_kv_heads;
   const int cap = a.max_blocks_per_seq * a.block_size;
   if (!a.early_reads) ptx::griddep_wait();  // seq_lens may come from the preceding grid
-  Slice<KT> sp;
+  Slice<KT, MASK> sp;
   sp.pre = pl_pre;
   sp.lim = (a.max_seq_len > 0 && a.max_seq_len < cap) ? a.max_seq_len : cap;
   for (int b = tid; b < B; b += blockDim.x) {
-    const int raw = a.seq_lens[b];
-    if ((raw < 0 || raw > sp.lim) && blockIdx.x == 0) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
+    if constexpr (!MASK) {
+      const int raw = a.seq_lens[b];
+      if ((raw < 0 || raw > sp.lim) && blockIdx.x == 0) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
+    }
     int L, lo;
     sp.seq_range(a, b, L, lo);
     pl_pre[b] = (max(0, L - lo) + KT - 1) / KT;  // tiles, for now
@@ -217,8 +228,8 @@ __device__ __forceinline__ void publish_slice(const DecodeArgs& a, const int* pl
 // [0, num_blocks) is flagged and its rows are not loaded.  Returns after
 // every copy it issued has landed, so the CTA never exits with a copy in
 // flight.
-template <class Gm, bool kBurst>
-__device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS>& sp, const CUtensorMap* tmk,
+template <class Gm, bool kBurst, bool MASK = false>
+__device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS, MASK>& sp, const CUtensorMap* tmk,
                         const CUtensorMap* tmv, uint8_t* ring, uint64_t* bar_full, uint64_t* bar_empty,
                         const int* pl_pre, const int* pl_misc) {
   constexpr int KT = Gm::KEYS;
@@ -246,7 +257,7 @@ __device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS>& sp, const CU
   for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
     int b, h, k0, k1, L, slot;
     sp.piece(a, gt, b, h, k0, k1, L, slot, next);
-    const int32_t* bt = a.block_table + (size_t)(b / a.bt_div) * a.max_blocks_per_seq;
+    const int32_t* bt = a.block_table + (size_t)(MASK ? a.vseq[b].brow : b / a.bt_div) * a.max_blocks_per_seq;
     const int p_last = (k1 - 1) >> a.log2_bs;
     int base = k0 >> a.log2_bs;
     int my_id = base + lane <= p_last ? bt[base + lane] : -1;
@@ -261,9 +272,11 @@ __device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS>& sp, const CU
       // ends; the producer runs a ring ahead of them, so it pulls those rows
       // into L2 now (G heads of one kv head are contiguous per token)
       const int lines = a.group * Gm::D * 2 / 128;
-      for (int i = lane; i < a.q_tokens * lines; i += 32) {
+      const size_t tok0 = MASK ? (size_t)a.vseq[b].tok0 : (size_t)b * a.q_tokens;
+      const int ntok = MASK ? a.vseq[b].ntok : a.q_tokens;
+      for (int i = lane; i < ntok * lines; i += 32) {
         const int t = i / lines, c = i - t * lines;
-        ptx::prefetch_l2(a.q + (((size_t)b * a.q_tokens + t) * a.num_q_heads + (size_t)h * a.group) * Gm::D + c * 64);
+        ptx::prefetch_l2(a.q + ((tok0 + t) * a.num_q_heads + (size_t)h * a.group) * Gm::D + c * 64);
       }
     }
     for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(S)) {

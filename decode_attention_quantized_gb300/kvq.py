@@ -22,6 +22,7 @@ LAYOUT_SEPARATE, LAYOUT_LATENT = 0, 1
 PER_ROW, PER_TENSOR, PER_CHANNEL, PER_GROUP = 1, 2, 3, 4
 DECODE_EARLY_INPUTS, DECODE_NO_TCGEN05, DECODE_EARLY_CACHE = 0x1, 0x2, 0x4  # kvq_decode_params.flags
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_POSITION = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_KEEP_INDEX = 0x20
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
           5: "device timeout"}
 
@@ -55,6 +56,16 @@ class NormRopeDesc(ctypes.Structure):
                 ("hadamard", ctypes.c_int32)]
 
 
+class ScoreMaskDesc(ctypes.Structure):
+    _fields_ = [("slopes", ctypes.c_void_p), ("key_begin", ctypes.c_void_p), ("key_end", ctypes.c_void_p)]
+
+
+class EvictParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32)]
+
+
 # every exported entry point of include/kvq.h with its ctypes signature
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 SIGNATURES = {
@@ -74,6 +85,19 @@ SIGNATURES = {
                            _VP, _SZ, _VP]),
     "kvq_append_norm_rope": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(NormRopeDesc), _VP, _VP, _VP, _VP,
                                     _I32, _VP]),
+    "kvq_attend_masked_workspace_size": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams),
+                                                ctypes.POINTER(_SZ)]),
+    "kvq_attend_masked": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams),
+                                 ctypes.POINTER(ScoreMaskDesc), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "kvq_key_mass_workspace_size": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams),
+                                           ctypes.POINTER(_SZ)]),
+    "kvq_key_mass": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams), ctypes.POINTER(ScoreMaskDesc),
+                            _VP, _VP, _VP, _VP, ctypes.c_float, _I32, _VP, _VP, _SZ, _VP]),
+    "kvq_evict_select": (_I32, [ctypes.POINTER(EvictParams), _VP, _VP, _VP, _VP, _VP, _VP]),
+    "kvq_evict_compact_workspace_size": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(EvictParams),
+                                                ctypes.POINTER(_SZ)]),
+    "kvq_evict_compact": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(EvictParams), _VP, _VP, _VP, _VP, _VP,
+                                 _VP, _SZ, _VP]),
     "kvq_attend_noalloc": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams), _VP, _VP, _VP, _VP, _VP,
                                   _VP, _VP]),
 }
@@ -325,3 +349,174 @@ def decode_step(cache: QuantizedPagedCache, params: DecodeParams, q, block_table
     kvq_decode(cache, params, q, block_table, seq_lens, bufs.workspace, stream)
     kvq_combine(cache, params, bufs.workspace, head_sink, bufs.out, bufs.lse, stream)
     return bufs.out, bufs.lse
+
+
+# ---------------------------------------------------------------------------
+# score rules (distance bias, key intervals) and eviction
+# ---------------------------------------------------------------------------
+
+def _need(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, device, optional: bool = False):
+    """The tensor's type, shape, order and device are what the C call takes for
+    granted; returns its device pointer."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype is not dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    return t.data_ptr()
+
+
+def _current(device: torch.device):
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, not on the current CUDA device")
+
+
+def _workspace(workspace: torch.Tensor, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@dataclass
+class ScoreMask:
+    """The score rule of a masked call (kvq_score_mask in kvq.h); tensors on the
+    device.  slopes fp32 [Hq]: logit of head h gets -slopes[h] * |pos - key|.
+    key_begin, key_end int32 [B, C]: token c sees keys [key_begin, key_end)
+    (None: 0, and the causal bound pos + 1)."""
+    slopes: Optional[torch.Tensor] = None
+    key_begin: Optional[torch.Tensor] = None
+    key_end: Optional[torch.Tensor] = None
+
+    def desc(self, params: DecodeParams, device) -> ScoreMaskDesc:
+        per_token = (params.batch, params.q_tokens)
+        return ScoreMaskDesc(_need("slopes", self.slopes, torch.float32, (params.num_q_heads,), device, True),
+                             _need("key_begin", self.key_begin, torch.int32, per_token, device, True),
+                             _need("key_end", self.key_end, torch.int32, per_token, device, True))
+
+
+def kvq_attend_masked_workspace_size(cache: QuantizedPagedCache, params: DecodeParams) -> int:
+    d, n = cache.desc(), ctypes.c_size_t(0)
+    _check("kvq_attend_masked_workspace_size",
+           load().kvq_attend_masked_workspace_size(ctypes.byref(d), ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def kvq_attend_masked(cache: QuantizedPagedCache, params: DecodeParams, mask: Optional[ScoreMask], q: torch.Tensor,
+                      block_table: torch.Tensor, seq_lens: torch.Tensor, head_sink: Optional[torch.Tensor],
+                      out: torch.Tensor, lse_out: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
+    """q bf16 [B, C, Hq, D], out bf16 [B, C, Hq, out_dim] with C = params.q_tokens
+    >= 1; lse_out fp32 [B, C, Hq] or None; mask None: causal, no bias."""
+    dev, B, C, Hq = cache.k_codes.device, params.batch, params.q_tokens, params.num_q_heads
+    _current(dev)
+    d = cache.desc()
+    m = None if mask is None else ctypes.byref(mask.desc(params, dev))
+    ws, nbytes = _workspace(workspace, dev)
+    _check("kvq_attend_masked", load().kvq_attend_masked(
+        ctypes.byref(d), ctypes.byref(params), m, _need("q", q, torch.bfloat16, (B, C, Hq, cache.head_dim), dev),
+        _need("block_table", block_table, torch.int32, (B, params.max_blocks_per_seq), dev),
+        _need("seq_lens", seq_lens, torch.int32, (B,), dev),
+        _need("head_sink", head_sink, torch.float32, (Hq,), dev, True),
+        _need("out", out, torch.bfloat16, (B, C, Hq, cache.out_dim), dev),
+        _need("lse_out", lse_out, torch.float32, (B, C, Hq), dev, True), ws, nbytes, _stream(stream)))
+
+
+def kvq_key_mass_workspace_size(cache: QuantizedPagedCache, params: DecodeParams) -> int:
+    d, n = cache.desc(), ctypes.c_size_t(0)
+    _check("kvq_key_mass_workspace_size",
+           load().kvq_key_mass_workspace_size(ctypes.byref(d), ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def kvq_key_mass(cache: QuantizedPagedCache, params: DecodeParams, mask: Optional[ScoreMask], q: torch.Tensor,
+                 block_table: torch.Tensor, seq_lens: torch.Tensor, lse: torch.Tensor, mass: torch.Tensor,
+                 workspace: torch.Tensor, decay: float = 1.0, fresh: Optional[int] = None, stream=None):
+    """Adds the attention weight of this call's query tokens to mass fp32
+    [num_blocks, Hkv, block_size]; lse fp32 [B, C, Hq] from the attention call.
+    fresh: trailing positions that held no weight before (None: the C tokens)."""
+    dev, B, C, Hq = cache.k_codes.device, params.batch, params.q_tokens, params.num_q_heads
+    _current(dev)
+    d = cache.desc()
+    m = None if mask is None else ctypes.byref(mask.desc(params, dev))
+    ws, nbytes = _workspace(workspace, dev)
+    _check("kvq_key_mass", load().kvq_key_mass(
+        ctypes.byref(d), ctypes.byref(params), m, _need("q", q, torch.bfloat16, (B, C, Hq, cache.head_dim), dev),
+        _need("block_table", block_table, torch.int32, (B, params.max_blocks_per_seq), dev),
+        _need("seq_lens", seq_lens, torch.int32, (B,), dev), _need("lse", lse, torch.float32, (B, C, Hq), dev),
+        float(decay), C if fresh is None else int(fresh),
+        _need("mass", mass, torch.float32, (cache.num_blocks, cache.num_kv_heads, cache.block_size), dev), ws, nbytes,
+        _stream(stream)))
+
+
+def make_evict_params(batch, max_blocks_per_seq, budget, *, num_blocks, block_size, num_kv_heads, sinks=0, recent=0,
+                      max_seq_len=0) -> EvictParams:
+    """Every sequence longer than `budget` rows is cut to it: its first `sinks`
+    and last `recent` rows stay, and those of the rest with the largest mass."""
+    return EvictParams(int(batch), int(max_blocks_per_seq), int(max_seq_len), int(num_blocks), int(block_size),
+                       int(num_kv_heads), int(budget), int(sinks), int(recent))
+
+
+def kvq_evict_select(params: EvictParams, mass: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     keep: torch.Tensor, kept_lens: torch.Tensor, stream=None):
+    """keep int32 [B, Hkv, budget] (ascending rows, then -1), kept_lens int32 [B]."""
+    dev, B = mass.device, params.batch
+    _current(dev)
+    _check("kvq_evict_select", load().kvq_evict_select(
+        ctypes.byref(params),
+        _need("mass", mass, torch.float32, (params.num_blocks, params.num_kv_heads, params.block_size), dev),
+        _need("block_table", block_table, torch.int32, (B, params.max_blocks_per_seq), dev),
+        _need("seq_lens", seq_lens, torch.int32, (B,), dev),
+        _need("keep", keep, torch.int32, (B, params.num_kv_heads, params.budget), dev),
+        _need("kept_lens", kept_lens, torch.int32, (B,), dev), _stream(stream)))
+
+
+def kvq_evict_compact_workspace_size(cache: QuantizedPagedCache, params: EvictParams) -> int:
+    d, n = cache.desc(), ctypes.c_size_t(0)
+    _check("kvq_evict_compact_workspace_size",
+           load().kvq_evict_compact_workspace_size(ctypes.byref(d), ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def kvq_evict_compact(cache: QuantizedPagedCache, params: EvictParams, block_table: torch.Tensor,
+                      dst_table: Optional[torch.Tensor], keep: torch.Tensor, kept_lens: torch.Tensor,
+                      mass: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
+    """Moves the kept rows (codes, row scales, mass) to the front of the pages of
+    block_table (dst_table None or block_table), or into dst_table's pages."""
+    dev, B = cache.k_codes.device, params.batch
+    _current(dev)
+    d = cache.desc()
+    ws, nbytes = _workspace(workspace, dev)
+    table = (B, params.max_blocks_per_seq)
+    _check("kvq_evict_compact", load().kvq_evict_compact(
+        ctypes.byref(d), ctypes.byref(params), _need("block_table", block_table, torch.int32, table, dev),
+        _need("dst_table", dst_table, torch.int32, table, dev, True),
+        _need("keep", keep, torch.int32, (B, params.num_kv_heads, params.budget), dev),
+        _need("kept_lens", kept_lens, torch.int32, (B,), dev),
+        _need("mass", mass, torch.float32, (cache.num_blocks, cache.num_kv_heads, cache.block_size), dev, True),
+        ws, nbytes, _stream(stream)))
+
+
+@dataclass
+class EvictBuffers:
+    workspace: torch.Tensor
+    keep: torch.Tensor
+    kept_lens: torch.Tensor
+
+
+def alloc_evict_buffers(cache: QuantizedPagedCache, params: EvictParams) -> EvictBuffers:
+    """Caller-side allocation of the workspace, the kept rows and the new lengths."""
+    dev = cache.k_codes.device
+    return EvictBuffers(
+        torch.empty(kvq_evict_compact_workspace_size(cache, params) // 4 + 64, dtype=torch.int32, device=dev),
+        torch.empty((params.batch, params.num_kv_heads, params.budget), dtype=torch.int32, device=dev),
+        torch.empty((params.batch,), dtype=torch.int32, device=dev))
+
+
+def evict_step(cache: QuantizedPagedCache, params: EvictParams, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               mass: torch.Tensor, bufs: EvictBuffers, dst_table: Optional[torch.Tensor] = None, stream=None):
+    """kvq_evict_select followed by kvq_evict_compact; returns the new lengths."""
+    kvq_evict_select(params, mass, block_table, seq_lens, bufs.keep, bufs.kept_lens, stream)
+    kvq_evict_compact(cache, params, block_table, dst_table, bufs.keep, bufs.kept_lens, mass, bufs.workspace, stream)
+    return bufs.kept_lens

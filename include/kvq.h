@@ -102,6 +102,7 @@ typedef enum {
 #define KVQ_DEVERR_SEQ_LEN 0x4u   /* decode: seq_len < 0, > capacity, or > max_seq_len */
 #define KVQ_DEVERR_TIMEOUT 0x8u   /* a bounded pipeline wait gave up */
 #define KVQ_DEVERR_POSITION 0x10u /* norm/RoPE prologue: position outside [0, max_position) */
+#define KVQ_DEVERR_KEEP_INDEX 0x20u /* kvq_evict_compact: a kept row outside [0, capacity) */
 
 /* Cache layouts (PR #29912, kv_cache_layout and v_head_size): SEPARATE K and V
  * caches, or LATENT (absorbed MLA): one cache whose rows serve as K, and whose
@@ -185,7 +186,8 @@ typedef struct {
  * decode then loads every older row while that operation is still running and
  * waits for it only before the 64- or 128-key tile that holds the new tokens,
  * so the first cache reads overlap its tail.  Without KVQ_DECODE_EARLY_INPUTS
- * the bit has no effect. */
+ * the bit has no effect.  A kvq_evict_compact must not be among the last two
+ * operations before such a decode: it moves older rows. */
 #define KVQ_DECODE_EARLY_CACHE 0x4u
 
 /* Human-readable name of a status code (static storage). */
@@ -339,6 +341,128 @@ KVQ_API kvq_status kvq_prefill(const kvq_cache* cache, const kvq_decode_params* 
                                const int32_t* block_table, const int32_t* seq_lens, const float* head_sink,
                                void* out, float* lse_out, void* workspace, size_t workspace_bytes,
                                kvq_stream_t stream);
+
+/* The score rule of a masked call: a bias that depends on distance, and an
+ * interval of visible keys per query token.  Query token c of sequence b sits
+ * at position pos = seq_lens[b] - C + c (C = params->q_tokens) and sees the
+ * keys j with key_begin[b, c] <= j < key_end[b, c] (cut to [0, seq_lens[b]);
+ * NULL: 0 and pos + 1, the causal rule) and, with params->window > 0,
+ * j > pos - window.  Intervals say:
+ *   document mask  key_begin = first position of the token's document
+ *   prefix mask    key_end = max(pos + 1, prefix length): the prefix is seen
+ *                  in both directions
+ *   padding        key_end <= key_begin: the token sees nothing; its output
+ *                  rows are zero and their lse is -inf
+ * The logit of query head h and key j is softcap(sm_scale <q, k_j>) -
+ * slopes[h] * |pos - j| (the bias comes after the cap and is not capped).
+ * Positions and distances count cache rows: after an eviction they are those
+ * of the rows that were kept.  The reference's pages name neither; the rules
+ * are the usual ones of models with linear distance biases, packed documents
+ * and bidirectional prefixes. */
+typedef struct {
+  const float* slopes;      /* fp32 [Hq] (device; finite, any sign), or NULL: no bias */
+  const int32_t* key_begin; /* int32 [B, C] (device; any values), or NULL */
+  const int32_t* key_end;   /* int32 [B, C] (device; any values), or NULL */
+} kvq_score_mask;
+
+/* kvq_attend_masked -- attention of C = params->q_tokens >= 1 query tokens per
+ * sequence under a score rule: one call for a decode step (C = 1, or 1 +
+ * drafts) and for a prompt's chunk (any C, not only multiples of a tile).
+ * Arguments and results as in kvq_prefill; mask may be NULL (causal, no
+ * bias).  Sequences are cut into groups of tokens; keys that no token of a
+ * group sees are not read.  With head_dim 128 or 256, no group-wise scales,
+ * KVQ_DECODE_NO_TCGEN05 unset and groups of at least 64 query rows per kv
+ * head, the groups are tiles of up to 128 rows on tcgen05 MMAs; otherwise of
+ * up to 8 tokens on the mma.sync kernel.  KVQ_DECODE_EARLY_INPUTS and
+ * KVQ_DECODE_EARLY_CACHE have no effect here.  batch <= 1024;
+ * batch * C < 2^31.  workspace: at least
+ * kvq_attend_masked_workspace_size bytes, 256-byte aligned; it belongs to
+ * this call until the call's kernels have run. */
+KVQ_API kvq_status kvq_attend_masked_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
+                                                    size_t* workspace_bytes);
+KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_params* params,
+                                     const kvq_score_mask* mask, const void* q, const int32_t* block_table,
+                                     const int32_t* seq_lens, const float* head_sink, void* out, float* lse_out,
+                                     void* workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/* kvq_key_mass -- the attention weight that every cached key receives from
+ * this step's query tokens, accumulated: for each sequence b, kv head g and
+ * position j in [0, seq_lens[b]), with slot(j) the key's place in the pages,
+ *   mass[slot(j)] = old + sum over tokens c and query heads h of group g that
+ *                   see j of exp(s[b, c, h, j] - lse[b, c, h]),
+ *   old = 0 for the last `fresh` positions (the step's new tokens, which held
+ *         no weight before), else decay * mass[slot(j)].
+ * s and the visible keys are those of kvq_attend_masked with the same params
+ * and mask (of kvq_decode / kvq_prefill with mask NULL); lse fp32
+ * [B, C, Hq] is their lse_out (before the head sink; -inf rows add nothing).
+ * mass fp32 [num_blocks, Hkv, block_size] (device), laid out like per-row
+ * scales; slots of other positions are left as they are.  C = q_tokens >= 1:
+ * one decode step, or the last tokens of a prompt looking back over it.
+ * decay in [0, 1]: 1 sums, 0 overwrites (mass is then not read).  The scores
+ * are fp32-accurate (a folded per-channel K scale enters as two f16 parts).
+ * Each key is written by one thread in a fixed order: repeated calls give the
+ * same bits.  A page must not be shared by two sequences of the call.
+ * workspace: at least kvq_key_mass_workspace_size bytes, 256-byte aligned; it
+ * belongs to this call until the call's kernels have run. */
+KVQ_API kvq_status kvq_key_mass_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
+                                               size_t* workspace_bytes);
+KVQ_API kvq_status kvq_key_mass(const kvq_cache* cache, const kvq_decode_params* params, const kvq_score_mask* mask,
+                                const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                                const float* lse, float decay, int32_t fresh, float* mass, void* workspace,
+                                size_t workspace_bytes, kvq_stream_t stream);
+
+/* An eviction: every sequence longer than `budget` rows is cut to `budget`. */
+typedef struct {
+  int32_t batch;              /* B */
+  int32_t max_blocks_per_seq; /* block_table row length; capacity = it * block_size */
+  int32_t max_seq_len;        /* host upper bound on seq_lens; 0 = capacity */
+  int32_t num_blocks;         /* pool size in blocks */
+  int32_t block_size;         /* tokens per block (power of two >= 16) */
+  int32_t num_kv_heads;       /* Hkv */
+  int32_t budget;             /* rows kept per sequence (>= 1) */
+  int32_t sinks;              /* the first `sinks` rows always stay */
+  int32_t recent;             /* the last `recent` rows always stay; sinks + recent <= budget */
+} kvq_evict_params;
+
+/* kvq_evict_select -- the rows that stay, for each sequence and kv head on its
+ * own: of a sequence of L > budget rows the first `sinks`, the last `recent`,
+ * and of the rest the budget - sinks - recent with the largest mass; among
+ * equal masses the lower row stays, -0 equals +0, and a NaN ranks below every
+ * number.  A sequence of at most `budget` rows stays whole.
+ * keep int32 [B, Hkv, budget]: the kept rows in ascending order, then -1.
+ * kept_lens int32 [B]: min(seq_lens[b], budget), the lengths after
+ * kvq_evict_compact (it may not be seq_lens itself).  An unreadable block id
+ * sets KVQ_DEVERR_BLOCK_ID and ranks its rows as NaN. */
+KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float* mass, const int32_t* block_table,
+                                    const int32_t* seq_lens, int32_t* keep, int32_t* kept_lens,
+                                    kvq_stream_t stream);
+
+/* kvq_evict_compact -- moves the kept rows together: position i of sequence b
+ * and kv head g becomes what position keep[b, g, i] was, for i < kept_lens[b]
+ * (at most budget): K and V codes, per-row or per-group scales, and mass when
+ * it is given.  keep must be strictly ascending with keep[i] >= i, as
+ * kvq_evict_select writes it.  The cache's block size, pool size and kv heads
+ * must be the params'.
+ * dst_table NULL or equal to block_table: in place; positions behind
+ * kept_lens[b] keep their contents, and the pages behind the last kept row
+ * are free for other use.  Otherwise dst_table [B, max_blocks_per_seq] names
+ * other pages, none of which is a source page of this call: for sequences
+ * whose pages are shared, which in-place moves would change for everyone.
+ * A kept row outside the capacity sets KVQ_DEVERR_KEEP_INDEX and is not
+ * moved (its destination's contents are unspecified).
+ * K is moved as it was written: with rotary positions it keeps the rotation
+ * of its first position.
+ * In place the kernel's blocks wait for one another (a cooperative launch with
+ * bounded waits; KVQ_DEVERR_TIMEOUT).  workspace: at least
+ * kvq_evict_compact_workspace_size bytes, 256-byte aligned (used in place
+ * only, but checked always); it belongs to this call until its kernel has
+ * run. */
+KVQ_API kvq_status kvq_evict_compact_workspace_size(const kvq_cache* cache, const kvq_evict_params* params,
+                                                    size_t* workspace_bytes);
+KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_params* params,
+                                     const int32_t* block_table, const int32_t* dst_table, const int32_t* keep,
+                                     const int32_t* kept_lens, float* mass, void* workspace,
+                                     size_t workspace_bytes, kvq_stream_t stream);
 
 /* kvq_attend_noalloc -- kvq_decode then kvq_combine, with the split-partial
  * scratch in a library-owned 16 MiB device array instead of a caller

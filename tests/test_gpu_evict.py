@@ -1,0 +1,437 @@
+"""The attention weight that keys receive (kvq_key_mass), the rows an eviction
+keeps (kvq_evict_select) and their moving (kvq_evict_compact), each against its
+64-bit or exact plain form, and all of them run together with the attention."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import score_ref as ref
+from guard import guarded
+from test_gpu_masked import CASES, check, dev, documents, gpu_cache, run, slopes_of
+
+pytestmark = pytest.mark.gpu
+
+INT8, FP8, INT4 = ref.INT8, ref.FP8, ref.INT4
+ROW, TENSOR, CHANNEL, GROUP = ref.ROW, ref.TENSOR, ref.CHANNEL, ref.GROUP
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from decode_attention_quantized_gb300 import kvq
+    kvq.load()
+    return kvq
+
+
+# ------------------------------------------------------------------ key mass
+
+def mass_call(kvq, c: ref.Cache, lse, mass, decay=1.0, fresh=None, slopes=None, key_begin=None, key_end=None):
+    case = c.case
+    g = gpu_cache(kvq, c)
+    B = len(case.lens)
+    p = kvq.make_params(B, case.hq, case.c, c.width, softcap=case.softcap, window=case.window)
+    ws = guarded(torch.zeros(kvq.kvq_key_mass_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda"), "ws")
+    m = guarded(dev(mass), "mass")
+    f32 = lambda a: None if a is None else dev(np.asarray(a, np.float32))  # noqa: E731
+    i32 = lambda a: None if a is None else dev(np.asarray(a, np.int32))  # noqa: E731
+    mask = kvq.ScoreMask(f32(slopes), i32(key_begin), i32(key_end))
+    q, table, lens = dev(c.q).to(torch.bfloat16), dev(c.table), dev(np.array(case.lens, np.int32))
+    kvq.kvq_key_mass(g, p, mask, q, table, lens, dev(lse.astype(np.float32)), m, ws, decay=decay, fresh=fresh)
+    assert kvq.kvq_get_device_error() == 0
+    return m.cpu().numpy()
+
+
+def random_mass(c: ref.Cache, seed=0):
+    r = np.random.default_rng(seed)
+    return r.exponential(0.1, (c.nb, c.case.hkv, c.case.bs)).astype(np.float32)
+
+
+def check_mass(got, c, lse, mass, decay, fresh, slopes=None, key_begin=None, key_end=None):
+    want, tol = ref.key_mass(c, lse.astype(np.float32), mass, decay, fresh, slopes, key_begin, key_end)
+    untouched = tol == 0
+    assert np.array_equal(got[untouched & (want == mass)], mass[untouched & (want == mass)], equal_nan=True)
+    worst = (np.abs(got - want) - tol).max()
+    assert worst <= 0, f"off by {worst:.2e} more than its bound"
+
+
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("c", [1, 4, 8, 11, 30])
+def test_mass(kvq, name, c):
+    base = CASES[name]
+    case = dataclasses.replace(base, c=c, seed=c, lens=tuple(max(L, c) for L in base.lens))
+    cache = ref.Cache(case)
+    lse = ref.attend(cache)[1]
+    mass = random_mass(cache)
+    got = mass_call(kvq, cache, lse, mass, decay=0.875)
+    check_mass(got, cache, lse, mass, 0.875, c)
+
+
+@pytest.mark.parametrize("name", ["int8 row d128", "int8 row d256 g6", "fp8 tensor cap", "int4 channel d256",
+                                  "latent d576", "int4 group"])
+@pytest.mark.parametrize("c", [1, 9, 40])
+@pytest.mark.parametrize("decay,fresh", [(1.0, 0), (0.0, 0), (0.5, 3), (1.0, 10 ** 6)])
+def test_mass_under_a_rule(kvq, name, c, decay, fresh):
+    """Bias, documents, window and empty rows; keys that nobody sees decay."""
+    case = dataclasses.replace(CASES[name], c=c, seed=7, lens=(170, max(c, 33)), window=60)
+    cache = ref.Cache(case)
+    s = slopes_of(case.hq)
+    begin, end = documents(case, (25, 101, 150))
+    end[0, -1] = 0
+    lse = ref.attend(cache, s, begin, end)[1]
+    mass = random_mass(cache)
+    if decay == 0.0:
+        mass[:] = np.nan  # not read
+    got = mass_call(kvq, cache, lse, mass, decay, fresh, s, begin, end)
+    if decay == 0.0:
+        keep = ~np.isnan(got)
+        want, tol = ref.key_mass(cache, lse.astype(np.float32), np.zeros_like(mass), 0.0, fresh, s, begin, end)
+        for b in range(2):
+            blk, row = cache.rows(b)
+            assert keep[blk, :, row].all()
+            assert (np.abs(got - want)[blk, :, row] <= tol[blk, :, row]).all()
+        assert keep.sum() == sum(case.lens) * case.hkv
+        return
+    check_mass(got, cache, lse, mass, decay, fresh, s, begin, end)
+
+
+def test_mass_of_a_row_sums_to_one(kvq):
+    """Over all keys the weights of each query row add up to one."""
+    case = ref.Case(lens=(500, 77), c=6, hq=8, hkv=2)
+    cache = ref.Cache(case)
+    _, lse = run(kvq, cache)
+    got = mass_call(kvq, cache, lse, np.zeros((cache.nb, 2, 16), np.float32))
+    for b in range(2):
+        blk, row = cache.rows(b)
+        # (lse as the attention gave it: 2^-15 and fp32; rows sum G * C)
+        assert np.abs(got[blk, :, row].sum(0) - 24).max() <= 24 * 2.0 ** -14
+
+
+@pytest.mark.parametrize("lens", [(1,), (0, 5), (64,), (65, 63, 1)])
+def test_mass_short(kvq, lens):
+    case = ref.Case(lens=lens, c=2)
+    cache = ref.Cache(case)
+    lse = ref.attend(cache)[1]
+    mass = random_mass(cache)
+    check_mass(mass_call(kvq, cache, lse, mass, 0.5), cache, lse, mass, 0.5, 2)
+
+
+def test_mass_is_reproducible_and_captured(kvq):
+    case = ref.Case(lens=(900, 411), c=24, d=128)
+    cache = ref.Cache(case)
+    g = gpu_cache(kvq, cache)
+    lse = dev(ref.attend(cache)[1].astype(np.float32))
+    p = kvq.make_params(2, 8, 24, cache.width)
+    ws = torch.zeros(kvq.kvq_key_mass_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+    q, table, lens = dev(cache.q).to(torch.bfloat16), dev(cache.table), dev(np.array(case.lens, np.int32))
+    start = dev(random_mass(cache))
+    m1, m2 = start.clone(), start.clone()
+    kvq.kvq_key_mass(g, p, None, q, table, lens, lse, m1, ws, decay=0.9)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        kvq.kvq_key_mass(g, p, None, q, table, lens, lse, m2, ws, decay=0.9)
+    m2.copy_(start)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(m1, m2)
+
+
+# -------------------------------------------------------------------- select
+
+def pages(lens, bs, seed, slack=2, width=None):
+    r = np.random.default_rng(seed)
+    need = [max(1, -(-L // bs)) for L in lens]
+    nb = sum(need) + slack
+    perm = r.permutation(nb).astype(np.int32)
+    table = np.full((len(lens), width or max(need)), nb - 1, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table, nb
+
+
+def select_call(kvq, mass, table, lens, nb, bs, budget, sinks, recent, max_seq_len=0):
+    hkv = mass.shape[1]
+    p = kvq.make_evict_params(len(lens), table.shape[1], budget, num_blocks=nb, block_size=bs, num_kv_heads=hkv,
+                              sinks=sinks, recent=recent, max_seq_len=max_seq_len)
+    keep = guarded(torch.full((len(lens), hkv, budget), -9, dtype=torch.int32, device="cuda"), "keep")
+    kept = guarded(torch.full((len(lens),), -9, dtype=torch.int32, device="cuda"), "kept")
+    kvq.kvq_evict_select(p, dev(mass), dev(table), dev(np.array(lens, np.int32)), keep, kept)
+    return keep.cpu().numpy(), kept.cpu().numpy()
+
+
+def check_select(kvq, mass, lens, bs, budget, sinks, recent, seed=0, **kw):
+    table, nb = pages(lens, bs, seed)
+    full = mass(nb)
+    got = select_call(kvq, full, table, lens, nb, bs, budget, sinks, recent, **kw)
+    assert kvq.kvq_get_device_error() == 0
+    want = ref.select(full, table, lens, bs, budget, sinks, recent)
+    assert np.array_equal(got[1], want[1])
+    assert np.array_equal(got[0], want[0])
+
+
+def masses(kind, hkv, bs, seed=0):
+    r = np.random.default_rng(seed)
+
+    def make(nb):
+        shape = (nb, hkv, bs)
+        if kind == "weights":
+            return r.exponential(0.01, shape).astype(np.float32)
+        if kind == "equal":
+            return np.full(shape, 0.25, np.float32)
+        if kind == "few":
+            return r.integers(0, 3, shape).astype(np.float32)
+        if kind == "close":  # differ in the last bits only
+            return (np.float32(1.0).view(np.uint32) + r.integers(0, 5, shape)).astype(np.uint32).view(np.float32)
+        x = r.standard_normal(shape).astype(np.float32)  # odd: both signs, zeros, infinities, NaN
+        x[r.random(shape) < 0.2] = 0.0
+        x[r.random(shape) < 0.2] = -0.0
+        x[r.random(shape) < 0.1] = np.nan
+        x[r.random(shape) < 0.05] = -np.nan
+        x[r.random(shape) < 0.05] = np.inf
+        x[r.random(shape) < 0.05] = -np.inf
+        x[r.random(shape) < 0.05] = 1e-42
+        return x
+    return make
+
+
+@pytest.mark.parametrize("kind", ["weights", "equal", "few", "close", "odd"])
+@pytest.mark.parametrize("lens,budget,sinks,recent", [
+    ((300,), 100, 4, 16), ((17, 16, 15, 0, 1), 16, 2, 3), ((5000, 2048, 33), 777, 0, 0), ((1000,), 999, 1, 0),
+    ((1000,), 20, 10, 10), ((4097,), 1, 0, 0), ((4097,), 1, 0, 1), ((9000, 8999), 4096, 4, 512),
+])
+def test_select(kvq, kind, lens, budget, sinks, recent):
+    check_select(kvq, masses(kind, 3, 16), lens, 16, budget, sinks, recent)
+
+
+def test_select_long_and_wide(kvq):
+    """Sixteen CTAs to a head; a part longer than the keys a CTA keeps on chip
+    (read again from global memory); lengths far below the bound."""
+    check_select(kvq, masses("weights", 1, 256), (70001,), 256, 20000, 4, 1000)
+    check_select(kvq, masses("few", 2, 256), (262144,), 256, 65536, 4, 8192)
+    check_select(kvq, masses("few", 1, 1024), (900_000, 5, 900_001), 1024, 450_000, 4, 1)
+    check_select(kvq, masses("weights", 8, 64), tuple(range(1, 3000, 61)), 64, 64, 4, 8)
+
+
+def test_select_flags(kvq):
+    table, nb = pages((100, 100), 16, 1)
+    m = masses("weights", 2, 16)(nb)
+    select_call(kvq, m, table, (100, 10 ** 6), nb, 16, 32, 0, 0)
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_SEQ_LEN
+    bad = table.copy()
+    bad[0, 2] = -1
+    got, _ = select_call(kvq, m, bad, (100, 100), nb, 16, 32, 0, 0)
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_BLOCK_ID
+    assert not np.isin(got[0], np.arange(32, 48)).any()  # its rows rank last
+
+
+# ------------------------------------------------------------------- compact
+
+def compact_call(kvq, c: ref.Cache, keep, kept, mass, dst=None):
+    case = c.case
+    g = gpu_cache(kvq, c)
+    p = kvq.make_evict_params(len(case.lens), c.width, keep.shape[2], num_blocks=c.nb, block_size=case.bs,
+                              num_kv_heads=case.hkv)
+    ws = guarded(torch.full((kvq.kvq_evict_compact_workspace_size(g, p) // 4,), 7, dtype=torch.int32, device="cuda"),
+                 "ws")
+    m = None if mass is None else guarded(dev(mass), "mass")
+    kvq.kvq_evict_compact(g, p, dev(c.table), None if dst is None else dev(dst), dev(keep), dev(kept), m, ws)
+    assert kvq.kvq_get_device_error() == 0
+    return g, m
+
+
+def check_compact(kvq, case, budget, seed=0, out_of_place=False, with_mass=True):
+    cache = ref.Cache(case)
+    r = np.random.default_rng(seed)
+    keep = np.full((len(case.lens), case.hkv, budget), -1, np.int32)
+    kept = np.minimum(case.lens, budget).astype(np.int32)
+    for b, L in enumerate(case.lens):
+        for h in range(case.hkv):
+            keep[b, h, :kept[b]] = np.sort(r.permutation(L)[:kept[b]])
+    mass = random_mass(cache) if with_mass else None
+    dst = cache.table
+    if out_of_place:
+        need = -(-budget // case.bs)
+        free = np.setdiff1d(np.arange(cache.nb), np.unique(cache.table))
+        assert len(free) >= need * len(case.lens)
+        dst = np.full_like(cache.table, -1)  # entries behind the kept rows are not read
+        dst[:, :need] = free[:need * len(case.lens)].reshape(len(case.lens), need)
+    g, m = compact_call(kvq, cache, keep, kept, mass, dst if out_of_place else None)
+    arrays = [cache.k_codes] + ([] if case.latent else [cache.v_codes])
+    names = ["k_codes"] + ([] if case.latent else ["v_codes"])
+    for side, mode in (("k", case.km), ("v", case.vm)):
+        if mode in (ROW, GROUP) and not (side == "v" and case.latent):
+            arrays.append(getattr(cache, side + "_scale"))
+            names.append(side + "_scale")
+    if with_mass:
+        arrays.append(mass)
+        names.append("mass")
+    want = ref.compact(arrays, cache.table, dst, keep, kept, case.bs)
+    for name, w in zip(names, want):
+        got = m.cpu().numpy() if name == "mass" else getattr(g, name).cpu().numpy()
+        assert np.array_equal(got.view(np.uint8), np.ascontiguousarray(w).view(np.uint8)), name
+
+
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("lens,budget", [((333, 100, 1), 60), ((200, 128), 128), ((64, 0, 63), 64), ((700,), 1)])
+def test_compact_in_place(kvq, name, lens, budget):
+    check_compact(kvq, dataclasses.replace(CASES[name], lens=lens), budget)
+
+
+@pytest.mark.parametrize("name", ["int8 row d128", "int4 group", "fp8 tensor cap", "latent d576"])
+@pytest.mark.parametrize("bs", [16, 128])
+def test_compact_out_of_place(kvq, name, bs):
+    check_compact(kvq, dataclasses.replace(CASES[name], lens=(333, 100, 1), bs=bs, slack=20), 90, out_of_place=True)
+
+
+@pytest.mark.parametrize("bs,d", [(16, 64), (256, 256), (1024, 128)])
+def test_compact_many_rounds(kvq, bs, d):
+    """Enough rows that every block takes several units of each head, most of
+    them reading rows that other blocks overwrite."""
+    check_compact(kvq, ref.Case(d=d, lens=(30011, 17000), bs=bs, hkv=4, hq=4), 16384, seed=bs)
+
+
+def test_compact_without_weights(kvq):
+    check_compact(kvq, ref.Case(lens=(500, 90)), 77, with_mass=False)
+
+
+def test_compact_bad_index_is_flagged(kvq):
+    case = ref.Case(lens=(100,))
+    cache = ref.Cache(case)
+    keep = np.sort(np.random.default_rng(1).permutation(100)[:20]).astype(np.int32)
+    keep = np.broadcast_to(keep, (1, 2, 20)).copy()
+    for bad in (-1, 10 ** 6):
+        k = keep.copy()
+        k[0, 1, 7] = bad
+        g = gpu_cache(kvq, cache)
+        p = kvq.make_evict_params(1, cache.width, 20, num_blocks=cache.nb, block_size=16, num_kv_heads=2)
+        ws = torch.zeros(kvq.kvq_evict_compact_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+        kvq.kvq_evict_compact(g, p, dev(cache.table), None, dev(k), dev(np.array([20], np.int32)), None, ws)
+        assert kvq.kvq_get_device_error() == kvq.DEVERR_KEEP_INDEX
+        # the other head's rows arrived
+        want = ref.compact([cache.k_codes], cache.table, cache.table, keep, np.array([20]), 16)[0]
+        i = np.arange(20)
+        got = g.k_codes.cpu().numpy()
+        assert np.array_equal(got[cache.table[0, i // 16], 0, i % 16], want[cache.table[0, i // 16], 0, i % 16])
+
+
+def test_compact_is_captured(kvq):
+    """A captured in-place move, replayed on restored contents."""
+    case = ref.Case(lens=(5000, 3000), d=128, hkv=4, hq=4)
+    cache = ref.Cache(case)
+    r = np.random.default_rng(3)
+    keep = np.stack([[np.sort(r.permutation(L)[:1500]) for _ in range(4)] for L in case.lens]).astype(np.int32)
+    g = gpu_cache(kvq, cache)
+    k0 = g.k_codes.clone()
+    p = kvq.make_evict_params(2, cache.width, 1500, num_blocks=cache.nb, block_size=16, num_kv_heads=4)
+    ws = torch.zeros(kvq.kvq_evict_compact_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+    table, kd, n = dev(cache.table), dev(keep), dev(np.array([1500, 1500], np.int32))
+    kvq.kvq_evict_compact(g, p, table, None, kd, n, None, ws)
+    torch.cuda.synchronize()
+    want = g.k_codes.clone()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        kvq.kvq_evict_compact(g, p, table, None, kd, n, None, ws)
+    for _ in range(3):
+        g.k_codes.copy_(k0)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(g.k_codes, want)
+    assert kvq.kvq_get_device_error() == 0
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("steps", [6])
+def test_decode_with_evictions(kvq, steps):
+    """Steps as a server runs them: append, attention under a bias, weights,
+    and an eviction whenever a sequence outgrows its budget; each step's
+    output against the 64-bit attention over the rows that are there."""
+    hq, hkv, d, bs, budget, cap = 8, 2, 128, 16, 48, 64
+    B, nb, width = 2, 10, 4
+    r = np.random.default_rng(0)
+    table = r.permutation(nb)[:B * width].reshape(B, width).astype(np.int32)
+    g = kvq.QuantizedPagedCache(INT8, ROW, ROW, nb, bs, hkv, d)
+    mass = torch.zeros((nb, hkv, bs), device="cuda")
+    slopes = dev(np.array(slopes_of(hq), np.float32))
+    tbl = dev(table)
+    lens = np.array([40, 57], np.int32)
+    ep = kvq.make_evict_params(B, width, budget, num_blocks=nb, block_size=bs, num_kv_heads=hkv, sinks=2, recent=8)
+    eb = kvq.alloc_evict_buffers(g, ep)
+
+    def append(counts):
+        k, v, s = [], [], []
+        for b in range(B):
+            for p in range(int(lens[b]) - counts, int(lens[b])):
+                s.append(table[b, p // bs] * bs + p % bs)
+        n = len(s)
+        k, v = (torch.from_numpy(ref.bf16(r.standard_normal((n, hkv, d)))).to(torch.bfloat16).cuda() for _ in "kv")
+        kvq.kvq_append(g, k, v, dev(np.array(s, np.int64)))
+
+    # the history, as one chunk of 40 tokens each
+    append(40)
+    evicted = 0
+    for step in range(steps):
+        c = 40 if step == 0 else 3
+        if step > 0:
+            lens = lens + 3
+            append(3)
+        case = ref.Case(d=d, hq=hq, hkv=hkv, bs=bs, lens=tuple(int(x) for x in lens), c=c)
+        cache = ref.Cache(case, width=width)
+        cache.nb, cache.table = nb, table
+        cache.q = ref.bf16(r.standard_normal((B, c, hq, d)))
+        p = kvq.make_params(B, hq, c, width)
+        n = max(kvq.kvq_attend_masked_workspace_size(g, p), kvq.kvq_key_mass_workspace_size(g, p))
+        ws = torch.zeros(n // 4, dtype=torch.int32, device="cuda")
+        out = torch.zeros((B, c, hq, d), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((B, c, hq), device="cuda")
+        rule = kvq.ScoreMask(slopes=slopes)
+        q, ld = dev(cache.q).to(torch.bfloat16), dev(lens)
+        before = mass.cpu().numpy()
+        cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale = (
+            t.cpu().numpy() for t in (g.k_codes, g.v_codes, g.k_scale, g.v_scale))
+        kvq.kvq_attend_masked(g, p, rule, q, tbl, ld, None, out, lse, ws)
+        kvq.kvq_key_mass(g, p, rule, q, tbl, ld, lse, mass, ws, decay=0.5)
+        s = slopes_of(hq)
+        check(cache, (out.double().cpu().numpy(), lse.double().cpu().numpy()), s)
+        check_mass(mass.cpu().numpy(), cache, lse.cpu().numpy(), before, 0.5, c, s)
+        if (lens > budget).any():
+            want, new = ref.select(mass.cpu().numpy(), table, [int(x) for x in lens], bs, budget, 2, 8)
+            arrays = [t.cpu().numpy() for t in (g.k_codes, g.v_codes, g.k_scale, g.v_scale, mass)]
+            moved = ref.compact(arrays, table, table, want, new, bs)
+            kept = kvq.evict_step(g, ep, tbl, ld, mass, eb)
+            assert np.array_equal(eb.keep.cpu().numpy(), want)
+            for t, w in zip((g.k_codes, g.v_codes, g.k_scale, g.v_scale, mass), moved):
+                assert np.array_equal(t.cpu().numpy(), w)
+            lens = kept.cpu().numpy()
+            evicted += 1
+    assert evicted >= 2 and cap >= budget
+    assert kvq.kvq_get_device_error() == 0
+
+
+def test_refuses_wrong_tensors(kvq):
+    case = ref.Case(lens=(50,), c=2)
+    cache = ref.Cache(case)
+    g = gpu_cache(kvq, cache)
+    p = kvq.make_params(1, 8, 2, cache.width)
+    ws = torch.zeros(4096, dtype=torch.int32, device="cuda")
+    q, table, lens = dev(cache.q).to(torch.bfloat16), dev(cache.table), dev(np.array([50], np.int32))
+    lse, mass = torch.zeros((1, 2, 8), device="cuda"), torch.zeros((cache.nb, 2, 16), device="cuda")
+    for a in ((q, table, lens, lse.double(), mass), (q, table, lens, lse, mass[1:]), (q[:, :1], table, lens, lse, mass),
+              (q, table, lens, lse, mass.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            kvq.kvq_key_mass(g, p, None, *a, ws)
+    for kw in (dict(decay=1.5), dict(decay=-0.1), dict(decay=float("nan")), dict(fresh=-1)):
+        with pytest.raises(kvq.KvqError):
+            kvq.kvq_key_mass(g, p, None, q, table, lens, lse, mass, ws, **kw)
+    ep = kvq.make_evict_params(1, cache.width, 20, num_blocks=cache.nb, block_size=16, num_kv_heads=2)
+    keep = torch.zeros((1, 2, 20), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        kvq.kvq_evict_select(ep, mass, table, lens, keep[:, :1], lens.clone())
+    with pytest.raises(kvq.KvqError):
+        kvq.kvq_evict_select(ep, mass, table, lens, keep, lens)  # lengths in and out are one tensor
+    other = kvq.make_evict_params(1, cache.width, 20, num_blocks=cache.nb + 1, block_size=16, num_kv_heads=2)
+    with pytest.raises(kvq.KvqError):
+        kvq.kvq_evict_compact(g, other, table, None, keep, lens.clone(), None, ws)
