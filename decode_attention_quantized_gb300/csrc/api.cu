@@ -174,8 +174,11 @@ size_t stage_stride(const kvq_cache* c, bool alias) {
   return ((alias ? 1 : 2) * code + sc + 1023) / 1024 * 1024;
 }
 
-size_t fixed_smem(const kvq_cache* c, int row_groups, int key_warps, int nt, int batch, int stages) {
+// split: room for the second part of the Q operand (the masked kernels).
+size_t fixed_smem(const kvq_cache* c, int row_groups, int key_warps, int nt, int batch, int stages,
+                  bool split = false) {
   size_t s = 1024;  // alignment slack of the ring
+  if (split) s += nt > 0 ? (size_t)16 * nt * c->head_dim * 2 : (size_t)row_groups * c->head_dim / 16 * 32 * 8;
   if (nt > 0)  // wide layout: P buffer, row maxima / sums, Q operand, logit factors
     s += (size_t)(16 * nt * 32 + 2 * 4 * 16 * nt + 32 + 16 * nt * (c->head_dim / 2) + (16 * nt + 31) / 32 * 32) * 4;
   else if (key_warps > 1)
@@ -189,12 +192,12 @@ size_t fixed_smem(const kvq_cache* c, int row_groups, int key_warps, int nt, int
 // wide), or -group_size for the grouped layout with per-group scales.
 int kernel_nt(const kvq_cache* c, const Plan& P) { return any_group(c) ? -c->group_size : P.nt; }
 
-cudaError_t occupancy(const kvq_cache* c, int nt, int threads, size_t smem, bool mask, int* n) {
+cudaError_t occupancy(const kvq_cache* c, int nt, int threads, size_t smem, bool mask, bool split, int* n) {
   if (mask) {
     switch (c->dtype) {
-      case KVQ_INT8: return occupancy_decode_mask_int8(c->head_dim, nt, threads, smem, n);
-      case KVQ_FP8_E4M3: return occupancy_decode_mask_fp8(c->head_dim, nt, threads, smem, n);
-      default: return occupancy_decode_mask_int4(c->head_dim, nt, threads, smem, n);
+      case KVQ_INT8: return occupancy_decode_mask_int8(c->head_dim, nt, split, threads, smem, n);
+      case KVQ_FP8_E4M3: return occupancy_decode_mask_fp8(c->head_dim, nt, split, threads, smem, n);
+      default: return occupancy_decode_mask_int4(c->head_dim, nt, split, threads, smem, n);
     }
   }
   switch (c->dtype) {
@@ -249,18 +252,19 @@ bool qt_ok(const kvq_cache* c, const kvq_decode_params* p) {
 // The query-tile kernel: one CTA per SM (it holds all of the SM's TMEM), the
 // mma.sync kernel's 64-key stages, as many of them as fit beside the two
 // double-buffered f16 tiles.
-kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, Plan* P) {
+kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool split, Plan* P) {
+  const bool exch = split && c->head_dim == 256;
   const int B = p->batch > 0 ? p->batch : 1;
   const size_t stride = stage_stride(c, false);
   constexpr size_t kMaxSmem = 227 * 1024;  // per CTA
   int stages = 0;
   for (int s = kQtMaxStages; s >= 2 && stages == 0; --s)
-    if ((size_t)qt_smem_layout(c->head_dim, s, B, (int)stride).total + 1024 <= kMaxSmem) stages = s;
+    if ((size_t)qt_smem_layout(c->head_dim, s, B, (int)stride, exch).total + 1024 <= kMaxSmem) stages = s;
   if (stages == 0) return KVQ_ERR_UNSUPPORTED;
   P->qt = 1;
   P->stages = stages;
   P->stride = stride;
-  P->smem = (size_t)qt_smem_layout(c->head_dim, stages, B, (int)stride).total + 1024;
+  P->smem = (size_t)qt_smem_layout(c->head_dim, stages, B, (int)stride, exch).total + 1024;
   P->threads = kQtWarps * 32;
   const long long cap = (long long)p->max_blocks_per_seq * c->block_size;
   const long long maxlen = (p->max_seq_len > 0 && p->max_seq_len < cap) ? p->max_seq_len : cap;
@@ -321,19 +325,20 @@ kvq_status make_plan_mass(const kvq_cache* c, const kvq_decode_params* p, const 
 }
 
 // Which kernels a plan is for: the attention kernels, their masked instances
-// (no tensor-memory layout of keys as MMA rows there), the key-mass kernel.
-enum PlanKind { kPlanDecode = 0, kPlanMasked = 1, kPlanMass = 2 };
+// (no tensor-memory layout of keys as MMA rows there; Split: a two-part Q
+// operand), the key-mass kernel.
+enum PlanKind { kPlanDecode = 0, kPlanMasked = 1, kPlanMass = 2, kPlanMaskedSplit = 3 };
 
 kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool qt,
                               PlanKind kind, Plan* out) {
   if (kind == kPlanMass) return make_plan_mass(c, p, dev, out);
-  const bool mask = kind == kPlanMasked;
+  const bool split = kind == kPlanMaskedSplit, mask = kind == kPlanMasked || split;
   Plan P{};
   const int G = p->num_q_heads / c->num_kv_heads;
   P.rows = G * p->q_tokens;
   if (qt) {
     if (!qt_ok(c, p) || P.rows > kQtRows) return KVQ_ERR_UNSUPPORTED;
-    if (kvq_status s = make_plan_qt(c, p, dev, &P)) return s;
+    if (kvq_status s = make_plan_qt(c, p, dev, split, &P)) return s;
     const int B = p->batch > 0 ? p->batch : 1;
     P.units_max = P.grid + B * c->num_kv_heads;
     P.ws_plan = align256((size_t)(4 + B + 1) * 4);
@@ -383,16 +388,16 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
   for (int target : {4, 3, 2, 1}) {
     // per-SM shared memory is 228 KiB with 1 KiB reserved per resident CTA
     const size_t budget = (size_t)228 * 1024 / target - 1024;
-    const size_t fixed = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, 0);
+    const size_t fixed = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, 0, split);
     // head_dim 576 stages are 37 KB: two CTAs of two stages each still keep
     // 148 KB in flight per SM, and twice the warps hide more latency
     const int min_stages = target > 1 && c->head_dim != 576 ? 3 : 2;
     if (fixed + (size_t)min_stages * (stride + 16) > budget) continue;
     int stages = (int)((budget - fixed) / (stride + 16));
     stages = stages > kMaxStages ? kMaxStages : stages;
-    const size_t smem = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, stages) + (size_t)stages * stride;
+    const size_t smem = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, stages, split) + (size_t)stages * stride;
     int n = 0;
-    if (occupancy(c, kernel_nt(c, P), P.threads, smem, mask, &n) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (occupancy(c, kernel_nt(c, P), P.threads, smem, mask, split, &n) != cudaSuccess) return KVQ_ERR_CUDA;
     if (n >= target) {
       occ = target;
       P.stages = stages;
@@ -568,7 +573,10 @@ struct MaskCall {
   const float* slopes;
   const int32_t* key_begin;
   const int32_t* key_end;
+  bool split;  // the Q operand in two parts
 };
+
+PlanKind plan_kind(const MaskCall* m) { return !m ? kPlanDecode : (m->split ? kPlanMaskedSplit : kPlanMasked); }
 
 // kvq_decode with the block-table row of sequence b at b / bt_div.  With
 // early_reads 1, q, the block table, seq_lens and the static scales are read
@@ -590,7 +598,7 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   Plan P;
-  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, mask ? kPlanMasked : kPlanDecode)) return s;
+  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, plan_kind(mask))) return s;
   if (workspace_bytes < P.ws_total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
 
   alignas(64) CUtensorMap tk, tv;
@@ -652,16 +660,16 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
   cudaError_t e;
   if (mask && P.qt) {
     switch (cache->dtype) {
-      case KVQ_INT8: e = launch_qt_mask_int8(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
-      case KVQ_FP8_E4M3: e = launch_qt_mask_fp8(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
-      default: e = launch_qt_mask_int4(cache->head_dim, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_INT8: e = launch_qt_mask_int8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_qt_mask_fp8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      default: e = launch_qt_mask_int4(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
     }
   } else if (mask) {
     const int nt = kernel_nt(cache, P);
     switch (cache->dtype) {
-      case KVQ_INT8: e = launch_decode_mask_int8(cache->head_dim, nt, tk, tv, a, P.grid, P.threads, P.smem, st); break;
-      case KVQ_FP8_E4M3: e = launch_decode_mask_fp8(cache->head_dim, nt, tk, tv, a, P.grid, P.threads, P.smem, st); break;
-      default: e = launch_decode_mask_int4(cache->head_dim, nt, tk, tv, a, P.grid, P.threads, P.smem, st); break;
+      case KVQ_INT8: e = launch_decode_mask_int8(cache->head_dim, nt, mask->split, tk, tv, a, P.grid, P.threads, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_decode_mask_fp8(cache->head_dim, nt, mask->split, tk, tv, a, P.grid, P.threads, P.smem, st); break;
+      default: e = launch_decode_mask_int4(cache->head_dim, nt, mask->split, tk, tv, a, P.grid, P.threads, P.smem, st); break;
     }
   } else if (P.qt) {
     switch (cache->dtype) {
@@ -740,7 +748,7 @@ kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params,
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   Plan P;
-  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, mask ? kPlanMasked : kPlanDecode)) return s;
+  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, plan_kind(mask))) return s;
   if (workspace_bytes < P.ws_total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
   const char* ws = static_cast<const char*>(workspace);
   CombineArgs a{};
@@ -780,7 +788,7 @@ kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params,
 
 
 kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params* params, bool qt,
-                                 size_t* workspace_bytes, bool mask = false) {
+                                 size_t* workspace_bytes, PlanKind kind = kPlanDecode) {
   kvq_cache eff_;
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
@@ -789,7 +797,7 @@ kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   Plan P;
-  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, mask ? kPlanMasked : kPlanDecode)) return s;
+  if (kvq_status s = make_plan(cache, params, *dev, &P, qt, kind)) return s;
   *workspace_bytes = P.ws_total;
   return KVQ_OK;
 }
@@ -798,22 +806,26 @@ kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params
 // sequence, the last one shorter.  The query-tile kernel takes as many tokens
 // as fill its 128 rows when that gives at least 64 rows (the rule kvq_prefill
 // uses); otherwise the mma.sync kernel takes up to 8 (head_dim 576: up to its
-// 48 rows).
+// 48 rows).  A two-part Q operand (split: a per-channel K scale whose call
+// wants the lse) leaves the tile 64 rows at head_dim 256; G times a whole
+// number of tokens fills at least 56 of them.
 struct MaskShape {
   int T, n;
-  bool qt;
+  bool qt, split;
   long long groups;  // batch * n
 };
 
-kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, MaskShape* out) {
+kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse, MaskShape* out) {
   if (!p || p->q_tokens < 1 || p->batch < 0 || p->num_q_heads <= 0) return KVQ_ERR_INVALID_ARG;
   if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
   const int C = p->q_tokens, G = p->num_q_heads / c->num_kv_heads;
   if (G > 8 || p->batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
   if ((long long)p->batch * C > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
   MaskShape s{};
-  s.T = kQtRows / G < C ? kQtRows / G : C;
-  s.qt = qt_ok(c, p) && s.T * G >= 64;
+  s.split = lse && c->k_mode == KVQ_SCALE_PER_CHANNEL;
+  const int tile = s.split && c->head_dim == 256 ? kQtRows / 2 : kQtRows;
+  s.T = tile / G < C ? tile / G : C;
+  s.qt = qt_ok(c, p) && s.T * G >= (tile == kQtRows ? 64 : 56);
   if (!s.qt) {
     const int most = c->head_dim == 576 && 48 / G < 8 ? 48 / G : 8;
     s.T = most < C ? most : C;
@@ -844,7 +856,7 @@ kvq_status masked_workspace(const kvq_cache* c, const kvq_decode_params* p, cons
   for (long long count : {s.groups >= kMaxBatch ? (long long)kMaxBatch : last, last}) {
     const kvq_decode_params v = masked_params(p, s, count);
     size_t ws = 0;
-    if (kvq_status st = decode_workspace_size(c, &v, s.qt, &ws, true)) return st;
+    if (kvq_status st = decode_workspace_size(c, &v, s.qt, &ws, s.split ? kPlanMaskedSplit : kPlanMasked)) return st;
     most = ws > most ? ws : most;
   }
   *total = *head + most;
@@ -1091,10 +1103,16 @@ KVQ_API kvq_status kvq_attend_masked_workspace_size(const kvq_cache* cache, cons
   if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
   kvq_cache eff_;
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
-  MaskShape shape;
-  if (kvq_status s = masked_shape(&eff_, params, &shape)) return s;
-  size_t head = 0;
-  return masked_workspace(&eff_, params, shape, &head, workspace_bytes);
+  size_t most = 0;  // with and without an lse
+  for (bool lse : {false, true}) {
+    MaskShape shape;
+    if (kvq_status s = masked_shape(&eff_, params, lse, &shape)) return s;
+    size_t head = 0, need = 0;
+    if (kvq_status s = masked_workspace(&eff_, params, shape, &head, &need)) return s;
+    most = need > most ? need : most;
+  }
+  *workspace_bytes = most;
+  return KVQ_OK;
 }
 
 KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_params* params,
@@ -1105,7 +1123,7 @@ KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_pa
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
   MaskShape shape;
-  if (kvq_status s = masked_shape(cache, params, &shape)) return s;
+  if (kvq_status s = masked_shape(cache, params, lse_out != nullptr, &shape)) return s;
   {
     const kvq_decode_params v = masked_params(params, shape, shape.groups < kMaxBatch ? shape.groups : kMaxBatch);
     if (kvq_status s = check_params(cache, &v, shape.qt)) return s;
@@ -1128,7 +1146,8 @@ KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_pa
                                     reinterpret_cast<cudaStream_t>(stream)))
     return s;
   char* ws = static_cast<char*>(workspace) + head;
-  MaskCall mc{table, mask ? mask->slopes : nullptr, mask ? mask->key_begin : nullptr, mask ? mask->key_end : nullptr};
+  MaskCall mc{table, mask ? mask->slopes : nullptr, mask ? mask->key_begin : nullptr, mask ? mask->key_end : nullptr,
+              shape.split};
   for (long long v0 = 0; v0 < shape.groups; v0 += kMaxBatch) {
     const long long left = shape.groups - v0;
     const kvq_decode_params v = masked_params(params, shape, left < kMaxBatch ? left : kMaxBatch);

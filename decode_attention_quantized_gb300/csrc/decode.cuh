@@ -276,14 +276,19 @@ __host__ __device__ constexpr int wide_scratch_floats() {
 // GS > 0: the grouped layout with the per-group scale paths for groups of GS
 // channels compiled in (a kernel of its own per group size, so that its
 // group boundaries are compile-time and the other modes carry none of it).
-// MASK: the score rule of a masked call (distance bias, an interval of keys
-// per query token) over its virtual sequences, in kernels of its own so that
-// the unmasked ones carry none of it.
-template <int DT, int D, int MINB, int NT, int GS, bool MASK>
+// RULE > 0: the score rule of a masked call (distance bias, an interval of
+// keys per query token) over its virtual sequences, in kernels of its own so
+// that the unmasked ones carry none of it.  RULE == 2 (a per-channel K scale
+// and an lse that is asked for): the Q operand in two f16 parts, the second
+// one in shared memory.  An f16 query with the scale folded in is 2^-12 off,
+// which the bf16 output hides but the fp32 lse shows (3e-5 of it under a
+// steep bias; 1e-7 with the second part).
+template <int DT, int D, int MINB, int NT, int GS, int RULE>
 __global__ void __launch_bounds__(288, MINB)
     decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const DecodeArgs a) {
   using Gm = Geo<DT, D>;
+  constexpr bool MASK = RULE > 0, SPLIT = RULE == 2;
   constexpr float kLog2e = 1.4426950408889634f;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -292,8 +297,13 @@ __global__ void __launch_bounds__(288, MINB)
   const int n_cw = a.row_groups * a.key_warps;
   constexpr int kScrPerRg = (Gm::NMT * 4 + 4) * 32;  // floats: accumulators + (m, l) of one warp, [elem][lane]
   float* scr = reinterpret_cast<float*>(ring + (size_t)a.stages * a.stage_stride);
-  const int scr_floats =
+  // floats of the second Q part: [row group][k-step][lane] fragments (grouped)
+  // or a second [rows][D] f16 operand (wide)
+  constexpr int kLoPerRg = Gm::NMT * 32 * 2;
+  const int lo_floats = !SPLIT ? 0 : (NT > 0 ? 16 * NT * (D / 2) : a.row_groups * kLoPerRg);
+  const int scr_only =
       NT > 0 ? wide_scratch_floats<NT, D>() : (a.key_warps > 1 ? a.row_groups * kScrPerRg : 0);
+  const int scr_floats = scr_only + lo_floats;
   int* pl_pre = reinterpret_cast<int*>(scr + scr_floats);  // [B + 1]
   int* pl_misc = pl_pre + a.batch + 1;                     // [4]
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(pl_misc + 4 + ((a.batch + 5) & 1));
@@ -348,6 +358,7 @@ __global__ void __launch_bounds__(288, MINB)
     const uint32_t p_base = ptx::smem_u32(scr);          // P: [ROWS][64 keys] f16, 128-byte rows
     float* s_q = s_vmax + 32;                            // Q: [ROWS][D] f16 in MMA k-slot order
     const uint32_t q_base = ptx::smem_u32(s_q);
+    const uint32_t ql_base = ptx::smem_u32(scr + scr_only);
     float* s_alpha = s_q + ROWS * (D / 2);               // [ROWS] logit factors
     const int rh = warp & 1, kq = warp >> 1;
     // a row half past the unit's rows (8 or fewer rows: head_dim 576 with
@@ -383,12 +394,16 @@ __global__ void __launch_bounds__(288, MINB)
       if constexpr (D <= 256) {
         if (kq < NT) {
           const int row = rh * RW + kq * 8 + g;
-          uint32_t qf[Gm::NMT][2];
-          const float ag = dev::q_prologue<DT, D>(a, row, tok0, rows, h, c, qf);
+          uint32_t qf[Gm::NMT][2], ql[SPLIT ? Gm::NMT : 1][2];
+          const float ag = dev::q_prologue<DT, D, SPLIT>(a, row, tok0, rows, h, c, qf, ql);
 #pragma unroll
           for (int ks = 0; ks < Gm::NMT; ++ks) {
             ptx::st_shared_u32(q_base + q_off(row, ks * 16 + 2 * c), qf[ks][0]);
             ptx::st_shared_u32(q_base + q_off(row, ks * 16 + 8 + 2 * c), qf[ks][1]);
+            if constexpr (SPLIT) {
+              ptx::st_shared_u32(ql_base + q_off(row, ks * 16 + 2 * c), ql[ks][0]);
+              ptx::st_shared_u32(ql_base + q_off(row, ks * 16 + 8 + 2 * c), ql[ks][1]);
+            }
           }
           if (c == 0) s_alpha[row] = ag;
         }
@@ -468,8 +483,13 @@ __global__ void __launch_bounds__(288, MINB)
 #pragma unroll
               for (int i = 0; i < 4; ++i) v[i] *= ksp[16 * j + 4 * c + i] * sk;
             }
-            ptx::st_shared_u32(q_base + q_off(r, 16 * j + 2 * c), dev::pack_h2(v[0] * sq, v[1] * sq));
-            ptx::st_shared_u32(q_base + q_off(r, 16 * j + 8 + 2 * c), dev::pack_h2(v[2] * sq, v[3] * sq));
+            const uint32_t w0 = dev::pack_h2(v[0] * sq, v[1] * sq), w1 = dev::pack_h2(v[2] * sq, v[3] * sq);
+            ptx::st_shared_u32(q_base + q_off(r, 16 * j + 2 * c), w0);
+            ptx::st_shared_u32(q_base + q_off(r, 16 * j + 8 + 2 * c), w1);
+            if constexpr (SPLIT) {
+              ptx::st_shared_u32(ql_base + q_off(r, 16 * j + 2 * c), dev::rest_h2(v[0] * sq, v[1] * sq, w0));
+              ptx::st_shared_u32(ql_base + q_off(r, 16 * j + 8 + 2 * c), dev::rest_h2(v[2] * sq, v[3] * sq, w1));
+            }
           }
           if (kq == 0 && c == 0) {
             float alpha = ldexpf(base, ek + eq);
@@ -536,7 +556,7 @@ __global__ void __launch_bounds__(288, MINB)
             for (int nt = 0; nt < NT; ++nt) sacc[ch][nt][0] = sacc[ch][nt][1] = sacc[ch][nt][2] = sacc[ch][nt][3] = 0.0f;
           const uint32_t row_off = (uint32_t)(kq * kSub + ld_key) * Gm::SPAN;
           // B fragments of k-step ks for every n-tile of this half, from Q
-          auto qfrag = [&](int ks, uint32_t (&bq)[NT][2]) {
+          auto qfrag = [&](uint32_t q_base, int ks, uint32_t (&bq)[NT][2]) {
             const int mi = lane >> 3;
 #pragma unroll
             for (int np = 0; np < NT / 2; ++np) {
@@ -573,19 +593,30 @@ __global__ void __launch_bounds__(288, MINB)
                   uint32_t A[4];
                   dev::k_frag<DT>(wl, wh, t, A);
                   uint32_t bq[NT][2];
-                  qfrag(2 * j + t, bq);
+                  qfrag(q_base, 2 * j + t, bq);
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt) ptx::mma_16816(sacc[0][nt], A, bq[nt][0], bq[nt][1]);
+                  if constexpr (SPLIT) {
+                    qfrag(ql_base, 2 * j + t, bq);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) ptx::mma_16816(sacc[0][nt], A, bq[nt][0], bq[nt][1]);
+                  }
                 }
               } else {
                 uint32_t A[4];
                 dev::k_frag<DT>(wl, wh, 0, A);
                 uint32_t bq[NT][2];
-                qfrag(j, bq);
+                qfrag(q_base, j, bq);
                 constexpr int chain = NCHAIN > 1 ? 1 : 0;  // (kk & 1) * 2 + h2 below when chained
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   ptx::mma_16816(sacc[chain ? ((kk & 1) * 2 + h2) % NCHAIN : 0][nt], A, bq[nt][0], bq[nt][1]);
+                if constexpr (SPLIT) {
+                  qfrag(ql_base, j, bq);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    ptx::mma_16816(sacc[chain ? ((kk & 1) * 2 + h2) % NCHAIN : 0][nt], A, bq[nt][0], bq[nt][1]);
+                }
               }
             }
           }
@@ -899,7 +930,22 @@ __global__ void __launch_bounds__(288, MINB)
     uint32_t qf[Gm::NMT][2];
     const size_t tok0 = MASK ? (size_t)a.vseq[b].tok0 : (size_t)b * T;
     const int rows = MASK ? a.vseq[b].ntok * G : a.rows;
-    const float alpha_g = dev::q_prologue<DT, D>(a, rg * 8 + g, tok0, rows, h, c, qf);
+    float alpha_g;
+    uint2* lo = reinterpret_cast<uint2*>(scr + scr_only + rg * kLoPerRg) + lane;  // [k-step][lane]
+    if constexpr (SPLIT) {
+      // the second part: the same for every key warp of the row group, so the
+      // first one writes it (all of them have left the previous piece: the
+      // merge's barriers, or a row group of one warp)
+      uint32_t ql[Gm::NMT][2];
+      alpha_g = dev::q_prologue<DT, D, true>(a, rg * 8 + g, tok0, rows, h, c, qf, ql);
+      if (kw == 0) {
+#pragma unroll
+        for (int ks = 0; ks < Gm::NMT; ++ks) lo[ks * 32] = make_uint2(ql[ks][0], ql[ks][1]);
+      }
+      if (a.key_warps > 1) ptx::named_bar_sync(1, (uint32_t)n_cw * 32);
+    } else {
+      alpha_g = dev::q_prologue<DT, D>(a, rg * 8 + g, tok0, rows, h, c, qf);
+    }
     const int r0 = rg * 8 + 2 * c, r1 = r0 + 1;
     // with a softcap the row factors also carry 1/softcap (clamped to FLT_MAX
     // like the factors themselves, so zero codes keep zero scores), and the
@@ -973,6 +1019,10 @@ __global__ void __launch_bounds__(288, MINB)
                   ptx::mma_16816(sa, A, qf[2 * j + t][0], qf[2 * j + t][1]);
                 else
                   ptx::mma_16816(sb, A, qf[2 * j + t][0], qf[2 * j + t][1]);
+                if constexpr (SPLIT) {
+                  const uint2 l2 = lo[(2 * j + t) * 32];
+                  ptx::mma_16816(t == 0 ? sb : sa, A, l2.x, l2.y);
+                }
               }
             } else {
               uint32_t A[4];
@@ -981,6 +1031,10 @@ __global__ void __launch_bounds__(288, MINB)
                 ptx::mma_16816(sa, A, qf[j][0], qf[j][1]);
               else
                 ptx::mma_16816(sb, A, qf[j][0], qf[j][1]);
+              if constexpr (SPLIT) {
+                const uint2 l2 = lo[j * 32];
+                ptx::mma_16816(h2 == 0 ? sb : sa, A, l2.x, l2.y);
+              }
             }
             if (k_grp && (((j + 1) * CH) & gmask) == 0) {
               const int grp = (j + 1) * CH / (GRP ? GS : 1) - 1;
@@ -1255,7 +1309,7 @@ __global__ void __launch_bounds__(288, MINB)
 // Raises (never lowers) the kernel's dynamic shared-memory limit on the
 // current device; shared by the occupancy query and the launch so that a
 // query for a small plan cannot undercut a larger plan launched later.
-template <int DT, int D, int MINB, int NT, int GS, bool MASK>
+template <int DT, int D, int MINB, int NT, int GS, int RULE>
 cudaError_t ensure_smem(size_t smem) {
   static int smem_set[64] = {};
   int dev = 0;
@@ -1263,7 +1317,7 @@ cudaError_t ensure_smem(size_t smem) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(decode_kernel<DT, D, MINB, NT, GS, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_kernel<DT, D, MINB, NT, GS, RULE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem);
     if (e != cudaSuccess) return e;
     smem_set[dev] = (int)smem;
@@ -1271,19 +1325,19 @@ cudaError_t ensure_smem(size_t smem) {
   return cudaSuccess;
 }
 
-template <int DT, int D, int MINB, int NT, int GS, bool MASK>
+template <int DT, int D, int MINB, int NT, int GS, int RULE>
 cudaError_t launch_decode_d(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid,
                             int threads, size_t smem, cudaStream_t stream) {
-  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS, MASK>(smem);
+  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS, RULE>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_kernel<DT, D, MINB, NT, GS, MASK>, grid, threads, smem, stream, tk, tv, a);
+  return launch_pdl(decode_kernel<DT, D, MINB, NT, GS, RULE>, grid, threads, smem, stream, tk, tv, a);
 }
 
-template <int DT, int D, int MINB, int NT, int GS, bool MASK>
+template <int DT, int D, int MINB, int NT, int GS, int RULE>
 cudaError_t occupancy_decode_d(int threads, size_t smem, int* blocks_per_sm) {
-  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS, MASK>(smem);
+  cudaError_t e = ensure_smem<DT, D, MINB, NT, GS, RULE>(smem);
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, decode_kernel<DT, D, MINB, NT, GS, MASK>,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, decode_kernel<DT, D, MINB, NT, GS, RULE>,
                                                        threads, smem);
 }
 
@@ -1299,15 +1353,15 @@ struct KernelCfg {
 // Dispatch on head_dim and on nt (0: grouped layout; -32, -64, -128: grouped
 // layout with per-group scales of that many channels; 2, 3: wide layout; head
 // dim 576, 8-bit codes only: the wide layout with nt = 1, 2 or 3).
-template <int DT, bool Query, bool MASK = false>
+template <int DT, bool Query, int RULE = 0>
 cudaError_t dispatch_decode(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv, const DecodeArgs* a,
                             int grid, int threads, size_t smem, cudaStream_t stream, int* blocks_per_sm) {
   auto go = [&](auto cfg) -> cudaError_t {
     using K = decltype(cfg);
     if constexpr (Query)
-      return occupancy_decode_d<DT, K::d, K::minb, K::nt, K::gs, MASK>(threads, smem, blocks_per_sm);
+      return occupancy_decode_d<DT, K::d, K::minb, K::nt, K::gs, RULE>(threads, smem, blocks_per_sm);
     else
-      return launch_decode_d<DT, K::d, K::minb, K::nt, K::gs, MASK>(*tk, *tv, *a, grid, threads, smem, stream);
+      return launch_decode_d<DT, K::d, K::minb, K::nt, K::gs, RULE>(*tk, *tv, *a, grid, threads, smem, stream);
   };
   auto by_nt = [&](auto dtag) -> cudaError_t {
     constexpr int d = decltype(dtag)::value;
@@ -1329,7 +1383,7 @@ cudaError_t dispatch_decode(int head_dim, int nt, const CUtensorMap* tk, const C
     case 256: return by_nt(std::integral_constant<int, 256>{});
     case 576:
       if constexpr (DT != KVQ_INT4) {
-        if (nt == 1) return go(KernelCfg<576, MASK ? 1 : 2, 1>{});  // two CTAs per SM (96 registers)
+        if (nt == 1) return go(KernelCfg<576, (RULE > 0) ? 1 : 2, 1>{});  // two CTAs per SM (96 registers)
         if (nt == 2) return go(KernelCfg<576, 1, 2>{});
         if (nt == 3) return go(KernelCfg<576, 1, 3>{});
       }

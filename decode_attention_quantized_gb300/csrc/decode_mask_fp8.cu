@@ -4,14 +4,24 @@
 
 namespace kvq {
 
-cudaError_t launch_decode_mask_fp8(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+// decode_split_fp8.cu
+cudaError_t dispatch_decode_split_fp8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                       const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                       int* blocks_per_sm);
+
+cudaError_t launch_decode_mask_fp8(int head_dim, int nt, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream) {
-  return dispatch_decode<KVQ_FP8_E4M3, false, true>(head_dim, nt, &tk, &tv, &a, grid, threads, smem, stream, nullptr);
+  if (split) return dispatch_decode_split_fp8(head_dim, nt, &tk, &tv, &a, grid, threads, smem, stream, nullptr);
+  return dispatch_decode<KVQ_FP8_E4M3, false, 1>(head_dim, nt, &tk, &tv, &a, grid, threads, smem, stream, nullptr);
 }
 
-cudaError_t occupancy_decode_mask_fp8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm) {
-  return dispatch_decode<KVQ_FP8_E4M3, true, true>(head_dim, nt, nullptr, nullptr, nullptr, 0, threads, smem, nullptr,
-                                               blocks_per_sm);
+cudaError_t occupancy_decode_mask_fp8(int head_dim, int nt, bool split, int threads, size_t smem,
+                                       int* blocks_per_sm) {
+  if (split)
+    return dispatch_decode_split_fp8(head_dim, nt, nullptr, nullptr, nullptr, 0, threads, smem, nullptr,
+                                      blocks_per_sm);
+  return dispatch_decode<KVQ_FP8_E4M3, true, 1>(head_dim, nt, nullptr, nullptr, nullptr, 0, threads, smem, nullptr,
+                                            blocks_per_sm);
 }
 
 }  // namespace kvq

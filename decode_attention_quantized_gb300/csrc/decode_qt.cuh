@@ -42,7 +42,8 @@
 
 namespace kvq {
 
-template <int DT, int D>
+// LO: columns of a second Q part (head_dim 128; see decode_qt_kernel).
+template <int DT, int D, bool LO = false>
 struct QtCfg {
   using Gm = Geo<DT, D, kTile>;
   static constexpr int KT = kTile;
@@ -50,7 +51,8 @@ struct QtCfg {
   static constexpr int TILE = (D / 64) * SLAB;     // bytes of one f16 tile (K or V)
   // TMEM columns (32-bit); lanes are query rows
   static constexpr int Q_COL = 0;                  // [128 rows x D] f16 pairs
-  static constexpr int O_COL = D / 2;              // [128 rows x D] fp32
+  static constexpr int QL_COL = D / 2;             // its second part
+  static constexpr int O_COL = D / 2 * (LO ? 2 : 1);  // [128 rows x D] fp32
   static constexpr int NSB = D == 128 ? 2 : 1;     // S buffers (one at head_dim 256: TMEM is full)
   static constexpr int S_COL = O_COL + D;          // NSB x [128 rows x 64 keys] fp32
   static constexpr int P_COL = S_COL + NSB * KT;   // 2 x [128 rows x 64 keys] f16 pairs
@@ -89,13 +91,19 @@ __device__ __forceinline__ uint32_t qt_chunk(uint32_t tile, int kk, int c) {
 
 }  // namespace dev
 
-// MASK: the score rule of a masked call over its virtual sequences, in a
-// kernel of its own.
-template <int DT, int D, bool MASK>
+// RULE > 0: the score rule of a masked call over its virtual sequences, in
+// kernels of its own.  RULE == 2: the Q operand in two f16 parts (decode.cuh).
+// At head_dim 128 the second part has tensor-memory columns of its own and a
+// second pass of QK^T adds into the same S.  At head_dim 256 tensor memory is
+// full: a unit then has at most 64 rows, the second parts are the operand's
+// rows 64..127, and warps 2 and 3 hand their rows of S to warps 0 and 1
+// through shared memory (as f16: 2^-11 of a 2^-12 correction).
+template <int DT, int D, int RULE>
 __global__ void __launch_bounds__(kQtWarps * 32, 1)
     decode_qt_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const DecodeArgs a) {
-  using C = QtCfg<DT, D>;
+  constexpr bool MASK = RULE > 0, SPLIT = RULE == 2, STACK = SPLIT && D == 256;
+  using C = QtCfg<DT, D, SPLIT && !STACK>;
   using Gm = typename C::Gm;
   constexpr int KT = C::KT;
   constexpr int kDqK = 4, kDqV = 8, kProducer = 12, kMma = 13, kMmaPv = 14;
@@ -104,7 +112,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* base = smem_raw + pad;
-  const QtSmem lay = qt_smem_layout(D, a.stages, a.batch, a.stage_stride);
+  const QtSmem lay = qt_smem_layout(D, a.stages, a.batch, a.stage_stride, STACK);
   uint8_t* ring = base + lay.ring;
   const uint32_t kf = ptx::smem_u32(base + lay.kf), vf = ptx::smem_u32(base + lay.vf);
   float* ksb = reinterpret_cast<float*>(base + lay.sc);  // [4][KT] K scales of tile it, at it & 3
@@ -319,6 +327,12 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           for (int sl = 0; sl < D / 64; ++sl)
             ptx::mma_f16_ts_x4(tmem + C::S_COL + KT * sb, tmem + C::Q_COL + 32 * sl, 8,
                                k_lo + ((buf * C::TILE + sl * C::SLAB) >> 4), d_hi, idesc_qk, sl > 0 ? 1u : 0u);
+          if constexpr (SPLIT && !STACK) {
+#pragma unroll 1
+            for (int sl = 0; sl < D / 64; ++sl)
+              ptx::mma_f16_ts_x4(tmem + C::S_COL + KT * sb, tmem + C::QL_COL + 32 * sl, 8,
+                                 k_lo + ((buf * C::TILE + sl * C::SLAB) >> 4), d_hi, idesc_qk, 1u);
+          }
           ptx::mma_commit(&b_qk[sb]);
           ptx::mma_commit(&b_kfree[buf]);
         } else {
@@ -336,7 +350,9 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
   } else {
     // ============================================================ softmax
     const int q = warp;
-    const int r = 32 * q + lane;  // query row = TMEM lane
+    // query row = TMEM lane (STACK: lanes 64..127 hold the second parts of rows 0..63)
+    const int r = STACK ? (32 * q + lane) & 63 : 32 * q + lane;
+    const bool second = STACK && q >= 2;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16);
     const int G = a.group, T = a.q_tokens, Hq = a.num_q_heads, W = a.window, rows = a.rows;
     const float softcap = a.softcap;
@@ -344,7 +360,12 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     // (a masked call's last group of a chunk may hold fewer tokens: its rows
     // past them are set aside per piece)
     bool valid = r < rows;
-    const bool pad_warp = 32 * q >= rows;  // every row of this warp is padding
+    const bool pad_warp = 32 * (STACK ? q & 1 : q) >= rows;  // every row of this warp is padding
+    // S of the second parts, [2][64 rows][KT keys] f16, 16-byte chunks XOR (row & 7)
+    const uint32_t exch = ptx::smem_u32(base + lay.exch);
+    auto exch_at = [&](uint32_t buf, int chunk) -> uint32_t {
+      return exch + buf * (64 * KT * 2) + (uint32_t)r * (KT * 2) + (((uint32_t)chunk ^ ((uint32_t)r & 7u)) << 4);
+    };
     const int t_row = valid ? dev::div_small(r, __frcp_rn((float)G)) : 0;
     const bool in_rows = valid;
     dev::RowRule ru{};
@@ -353,7 +374,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     // to the workspace with the base-2 log-sum-exp.
     auto epilogue = [&](int u, uint32_t last, float mu, float l, int F, bool valid) {
       wait(&b_pv[last & 1], (last >> 1) & 1);
-      if (pad_warp) return;
+      if (pad_warp || second) return;
       ptx::tc_fence_after();
       float to_true = v_row ? dev::pow2i(F) : 1.0f;
       if constexpr (DT == KVQ_FP8_E4M3) to_true *= 256.0f;
@@ -478,6 +499,31 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
               }
             }
           }
+          if constexpr (SPLIT) {
+            uint32_t lo[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float qv[8];
+              unpack(raw[i], 4 * c32 + i, qv);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                if constexpr (DT == KVQ_INT4) {
+                  const float f = (m & 1) ? sq * dev::odd_channel_factor<DT>() : sq;
+                  lo[4 * i + m] = dev::rest_h2(qv[m] * f, qv[m + 4] * f, w[4 * i + m]);
+                } else {
+                  lo[4 * i + m] = dev::rest_h2(qv[2 * m] * sq, qv[2 * m + 1] * sq, w[4 * i + m]);
+                }
+              }
+            }
+            if constexpr (STACK) {
+              if (second) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = lo[i];
+              }
+            } else {
+              ptx::tmem_st16(t_lane + C::QL_COL + 16 * c32, lo);
+            }
+          }
           ptx::tmem_st16(t_lane + C::Q_COL + 16 * c32, w);
         }
         ptx::tmem_wait_st();
@@ -532,6 +578,44 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         ptx::tc_fence_after();
         float y[KT];
         dev::tmem_ld_cols<KT>(t_lane + C::S_COL + KT * sb, y);
+        if constexpr (STACK) {
+          // one barrier a tile between a row's two warps (q & 1 and 2 + (q & 1)):
+          // a buffer is written again two tiles on, after the other side has
+          // passed the barrier of the tile between
+          if (second) {
+#pragma unroll
+            for (int c8 = 0; c8 < KT / 8; ++c8) {
+              const uint32_t w0 = dev::pack_h2(y[8 * c8], y[8 * c8 + 1]), w1 = dev::pack_h2(y[8 * c8 + 2], y[8 * c8 + 3]);
+              const uint32_t w2 = dev::pack_h2(y[8 * c8 + 4], y[8 * c8 + 5]), w3 = dev::pack_h2(y[8 * c8 + 6], y[8 * c8 + 7]);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(exch_at(buf, c8)), "r"(w0), "r"(w1), "r"(w2),
+                           "r"(w3)
+                           : "memory");
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&b_sfree[sb]);
+            ptx::named_bar_sync(1 + (q & 1), 64);
+            if (it >= 2) wait(&b_pv[buf], ((it - 2) >> 1) & 1);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&b_pfull[buf]);
+            continue;
+          }
+          ptx::named_bar_sync(1 + (q & 1), 64);
+#pragma unroll
+          for (int c8 = 0; c8 < KT / 8; ++c8) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(exch_at(buf, c8))
+                         : "memory");
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+              y[8 * c8 + 2 * j] += f.x;
+              y[8 * c8 + 2 * j + 1] += f.y;
+            }
+          }
+        }
 
         // logits in log2 units: y = S * k_scale * alpha (softcapped), masked
         // keys -inf; the products two at a time (f32x2)
@@ -678,7 +762,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
 // Raises (never lowers) the kernel's dynamic shared-memory limit on the
 // current device, then launches one CTA per grid slot.
-template <int DT, int D, bool MASK>
+template <int DT, int D, int RULE>
 cudaError_t launch_decode_qt_d(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid,
                                size_t smem, cudaStream_t stream) {
   static int smem_set[64] = {};
@@ -687,18 +771,18 @@ cudaError_t launch_decode_qt_d(const CUtensorMap& tk, const CUtensorMap& tv, con
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(decode_qt_kernel<DT, D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(decode_qt_kernel<DT, D, RULE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     smem_set[dev] = (int)smem;
   }
-  return launch_pdl(decode_qt_kernel<DT, D, MASK>, grid, kQtWarps * 32, smem, stream, tk, tv, a);
+  return launch_pdl(decode_qt_kernel<DT, D, RULE>, grid, kQtWarps * 32, smem, stream, tk, tv, a);
 }
 
-template <int DT, bool MASK = false>
+template <int DT, int RULE = 0>
 cudaError_t dispatch_decode_qt(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                int grid, size_t smem, cudaStream_t stream) {
-  if (head_dim == 256) return launch_decode_qt_d<DT, 256, MASK>(tk, tv, a, grid, smem, stream);
-  if (head_dim == 128) return launch_decode_qt_d<DT, 128, MASK>(tk, tv, a, grid, smem, stream);
+  if (head_dim == 256) return launch_decode_qt_d<DT, 256, RULE>(tk, tv, a, grid, smem, stream);
+  if (head_dim == 128) return launch_decode_qt_d<DT, 128, RULE>(tk, tv, a, grid, smem, stream);
   return cudaErrorInvalidValue;
 }
 

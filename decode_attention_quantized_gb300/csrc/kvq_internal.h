@@ -180,21 +180,24 @@ constexpr int kQtWarps = 15;
 constexpr int kQtRows = 128;
 
 struct QtSmem {
-  int ring, kf, vf, sc, pre, bars, slot, total;
+  int ring, kf, vf, sc, exch, pre, bars, slot, total;
 };
 
+// exch (two-part Q at head_dim 256 only): two [64 rows][kTile keys] f16 blocks;
 // ring: stages x stage stride; kf, vf: two [D/64 slabs][kTile keys][128 B] f16
 // tiles each; sc: four [kTile] K scales and four V-normaliser exponents (the
 // per-row scales a tile's softmax needs, copied out of the stage so that the
 // stage is released early); pre: split plan; bars: mbarriers; slot: TMEM
 // address + abort flag.
-__host__ __device__ constexpr QtSmem qt_smem_layout(int head_dim, int stages, int batch, int stage_stride) {
+__host__ __device__ constexpr QtSmem qt_smem_layout(int head_dim, int stages, int batch, int stage_stride,
+                                                    bool exchange = false) {
   QtSmem s{};
   s.ring = 0;
   s.kf = stages * stage_stride;
   s.vf = s.kf + 2 * (head_dim / 64) * kTile * 128;
   s.sc = s.vf + 2 * (head_dim / 64) * kTile * 128;
-  s.pre = s.sc + 4 * kTile * 4 + 4 * 4;
+  s.exch = s.sc + 4 * kTile * 4 + 4 * 4;
+  s.pre = s.exch + (exchange ? 2 * 64 * kTile * 2 : 0);
   s.bars = (s.pre + (batch + 5) * 4 + 7) / 8 * 8;
   s.slot = s.bars + (2 * stages + 16) * 8;
   s.total = s.slot + 16;
@@ -343,21 +346,22 @@ cudaError_t launch_decode_qt_fp8(int head_dim, const CUtensorMap& tk, const CUte
 cudaError_t launch_decode_qt_int4(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                   int grid, size_t smem, cudaStream_t stream);
 
-// The same kernels with the score rule of a masked call (kvq_score_mask).
-cudaError_t launch_decode_mask_int8(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+// The same kernels with the score rule of a masked call (kvq_score_mask);
+// split: the Q operand in two parts.
+cudaError_t launch_decode_mask_int8(int head_dim, int nt, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream);
-cudaError_t launch_decode_mask_fp8(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_decode_mask_fp8(int head_dim, int nt, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream);
-cudaError_t launch_decode_mask_int4(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_decode_mask_int4(int head_dim, int nt, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const DecodeArgs& a, int grid, int threads, size_t smem, cudaStream_t stream);
-cudaError_t occupancy_decode_mask_int8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
-cudaError_t occupancy_decode_mask_fp8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
-cudaError_t occupancy_decode_mask_int4(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
-cudaError_t launch_qt_mask_int8(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
+cudaError_t occupancy_decode_mask_int8(int head_dim, int nt, bool split, int threads, size_t smem, int* blocks_per_sm);
+cudaError_t occupancy_decode_mask_fp8(int head_dim, int nt, bool split, int threads, size_t smem, int* blocks_per_sm);
+cudaError_t occupancy_decode_mask_int4(int head_dim, int nt, bool split, int threads, size_t smem, int* blocks_per_sm);
+cudaError_t launch_qt_mask_int8(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                 int grid, size_t smem, cudaStream_t stream);
-cudaError_t launch_qt_mask_fp8(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
+cudaError_t launch_qt_mask_fp8(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                int grid, size_t smem, cudaStream_t stream);
-cudaError_t launch_qt_mask_int4(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
+cudaError_t launch_qt_mask_int4(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                 int grid, size_t smem, cudaStream_t stream);
 
 cudaError_t occupancy_decode_int8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);

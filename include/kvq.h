@@ -374,7 +374,10 @@ typedef struct {
  * KVQ_DECODE_NO_TCGEN05 unset and groups of at least 64 query rows per kv
  * head, the groups are tiles of up to 128 rows on tcgen05 MMAs; otherwise of
  * up to 8 tokens on the mma.sync kernel.  KVQ_DECODE_EARLY_INPUTS and
- * KVQ_DECODE_EARLY_CACHE have no effect here.  batch <= 1024;
+ * KVQ_DECODE_EARLY_CACHE have no effect here.  lse_out is fp32-accurate: with
+ * a per-channel K scale the query operand is then carried in two f16 parts,
+ * which costs time (a prompt's tiles about half as much again at head_dim 128
+ * and twice at 256); lse_out NULL leaves that out.  batch <= 1024;
  * batch * C < 2^31.  workspace: at least
  * kvq_attend_masked_workspace_size bytes, 256-byte aligned; it belongs to
  * this call until the call's kernels have run. */
