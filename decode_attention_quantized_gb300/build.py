@@ -29,7 +29,7 @@ SOURCES = ["api.cu", "append.cu", "combine.cu", "decode_int8.cu", "decode_fp8.cu
            "decode_tc_grp_fp8.cu", "decode_tc_grp_int4.cu", "decode_qt_int8.cu", "decode_qt_fp8.cu",
            "decode_qt_int4.cu", "noalloc.cu", "masked.cu", "decode_mask_int8.cu", "decode_mask_fp8.cu",
            "decode_mask_int4.cu", "decode_split_int8.cu", "decode_split_fp8.cu", "decode_split_int4.cu", "qt_mask_int8.cu", "qt_mask_fp8.cu", "qt_mask_int4.cu", "key_mass_int8.cu",
-           "key_mass_fp8.cu", "key_mass_int4.cu", "evict.cu"]
+           "key_mass_fp8.cu", "key_mass_int4.cu", "key_mass_tc_int8.cu", "key_mass_tc_fp8.cu", "key_mass_tc_int4.cu", "evict.cu"]
 
 
 def _nvcc() -> str:
@@ -40,7 +40,7 @@ def _nvcc() -> str:
 
 
 HEADERS = ["kvq_internal.h", "ptx.cuh", "pipeline.cuh", "decode.cuh", "decode_tc.cuh", "decode_qt.cuh",
-           "score_rule.cuh", "key_mass.cuh"]
+           "score_rule.cuh", "key_mass.cuh", "key_mass_tc.cuh"]
 
 
 def _stamp() -> str:

@@ -275,6 +275,42 @@ kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const De
   return KVQ_OK;
 }
 
+// The tensor-memory key-mass kernel: more query rows than the mma.sync kernel
+// keeps memory-bound, at head_dim 128 or 256; not for per-group K scales,
+// whose f16 products with the codes would be rounded, nor with
+// KVQ_DECODE_NO_TCGEN05.
+bool mass_tc_ok(const kvq_cache* c, const kvq_decode_params* p, int rows) {
+  return rows > 16 && (c->head_dim == 128 || c->head_dim == 256) && c->k_mode != KVQ_SCALE_PER_GROUP &&
+         !(p->flags & KVQ_DECODE_NO_TCGEN05);
+}
+
+kvq_status make_plan_mass_tc(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, Plan* out) {
+  Plan P{};
+  P.rows = p->num_q_heads / c->num_kv_heads * p->q_tokens;
+  if (P.rows > kMassTcRows) return KVQ_ERR_UNSUPPORTED;
+  P.tc_nr = (P.rows + 31) / 32 * 32;
+  P.threads = kMassTcWarps * 32;
+  const int B = p->batch > 0 ? p->batch : 1;
+  const bool split = c->k_mode == KVQ_SCALE_PER_CHANNEL;
+  P.stride = ((size_t)kTcKeys * (row_bytes(c) + 4 * scales_per_row(c, c->k_mode)) + 1023) / 1024 * 1024;
+  constexpr size_t kMaxSmem = 227 * 1024;  // per CTA
+  for (int s = kMaxStages; s >= 2 && P.stages == 0; --s) {
+    P.smem = (size_t)mass_tc_layout(c->head_dim, P.tc_nr, split, s, B, (int)P.stride).total + 1024;
+    if (P.smem <= kMaxSmem) P.stages = s;
+  }
+  if (P.stages == 0) return KVQ_ERR_UNSUPPORTED;
+  const long long cap = (long long)p->max_blocks_per_seq * c->block_size;
+  const long long maxlen = (p->max_seq_len > 0 && p->max_seq_len < cap) ? p->max_seq_len : cap;
+  long long grid = dev.sms;  // one CTA per SM: it holds all of the SM's tensor memory
+  const long long useful = (long long)B * c->num_kv_heads * ((maxlen + kTcKeys - 1) / kTcKeys + 1);
+  if (grid > useful) grid = useful;
+  P.grid = (int)(grid < 1 ? 1 : grid);
+  P.ws_plan = align256((size_t)(4 + B + 1) * 4);
+  P.ws_total = P.ws_plan;
+  *out = P;
+  return KVQ_OK;
+}
+
 // The key-mass kernel: K-side stages for its four 16-key warps, the query rows
 // in tiles of 8 (1, 2, 4 or 8 of them), as many CTAs per SM as leave each at
 // least three stages.
@@ -282,6 +318,7 @@ kvq_status make_plan_mass(const kvq_cache* c, const kvq_decode_params* p, const 
   Plan P{};
   P.rows = p->num_q_heads / c->num_kv_heads * p->q_tokens;
   P.nt = P.rows <= 8 ? 1 : (P.rows <= 16 ? 2 : (P.rows <= 32 ? 4 : 8));
+  if (mass_tc_ok(c, p, P.rows)) return make_plan_mass_tc(c, p, dev, out);
   if (P.rows > 64 || (c->head_dim == 576 && P.nt > 4)) return KVQ_ERR_UNSUPPORTED;
   P.threads = kMassThreads;
   P.stride = stage_stride(c, true);
@@ -892,8 +929,8 @@ kvq_status prepare_groups(const kvq_cache* c, const kvq_decode_params* p, const 
   return from_cuda(launch_vseq(a, st));
 }
 
-// The key-mass kernel's groups: T tokens (at most 64 query rows) of every
-// sequence at a time, n launches of B groups each.
+// The key-mass kernels' groups: T tokens (at most 64 query rows, 128 on tensor
+// memory) of every sequence at a time, n launches of B groups each.
 struct MassShape {
   int T, n;
   kvq_decode_params v;  // one launch
@@ -906,7 +943,8 @@ kvq_status mass_shape(const kvq_cache* c, const kvq_decode_params* p, MassShape*
   if (G > 8 || p->batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
   if ((long long)p->batch * C > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
   MassShape s{};
-  const int most = (c->head_dim == 576 ? 32 : 64) / G;
+  const bool tc = mass_tc_ok(c, p, C < kMassTcRows ? C * G : kMassTcRows);
+  const int most = (c->head_dim == 576 ? 32 : (tc ? kMassTcRows : 64)) / G;
   s.n = (C + most - 1) / most;
   if ((long long)p->batch * s.n > (1LL << 26)) return KVQ_ERR_UNSUPPORTED;
   s.T = (C + s.n - 1) / s.n;
@@ -1233,7 +1271,7 @@ KVQ_API kvq_status kvq_key_mass(const kvq_cache* cache, const kvq_decode_params*
   a.window = params->window;
   a.stages = P.stages;
   a.stage_stride = (int)P.stride;
-  a.piece_cost = kPieceCost;
+  a.piece_cost = P.tc_nr ? kTcPieceCost : kPieceCost;
   a.bt_div = 1;
   a.v_alias = 1;  // a stage holds the K side only
   a.plan = reinterpret_cast<int*>(static_cast<char*>(workspace) +
@@ -1242,7 +1280,7 @@ KVQ_API kvq_status kvq_key_mass(const kvq_cache* cache, const kvq_decode_params*
   a.slopes = mask ? mask->slopes : nullptr;
   a.key_begin = mask ? mask->key_begin : nullptr;
   a.key_end = mask ? mask->key_end : nullptr;
-  MassArgs m{lse, mass, decay, fresh};
+  MassArgs m{lse, mass, decay, fresh, P.tc_nr ? kTcKeys : kTile};
 
   // keys that the launches below do not hold, or (several launches, each
   // adding to the last) all of them, take their decay first
@@ -1260,6 +1298,15 @@ KVQ_API kvq_status kvq_key_mass(const kvq_cache* cache, const kvq_decode_params*
   for (int j = 0; j < shape.n; ++j) {
     a.vseq = table + (size_t)j * params->batch;
     cudaError_t e;
+    if (P.tc_nr) {
+      switch (cache->dtype) {
+        case KVQ_INT8: e = launch_key_mass_tc_int8(cache->head_dim, tk, a, m, P.tc_nr, P.grid, P.smem, st); break;
+        case KVQ_FP8_E4M3: e = launch_key_mass_tc_fp8(cache->head_dim, tk, a, m, P.tc_nr, P.grid, P.smem, st); break;
+        default: e = launch_key_mass_tc_int4(cache->head_dim, tk, a, m, P.tc_nr, P.grid, P.smem, st); break;
+      }
+      if (e != cudaSuccess) return from_cuda(e);
+      continue;
+    }
     switch (cache->dtype) {
       case KVQ_INT8: e = launch_key_mass_int8(cache->head_dim, P.nt, tk, a, m, P.grid, P.smem, st); break;
       case KVQ_FP8_E4M3: e = launch_key_mass_fp8(cache->head_dim, P.nt, tk, a, m, P.grid, P.smem, st); break;
@@ -1299,19 +1346,16 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
   a.sinks = params->sinks;
   a.recent = params->recent;
   a.err = dev->err;
-  // parts of at least 2048 rows, up to 16 of them, as long as more of them
-  // find free SMs; more parts when a part would not fit in shared memory
-  constexpr int kMostResident = 48 * 1024;
+  // a CTA keeps 16,384 rows in registers: as many CTAs (up to 16) as hold the
+  // longest head, more while SMs are free and each still has 2048 rows
   const long long segs = (long long)params->batch * params->num_kv_heads;
   const long long rows = a.lim;
+  constexpr long long kHeld = (long long)kSelThreads * kSelKeys;
   int cluster = 1;
-  while (cluster < 16 && rows / (2 * cluster) >= 2048 && (segs * cluster < dev->sms || rows / cluster > 16384))
+  while (cluster < 16 && (rows > kHeld * cluster || (segs * cluster < dev->sms && rows / (2 * cluster) >= 2048)))
     cluster *= 2;
-  const long long part = (rows + cluster - 1) / cluster;
-  a.resident = (int)(part < kMostResident ? part : kMostResident);
-  a.resident = (a.resident + 3) & ~3;
   if (segs * cluster > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
-  return from_cuda(launch_evict_select(a, cluster, select_smem(a.resident), reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_evict_select(a, cluster, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 KVQ_API kvq_status kvq_evict_compact_workspace_size(const kvq_cache* cache, const kvq_evict_params* params,

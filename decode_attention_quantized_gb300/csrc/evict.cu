@@ -11,16 +11,22 @@ namespace {
 //
 // The `need` largest of M weights with ties to the lower index, in ascending
 // index order: a radix select of the threshold (the weight as an ordered
-// 32-bit key; digits of 11, 11 and 10 bits from the top, a 2048-bin histogram
-// of the keys that still match), then one ordered pass that writes every row
-// above the threshold and the first rows equal to it.
+// 32-bit key, four digits of 8 bits from the top, a histogram of the keys that
+// still match), then one ordered pass that writes every row above the
+// threshold and the first rows equal to it.
 //
-// A cluster of CTAs holds one (sequence, kv head): each CTA reads a contiguous
-// part of the weights from global memory once and keeps their keys in shared
-// memory, so the later passes run on chip; the histograms and the counts of
-// the parts meet through the cluster's shared memory, where every CTA sums
-// them for itself (one cluster barrier a digit, no second exchange).  The
-// histogram's atomics are integer adds: their order cannot show.
+// A cluster of CTAs holds one (sequence, kv head): each warp reads a
+// contiguous stretch of the weights from global memory once and keeps it in
+// registers, so the passes touch no memory but the histogram.  Weights of one
+// head share a few exponents and may all be equal, so a histogram has a column
+// per lane (bank = lane): no two lanes of a warp ever meet, whatever the
+// values (with one 2048-bin histogram a CTA and its collisions the select of
+// 4 x 262,144 rows took 118 us, that of 512 heads of up to 131,072 rows
+// 1356 us).  The columns' sums meet through the cluster's shared memory, where
+// every CTA adds them up for itself: one cluster barrier a digit.  Integer
+// adds: their order cannot show.
+
+constexpr int kSelWarps = kSelThreads / 32;
 
 // Ascending keys of ascending weights: -0 as +0, NaN below everything.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -29,14 +35,10 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
-  extern __shared__ __align__(16) uint32_t sel_smem[];
-  uint32_t* keys = sel_smem;
-  uint32_t* hist = keys + a.resident;        // [2][kSelBins]
-  uint32_t* wsum = hist + 2 * kSelBins;      // [2][warps]
-  uint32_t* misc = wsum + 2 * (kSelThreads / 32);  // digit, count above it, this CTA's totals
-  constexpr int kWarps = kSelThreads / 32;
-  constexpr int kBinsPer = kSelBins / kSelThreads;
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectArgs a) {
+  __shared__ uint32_t hist[256 * 32];     // [bin][lane]
+  __shared__ uint32_t total[2][256];      // this CTA's counts of a digit (two passes' worth)
+  __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps], s_scan[8], s_digit[2], s_cta[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t cs = ptx::cluster_size(), rank = ptx::cluster_rank();
   const int seg = (int)(blockIdx.x / cs);
@@ -63,126 +65,143 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
     else keep[need_all + i] = L - a.recent + (i - a.sinks);
   }
 
-  // this CTA's part of the M rows between the ends: [p0, p0 + m)
+  // this warp's stretch of the M rows between the ends: [w0, w0 + m), the
+  // stretches in (CTA, warp) order
   const int M = L - a.sinks - a.recent;
-  const int part = (M + (int)cs - 1) / (int)cs;
-  const int p0 = min(M, (int)rank * part);
-  const int m = min(M, p0 + part) - p0;
+  const int warps = (int)cs * kSelWarps;
+  const int stretch = ((M + warps - 1) / warps + 31) & ~31;
+  const long long w0l = (long long)((int)rank * kSelWarps + warp) * stretch;
+  const int w0 = (int)(w0l < M ? w0l : M);
+  const int m = min(M, w0 + stretch) - w0;
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks_per_seq;
-  auto load = [&](int i) -> uint32_t {
-    const int pos = a.sinks + p0 + i;
+  bool bad = false;
+  auto load = [&](int i) -> uint32_t {  // row w0 + i; branch-free, so that loads run ahead
+    const int pos = a.sinks + w0 + i;
     const int id = bt[pos >> a.log2_bs];
-    if (id < 0 || id >= a.num_blocks) {
-      atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
-      return 0u;
-    }
-    return order_key(a.mass[((size_t)id * a.num_kv_heads + h) * a.block_size + (pos & (a.block_size - 1))]);
+    const bool fine = (unsigned)id < (unsigned)a.num_blocks;
+    bad = bad || !fine;
+    const float* p = a.mass + (fine ? ((size_t)id * a.num_kv_heads + h) * a.block_size + (pos & (a.block_size - 1)) : 0);
+    const uint32_t k = order_key(*p);
+    return fine ? k : 0u;
   };
-  auto key_at = [&](int i) -> uint32_t { return i < a.resident ? keys[i] : load(i); };
-
-  for (int i = tid; i < 2 * kSelBins; i += kSelThreads) hist[i] = 0;
-  __syncthreads();
-  // first digit's histogram while the keys come in
-#pragma unroll 8
-  for (int i = tid; i < m; i += kSelThreads) {
-    const uint32_t k = load(i);
-    if (i < a.resident) keys[i] = k;
-    atomicAdd(&hist[k >> 21], 1u);
+  // the first kSelKeys x 32 rows of the stretch in registers, a longer
+  // stretch's rest read again in each pass
+  uint32_t key[kSelKeys];
+#pragma unroll
+  for (int j = 0; j < kSelKeys; ++j) key[j] = 0u;
+#pragma unroll
+  for (int j0 = 0; j0 < kSelKeys; j0 += 8) {
+    if (j0 * 32 < m) {
+#pragma unroll
+      for (int j = j0; j < j0 + 8; ++j) {
+        const int i = min(j * 32 + lane, m - 1);
+        key[j] = load(i);
+      }
+    }
   }
+  // f(index in the stretch, key) for each of this lane's rows
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < kSelKeys; ++j) {
+      if (j * 32 < m) {
+        if (j * 32 + lane < m) f(key[j]);
+      }
+    }
+    for (int i = kSelKeys * 32 + lane; i < m; i += 32) f(load(i));
+  };
 
   uint32_t prefix = 0;
   int need = need_all;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const int bits = pass == 2 ? 10 : 11;
-    uint32_t* hp = hist + (pass & 1) * kSelBins;
-    if (pass > 0) {
-      if (pass == 2) {
-        // (its first use was read by everyone before the last barrier)
-        for (int i = tid; i < kSelBins; i += kSelThreads) hp[i] = 0;
-        __syncthreads();
-      }
-#pragma unroll 4
-      for (int i = tid; i < m; i += kSelThreads) {
-        const uint32_t k = key_at(i);
-        if ((k >> (shift + bits)) == prefix) atomicAdd(&hp[(k >> shift) & ((1u << bits) - 1u)], 1u);
-      }
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = tid; i < 256 * 32 / 4; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (pass == 0)
+      each([&](uint32_t k) { atomicAdd(&hist[(k >> 24) * 32 + lane], 1u); });
+    else
+      each([&](uint32_t k) {
+        if ((k >> shift) >> 8 == prefix) atomicAdd(&hist[((k >> shift) & 255u) * 32 + lane], 1u);
+      });
+    __syncthreads();
+    {
+      // two threads a bin, sixteen columns each, starting apart by bin so that
+      // a warp's lanes read different banks
+      const int bin = tid >> 1, c0 = (tid & 1) * 16;
+      uint32_t s = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s += hist[bin * 32 + c0 + ((j + bin) & 15)];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      if ((tid & 1) == 0) total[pass & 1][bin] = s;
     }
     ptx::cluster_sync();
-    // the cluster's counts of this thread's bins (thread 0 has the highest),
-    // then the scan from the top that finds the digit
-    uint32_t cnt[kBinsPer], mine = 0;
-    const int bin0 = kSelBins - kBinsPer * (tid + 1);
+    // the cluster's counts, highest bin first, and the scan that finds the digit
+    if (tid < 256) {
+      const int bin = 255 - tid;
+      const uint32_t at = ptx::smem_u32(&total[pass & 1][bin]);
+      uint32_t cnt = 0;
+      for (uint32_t r = 0; r < cs; r += 4) {
+        uint32_t v[4];
 #pragma unroll
-    for (int j = 0; j < kBinsPer; ++j) cnt[j] = 0;
-    for (uint32_t r = 0; r < cs; ++r) {
+        for (int j = 0; j < 4; ++j) v[j] = r + j < cs ? ptx::ld_cluster_u32(at, r + j) : 0u;
+        cnt += (v[0] + v[1]) + (v[2] + v[3]);
+      }
+      uint32_t incl = cnt;
 #pragma unroll
-      for (int j = 0; j < kBinsPer; ++j) cnt[j] += ptx::ld_cluster_u32(ptx::smem_u32(hp + bin0 + j), r);
-    }
-#pragma unroll
-    for (int j = 0; j < kBinsPer; ++j) mine += cnt[j];
-    uint32_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - mine;  // keys in higher bins than this thread's
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (before < (uint32_t)need && before + mine >= (uint32_t)need) {
-      uint32_t above = before;
-      int j = kBinsPer - 1;
-      while (above + cnt[j] < (uint32_t)need) above += cnt[j--];
-      misc[0] = (uint32_t)(bin0 + j);
-      misc[1] = above;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_scan[warp] = incl;
+      ptx::named_bar_sync(1, 256);
+      uint32_t before = incl - cnt;  // keys in higher bins
+      for (int w = 0; w < warp; ++w) before += s_scan[w];
+      if (before < (uint32_t)need && before + cnt >= (uint32_t)need) {
+        s_digit[0] = (uint32_t)bin;
+        s_digit[1] = before;
+      }
     }
     __syncthreads();
-    prefix = (prefix << bits) | misc[0];
-    need -= (int)misc[1];
-    __syncthreads();
+    prefix = (prefix << 8) | s_digit[0];
+    need -= (int)s_digit[1];
   }
+  if (bad) atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
 
-  // ---- ordered output: warps own contiguous stretches of the part
+  // ---- ordered output
   const uint32_t T = prefix;  // `need` rows equal to it stay, the lowest
-  const int stretch = ((m + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(m, warp * stretch), w1 = min(m, w0 + stretch);
   uint32_t gt = 0, eq = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = key_at(i);
+  each([&](uint32_t k) {
     gt += k > T;
     eq += k == T;
-  }
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     gt += __shfl_xor_sync(0xffffffffu, gt, o);
     eq += __shfl_xor_sync(0xffffffffu, eq, o);
   }
   if (lane == 0) {
-    wsum[warp] = gt;
-    wsum[kWarps + warp] = eq;
+    s_gt[warp] = gt;
+    s_eq[warp] = eq;
   }
   __syncthreads();
   if (tid == 0) {
     uint32_t g = 0, e = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      g += wsum[w];
-      e += wsum[kWarps + w];
+    for (int w = 0; w < kSelWarps; ++w) {
+      g += s_gt[w];
+      e += s_eq[w];
     }
-    misc[2] = g;
-    misc[3] = e;
+    s_cta[0] = g;
+    s_cta[1] = e;
   }
   ptx::cluster_sync();
   uint32_t bg = 0, be = 0;  // rows above / equal before this warp's stretch
   if (lane < (int)rank) {
-    bg = ptx::ld_cluster_u32(ptx::smem_u32(misc + 2), (uint32_t)lane);
-    be = ptx::ld_cluster_u32(ptx::smem_u32(misc + 3), (uint32_t)lane);
+    bg = ptx::ld_cluster_u32(ptx::smem_u32(&s_cta[0]), (uint32_t)lane);
+    be = ptx::ld_cluster_u32(ptx::smem_u32(&s_cta[1]), (uint32_t)lane);
   }
   if (lane < warp) {
-    bg += wsum[lane];
-    be += wsum[kWarps + lane];
+    bg += s_gt[lane];
+    be += s_eq[lane];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -190,17 +209,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
     be += __shfl_xor_sync(0xffffffffu, be, o);
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < w1 ? key_at(i) : 0u;
-    const bool is_gt = i < w1 && k > T, is_eq = i < w1 && k == T;
+  auto put = [&](int i0, uint32_t k) {  // rows i0 + lane of the stretch, whole warp
+    const bool in = i0 + lane < m;
+    const bool is_gt = in && k > T, is_eq = in && k == T;
     const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
     const uint32_t g = bg + __popc(mg & below), e = be + __popc(me & below);
-    if (is_gt || (is_eq && e < (uint32_t)need))
-      keep[a.sinks + g + min(e, (uint32_t)need)] = a.sinks + p0 + i;
+    if (is_gt || (is_eq && e < (uint32_t)need)) keep[a.sinks + g + min(e, (uint32_t)need)] = a.sinks + w0 + i0 + lane;
     bg += __popc(mg);
     be += __popc(me);
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kSelKeys; ++j)
+    if (j * 32 < m) put(j * 32, key[j]);
+  for (int i0 = kSelKeys * 32; i0 < m; i0 += 32) put(i0, load(min(i0 + lane, m - 1)));
   ptx::cluster_sync();  // no CTA leaves while another reads its counts
 }
 
@@ -376,23 +397,20 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Co
 
 }  // namespace
 
-cudaError_t launch_evict_select(const SelectArgs& a, int cluster, size_t smem, cudaStream_t stream) {
-  static int smem_set[64] = {};
+cudaError_t launch_evict_select(const SelectArgs& a, int cluster, cudaStream_t stream) {
+  static bool wide[64] = {};  // clusters of 16 allowed on the device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem_set[dev] < (int)smem) {
+  if (!wide[dev]) {
     e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    smem_set[dev] = (int)smem;
+    wide[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = (unsigned)((long long)a.batch * a.num_kv_heads * cluster);
   cfg.blockDim = kSelThreads;
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,0 +1,411 @@
+// key_mass_tc.cuh -- kvq_key_mass for many query rows per kv head (17..128 a
+// launch: drafts x GQA group, or the last tokens of a prompt) on the tcgen05
+// tensor cores.
+//
+// What key_mass.cuh computes, with 128 keys as the MMA's M dimension and the
+// rows (padded to NR, a multiple of 32) as N:
+//
+//   S [128 keys x NR] = K [128 keys x D] . Q [NR x D]^T      A = K in TMEM, B = Q (f16, shared)
+//   weight of a key   = sum over its row of S of exp2(S alpha_r - c_r)
+//
+// so a key's weight is a sum along one thread's TMEM columns: no exchange
+// between lanes.  K and S are double-buffered in TMEM (2 x D/2 and 2 x 128
+// columns: all of it at head_dim 256), Q stays in shared memory for the whole
+// piece, and a K tile's codes never leave shared memory but into TMEM.  A
+// per-channel K scale's second Q part (SPLIT, see key_mass.cuh) is a second
+// pass of the MMAs into the same S.
+//
+// Warp roles (14 warps):
+//   0-7   weights: warp w takes lane quarter w & 3 (32 keys, one a thread) and
+//         half w >> 2 of the rows; also the Q prologue of each piece.  The two
+//         halves of a key meet in shared memory, in a fixed order.
+//   8-11  K dequant: one key row per thread -> f16 K columns in TMEM
+//   12    TMA producer of the code stages (shared with decode.cuh)
+//   13    TMEM allocation; issues the MMAs
+#pragma once
+
+#include "decode_tc.cuh"
+
+namespace kvq {
+
+// A query row's rule in shared memory, for tiles that some row does not see
+// whole or that reach past some row's position.
+struct __align__(16) MassTcRule {
+  int begin, end, pos, d0;
+};
+
+template <int DT, int D, bool SPLIT>
+__global__ void __launch_bounds__(kMassTcWarps * 32, 1)
+    key_mass_tc_kernel(const __grid_constant__ CUtensorMap tmk, const DecodeArgs a, const MassArgs ms, const int NR) {
+  using Gm = Geo<DT, D, kTcKeys>;
+  constexpr int KT = kTcKeys;
+  constexpr int kDqK = 8, kProducer = 12, kMma = 13;
+  constexpr int K_COL = 0, S_COL = D;  // K: 2 x D/2 columns, S: 2 x 128
+  constexpr float kLog2e = 1.4426950408889634f;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* base = smem_raw + pad;
+  const MassTcSmem lay = mass_tc_layout(D, NR, SPLIT, a.stages, a.batch, a.stage_stride);
+  uint8_t* ring = base + lay.ring;
+  uint8_t* q_s = base + lay.q;                                       // [parts][D/64 slabs][NR rows][128 B]
+  const uint32_t q_part = (uint32_t)NR * D * 2;
+  float2* r_ac = reinterpret_cast<float2*>(base + lay.rows);         // [NR] logit factor, log-sum-exp
+  float2* r_ne = r_ac + NR;                                          // [NR] bias per key, pos - d0 - k0
+  MassTcRule* r_rule = reinterpret_cast<MassTcRule*>(r_ne + NR);     // [NR]
+  float* half_sum = reinterpret_cast<float*>(r_rule + NR);           // [2][KT] the second half's sums
+  int* pl_pre = reinterpret_cast<int*>(base + lay.pre);
+  int* pl_misc = pl_pre + a.batch + 1;
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(base + lay.bars);
+  uint64_t* bar_empty = bar_full + a.stages;
+  uint64_t* b_s = bar_empty + a.stages;  // [2] MMAs of tile it complete: S written, K columns it & 1 free
+  uint64_t* b_sfree = b_s + 2;           // [2] S buffer read
+  uint64_t* b_kfull = b_s + 4;           // [2] K tile in TMEM
+  uint64_t* b_qfull = b_s + 6;           // Q of a piece written
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_s + 7);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      ptx::mbar_init(&bar_full[s], 1);
+      ptx::mbar_init(&bar_empty[s], 12);  // K dequant and weight warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&b_s[i], 1);
+      ptx::mbar_init(&b_sfree[i], 8);
+      ptx::mbar_init(&b_kfull[i], 4);
+    }
+    ptx::mbar_init(b_qfull, 8);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMma) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tc_fence_before();
+  }
+  const Slice<KT, true> sp = build_slice<KT, true>(a, pl_pre, pl_misc);
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!ptx::mbar_try_wait(bar, parity)) dev::wait_or_abort(bar, parity, abort_flag, a.err);
+  };
+  const bool k_row = a.k_mode == KVQ_SCALE_PER_ROW;
+
+  if (warp == kProducer) {
+    // ============================================================ producer
+    produce<Gm, false, true>(a, sp, &tmk, &tmk, ring, bar_full, bar_empty, pl_pre, pl_misc);
+  } else if (warp >= kDqK && warp < kDqK + 4) {
+    // ========================================================== K dequant
+    const int q = warp - kDqK, kk = 32 * q + lane;
+    const uint32_t t_k = tmem + ((uint32_t)(32 * q) << 16) + K_COL;
+    constexpr int HCH = Gm::NCH / 2;             // 16-byte chunks of a channel half
+    constexpr int CW = DT == KVQ_INT4 ? 16 : 8;  // K columns per chunk
+    uint32_t it = 0;
+    RingPos rp;
+    for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
+      int b, h, k0, k1, L, u;
+      sp.piece(a, gt, b, h, k0, k1, L, u, next);
+      for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(a.stages)) {
+        wait(&bar_full[rp.stage], rp.phase);
+        const uint8_t* st = ring + (size_t)rp.stage * a.stage_stride;
+        const uint32_t buf = it & 1;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[HCH * CW];
+#pragma unroll
+          for (int jj = 0; jj < HCH; ++jj) {
+            const uint32_t byte = (uint32_t)(half * HCH + jj) * 16;
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                st + (byte / Gm::SPAN) * (KT * Gm::SPAN) + dev::swz<Gm::SPAN>(kk * Gm::SPAN + byte % Gm::SPAN));
+            dev::k_cols<DT>(w, v + CW * jj);
+          }
+          if (half == 0 && it >= 2) wait(&b_s[buf], ((it - 2) >> 1) & 1);  // the MMAs two tiles back are done
+          ptx::tc_fence_after();
+          if constexpr (HCH * CW == 64)
+            ptx::tmem_st64(t_k + (D / 2) * buf + 64 * half, v);
+          else
+            ptx::tmem_st32(t_k + (D / 2) * buf + 32 * half, v);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&b_kfull[buf]);
+          ptx::mbar_arrive(&bar_empty[rp.stage]);
+        }
+      }
+    }
+  } else if (warp == kMma) {
+    // ================================================================ MMA
+    const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    const uint64_t q_desc = ptx::smem_desc_sw128(ptx::smem_u32(q_s));
+    const uint32_t q_lo = (uint32_t)q_desc, d_hi = (uint32_t)(q_desc >> 32);
+    const uint32_t slab = ((uint32_t)NR * 128) >> 4, part = q_part >> 4;
+    uint32_t it = 0;
+    int pc = 0;
+    for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next, ++pc) {
+      int b, h, k0, k1, L, u;
+      sp.piece(a, gt, b, h, k0, k1, L, u, next);
+      for (int key0 = k0; key0 < k1; key0 += KT, ++it) {
+        const uint32_t buf = it & 1;
+        if (key0 == k0) wait(b_qfull, pc & 1);
+        wait(&b_kfull[buf], (it >> 1) & 1);
+        if (it >= 2) wait(&b_sfree[buf], ((it - 2) >> 1) & 1);
+        __syncwarp();
+        ptx::tc_fence_after();
+        const uint32_t s_col = tmem + S_COL + 128 * buf, k_col = tmem + K_COL + (D / 2) * buf;
+#pragma unroll 1
+        for (int p = 0; p < (SPLIT ? 2 : 1); ++p) {
+#pragma unroll 1
+          for (int sl = 0; sl < D / 64; ++sl)
+            ptx::mma_f16_ts_x4(s_col, k_col + 32 * sl, 8, q_lo + p * part + sl * slab, d_hi, idesc,
+                               sl + p > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(&b_s[buf]);
+      }
+    }
+    if (it > 0) {
+      // every MMA has completed before TMEM can be released
+      const uint32_t last = it - 1;
+      if (!ptx::mbar_wait_bounded(&b_s[last & 1], (last >> 1) & 1) && lane == 0) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ weights
+    const int q = warp & 3, side = warp >> 2, kk = 32 * q + lane;
+    const uint32_t t_s = tmem + ((uint32_t)(32 * q) << 16) + S_COL;
+    const int G = a.group, Hq = a.num_q_heads;
+    const float inv_g = __frcp_rn((float)G);
+    const float softcap = a.softcap, inv_cap = softcap > 0.0f ? 1.0f / softcap : 1.0f;
+    const float cap_l2 = softcap * kLog2e;
+    constexpr int LPR = D / 8, RPP = 32 / LPR;  // lanes per row (8 channels each), rows per warp pass
+    const int rsub = lane / LPR, cl = lane % LPR;
+    uint32_t it = 0;
+    RingPos rp;
+    for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
+      int b, h, k0, k1, L, u;
+      sp.piece(a, gt, b, h, k0, k1, L, u, next);
+      const VSeq vs = a.vseq[b];
+      const int rows = vs.ntok * G;
+      // every warp has read the previous piece's rows (and waited for its last
+      // MMAs, so the Q operand is free)
+      ptx::named_bar_sync(5, 256);
+      // ---- the piece's Q operand and row rules
+      {
+        const bool kc = a.k_mode == KVQ_SCALE_PER_CHANNEL;
+        float ksv[8];
+        int ek = 0;
+        if (kc) {
+          const float4* ksp = reinterpret_cast<const float4*>(a.k_scale + (size_t)h * D + 8 * cl);
+          const float4 s0 = __ldg(ksp), s1 = __ldg(ksp + 1);
+          ksv[0] = s0.x; ksv[1] = s0.y; ksv[2] = s0.z; ksv[3] = s0.w;
+          ksv[4] = s1.x; ksv[5] = s1.y; ksv[6] = s1.z; ksv[7] = s1.w;
+          float km = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) km = fmaxf(km, fabsf(ksv[i]));
+          km = ptx::redux_max(km);
+          ek = km > 0.0f ? min(126, max(-126, dev::ceil_log2(km))) : 0;
+          const float sk = dev::pow2i(-ek);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ksv[i] *= sk;
+        }
+        float fac = a.sm_scale;
+        if (a.k_mode == KVQ_SCALE_PER_TENSOR) fac *= a.k_scale[0];
+        fac *= softcap > 0.0f ? inv_cap : kLog2e;
+#pragma unroll 2
+        for (int r = warp * RPP + rsub; r < NR; r += 8 * RPP) {
+          const int t = dev::div_small(r, inv_g), hq = h * G + r - t * G;
+          const bool valid = r < rows;
+          const uint4 raw = valid ? ptx::ldg_nc_v4(a.q + (((size_t)vs.tok0 + t) * Hq + hq) * D + 8 * cl)
+                                  : make_uint4(0, 0, 0, 0);
+          float qv[8];
+          const uint32_t ww[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            qv[2 * j] = __uint_as_float(ww[j] << 16);
+            qv[2 * j + 1] = __uint_as_float(ww[j] & 0xFFFF0000u);
+          }
+          if (kc) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) qv[j] *= ksv[j];
+          }
+          float qm = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) qm = fmaxf(qm, fabsf(qv[j]));
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, o));
+          const int eq = qm > 0.0f ? min(126, max(-126, dev::ceil_log2(qm))) : 0;
+          const float sq = dev::pow2i(-eq);
+          uint32_t w[4], lo[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            float x0, x1;
+            if constexpr (DT == KVQ_INT4) {
+              const float f = (m & 1) ? sq * dev::odd_channel_factor<DT>() : sq;  // channels m, m + 4
+              x0 = qv[m] * f;
+              x1 = qv[m + 4] * f;
+            } else {
+              x0 = qv[2 * m] * sq;
+              x1 = qv[2 * m + 1] * sq;
+            }
+            w[m] = dev::pack_h2(x0, x1);
+            lo[m] = dev::rest_h2(x0, x1, w[m]);
+          }
+          uint8_t* dst = q_s + (cl >> 3) * (NR * 128) + r * 128 + ((((uint32_t)cl & 7u) ^ ((uint32_t)r & 7u)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          if constexpr (SPLIT) *reinterpret_cast<uint4*>(dst + q_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (cl == 0) {
+            // a row that is padding, sees nothing or has no weight: factor 0
+            // and log-sum-exp +inf give it a weight of exactly 0 everywhere
+            float2 ac = make_float2(0.0f, INFINITY), ne = make_float2(0.0f, 0.0f);
+            MassTcRule ru{0, 0, 0, 0};
+            if (valid) {
+              const size_t tok = (size_t)vs.tok0 + t;
+              const dev::RowRule rr = dev::row_rule(a, tok, vs.pos0 + t, hq, L);
+              const float lse = ms.lse[tok * Hq + hq];
+              if (rr.begin < rr.end && lse != -INFINITY) {
+                const double s = a.slopes ? (double)a.slopes[hq] * (double)rr.d0 : 0.0;
+                const int e = ek + eq, e1 = e / 2;
+                ac.x = fminf(fac * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f);
+                ac.y = (float)(((double)lse + s) * 1.4426950408889634);
+                ne = make_float2(rr.ns, (float)(rr.pos - rr.d0 - k0));
+                ru = MassTcRule{rr.begin, rr.end, rr.pos, rr.d0};
+              }
+            }
+            r_ac[r] = ac;
+            r_ne[r] = ne;
+            r_rule[r] = ru;
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(b_qfull);
+      }
+      ptx::named_bar_sync(5, 256);  // the rows are visible
+      // tiles inside [bmax, emin) and, under a bias, at or below pmin need no
+      // mask and have linear distances for every row
+      int bmax = 0, emin = 0x7FFFFFFF, pmin = 0x7FFFFFFF;
+      for (int r = lane; r < rows; r += 32) {
+        const MassTcRule ru = r_rule[r];
+        if (ru.begin < ru.end) {
+          bmax = max(bmax, ru.begin);
+          emin = min(emin, ru.end);
+          pmin = min(pmin, ru.pos);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        bmax = max(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
+        emin = min(emin, __shfl_xor_sync(0xffffffffu, emin, o));
+        pmin = min(pmin, __shfl_xor_sync(0xffffffffu, pmin, o));
+      }
+      const bool bias = a.slopes != nullptr;
+      const int32_t* bt = a.block_table + (size_t)vs.brow * a.max_blocks_per_seq;
+      const int c_lo = side * (NR / 2), c_hi = c_lo + NR / 2;
+
+      for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(a.stages)) {
+        const uint32_t buf = it & 1;
+        const int key = key0 + kk;
+        float* out = nullptr;
+        float old = 0.0f;
+        if (side == 0 && key < k1) {
+          const int id = bt[key >> a.log2_bs];
+          if (id >= 0 && id < a.num_blocks) {
+            out = ms.mass + ((size_t)id * a.num_kv_heads + h) * a.block_size + (key & (a.block_size - 1));
+            if (ms.decay != 0.0f && key < vs.len - ms.fresh) old = ms.decay * *out;
+          }
+        }
+        float ks = 1.0f;
+        if (k_row) {
+          wait(&bar_full[rp.stage], rp.phase);
+          ks = reinterpret_cast<const float*>(ring + (size_t)rp.stage * a.stage_stride + Gm::CODE_BYTES)[kk];
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar_empty[rp.stage]);
+        wait(&b_s[buf], (it >> 1) & 1);
+        ptx::tc_fence_after();
+        const bool fast = key0 >= bmax && key0 + KT <= emin && (!bias || key0 + KT - 1 <= pmin);
+        const float kf = (float)(key - k0);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+        for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
+          float y[16];
+          dev::tmem_ld_cols<16>(t_s + 128 * buf + c0, y);
+          if (fast && softcap <= 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 ac = *reinterpret_cast<const float4*>(r_ac + c0 + i);
+              float x0 = fmaf(y[i] * ks, ac.x, -ac.y), x1 = fmaf(y[i + 1] * ks, ac.z, -ac.w);
+              if (bias) {
+                const float4 ne = *reinterpret_cast<const float4*>(r_ne + c0 + i);
+                x0 = fmaf(ne.x, ne.y - kf, x0);
+                x1 = fmaf(ne.z, ne.w - kf, x1);
+              }
+              s0 += ptx::fast_exp2(x0);
+              s1 += ptx::fast_exp2(x1);
+            }
+          } else {
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+              const float2 ac = r_ac[c0 + i], ne = r_ne[c0 + i];
+              const MassTcRule ru = r_rule[c0 + i];
+              float x = y[i] * ks * ac.x;
+              if (softcap > 0.0f) x = cap_l2 * tanhf(x);
+              if (bias) x = fmaf(ne.x, (float)(abs(ru.pos - key) - ru.d0), x);
+              s0 += key >= ru.begin && key < ru.end ? ptx::fast_exp2(x - ac.y) : 0.0f;
+            }
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&b_sfree[buf]);
+        // one barrier a tile between a key's two warps: the second half's sums
+        // are written again two tiles on, behind the next tile's barrier
+        s0 += s1;
+        if (side == 1) half_sum[buf * KT + kk] = s0;
+        ptx::named_bar_sync(1 + q, 64);
+        if (out) *out = old + (s0 + half_sum[buf * KT + kk]);
+      }
+    }
+  }
+
+  // every role ends here; TMEM is released once no warp can touch it
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DT, int D, bool SPLIT>
+cudaError_t launch_key_mass_tc_d(const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m, int nr, int grid,
+                                 size_t smem, cudaStream_t stream) {
+  static int smem_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (smem_set[dev] < (int)smem) {
+    e = cudaFuncSetAttribute(key_mass_tc_kernel<DT, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    smem_set[dev] = (int)smem;
+  }
+  return launch_pdl(key_mass_tc_kernel<DT, D, SPLIT>, grid, kMassTcWarps * 32, smem, stream, tk, a, m, nr);
+}
+
+// head_dim 128 or 256, any K scale mode but PER_GROUP.
+template <int DT>
+cudaError_t dispatch_key_mass_tc(int head_dim, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m, int nr,
+                                 int grid, size_t smem, cudaStream_t stream) {
+  const bool split = a.k_mode == KVQ_SCALE_PER_CHANNEL;
+  if (head_dim == 256)
+    return split ? launch_key_mass_tc_d<DT, 256, true>(tk, a, m, nr, grid, smem, stream)
+                 : launch_key_mass_tc_d<DT, 256, false>(tk, a, m, nr, grid, smem, stream);
+  if (head_dim == 128)
+    return split ? launch_key_mass_tc_d<DT, 128, true>(tk, a, m, nr, grid, smem, stream)
+                 : launch_key_mass_tc_d<DT, 128, false>(tk, a, m, nr, grid, smem, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvq

@@ -237,6 +237,7 @@ struct MassArgs {
   float* mass;       // [num_blocks, Hkv, block_size]
   float decay;       // factor of the weight held before (0: it is not read)
   int fresh;         // the last `fresh` rows of a sequence held none before
+  int tile;          // keys per tile of the kernel (64 or, on tensor memory, 128)
 };
 constexpr int kMassWarps = 4;  // consumer warps: one 16-key sub-tile of a stage each
 constexpr int kMassThreads = 32 * (kMassWarps + 1);
@@ -256,6 +257,35 @@ __host__ __device__ constexpr size_t mass_fixed_smem(int head_dim, int nt, bool 
   return 1024 + (qs ? (size_t)8 * nt * head_dim * 2 * (split ? 2 : 1) : 0) + (size_t)8 * nt * sizeof(MassRow) +
          ((size_t)batch + 5 + ((batch + 5) & 1)) * 4 + (size_t)stages * 2 * 8;
 }
+
+// The tensor-memory kernel: 14 warps, up to 128 query rows, its shared memory.
+constexpr int kMassTcWarps = 14;
+constexpr int kMassTcRows = 128;
+
+struct MassTcSmem {
+  int ring, q, rows, pre, bars, total;
+};
+
+// ring: stages x stage stride; q: one or two [D/64 slabs][nr rows][128 B] f16
+// operands; rows: 32 bytes a row and the two [128] half sums; pre: split plan;
+// bars: mbarriers, then TMEM address and abort flag.
+__host__ __device__ constexpr MassTcSmem mass_tc_layout(int head_dim, int nr, bool split, int stages, int batch,
+                                                        int stage_stride) {
+  MassTcSmem s{};
+  s.ring = 0;
+  s.q = stages * stage_stride;
+  s.rows = s.q + nr * head_dim * 2 * (split ? 2 : 1);
+  s.pre = s.rows + nr * 32 + 2 * kTcKeys * 4;
+  s.bars = (s.pre + (batch + 5) * 4 + 7) / 8 * 8;
+  s.total = s.bars + (2 * stages + 7) * 8 + 16;
+  return s;
+}
+cudaError_t launch_key_mass_tc_int8(int head_dim, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
+                                    int nr, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_key_mass_tc_fp8(int head_dim, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
+                                   int nr, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_key_mass_tc_int4(int head_dim, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
+                                    int nr, int grid, size_t smem, cudaStream_t stream);
 
 // Keys outside the group's [lo, hi) (all of them when `all`): decay only.
 cudaError_t launch_mass_rest(const DecodeArgs& a, const MassArgs& m, bool all, int max_keys, cudaStream_t stream);
@@ -278,16 +308,11 @@ struct SelectArgs {
   int32_t* kept_lens;          // [B]
   int batch, num_kv_heads, max_blocks_per_seq, num_blocks, block_size, log2_bs, lim;
   int budget, sinks, recent;
-  int resident;                // rows whose keys a CTA keeps in shared memory
   unsigned int* err;
 };
 constexpr int kSelThreads = 512;
-constexpr int kSelBins = 2048;
-// Shared bytes of a CTA that keeps `resident` keys: them, two histograms, scratch.
-__host__ __device__ constexpr size_t select_smem(int resident) {
-  return (size_t)resident * 4 + 2 * kSelBins * 4 + (2 * (kSelThreads / 32) + 16) * 4;
-}
-cudaError_t launch_evict_select(const SelectArgs& a, int cluster, size_t smem, cudaStream_t stream);
+constexpr int kSelKeys = 32;  // rows that a lane keeps in registers
+cudaError_t launch_evict_select(const SelectArgs& a, int cluster, cudaStream_t stream);
 
 // kvq_evict_compact.
 struct CompactArgs {

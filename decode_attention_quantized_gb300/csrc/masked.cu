@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) mass_rest_kernel(const DecodeArgs a, cons
   for (int seg = blockIdx.y; seg < segs; seg += gridDim.y) {
     const int b = seg / a.num_kv_heads, h = seg - b * a.num_kv_heads;
     const VSeq v = a.vseq[b];
-    const int lo = v.lo & ~(kTile - 1);
+    const int lo = v.lo & ~(m.tile - 1);
     const int32_t* bt = a.block_table + (size_t)v.brow * a.max_blocks_per_seq;
     for (int key = blockIdx.x * blockDim.x + threadIdx.x; key < v.len; key += gridDim.x * blockDim.x) {
       if (!all && key >= lo && key < v.hi) continue;
