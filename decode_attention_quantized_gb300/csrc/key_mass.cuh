@@ -85,6 +85,22 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
     // ---- the piece's query rows: operand and rule
     uint32_t qf[QS ? 1 : Gm::NMT][2], ql[SPLIT && !QS ? Gm::NMT : 1][2];
     ptx::named_bar_sync(1, kMassWarps * 32);  // the previous piece's rows are read
+    // (a thread a row; its loads run while the operand is made)
+    MassRow mr{};
+    if (tid < rows) {
+      const int t = dev::div_small(tid, inv_g), hq = h * G + tid - t * G;
+      const size_t tok = (size_t)vs.tok0 + t;
+      const float lse = ms.lse[tok * a.num_q_heads + hq];
+      const dev::RowRule ru = dev::row_rule(a, tok, vs.pos0 + t, hq, L);
+      // lse less the anchor's bias: in fp64, both may be large
+      const double s = a.slopes ? (double)a.slopes[hq] * (double)ru.d0 : 0.0;
+      mr.c = (float)(((double)lse + s) * 1.4426950408889634);
+      mr.ns = ru.ns;
+      mr.begin = ru.begin;
+      mr.end = lse == -INFINITY ? 0 : ru.end;  // a row without weight
+      mr.pos = ru.pos;
+      mr.d0 = ru.d0;
+    }
 #pragma unroll 1
     for (int nt = QS ? warp : 0; nt < NT; nt += QS ? kMassWarps : 1) {
       const int row = nt * 8 + g;
@@ -112,38 +128,30 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
         }
       }
       if (c == 0 && (QS || warp == 0)) {
-        MassRow r{};
         if (softcap > 0.0f) al = fminf(al / softcap, 3.4028234e38f);
-        r.alpha = al;
-        if (row < rows) {
-          const int t = dev::div_small(row, inv_g), hq = h * G + row - t * G;
-          const size_t tok = (size_t)vs.tok0 + t;
-          const dev::RowRule ru = dev::row_rule(a, tok, vs.pos0 + t, hq, L);
-          const float lse = ms.lse[tok * a.num_q_heads + hq];
-          // lse less the anchor's bias: in fp64, both may be large
-          const double s = a.slopes ? (double)a.slopes[hq] * (double)ru.d0 : 0.0;
-          r.c = (float)(((double)lse + s) * 1.4426950408889634);
-          r.ns = ru.ns;
-          r.begin = ru.begin;
-          r.end = lse == -INFINITY ? 0 : ru.end;  // a row without weight
-          r.pos = ru.pos;
-          r.d0 = ru.d0;
-        }
-        rows_s[row] = r;
+        rows_s[row].alpha = al;
       }
+    }
+    ptx::named_bar_sync(1, kMassWarps * 32);
+    if (tid < ROWS) {
+      mr.alpha = tid < rows ? rows_s[tid].alpha : 0.0f;
+      rows_s[tid] = mr;
     }
     ptx::named_bar_sync(1, kMassWarps * 32);
 
     const int32_t* bt = a.block_table + (size_t)vs.brow * a.max_blocks_per_seq;
+    // the page of this warp's next sub-tile is looked up a tile ahead
+    int id_next = k0 + warp * kSub < k1 ? bt[(k0 + warp * kSub) >> a.log2_bs] : -1;
     for (int key0 = k0; key0 < k1; key0 += kTile, rp.next(a.stages)) {
       const int kb = key0 + warp * kSub;
       const int key_a = kb + g, key_b = key_a + 8;
+      const int id = id_next;
+      if (kb + kTile < k1) id_next = bt[(kb + kTile) >> a.log2_bs];
       // where this sub-tile's weights live (its 16 keys share a page), and
       // what they held
       float* out = nullptr;
       float old_a = 0.0f, old_b = 0.0f;
       if (kb < k1) {
-        const int id = bt[kb >> a.log2_bs];
         if (id >= 0 && id < a.num_blocks)
           out = ms.mass + ((size_t)id * a.num_kv_heads + h) * a.block_size + (kb & (a.block_size - 1));
         if (out && c == 0 && ms.decay != 0.0f) {

@@ -190,7 +190,25 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
       // every warp has read the previous piece's rows (and waited for its last
       // MMAs, so the Q operand is free)
       ptx::named_bar_sync(5, 256);
-      // ---- the piece's Q operand and row rules
+      // ---- the piece's row rules (a thread a row; its loads run while the
+      // operand below is made) and Q operand
+      float2 ac = make_float2(0.0f, INFINITY), ne = make_float2(0.0f, 0.0f);
+      MassTcRule ru{0, 0, 0, 0};
+      bool live = false;
+      if (tid < rows) {
+        const int t = dev::div_small(tid, inv_g), hq = h * G + tid - t * G;
+        const size_t tok = (size_t)vs.tok0 + t;
+        const float lse = ms.lse[tok * Hq + hq];
+        const dev::RowRule rr = dev::row_rule(a, tok, vs.pos0 + t, hq, L);
+        live = rr.begin < rr.end && lse != -INFINITY;
+        if (live) {
+          // lse less the anchor's bias: in fp64, both may be large
+          const double s = a.slopes ? (double)a.slopes[hq] * (double)rr.d0 : 0.0;
+          ac.y = (float)(((double)lse + s) * 1.4426950408889634);
+          ne = make_float2(rr.ns, (float)(rr.pos - rr.d0 - k0));
+          ru = MassTcRule{rr.begin, rr.end, rr.pos, rr.d0};
+        }
+      }
       {
         const bool kc = a.k_mode == KVQ_SCALE_PER_CHANNEL;
         float ksv[8];
@@ -212,74 +230,75 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         float fac = a.sm_scale;
         if (a.k_mode == KVQ_SCALE_PER_TENSOR) fac *= a.k_scale[0];
         fac *= softcap > 0.0f ? inv_cap : kLog2e;
-#pragma unroll 2
-        for (int r = warp * RPP + rsub; r < NR; r += 8 * RPP) {
-          const int t = dev::div_small(r, inv_g), hq = h * G + r - t * G;
-          const bool valid = r < rows;
-          const uint4 raw = valid ? ptx::ldg_nc_v4(a.q + (((size_t)vs.tok0 + t) * Hq + hq) * D + 8 * cl)
-                                  : make_uint4(0, 0, 0, 0);
-          float qv[8];
-          const uint32_t ww[4] = {raw.x, raw.y, raw.z, raw.w};
+        constexpr int BAT = 4;  // row loads in flight
+#pragma unroll 1
+        for (int r0 = warp * RPP + rsub; r0 < NR; r0 += BAT * 8 * RPP) {
+          uint4 raw[BAT];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            qv[2 * j] = __uint_as_float(ww[j] << 16);
-            qv[2 * j + 1] = __uint_as_float(ww[j] & 0xFFFF0000u);
+          for (int i = 0; i < BAT; ++i) {
+            const int r = r0 + i * 8 * RPP, t = dev::div_small(r, inv_g);
+            raw[i] = r < rows ? ptx::ldg_nc_v4(a.q + (((size_t)vs.tok0 + t) * Hq + h * G + r - t * G) * D + 8 * cl)
+                              : make_uint4(0, 0, 0, 0);
           }
-          if (kc) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) qv[j] *= ksv[j];
-          }
-          float qm = 0.0f;
+          for (int i = 0; i < BAT; ++i) {
+            const int r = r0 + i * 8 * RPP;
+            float qv[8];
+            const uint32_t ww[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) qm = fmaxf(qm, fabsf(qv[j]));
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, o));
-          const int eq = qm > 0.0f ? min(126, max(-126, dev::ceil_log2(qm))) : 0;
-          const float sq = dev::pow2i(-eq);
-          uint32_t w[4], lo[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            float x0, x1;
-            if constexpr (DT == KVQ_INT4) {
-              const float f = (m & 1) ? sq * dev::odd_channel_factor<DT>() : sq;  // channels m, m + 4
-              x0 = qv[m] * f;
-              x1 = qv[m + 4] * f;
-            } else {
-              x0 = qv[2 * m] * sq;
-              x1 = qv[2 * m + 1] * sq;
+            for (int j = 0; j < 4; ++j) {
+              qv[2 * j] = __uint_as_float(ww[j] << 16);
+              qv[2 * j + 1] = __uint_as_float(ww[j] & 0xFFFF0000u);
             }
-            w[m] = dev::pack_h2(x0, x1);
-            lo[m] = dev::rest_h2(x0, x1, w[m]);
-          }
-          uint8_t* dst = q_s + (cl >> 3) * (NR * 128) + r * 128 + ((((uint32_t)cl & 7u) ^ ((uint32_t)r & 7u)) << 4);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-          if constexpr (SPLIT) *reinterpret_cast<uint4*>(dst + q_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (cl == 0) {
-            // a row that is padding, sees nothing or has no weight: factor 0
-            // and log-sum-exp +inf give it a weight of exactly 0 everywhere
-            float2 ac = make_float2(0.0f, INFINITY), ne = make_float2(0.0f, 0.0f);
-            MassTcRule ru{0, 0, 0, 0};
-            if (valid) {
-              const size_t tok = (size_t)vs.tok0 + t;
-              const dev::RowRule rr = dev::row_rule(a, tok, vs.pos0 + t, hq, L);
-              const float lse = ms.lse[tok * Hq + hq];
-              if (rr.begin < rr.end && lse != -INFINITY) {
-                const double s = a.slopes ? (double)a.slopes[hq] * (double)rr.d0 : 0.0;
+            if (kc) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) qv[j] *= ksv[j];
+            }
+            float qm = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) qm = fmaxf(qm, fabsf(qv[j]));
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, o));
+            const int eq = qm > 0.0f ? min(126, max(-126, dev::ceil_log2(qm))) : 0;
+            const float sq = dev::pow2i(-eq);
+            uint32_t w[4], lo[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              float x0, x1;
+              if constexpr (DT == KVQ_INT4) {
+                const float f = (m & 1) ? sq * dev::odd_channel_factor<DT>() : sq;  // channels m, m + 4
+                x0 = qv[m] * f;
+                x1 = qv[m + 4] * f;
+              } else {
+                x0 = qv[2 * m] * sq;
+                x1 = qv[2 * m + 1] * sq;
+              }
+              w[m] = dev::pack_h2(x0, x1);
+              lo[m] = dev::rest_h2(x0, x1, w[m]);
+            }
+            if (r < NR) {
+              uint8_t* dst = q_s + (cl >> 3) * (NR * 128) + r * 128 + ((((uint32_t)cl & 7u) ^ ((uint32_t)r & 7u)) << 4);
+              *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+              if constexpr (SPLIT) *reinterpret_cast<uint4*>(dst + q_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              if (cl == 0) {
                 const int e = ek + eq, e1 = e / 2;
-                ac.x = fminf(fac * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f);
-                ac.y = (float)(((double)lse + s) * 1.4426950408889634);
-                ne = make_float2(rr.ns, (float)(rr.pos - rr.d0 - k0));
-                ru = MassTcRule{rr.begin, rr.end, rr.pos, rr.d0};
+                r_ac[r].x = fminf(fac * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f);
               }
             }
-            r_ac[r] = ac;
-            r_ne[r] = ne;
-            r_rule[r] = ru;
           }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(b_qfull);
+      }
+      ptx::named_bar_sync(5, 256);  // the logit factors are visible
+      if (tid < NR) {
+        // a row that is padding, sees nothing or has no weight: factor 0 and
+        // log-sum-exp +inf give it a weight of exactly 0 everywhere
+        if (!live) r_ac[tid].x = 0.0f;
+        r_ac[tid].y = ac.y;
+        r_ne[tid] = ne;
+        r_rule[tid] = ru;
       }
       ptx::named_bar_sync(5, 256);  // the rows are visible
       // tiles inside [bmax, emin) and, under a bias, at or below pmin need no
@@ -303,13 +322,16 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
       const int32_t* bt = a.block_table + (size_t)vs.brow * a.max_blocks_per_seq;
       const int c_lo = side * (NR / 2), c_hi = c_lo + NR / 2;
 
+      // the page of this thread's next key is looked up a tile ahead
+      int id_next = side == 0 && k0 + kk < k1 ? bt[(k0 + kk) >> a.log2_bs] : -1;
       for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(a.stages)) {
         const uint32_t buf = it & 1;
         const int key = key0 + kk;
         float* out = nullptr;
         float old = 0.0f;
+        const int id = id_next;
+        if (side == 0 && key + KT < k1) id_next = bt[(key + KT) >> a.log2_bs];
         if (side == 0 && key < k1) {
-          const int id = bt[key >> a.log2_bs];
           if (id >= 0 && id < a.num_blocks) {
             out = ms.mass + ((size_t)id * a.num_kv_heads + h) * a.block_size + (key & (a.block_size - 1));
             if (ms.decay != 0.0f && key < vs.len - ms.fresh) old = ms.decay * *out;
