@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
         if (id >= 0 && id < a.num_blocks)
           out = ms.mass + ((size_t)id * a.num_kv_heads + h) * a.block_size + (kb & (a.block_size - 1));
         if (out && c == 0 && ms.decay != 0.0f) {
-          if (key_a < k1 && key_a < vs.len - ms.fresh) old_a = ms.decay * out[g];
-          if (key_b < k1 && key_b < vs.len - ms.fresh) old_b = ms.decay * out[g + 8];
+          if (key_a < k1 && key_a < vs.len - ms.fresh) old_a = out[g];
+          if (key_b < k1 && key_b < vs.len - ms.fresh) old_b = out[g + 8];
         }
       }
       if (ok) {
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
       sum_a += __shfl_xor_sync(0xffffffffu, sum_a, 2);
       sum_b += __shfl_xor_sync(0xffffffffu, sum_b, 2);
       if (out && ok && c == 0) {
-        if (key_a < k1) out[g] = old_a + sum_a;
-        if (key_b < k1) out[g + 8] = old_b + sum_b;
+        if (key_a < k1) out[g] = ms.decay * old_a + sum_a;
+        if (key_b < k1) out[g + 8] = ms.decay * old_b + sum_b;
       }
     }
   }

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
   float2* r_ne = r_ac + NR;                                          // [NR] bias per key, pos - d0 - k0
   MassTcRule* r_rule = reinterpret_cast<MassTcRule*>(r_ne + NR);     // [NR]
   float* half_sum = reinterpret_cast<float*>(r_rule + NR);           // [2][KT] the second half's sums
+  float* k_scale = half_sum + 2 * KT;                                // [4][KT] K scales of tile it, at it & 3
   int* pl_pre = reinterpret_cast<int*>(base + lay.pre);
   int* pl_misc = pl_pre + a.batch + 1;
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(base + lay.bars);
@@ -61,14 +62,15 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
   uint64_t* b_sfree = b_s + 2;           // [2] S buffer read
   uint64_t* b_kfull = b_s + 4;           // [2] K tile in TMEM
   uint64_t* b_qfull = b_s + 6;           // Q of a piece written
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_s + 7);
+  uint64_t* b_ksc = b_s + 7;             // [4] K scales of tile it in k_scale slot it & 3 (per-row K)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_s + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       ptx::mbar_init(&bar_full[s], 1);
-      ptx::mbar_init(&bar_empty[s], 12);  // K dequant and weight warps
+      ptx::mbar_init(&bar_empty[s], 4);  // K dequant warps
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&b_s[i], 1);
@@ -76,6 +78,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
       ptx::mbar_init(&b_kfull[i], 4);
     }
     ptx::mbar_init(b_qfull, 8);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(&b_ksc[i], 4);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -109,16 +112,26 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         wait(&bar_full[rp.stage], rp.phase);
         const uint8_t* st = ring + (size_t)rp.stage * a.stage_stride;
         const uint32_t buf = it & 1;
-#pragma unroll 1
+        // the key's whole code row (and scale) first, so that the stage goes
+        // back to the producer at once
+        uint4 w[2 * HCH];
+#pragma unroll
+        for (int jj = 0; jj < 2 * HCH; ++jj) {
+          const uint32_t byte = (uint32_t)jj * 16;
+          w[jj] = *reinterpret_cast<const uint4*>(
+              st + (byte / Gm::SPAN) * (KT * Gm::SPAN) + dev::swz<Gm::SPAN>(kk * Gm::SPAN + byte % Gm::SPAN));
+        }
+        // the scale for the weight warps: slot it & 3 was last read for tile
+        // it - 4, before the MMAs of tile it - 2 that this warp waits for below
+        float ksv = 1.0f;
+        if (k_row) ksv = reinterpret_cast<const float*>(st + Gm::CODE_BYTES)[kk];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar_empty[rp.stage]);
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t v[HCH * CW];
 #pragma unroll
-          for (int jj = 0; jj < HCH; ++jj) {
-            const uint32_t byte = (uint32_t)(half * HCH + jj) * 16;
-            const uint4 w = *reinterpret_cast<const uint4*>(
-                st + (byte / Gm::SPAN) * (KT * Gm::SPAN) + dev::swz<Gm::SPAN>(kk * Gm::SPAN + byte % Gm::SPAN));
-            dev::k_cols<DT>(w, v + CW * jj);
-          }
+          for (int jj = 0; jj < HCH; ++jj) dev::k_cols<DT>(w[half * HCH + jj], v + CW * jj);
           if (half == 0 && it >= 2) wait(&b_s[buf], ((it - 2) >> 1) & 1);  // the MMAs two tiles back are done
           ptx::tc_fence_after();
           if constexpr (HCH * CW == 64)
@@ -126,12 +139,13 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
           else
             ptx::tmem_st32(t_k + (D / 2) * buf + 32 * half, v);
         }
+        if (k_row) k_scale[(it & 3) * KT + kk] = ksv;
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(&b_kfull[buf]);
-          ptx::mbar_arrive(&bar_empty[rp.stage]);
+          if (k_row) ptx::mbar_arrive(&b_ksc[it & 3]);
         }
       }
     }
@@ -181,7 +195,6 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
     constexpr int LPR = D / 8, RPP = 32 / LPR;  // lanes per row (8 channels each), rows per warp pass
     const int rsub = lane / LPR, cl = lane % LPR;
     uint32_t it = 0;
-    RingPos rp;
     for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
       int b, h, k0, k1, L, u;
       sp.piece(a, gt, b, h, k0, k1, L, u, next);
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
 
       // the page of this thread's next key is looked up a tile ahead
       int id_next = side == 0 && k0 + kk < k1 ? bt[(k0 + kk) >> a.log2_bs] : -1;
-      for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(a.stages)) {
+      for (int key0 = k0; key0 < k1; key0 += KT, ++it) {
         const uint32_t buf = it & 1;
         const int key = key0 + kk;
         float* out = nullptr;
@@ -334,16 +347,15 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         if (side == 0 && key < k1) {
           if (id >= 0 && id < a.num_blocks) {
             out = ms.mass + ((size_t)id * a.num_kv_heads + h) * a.block_size + (key & (a.block_size - 1));
-            if (ms.decay != 0.0f && key < vs.len - ms.fresh) old = ms.decay * *out;
+            // (scaled where it is used: the load stays in flight until then)
+            if (ms.decay != 0.0f && key < vs.len - ms.fresh) old = *out;
           }
         }
         float ks = 1.0f;
         if (k_row) {
-          wait(&bar_full[rp.stage], rp.phase);
-          ks = reinterpret_cast<const float*>(ring + (size_t)rp.stage * a.stage_stride + Gm::CODE_BYTES)[kk];
+          wait(&b_ksc[it & 3], (it >> 2) & 1);
+          ks = k_scale[(it & 3) * KT + kk];
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bar_empty[rp.stage]);
         wait(&b_s[buf], (it >> 1) & 1);
         ptx::tc_fence_after();
         const bool fast = key0 >= bmax && key0 + KT <= emin && (!bias || key0 + KT - 1 <= pmin);
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         s0 += s1;
         if (side == 1) half_sum[buf * KT + kk] = s0;
         ptx::named_bar_sync(1 + q, 64);
-        if (out) *out = old + (s0 + half_sum[buf * KT + kk]);
+        if (out) *out = ms.decay * old + (s0 + half_sum[buf * KT + kk]);
       }
     }
   }

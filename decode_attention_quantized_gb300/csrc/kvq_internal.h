@@ -267,7 +267,7 @@ struct MassTcSmem {
 };
 
 // ring: stages x stage stride; q: one or two [D/64 slabs][nr rows][128 B] f16
-// operands; rows: 32 bytes a row and the two [128] half sums; pre: split plan;
+// operands; rows: 32 bytes a row, the two [128] half sums and four [128] K scales; pre: split plan;
 // bars: mbarriers, then TMEM address and abort flag.
 __host__ __device__ constexpr MassTcSmem mass_tc_layout(int head_dim, int nr, bool split, int stages, int batch,
                                                         int stage_stride) {
@@ -275,9 +275,9 @@ __host__ __device__ constexpr MassTcSmem mass_tc_layout(int head_dim, int nr, bo
   s.ring = 0;
   s.q = stages * stage_stride;
   s.rows = s.q + nr * head_dim * 2 * (split ? 2 : 1);
-  s.pre = s.rows + nr * 32 + 2 * kTcKeys * 4;
+  s.pre = s.rows + nr * 32 + 6 * kTcKeys * 4;
   s.bars = (s.pre + (batch + 5) * 4 + 7) / 8 * 8;
-  s.total = s.bars + (2 * stages + 7) * 8 + 16;
+  s.total = s.bars + (2 * stages + 11) * 8 + 16;
   return s;
 }
 cudaError_t launch_key_mass_tc_int8(int head_dim, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m,
