@@ -335,7 +335,10 @@ __global__ void __launch_bounds__(288, MINB)
 
   // =============================================================== producer
   if (warp == n_cw) {
-    produce<Gm, true, MASK>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    if constexpr (MASK)
+      produce_lanes<Gm>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    else
+      produce<Gm, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
     return;
   }
 

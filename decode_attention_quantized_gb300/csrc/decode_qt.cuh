@@ -174,7 +174,10 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
   if (warp == kProducer) {
     // ============================================================ producer
-    produce<Gm, false, MASK>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    if constexpr (MASK)
+      produce_lanes<Gm>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    else
+      produce<Gm, false>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
   } else if (warp >= kDqK && warp < kDqV + 4) {
     // ==================================================== K and V dequant
     // thread: key kk of the tile, channel half hf; its code chunks are read

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
   }
   const Slice<kTile, true> sp = build_slice<kTile, true>(a, pl_pre, pl_misc);
   if (warp == kMassWarps) {
-    produce<Gm, true, true>(a, sp, &tmk, &tmk, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    produce_lanes<Gm>(a, sp, &tmk, &tmk, ring, bar_full, bar_empty, pl_pre, pl_misc);
     return;
   }
 

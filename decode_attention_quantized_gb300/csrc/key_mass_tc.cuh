@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
 
   if (warp == kProducer) {
     // ============================================================ producer
-    produce<Gm, false, true>(a, sp, &tmk, &tmk, ring, bar_full, bar_empty, pl_pre, pl_misc);
+    produce_lanes<Gm>(a, sp, &tmk, &tmk, ring, bar_full, bar_empty, pl_pre, pl_misc);
   } else if (warp >= kDqK && warp < kDqK + 4) {
     // ========================================================== K dequant
     const int q = warp - kDqK, kk = 32 * q + lane;

@@ -228,8 +228,8 @@ __device__ __forceinline__ void publish_slice(const DecodeArgs& a, const int* pl
 // [0, num_blocks) is flagged and its rows are not loaded.  Returns after
 // every copy it issued has landed, so the CTA never exits with a copy in
 // flight.
-template <class Gm, bool kBurst, bool MASK = false>
-__device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS, MASK>& sp, const CUtensorMap* tmk,
+template <class Gm, bool kBurst>
+__device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS>& sp, const CUtensorMap* tmk,
                         const CUtensorMap* tmv, uint8_t* ring, uint64_t* bar_full, uint64_t* bar_empty,
                         const int* pl_pre, const int* pl_misc) {
   constexpr int KT = Gm::KEYS;
@@ -257,7 +257,7 @@ __device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS, MASK>& sp, co
   for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
     int b, h, k0, k1, L, slot;
     sp.piece(a, gt, b, h, k0, k1, L, slot, next);
-    const int32_t* bt = a.block_table + (size_t)(MASK ? a.vseq[b].brow : b / a.bt_div) * a.max_blocks_per_seq;
+    const int32_t* bt = a.block_table + (size_t)(b / a.bt_div) * a.max_blocks_per_seq;
     const int p_last = (k1 - 1) >> a.log2_bs;
     int base = k0 >> a.log2_bs;
     int my_id = base + lane <= p_last ? bt[base + lane] : -1;
@@ -272,11 +272,9 @@ __device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS, MASK>& sp, co
       // ends; the producer runs a ring ahead of them, so it pulls those rows
       // into L2 now (G heads of one kv head are contiguous per token)
       const int lines = a.group * Gm::D * 2 / 128;
-      const size_t tok0 = MASK ? (size_t)a.vseq[b].tok0 : (size_t)b * a.q_tokens;
-      const int ntok = MASK ? a.vseq[b].ntok : a.q_tokens;
-      for (int i = lane; i < ntok * lines; i += 32) {
+      for (int i = lane; i < a.q_tokens * lines; i += 32) {
         const int t = i / lines, c = i - t * lines;
-        ptx::prefetch_l2(a.q + ((tok0 + t) * a.num_q_heads + (size_t)h * a.group) * Gm::D + c * 64);
+        ptx::prefetch_l2(a.q + (((size_t)b * a.q_tokens + t) * a.num_q_heads + (size_t)h * a.group) * Gm::D + c * 64);
       }
     }
     for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(S)) {
@@ -376,6 +374,91 @@ __device__ void produce(const DecodeArgs& a, const Slice<Gm::KEYS, MASK>& sp, co
     }
   }
   gate();  // (an empty slice still publishes the plan from CTA 0)
+  // let every copy this warp issued land before the CTA can exit
+  if (lane == 0) {
+    for (uint32_t s = 0; s < S && s < it; ++s) {
+      const uint32_t last = it - 1 - ((it - 1 - s) % S);
+      if (!ptx::mbar_wait_bounded(&bar_full[s], (last / S) & 1)) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+    }
+  }
+  __syncwarp();
+}
+
+// The producer warp of the masked kernels (no early reads): the same stages,
+// with a page segment per lane.  Lane s < KEYS / segment rows looks up its own
+// segment's page a tile ahead, and the lanes issue their copies side by side
+// under one expect-tx arrival of the stage's bytes.  (With lane 0 alone
+// working through the segments, a stage of 128 keys took it 2000 to 3400
+// clocks, about 850 a segment, and one CTA per SM waited for that.)
+template <class Gm>
+__device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& sp, const CUtensorMap* tmk,
+                              const CUtensorMap* tmv, uint8_t* ring, uint64_t* bar_full, uint64_t* bar_empty,
+                              const int* pl_pre, const int* pl_misc) {
+  constexpr int KT = Gm::KEYS;
+  const int lane = threadIdx.x & 31;
+  ptx::griddep_wait();
+  publish_slice(a, pl_pre, pl_misc);
+  const int nk = a.sk_n, nv = a.v_alias ? 0 : a.sv_n;
+  const uint32_t sc_off = (a.v_alias ? 1 : 2) * Gm::CODE_BYTES;
+  const uint32_t v_sc = sc_off + KT * 4 * (nk > 1 ? nk : 1);
+  const int Hkv = a.num_kv_heads;
+  const int seg_rows = min(a.block_size, kTile);  // rows of one TMA box
+  const uint32_t seg_bytes = (uint32_t)seg_rows * ((a.v_alias ? 1 : 2) * Gm::DP + 4 * nk + 4 * nv);
+  const int my_row = lane * seg_rows;  // this lane's first row in a stage
+  const bool mine = my_row < KT;
+  const uint32_t S = (uint32_t)a.stages;
+  uint32_t it = 0;
+  RingPos rp;
+  int ok = 1;
+  for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
+    int b, h, k0, k1, L, slot;
+    sp.piece(a, gt, b, h, k0, k1, L, slot, next);
+    const VSeq vs = a.vseq[b];
+    const int32_t* bt = a.block_table + (size_t)vs.brow * a.max_blocks_per_seq;
+    int id_next = mine && k0 + my_row < k1 ? bt[(k0 + my_row) >> a.log2_bs] : -1;
+    if (gt != sp.t_begin) {
+      // (as in produce: the piece's query rows into L2)
+      const int lines = a.group * Gm::D * 2 / 128;
+      for (int i = lane; i < vs.ntok * lines; i += 32) {
+        const int t = i / lines, c = i - t * lines;
+        ptx::prefetch_l2(a.q + (((size_t)vs.tok0 + t) * a.num_q_heads + (size_t)h * a.group) * Gm::D + c * 64);
+      }
+    }
+    for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(S)) {
+      const int stage = (int)rp.stage, key = key0 + my_row;
+      const int id = id_next;
+      if (mine && key + KT < k1) id_next = bt[(key + KT) >> a.log2_bs];
+      if (lane == 0 && it >= S && ok) {
+        ok = ptx::mbar_wait_bounded(&bar_empty[stage], rp.phase ^ 1u) ? 1 : 0;
+        if (!ok) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      bool load = mine && key < k1 && ok;  // nothing is loaded after a timeout
+      if (load && (id < 0 || id >= a.num_blocks)) {
+        atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
+        load = false;
+      }
+      const uint32_t loads = __ballot_sync(0xffffffffu, load);
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&bar_full[stage], seg_bytes * (uint32_t)__popc(loads));
+      __syncwarp();
+      if (load) {
+        uint8_t* st = ring + (size_t)stage * a.stage_stride;
+        const int row0 = key & (a.block_size - 1);
+#pragma unroll
+        for (int sl = 0; sl < Gm::SLABS; ++sl) {
+          uint8_t* dk = st + sl * (KT * Gm::SPAN) + my_row * Gm::SPAN;
+          ptx::tma_load_4d(dk, tmk, sl * Gm::SPAN, row0, h, id, &bar_full[stage]);
+          if (!a.v_alias) ptx::tma_load_4d(dk + Gm::CODE_BYTES, tmv, sl * Gm::SPAN, row0, h, id, &bar_full[stage]);
+        }
+        const size_t srow = ((size_t)id * Hkv + h) * a.block_size + row0;
+        if (nk)
+          ptx::bulk_load(st + sc_off + my_row * 4 * nk, a.k_scale + srow * nk, seg_rows * 4 * nk, &bar_full[stage]);
+        if (nv)
+          ptx::bulk_load(st + v_sc + my_row * 4 * nv, a.v_scale + srow * nv, seg_rows * 4 * nv, &bar_full[stage]);
+      }
+      __syncwarp();
+    }
+  }
   // let every copy this warp issued land before the CTA can exit
   if (lane == 0) {
     for (uint32_t s = 0; s < S && s < it; ++s) {
