@@ -174,10 +174,12 @@ size_t stage_stride(const kvq_cache* c, bool alias) {
   return ((alias ? 1 : 2) * code + sc + 1023) / 1024 * 1024;
 }
 
-// split: room for the second part of the Q operand (the masked kernels).
+// mask: the rows' rules; split: the second part of the Q operand (the masked
+// kernels).
 size_t fixed_smem(const kvq_cache* c, int row_groups, int key_warps, int nt, int batch, int stages,
-                  bool split = false) {
+                  bool mask = false, bool split = false) {
   size_t s = 1024;  // alignment slack of the ring
+  if (mask) s += (size_t)(nt > 0 ? 16 * nt * 32 : row_groups * 8 * 40) + 16;
   if (split) s += nt > 0 ? (size_t)16 * nt * c->head_dim * 2 : (size_t)row_groups * c->head_dim / 16 * 32 * 8;
   if (nt > 0)  // wide layout: P buffer, row maxima / sums, Q operand, logit factors
     s += (size_t)(16 * nt * 32 + 2 * 4 * 16 * nt + 32 + 16 * nt * (c->head_dim / 2) + (16 * nt + 31) / 32 * 32) * 4;
@@ -425,14 +427,14 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
   for (int target : {4, 3, 2, 1}) {
     // per-SM shared memory is 228 KiB with 1 KiB reserved per resident CTA
     const size_t budget = (size_t)228 * 1024 / target - 1024;
-    const size_t fixed = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, 0, split);
+    const size_t fixed = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, 0, mask, split);
     // head_dim 576 stages are 37 KB: two CTAs of two stages each still keep
     // 148 KB in flight per SM, and twice the warps hide more latency
     const int min_stages = target > 1 && c->head_dim != 576 ? 3 : 2;
     if (fixed + (size_t)min_stages * (stride + 16) > budget) continue;
     int stages = (int)((budget - fixed) / (stride + 16));
     stages = stages > kMaxStages ? kMaxStages : stages;
-    const size_t smem = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, stages, split) + (size_t)stages * stride;
+    const size_t smem = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, stages, mask, split) + (size_t)stages * stride;
     int n = 0;
     if (occupancy(c, kernel_nt(c, P), P.threads, smem, mask, split, &n) != cudaSuccess) return KVQ_ERR_CUDA;
     if (n >= target) {
@@ -979,8 +981,9 @@ kvq_status check_evict(const kvq_evict_params* p) {
   return KVQ_OK;
 }
 
-// Launch shape of kvq_evict_compact: units of up to 128 rows and about 32 KB,
+// Launch shape of kvq_evict_compact: units of up to 128 rows and kUnitBytes,
 // two CTAs per SM with as many ring stages as fit.
+constexpr int kUnitBytes = 16 * 1024;
 struct CompactPlan {
   int rows, stages, stage_bytes, grid, units;
   size_t smem, ws;
@@ -994,10 +997,10 @@ kvq_status compact_plan(const kvq_cache* c, const kvq_evict_params* p, bool mass
   const int sides = c->layout == KVQ_LAYOUT_LATENT ? 1 : 2, rb = row_bytes(c);
   const int nf = scales_per_row(c, c->k_mode) + (sides == 2 ? scales_per_row(c, c->v_mode) : 0) + (mass ? 1 : 0);
   P.rows = kCompactRows;
-  while (P.rows > 16 && P.rows * rb * sides > 32 * 1024) P.rows >>= 1;
+  while (P.rows > 16 && P.rows * rb * sides > kUnitBytes) P.rows >>= 1;
   P.stage_bytes = (P.rows * (rb * sides + 4 * nf) + 127) / 128 * 128;
   constexpr int kCtas = 2;
-  const int budget = 228 * 1024 / kCtas - 2048;
+  const int budget = 228 * 1024 / kCtas - 1024 - 12 * 1024;  // (beside the kernel's own 11 KB)
   P.stages = budget / P.stage_bytes;
   P.stages = P.stages > kCompactStages ? kCompactStages : P.stages;
   if (P.stages < 2) return KVQ_ERR_UNSUPPORTED;

@@ -303,7 +303,12 @@ __global__ void __launch_bounds__(288, MINB)
   const int lo_floats = !SPLIT ? 0 : (NT > 0 ? 16 * NT * (D / 2) : a.row_groups * kLoPerRg);
   const int scr_only =
       NT > 0 ? wide_scratch_floats<NT, D>() : (a.key_warps > 1 ? a.row_groups * kScrPerRg : 0);
-  const int scr_floats = scr_only + lo_floats;
+  // the rows' rules (masked): wide, or [row group][8]
+  const int rule_off = (scr_only + lo_floats + 3) & ~3;
+  // (grouped: and 8 bytes a row for its linear form)
+  const int rule_floats = !MASK ? 0 : (NT > 0 ? 16 * NT * 8 : a.row_groups * 8 * (8 + 2));
+  const int scr_floats = MASK ? rule_off + rule_floats : scr_only + lo_floats;
+  dev::RowRule* s_rule = reinterpret_cast<dev::RowRule*>(scr + rule_off);
   int* pl_pre = reinterpret_cast<int*>(scr + scr_floats);  // [B + 1]
   int* pl_misc = pl_pre + a.batch + 1;                     // [4]
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(pl_misc + 4 + ((a.batch + 5) & 1));
@@ -503,7 +508,6 @@ __global__ void __launch_bounds__(288, MINB)
       ptx::named_bar_sync(1, 8 * 32);
       float al[NT][2], m[NT][2], l[NT][2];
       int pos[NT][2];
-      dev::RowRule rule[MASK ? NT : 1][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -511,8 +515,10 @@ __global__ void __launch_bounds__(288, MINB)
           const int r = rh * RW + nt * 8 + 2 * c + i;
           al[nt][i] = s_alpha[r];
           if constexpr (MASK) {
+            // (the four key quarters write the same; lane group 0 of each does,
+            // behind the barriers that ended the previous piece)
             const int rr = r < rows ? r : 0, t = dev::div_small(rr, inv_g);
-            rule[nt][i] = dev::row_rule(a, tok0 + t, a.vseq[b].pos0 + t, h * G + rr - t * G, L);
+            if (g == 0) s_rule[r] = dev::row_rule(a, tok0 + t, a.vseq[b].pos0 + t, h * G + rr - t * G, L);
             pos[nt][i] = 0;
           } else {
             pos[nt][i] = r < rows ? L - T + dev::div_small(r, inv_g) : -1;
@@ -521,6 +527,7 @@ __global__ void __launch_bounds__(288, MINB)
           l[nt][i] = 0.0f;
         }
       }
+      if constexpr (MASK) __syncwarp();
       int F = v_row ? -126 : 0;  // V-scale normaliser exponent, the same in every warp
       float acc[MTW][NT][4];
 #pragma unroll
@@ -634,6 +641,7 @@ __global__ void __launch_bounds__(288, MINB)
             ksa = ks_row[kq * kSub + g];
             ksb = ks_row[kq * kSub + g + 8];
           }
+          bool see_a = false, see_b = false;  // masked: some row of this lane sees the key
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             x[nt][0] = sacc[0][nt][0] * al[nt][0] * ksa;
@@ -648,27 +656,20 @@ __global__ void __launch_bounds__(288, MINB)
             for (int e = 0; e < 4; ++e) {
               const int key = e < 2 ? key_a : key_b, p = pos[nt][e & 1];
               if constexpr (MASK) {
-                const dev::RowRule& ru = rule[nt][e & 1];
-                if (a.slopes) x[nt][e] = fmaf(ru.ns, (float)(abs(ru.pos - key) - ru.d0), x[nt][e]);
-                if (!(key >= ru.begin && key < ru.end)) x[nt][e] = -INFINITY;
+                bool seen;
+                x[nt][e] = dev::rule_score(s_rule[rh * RW + nt * 8 + 2 * c + (e & 1)], x[nt][e], key,
+                                           a.slopes != nullptr, seen);
+                if (e < 2) see_a = see_a || seen;
+                else see_b = see_b || seen;
               } else {
                 if (!(key <= p && (W == 0 || key > p - W))) x[nt][e] = -INFINITY;
               }
             }
           }
           if (v_row) {
-            bool use_a = key_a < L, use_b = key_b < L;
-            if constexpr (MASK) {
-              // a row that none of this lane's query rows sees may hold anything
-              use_a = use_b = false;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  use_a = use_a || (key_a >= rule[nt][i].begin && key_a < rule[nt][i].end);
-                  use_b = use_b || (key_b >= rule[nt][i].begin && key_b < rule[nt][i].end);
-                }
-            }
+            // (masked: a row that none of this lane's query rows sees may hold
+            // anything)
+            const bool use_a = MASK ? see_a : key_a < L, use_b = MASK ? see_b : key_b < L;
             vpa = use_a ? vs_row[kq * kSub + g] : 0.0f;
             vpb = use_b ? vs_row[kq * kSub + g + 8] : 0.0f;
           }
@@ -963,12 +964,33 @@ __global__ void __launch_bounds__(288, MINB)
     const int W = a.window;
     // (padding rows take row 0's rule: their scores only feed their own
     // unwritten outputs)
-    dev::RowRule ru0{}, ru1{};
+    // Sub-tiles inside [f_lo, f_hi) need no mask for any row of the group and,
+    // under a bias, have linear distances: pos - d0 - key as e - (key - k0),
+    // exact in fp32 wherever a weight is not 0.  The others go by the rules in
+    // shared memory (the key warps write the same; all of them have left the
+    // previous piece), where e and ns are kept too.
+    int f_lo = 0, f_hi = 0;
+    dev::RowRule* rules = s_rule + rg * 8;
+    float4* lines = reinterpret_cast<float4*>(s_rule + a.row_groups * 8) + rg * 4;  // [row pair] e, ns, e, ns
     if constexpr (MASK) {
       const int q0 = r0 < rows ? r0 : 0, q1 = r1 < rows ? r1 : 0;
       const int t0 = dev::div_small(q0, inv_g), t1 = dev::div_small(q1, inv_g);
-      ru0 = dev::row_rule(a, tok0 + t0, a.vseq[b].pos0 + t0, h * G + q0 - t0 * G, L);
-      ru1 = dev::row_rule(a, tok0 + t1, a.vseq[b].pos0 + t1, h * G + q1 - t1 * G, L);
+      const dev::RowRule ru0 = dev::row_rule(a, tok0 + t0, a.vseq[b].pos0 + t0, h * G + q0 - t0 * G, L);
+      const dev::RowRule ru1 = dev::row_rule(a, tok0 + t1, a.vseq[b].pos0 + t1, h * G + q1 - t1 * G, L);
+      if (g == 0) {
+        rules[2 * c] = ru0;
+        rules[2 * c + 1] = ru1;
+        lines[c] = make_float4((float)(ru0.pos - ru0.d0 - k0), ru0.ns, (float)(ru1.pos - ru1.d0 - k0), ru1.ns);
+      }
+      f_lo = max(ru0.begin, ru1.begin);
+      f_hi = min(ru0.end, ru1.end);
+      if (a.slopes) f_hi = min(f_hi, min(ru0.pos, ru1.pos) + 1);
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        f_lo = max(f_lo, __shfl_xor_sync(0xffffffffu, f_lo, o));
+        f_hi = min(f_hi, __shfl_xor_sync(0xffffffffu, f_hi, o));
+      }
+      __syncwarp();
     }
 
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
@@ -1080,20 +1102,24 @@ __global__ void __launch_bounds__(288, MINB)
         // keep finite scores, which only feed their own unwritten outputs
         bool use_a = key_a < L, use_b = key_b < L, full = true;
         if constexpr (MASK) {
-          if (a.slopes) {
-            x[0] = fmaf(ru0.ns, (float)(abs(ru0.pos - key_a) - ru0.d0), x[0]);
-            x[1] = fmaf(ru1.ns, (float)(abs(ru1.pos - key_a) - ru1.d0), x[1]);
-            x[2] = fmaf(ru0.ns, (float)(abs(ru0.pos - key_b) - ru0.d0), x[2]);
-            x[3] = fmaf(ru1.ns, (float)(abs(ru1.pos - key_b) - ru1.d0), x[3]);
-          }
-          full = kb >= max(ru0.begin, ru1.begin) && kb + kSub <= min(ru0.end, ru1.end);
-          if (!full) {
-            const bool va0 = key_a >= ru0.begin && key_a < ru0.end, va1 = key_a >= ru1.begin && key_a < ru1.end;
-            const bool vb0 = key_b >= ru0.begin && key_b < ru0.end, vb1 = key_b >= ru1.begin && key_b < ru1.end;
-            x[0] = va0 ? x[0] : -INFINITY;
-            x[1] = va1 ? x[1] : -INFINITY;
-            x[2] = vb0 ? x[2] : -INFINITY;
-            x[3] = vb1 ? x[3] : -INFINITY;
+          full = kb >= f_lo && kb + kSub <= f_hi;  // the same in every lane
+          if (full) {
+            if (a.slopes) {
+              const float4 ln = lines[c];
+              const float ka = (float)(key_a - k0), kb8 = ka + 8.0f;
+              x[0] = fmaf(ln.y, ln.x - ka, x[0]);
+              x[1] = fmaf(ln.w, ln.z - ka, x[1]);
+              x[2] = fmaf(ln.y, ln.x - kb8, x[2]);
+              x[3] = fmaf(ln.w, ln.z - kb8, x[3]);
+            }
+          } else {
+            const dev::RowRule ru0 = rules[2 * c], ru1 = rules[2 * c + 1];
+            const bool bias = a.slopes != nullptr;
+            bool va0, va1, vb0, vb1;
+            x[0] = dev::rule_score(ru0, x[0], key_a, bias, va0);
+            x[1] = dev::rule_score(ru1, x[1], key_a, bias, va1);
+            x[2] = dev::rule_score(ru0, x[2], key_b, bias, vb0);
+            x[3] = dev::rule_score(ru1, x[3], key_b, bias, vb1);
             // the V row of a key that neither of this lane's query rows sees
             // may hold anything: its scales are not used
             use_a = va0 || va1;
@@ -1232,7 +1258,7 @@ __global__ void __launch_bounds__(288, MINB)
           }
         };
         if constexpr (DT == KVQ_FP8_E4M3) {
-          const bool plain = MASK ? __all_sync(0xffffffffu, full) : kb + kSub <= L;
+          const bool plain = MASK ? full : kb + kSub <= L;
           if (plain) pv(dev::Flag<false>{}); else pv(dev::Flag<true>{});
         } else {
           pv(dev::Flag<false>{});
@@ -1368,11 +1394,16 @@ cudaError_t dispatch_decode(int head_dim, int nt, const CUtensorMap* tk, const C
   };
   auto by_nt = [&](auto dtag) -> cudaError_t {
     constexpr int d = decltype(dtag)::value;
-    if (nt == 0) return go(KernelCfg<d, d == 256 ? 1 : 2, 0>{});
-    if (nt == -32) return go(KernelCfg<d, d == 256 ? 1 : 2, 0, 32>{});
-    if (nt == -64) return go(KernelCfg<d, d == 256 ? 1 : 2, 0, 64>{});
+    // head_dim 128: 96 registers for two CTAs of nine warps (four of five);
+    // the masked instances need a few more, and spilled inside the loop, past
+    // the little L1 that the stages leave: with them three CTAs of five warps
+    // fit, and a ragged fp8 batch of 575 MB took 115 us instead of 288
+    constexpr int mb = d == 256 || (RULE > 0 && d == 128) ? 1 : 2;
+    if (nt == 0) return go(KernelCfg<d, mb, 0>{});
+    if (nt == -32) return go(KernelCfg<d, mb, 0, 32>{});
+    if (nt == -64) return go(KernelCfg<d, mb, 0, 64>{});
     if constexpr (d >= 128) {
-      if (nt == -128) return go(KernelCfg<d, d == 256 ? 1 : 2, 0, 128>{});
+      if (nt == -128) return go(KernelCfg<d, mb, 0, 128>{});
     }
     if constexpr (wide_ok<DT, d>()) {
       if (nt == 2) return go(KernelCfg<d, 1, 2>{});

@@ -540,7 +540,8 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         if constexpr (MASK) {
           // a row with no token sees the piece's keys with no bias: finite
           // scores that feed only its own unwritten output
-          ru = dev::RowRule{0, L, 0, 0, 0.0f};
+          ru = dev::RowRule{};
+          ru.end = L;
           if (valid) ru = dev::row_rule(a, tok0 + t_row, a.vseq[b].pos0 + t_row, h * G + (r - t_row * G), L);
         } else {
           pos = valid ? L - T + t_row : -1;

@@ -231,30 +231,52 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 // gather of rows of Dp bytes and a dense, page-wise store, so bound by HBM
 // (kept rows read once, written once).  The units are `rows` consecutive
 // destination rows of one (sequence, kv head); a CTA takes units grid apart,
-// one a round, through a ring of shared-memory stages: one bulk copy per row
-// and side in (cp.async.bulk, completion on the stage's mbarrier; 4-byte
-// scales and weights by cp.async beside them), one bulk copy per page run and
-// side out.  Data never passes through registers, and the loads of the next
-// rounds are in flight while a round waits and stores.
+// one a round, through a ring of shared-memory stages.
 //
 // In place, a unit's destination rows may hold rows that its own or an earlier
 // unit of the same (sequence, kv head) has yet to read -- never a later one's,
 // whose sources lie at or behind its own destination.  Units are numbered so
 // that earlier chunks come in the same or an earlier round; a round's stores
 // therefore wait until every CTA has loaded its unit of that round (a counter
-// per round, all CTAs resident: a cooperative launch).  Every wait is bounded.
+// per round, all CTAs resident: a cooperative launch).  The loads of later
+// rounds need no wait, so they are in flight meanwhile.  Every wait is bounded.
+//
+// Roles, so that no latency of a round stands behind another's (with one group
+// of threads doing all of it in turn, 4 heads of 131,072 kept rows of 520
+// bytes took 197 us):
+//   warps 0-3  load: 16-byte cp.async per chunk of a row, 4-byte ones for the
+//              scales and weights; the kept rows and pages of the next two
+//              units are looked up meanwhile
+//   warps 4-7  store: shared memory -> destination pages
+//   warp 8     reports this CTA's loaded rounds
+//   warp 9     waits for a round's reports and lets the stores go
+constexpr int kLoaders = 128, kStorers = 128;
+
+// What the storers need to know of a stage's unit.
+struct CompactUnit {
+  int n;  // rows to move (0: none)
+};
 
 __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const CompactArgs a) {
   extern __shared__ __align__(128) uint8_t cmp_smem[];
-  const int tid = threadIdx.x;
-  __shared__ __align__(8) uint64_t bar[kCompactStages];
-  __shared__ int s_ok;
+  __shared__ long long s_src[2][kCompactRows];               // source rows of a unit, -1: none
+  __shared__ long long s_dst[kCompactStages][kCompactRows];  // destination rows
+  __shared__ CompactUnit s_unit[kCompactStages];
+  __shared__ int s_moves[2];                                 // some row of the unit is not in its place
+  __shared__ __align__(8) uint64_t full[kCompactStages], empty[kCompactStages], go[kCompactStages];
+  __shared__ int s_stop;                                     // a wait gave up: nothing is stored from there on
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = a.stages;
   if (tid == 0) {
-    // every thread arrives twice: with its bulk bytes, and for its small copies
-    for (int s = 0; s < S; ++s) ptx::mbar_init(&bar[s], 2 * kCompactThreads);
+    for (int s = 0; s < S; ++s) {
+      // a loader arrives twice: itself, and behind its copies
+      ptx::mbar_init(&full[s], 2 * kLoaders);
+      ptx::mbar_init(&empty[s], kStorers / 32);
+      ptx::mbar_init(&go[s], 1);
+    }
     ptx::fence_mbar_init();
-    s_ok = 1;
+    s_stop = 0;
+    s_moves[0] = s_moves[1] = 0;
   }
   __syncthreads();
   ptx::griddep_wait();
@@ -263,136 +285,180 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Co
   const int code_bytes = a.rows * a.row_bytes;  // one side of a stage
   const int nf = a.n_scale[0] + a.n_scale[1] + (a.mass ? 1 : 0);
   const int cap = a.max_blocks_per_seq << a.log2_bs;
-
-  // unit of round k: its (sequence, kv head), first destination row and count
-  // (0: nothing to move)
-  auto unit = [&](int k, int& b, int& h, int& i0, int& n) {
-    const long long u = (long long)k * gridDim.x + blockIdx.x;
-    n = 0;
-    b = h = i0 = 0;
-    if (u >= a.units) return;
-    const int chunk = (int)(u / segs), seg = (int)(u - (long long)chunk * segs);
-    b = seg / a.num_kv_heads;
-    h = seg - b * a.num_kv_heads;
-    i0 = chunk << a.log2_rows;
-    n = min(a.rows, min(a.kept_lens[b], a.budget) - i0);
-    if (n <= 0) {
-      n = 0;
-      return;
-    }
-    // ascending rows whose last is in its place all are
-    if (a.in_place && a.keep[(size_t)seg * a.budget + i0 + n - 1] == i0 + n - 1) n = 0;
-  };
-  // [block, kv head, row] index of position p of sequence b, or -1
-  auto row_of = [&](const int32_t* table, int b, int h, int p, unsigned int flag) -> long long {
-    if (p < 0 || p >= cap) {
-      atomicOr(a.err, flag);
-      return -1;
-    }
-    const int id = table[(size_t)b * a.max_blocks_per_seq + (p >> a.log2_bs)];
-    if (id < 0 || id >= a.num_blocks) {
-      atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
-      return -1;
-    }
-    return ((long long)id * a.num_kv_heads + h) * a.block_size + (p & (a.block_size - 1));
-  };
-
-  auto issue = [&](int k) {
-    const int s = k % S;
-    uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
-    int b, h, i0, n;
-    unit(k, b, h, i0, n);
-    const int32_t* keep = a.keep + ((size_t)b * a.num_kv_heads + h) * a.budget + i0;
-    // at most kCompactRows rows of two sides: kItems (row, side) pairs a thread
-    constexpr int kItems = 2 * kCompactRows / kCompactThreads;
-    long long src[kItems];
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int it = tid + i * kCompactThreads, r = it & (a.rows - 1);
-      src[i] = -1;
-      if (it < a.rows * a.sides && r < n) src[i] = row_of(a.block_table, b, h, keep[r], KVQ_DEVERR_KEEP_INDEX);
-      if (src[i] >= 0) bytes += (uint32_t)a.row_bytes;
-    }
-    ptx::mbar_expect_tx(&bar[s], bytes);
-    float* f = reinterpret_cast<float*>(st + a.sides * code_bytes);
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      if (src[i] < 0) continue;
-      const int it = tid + i * kCompactThreads, r = it & (a.rows - 1), side = it >> a.log2_rows;
-      ptx::bulk_load(st + side * code_bytes + r * a.row_bytes, a.codes[side] + (size_t)src[i] * a.row_bytes,
-                     (uint32_t)a.row_bytes, &bar[s]);
-      const int ns = a.n_scale[side];
-      for (int j = 0; j < ns; ++j)
-        ptx::cp_async4(f + (side * a.n_scale[0] + j) * a.rows + r, a.scale[side] + (size_t)src[i] * ns + j);
-      if (side == 0 && a.mass) ptx::cp_async4(f + (nf - 1) * a.rows + r, a.mass + src[i]);
-    }
-    ptx::cp_async_arrive(&bar[s]);
-    ptx::mbar_arrive(&bar[s]);
-  };
-
-  for (int k = 0; k < S - 1 && k < rounds; ++k) issue(k);
-  bool ok = true;
-  for (int k = 0; k < rounds; ++k) {
-    const int s = k % S;
-    if (!ptx::mbar_wait_bounded(&bar[s], (uint32_t)(k / S) & 1u)) {
+  const int row_chunks = a.row_bytes / 16, unit_chunks = row_chunks * a.sides;  // 16-byte chunks of a row, of both sides
+  const float inv_chunks = 1.0f / (float)unit_chunks;
+  volatile int* stop = &s_stop;
+  auto wait = [&](uint64_t* bar, int k) {  // the phase of round k
+    if (!*stop && !ptx::mbar_wait_bounded(bar, (uint32_t)(k / S) & 1u)) {
       atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
-      s_ok = 0;
+      *stop = 1;
     }
-    __syncthreads();  // the whole unit is in shared memory
-    int b, h, i0, n;
-    unit(k, b, h, i0, n);
-    if (a.in_place) {
-      if (tid == 0) {
-        ptx::red_release_add(&a.round_count[k], 1u);
-        if (n > 0 && s_ok) {
-          const uint64_t t0 = ptx::globaltimer_ns();
-          uint32_t i = 0;
-          while (ptx::ld_acquire(&a.round_count[k]) < gridDim.x) {
-            if ((++i & 63u) == 0u && ptx::globaltimer_ns() - t0 > ptx::kWaitLimitNs) {
-              atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
-              s_ok = 0;
-              break;
-            }
+  };
+  // chunk i of a unit: row, and byte offset in a row of the side it is on
+  auto chunk = [&](int i, int& r, int& side, int& off) {
+    r = (int)(((float)i + 0.5f) * inv_chunks);  // exact: i < 2^16, the quotient 2^-7 away from an integer
+    const int c = i - r * unit_chunks;
+    side = c >= row_chunks ? 1 : 0;
+    off = (c - side * row_chunks) * 16;
+  };
+
+  if (warp < 4) {
+    // ============================================================== loaders
+    // unit of round k: (sequence, kv head) and first destination row; false past the last
+    auto unit = [&](int k, int& b, int& h, int& i0) -> bool {
+      const long long u = (long long)k * gridDim.x + blockIdx.x;
+      if (k >= rounds || u >= a.units) return false;
+      const int chunk_i = (int)(u / segs), seg = (int)(u - (long long)chunk_i * segs);
+      b = seg / a.num_kv_heads;
+      h = seg - b * a.num_kv_heads;
+      i0 = chunk_i << a.log2_rows;
+      return true;
+    };
+    // this thread's row of a unit, looked up in two steps
+    struct Look {
+      int p, n;        // source position; rows of the unit
+      int src, dst;    // their pages (-1: none)
+    };
+    auto look_keep = [&](int k) -> Look {
+      Look l{-1, 0, -1, -1};
+      int b, h, i0;
+      if (!unit(k, b, h, i0)) return l;
+      l.n = max(0, min(a.rows, min(a.kept_lens[b], a.budget) - i0));
+      if (tid < l.n) l.p = a.keep[((size_t)b * a.num_kv_heads + h) * a.budget + i0 + tid];
+      return l;
+    };
+    auto look_pages = [&](int k, Look& l) {
+      int b, h, i0;
+      if (!unit(k, b, h, i0) || tid >= l.n) return;
+      if (l.p < 0 || l.p >= cap) {
+        atomicOr(a.err, KVQ_DEVERR_KEEP_INDEX);
+        l.p = -1;
+      } else {
+        l.src = a.block_table[(size_t)b * a.max_blocks_per_seq + (l.p >> a.log2_bs)];
+      }
+      // (budget <= capacity: i0 + tid is inside the table)
+      l.dst = a.dst_table[(size_t)b * a.max_blocks_per_seq + ((i0 + tid) >> a.log2_bs)];
+    };
+    auto row_at = [&](int id, int h, int p) -> long long {
+      if (id < 0 || id >= a.num_blocks) {
+        atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
+        return -1;
+      }
+      return ((long long)id * a.num_kv_heads + h) * a.block_size + (p & (a.block_size - 1));
+    };
+
+    Look cur = look_keep(0);
+    look_pages(0, cur);
+    Look next = look_keep(1);
+    for (int k = 0; k < rounds; ++k) {
+      const int s = k % S, par = k & 1;
+      uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
+      if (k >= S) wait(&empty[s], k - S);
+      int b = 0, h = 0, i0 = 0;
+      unit(k, b, h, i0);
+      if (tid < a.rows) {
+        const bool in = tid < cur.n;
+        s_src[par][tid] = in && cur.p >= 0 ? row_at(cur.src, h, cur.p) : -1;
+        s_dst[s][tid] = in ? row_at(cur.dst, h, i0 + tid) : -1;
+        if (in && (!a.in_place || cur.p != i0 + tid)) s_moves[par] = 1;
+      }
+      ptx::named_bar_sync(1, kLoaders);
+      // a unit whose rows all lie in their place is left alone
+      const int n = s_moves[par] && !*stop ? cur.n : 0;
+      for (int i = tid; i < n * unit_chunks; i += kLoaders) {
+        int r, side, off;
+        chunk(i, r, side, off);
+        const long long row = s_src[par][r];
+        if (row >= 0)
+          ptx::cp_async16(st + side * code_bytes + r * a.row_bytes + off, a.codes[side] + (size_t)row * a.row_bytes + off);
+      }
+      if (tid < n && nf > 0) {
+        const long long row = s_src[par][tid];
+        float* f = reinterpret_cast<float*>(st + a.sides * code_bytes) + tid;
+        if (row >= 0) {
+          for (int side = 0; side < a.sides; ++side)
+            for (int j = 0; j < a.n_scale[side]; ++j, f += a.rows)
+              ptx::cp_async4(f, a.scale[side] + (size_t)row * a.n_scale[side] + j);
+          if (a.mass) ptx::cp_async4(f, a.mass + row);
+        }
+      }
+      if (tid == 0) s_unit[s].n = n;
+      ptx::cp_async_arrive(&full[s]);
+      ptx::mbar_arrive(&full[s]);
+      // the next units' rows, while the copies fly
+      cur = next;
+      look_pages(k + 1, cur);
+      next = look_keep(k + 2);
+      ptx::named_bar_sync(1, kLoaders);  // everyone has read s_moves[par]
+      if (tid == 0) s_moves[par] = 0;
+    }
+  } else if (warp < 8) {
+    // ============================================================== storers
+    const int t = tid - kLoaders;
+    for (int k = 0; k < rounds; ++k) {
+      const int s = k % S;
+      const uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
+      wait(&full[s], k);
+      if (a.in_place) wait(&go[s], k);
+      const int n = *stop ? 0 : s_unit[s].n;
+      const int items = n * unit_chunks;
+      for (int i0 = t; i0 < items; i0 += 4 * kStorers) {
+        uint4 v[4];
+        uint8_t* dst[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * kStorers;
+          dst[j] = nullptr;
+          if (i < items) {
+            int r, side, off;
+            chunk(i, r, side, off);
+            v[j] = *reinterpret_cast<const uint4*>(st + side * code_bytes + r * a.row_bytes + off);
+            const long long row = s_dst[s][r];
+            if (row >= 0) dst[j] = a.codes[side] + (size_t)row * a.row_bytes + off;
           }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (dst[j]) *reinterpret_cast<uint4*>(dst[j]) = v[j];
       }
-      __syncthreads();
-    }
-    ok = s_ok != 0;
-    if (n > 0 && ok) {
-      const uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
-      // runs of rows in one destination page
-      const int run = min(a.rows, a.block_size), runs = (n + run - 1) / run;
-      asm volatile("fence.proxy.async;" ::: "memory");
-      for (int it = tid; it < runs * a.sides; it += kCompactThreads) {
-        const int side = it / runs, r0 = (it - side * runs) * run;
-        const long long row = row_of(a.dst_table, b, h, i0 + r0, KVQ_DEVERR_KEEP_INDEX);
-        if (row >= 0)
-          ptx::bulk_store(a.codes[side] + (size_t)row * a.row_bytes, st + side * code_bytes + r0 * a.row_bytes,
-                          (uint32_t)(min(run, n - r0) * a.row_bytes));
-      }
-      if (nf > 0) {
-        const float* f = reinterpret_cast<const float*>(st + a.sides * code_bytes);
-        for (int r = tid; r < n; r += kCompactThreads) {
-          const long long row = row_of(a.dst_table, b, h, i0 + r, KVQ_DEVERR_KEEP_INDEX);
-          if (row < 0) continue;
+      if (t < n && nf > 0) {
+        const long long row = s_dst[s][t];
+        const float* f = reinterpret_cast<const float*>(st + a.sides * code_bytes) + t;
+        if (row >= 0) {
           for (int side = 0; side < a.sides; ++side)
-            for (int j = 0; j < a.n_scale[side]; ++j)
-              a.scale[side][(size_t)row * a.n_scale[side] + j] = f[(side * a.n_scale[0] + j) * a.rows + r];
-          if (a.mass) a.mass[row] = f[(nf - 1) * a.rows + r];
+            for (int j = 0; j < a.n_scale[side]; ++j, f += a.rows)
+              a.scale[side][(size_t)row * a.n_scale[side] + j] = *f;
+          if (a.mass) a.mass[row] = *f;
         }
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&empty[s]);
     }
-    ptx::bulk_commit();
-    if (k + S - 1 < rounds) {
-      // stage (k - 1) % S takes round k + S - 1: its stores have read it
-      ptx::bulk_wait_read<1>();
-      __syncthreads();
-      issue(k + S - 1);
+  } else if (a.in_place && lane == 0) {
+    for (int k = 0; k < rounds; ++k) {
+      const int s = k % S;
+      if (warp == 8) {
+        // ======================================================== reporter
+        // (the copies' completion is observed through the barrier; the add
+        // releases it to whoever reads the full count)
+        wait(&full[s], k);
+        ptx::red_release_add(&a.round_count[k], 1u);
+      } else {
+        // ========================================================== poller
+        // Round k's count is full only once this CTA has loaded its own unit,
+        // hence freed the stage of round k - S: `go` is never a phase ahead.
+        const uint64_t t0 = ptx::globaltimer_ns();
+        uint32_t i = 0;
+        while (!*stop && ptx::ld_acquire(&a.round_count[k]) < gridDim.x) {
+          if ((++i & 63u) == 0u && ptx::globaltimer_ns() - t0 > ptx::kWaitLimitNs) {
+            atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+            *stop = 1;
+          }
+        }
+        ptx::mbar_arrive(&go[s]);
+      }
     }
   }
-  ptx::bulk_wait_all();
 }
 
 }  // namespace

@@ -17,10 +17,19 @@ namespace dev {
 // the softmax as it is and keeps the biases of the keys that matter near 0,
 // where fp32 resolves them, however far from the query they lie; the combine
 // puts ns * d0 back into the log-sum-exp.
-struct RowRule {
+struct __align__(16) RowRule {
   int begin, end, pos, d0;
   float ns;
+  int pad[3];
 };
+
+// The score x of `key` under a row's rule, key by key: the slow form, for
+// tiles that some row does not see whole or that reach past a position.
+__device__ __forceinline__ float rule_score(const RowRule& r, float x, int key, bool bias, bool& seen) {
+  if (bias) x = fmaf(r.ns, (float)(abs(r.pos - key) - r.d0), x);
+  seen = key >= r.begin && key < r.end;
+  return seen ? x : -INFINITY;
+}
 
 // tok: index of the row's token in [B, C]; hi: one past the last key loaded.
 __device__ __forceinline__ void row_range(const int32_t* key_begin, const int32_t* key_end, int window, size_t tok,
@@ -38,7 +47,7 @@ __device__ __forceinline__ int row_anchor(float slope, int pos, int begin, int e
 }
 
 __device__ __forceinline__ RowRule row_rule(const DecodeArgs& a, size_t tok, int pos, int hq, int hi) {
-  RowRule r;
+  RowRule r{};
   r.pos = pos;
   row_range(a.key_begin, a.key_end, a.window, tok, pos, hi, r.begin, r.end);
   r.ns = 0.0f;
