@@ -983,7 +983,7 @@ kvq_status check_evict(const kvq_evict_params* p) {
 
 // Launch shape of kvq_evict_compact: units of up to 128 rows and kUnitBytes,
 // two CTAs per SM with as many ring stages as fit.
-constexpr int kUnitBytes = 16 * 1024;
+constexpr int kUnitBytes = 32 * 1024;
 struct CompactPlan {
   int rows, stages, stage_bytes, grid, units;
   size_t smem, ws;
@@ -1000,7 +1000,7 @@ kvq_status compact_plan(const kvq_cache* c, const kvq_evict_params* p, bool mass
   while (P.rows > 16 && P.rows * rb * sides > kUnitBytes) P.rows >>= 1;
   P.stage_bytes = (P.rows * (rb * sides + 4 * nf) + 127) / 128 * 128;
   constexpr int kCtas = 2;
-  const int budget = 228 * 1024 / kCtas - 1024 - 12 * 1024;  // (beside the kernel's own 11 KB)
+  const int budget = 228 * 1024 / kCtas - 1024 - 9 * 1024;  // (beside the kernel's own 8.5 KB)
   P.stages = budget / P.stage_bytes;
   P.stages = P.stages > kCompactStages ? kCompactStages : P.stages;
   if (P.stages < 2) return KVQ_ERR_UNSUPPORTED;

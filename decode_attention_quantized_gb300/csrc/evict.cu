@@ -243,40 +243,40 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 //
 // Roles, so that no latency of a round stands behind another's (with one group
 // of threads doing all of it in turn, 4 heads of 131,072 kept rows of 520
-// bytes took 197 us):
-//   warps 0-3  load: 16-byte cp.async per chunk of a row, 4-byte ones for the
-//              scales and weights; the kept rows and pages of the next two
-//              units are looked up meanwhile
-//   warps 4-7  store: shared memory -> destination pages
-//   warp 8     reports this CTA's loaded rounds
-//   warp 9     waits for a round's reports and lets the stores go
-constexpr int kLoaders = 128, kStorers = 128;
-
-// What the storers need to know of a stage's unit.
-struct CompactUnit {
-  int n;  // rows to move (0: none)
-};
+// bytes took 197 us; with the look-ups in the loading warps 119):
+//   warps 0-3   load: 16-byte cp.async per chunk of a row, 4-byte ones for the
+//               scales and weights
+//   warps 4-7   store: shared memory -> destination pages
+//   warps 8-11  look up the kept rows and pages of the units ahead
+//   warp 12     reports this CTA's loaded rounds
+//   warp 13     waits for a round's reports and lets the stores go
+constexpr int kRole = 128;    // threads of a loading, storing or looking-up role
+constexpr int kLookAhead = 8; // units looked up ahead
 
 __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const CompactArgs a) {
   extern __shared__ __align__(128) uint8_t cmp_smem[];
-  __shared__ long long s_src[2][kCompactRows];               // source rows of a unit, -1: none
-  __shared__ long long s_dst[kCompactStages][kCompactRows];  // destination rows
-  __shared__ CompactUnit s_unit[kCompactStages];
-  __shared__ int s_moves[2];                                 // some row of the unit is not in its place
+  // looked-up units, by round mod kLookAhead: cache slots (block * block size
+  // + row) of the rows' sources and destinations, -1: none
+  __shared__ int s_src[kLookAhead][kCompactRows], s_dst[kLookAhead][kCompactRows];
+  __shared__ int s_n[kLookAhead], s_h[kLookAhead];  // rows to move (0: none), kv head
+  __shared__ __align__(8) uint64_t look_full[kLookAhead], look_empty[kLookAhead];
   __shared__ __align__(8) uint64_t full[kCompactStages], empty[kCompactStages], go[kCompactStages];
-  __shared__ int s_stop;                                     // a wait gave up: nothing is stored from there on
+  __shared__ int s_stop;  // a wait gave up: nothing is stored from there on
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = a.stages;
   if (tid == 0) {
+    for (int q = 0; q < kLookAhead; ++q) {
+      ptx::mbar_init(&look_full[q], kRole);
+      ptx::mbar_init(&look_empty[q], kRole / 32);
+    }
     for (int s = 0; s < S; ++s) {
       // a loader arrives twice: itself, and behind its copies
-      ptx::mbar_init(&full[s], 2 * kLoaders);
-      ptx::mbar_init(&empty[s], kStorers / 32);
+      ptx::mbar_init(&full[s], 2 * kRole);
+      ptx::mbar_init(&empty[s], kRole / 32);
       ptx::mbar_init(&go[s], 1);
     }
     ptx::fence_mbar_init();
     s_stop = 0;
-    s_moves[0] = s_moves[1] = 0;
   }
   __syncthreads();
   ptx::griddep_wait();
@@ -284,164 +284,137 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Co
   const int rounds = (a.units + (int)gridDim.x - 1) / (int)gridDim.x;
   const int code_bytes = a.rows * a.row_bytes;  // one side of a stage
   const int nf = a.n_scale[0] + a.n_scale[1] + (a.mass ? 1 : 0);
-  const int cap = a.max_blocks_per_seq << a.log2_bs;
   const int row_chunks = a.row_bytes / 16, unit_chunks = row_chunks * a.sides;  // 16-byte chunks of a row, of both sides
-  const float inv_chunks = 1.0f / (float)unit_chunks;
   volatile int* stop = &s_stop;
-  auto wait = [&](uint64_t* bar, int k) {  // the phase of round k
-    if (!*stop && !ptx::mbar_wait_bounded(bar, (uint32_t)(k / S) & 1u)) {
+  auto wait = [&](uint64_t* bar, int phase) {
+    if (!*stop && !ptx::mbar_wait_bounded(bar, (uint32_t)phase & 1u)) {
       atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
       *stop = 1;
     }
   };
-  // chunk i of a unit: row, and byte offset in a row of the side it is on
-  auto chunk = [&](int i, int& r, int& side, int& off) {
-    r = (int)(((float)i + 0.5f) * inv_chunks);  // exact: i < 2^16, the quotient 2^-7 away from an integer
-    const int c = i - r * unit_chunks;
-    side = c >= row_chunks ? 1 : 0;
-    off = (c - side * row_chunks) * 16;
+  // [block, kv head, row] index of a cache slot
+  auto row_at = [&](int slot, int h) -> size_t {
+    return (((size_t)(slot >> a.log2_bs) * a.num_kv_heads + h) << a.log2_bs) + (slot & (a.block_size - 1));
+  };
+  // f(row, side, byte offset in the side's row) for this thread's 16-byte
+  // chunks of an n-row unit (t of kRole threads)
+  auto chunks = [&](int t, int n, auto f) {
+    const int dr = kRole / unit_chunks, dc = kRole - dr * unit_chunks;
+    int r = t / unit_chunks, c = t - r * unit_chunks;
+    while (r < n) {
+      const int side = c >= row_chunks ? 1 : 0;
+      f(r, side, (c - side * row_chunks) * 16);
+      r += dr;
+      c += dc;
+      if (c >= unit_chunks) {
+        c -= unit_chunks;
+        ++r;
+      }
+    }
   };
 
   if (warp < 4) {
     // ============================================================== loaders
-    // unit of round k: (sequence, kv head) and first destination row; false past the last
-    auto unit = [&](int k, int& b, int& h, int& i0) -> bool {
-      const long long u = (long long)k * gridDim.x + blockIdx.x;
-      if (k >= rounds || u >= a.units) return false;
-      const int chunk_i = (int)(u / segs), seg = (int)(u - (long long)chunk_i * segs);
-      b = seg / a.num_kv_heads;
-      h = seg - b * a.num_kv_heads;
-      i0 = chunk_i << a.log2_rows;
-      return true;
-    };
-    // this thread's row of a unit, looked up in two steps
-    struct Look {
-      int p, n;        // source position; rows of the unit
-      int src, dst;    // their pages (-1: none)
-    };
-    auto look_keep = [&](int k) -> Look {
-      Look l{-1, 0, -1, -1};
-      int b, h, i0;
-      if (!unit(k, b, h, i0)) return l;
-      l.n = max(0, min(a.rows, min(a.kept_lens[b], a.budget) - i0));
-      if (tid < l.n) l.p = a.keep[((size_t)b * a.num_kv_heads + h) * a.budget + i0 + tid];
-      return l;
-    };
-    auto look_pages = [&](int k, Look& l) {
-      int b, h, i0;
-      if (!unit(k, b, h, i0) || tid >= l.n) return;
-      if (l.p < 0 || l.p >= cap) {
-        atomicOr(a.err, KVQ_DEVERR_KEEP_INDEX);
-        l.p = -1;
-      } else {
-        l.src = a.block_table[(size_t)b * a.max_blocks_per_seq + (l.p >> a.log2_bs)];
+    for (int k = 0; k < rounds; ++k) {
+      const int s = k % S, q = k % kLookAhead;
+      uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
+      wait(&look_full[q], k / kLookAhead);
+      if (k >= S) wait(&empty[s], k / S - 1);
+      const int n = *stop ? 0 : s_n[q], h = s_h[q];
+      chunks(tid, n, [&](int r, int side, int off) {
+        const int slot = s_src[q][r];
+        if (slot >= 0)
+          ptx::cp_async16(st + side * code_bytes + r * a.row_bytes + off,
+                          a.codes[side] + row_at(slot, h) * a.row_bytes + off);
+      });
+      if (tid < n && nf > 0 && s_src[q][tid] >= 0) {
+        const size_t row = row_at(s_src[q][tid], h);
+        float* f = reinterpret_cast<float*>(st + a.sides * code_bytes) + tid;
+        for (int side = 0; side < a.sides; ++side)
+          for (int j = 0; j < a.n_scale[side]; ++j, f += a.rows)
+            ptx::cp_async4(f, a.scale[side] + row * a.n_scale[side] + j);
+        if (a.mass) ptx::cp_async4(f, a.mass + row);
       }
-      // (budget <= capacity: i0 + tid is inside the table)
-      l.dst = a.dst_table[(size_t)b * a.max_blocks_per_seq + ((i0 + tid) >> a.log2_bs)];
-    };
-    auto row_at = [&](int id, int h, int p) -> long long {
+      ptx::cp_async_arrive(&full[s]);
+      ptx::mbar_arrive(&full[s]);
+    }
+  } else if (warp < 8) {
+    // ============================================================== storers
+    const int t = tid - kRole;
+    for (int k = 0; k < rounds; ++k) {
+      const int s = k % S, q = k % kLookAhead;
+      const uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
+      wait(&full[s], k / S);
+      if (a.in_place) wait(&go[s], k / S);
+      const int n = *stop ? 0 : s_n[q], h = s_h[q];
+      chunks(t, n, [&](int r, int side, int off) {
+        const uint4 v = *reinterpret_cast<const uint4*>(st + side * code_bytes + r * a.row_bytes + off);
+        const int slot = s_dst[q][r];
+        if (slot >= 0) *reinterpret_cast<uint4*>(a.codes[side] + row_at(slot, h) * a.row_bytes + off) = v;
+      });
+      if (t < n && nf > 0 && s_dst[q][t] >= 0) {
+        const size_t row = row_at(s_dst[q][t], h);
+        const float* f = reinterpret_cast<const float*>(st + a.sides * code_bytes) + t;
+        for (int side = 0; side < a.sides; ++side)
+          for (int j = 0; j < a.n_scale[side]; ++j, f += a.rows) a.scale[side][row * a.n_scale[side] + j] = *f;
+        if (a.mass) a.mass[row] = *f;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&empty[s]);
+        ptx::mbar_arrive(&look_empty[q]);
+      }
+    }
+  } else if (warp < 12) {
+    // ============================================================= look-ups
+    const int r = tid - 2 * kRole;
+    const int cap = a.max_blocks_per_seq << a.log2_bs;
+    auto slot_of = [&](const int32_t* table, int b, int p) -> int {
+      const int id = table[(size_t)b * a.max_blocks_per_seq + (p >> a.log2_bs)];
       if (id < 0 || id >= a.num_blocks) {
         atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
         return -1;
       }
-      return ((long long)id * a.num_kv_heads + h) * a.block_size + (p & (a.block_size - 1));
+      return (id << a.log2_bs) + (p & (a.block_size - 1));
     };
-
-    Look cur = look_keep(0);
-    look_pages(0, cur);
-    Look next = look_keep(1);
     for (int k = 0; k < rounds; ++k) {
-      const int s = k % S, par = k & 1;
-      uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
-      if (k >= S) wait(&empty[s], k - S);
-      int b = 0, h = 0, i0 = 0;
-      unit(k, b, h, i0);
-      if (tid < a.rows) {
-        const bool in = tid < cur.n;
-        s_src[par][tid] = in && cur.p >= 0 ? row_at(cur.src, h, cur.p) : -1;
-        s_dst[s][tid] = in ? row_at(cur.dst, h, i0 + tid) : -1;
-        if (in && (!a.in_place || cur.p != i0 + tid)) s_moves[par] = 1;
-      }
-      ptx::named_bar_sync(1, kLoaders);
-      // a unit whose rows all lie in their place is left alone
-      const int n = s_moves[par] && !*stop ? cur.n : 0;
-      for (int i = tid; i < n * unit_chunks; i += kLoaders) {
-        int r, side, off;
-        chunk(i, r, side, off);
-        const long long row = s_src[par][r];
-        if (row >= 0)
-          ptx::cp_async16(st + side * code_bytes + r * a.row_bytes + off, a.codes[side] + (size_t)row * a.row_bytes + off);
-      }
-      if (tid < n && nf > 0) {
-        const long long row = s_src[par][tid];
-        float* f = reinterpret_cast<float*>(st + a.sides * code_bytes) + tid;
-        if (row >= 0) {
-          for (int side = 0; side < a.sides; ++side)
-            for (int j = 0; j < a.n_scale[side]; ++j, f += a.rows)
-              ptx::cp_async4(f, a.scale[side] + (size_t)row * a.n_scale[side] + j);
-          if (a.mass) ptx::cp_async4(f, a.mass + row);
-        }
-      }
-      if (tid == 0) s_unit[s].n = n;
-      ptx::cp_async_arrive(&full[s]);
-      ptx::mbar_arrive(&full[s]);
-      // the next units' rows, while the copies fly
-      cur = next;
-      look_pages(k + 1, cur);
-      next = look_keep(k + 2);
-      ptx::named_bar_sync(1, kLoaders);  // everyone has read s_moves[par]
-      if (tid == 0) s_moves[par] = 0;
-    }
-  } else if (warp < 8) {
-    // ============================================================== storers
-    const int t = tid - kLoaders;
-    for (int k = 0; k < rounds; ++k) {
-      const int s = k % S;
-      const uint8_t* st = cmp_smem + (size_t)s * a.stage_bytes;
-      wait(&full[s], k);
-      if (a.in_place) wait(&go[s], k);
-      const int n = *stop ? 0 : s_unit[s].n;
-      const int items = n * unit_chunks;
-      for (int i0 = t; i0 < items; i0 += 4 * kStorers) {
-        uint4 v[4];
-        uint8_t* dst[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = i0 + j * kStorers;
-          dst[j] = nullptr;
-          if (i < items) {
-            int r, side, off;
-            chunk(i, r, side, off);
-            v[j] = *reinterpret_cast<const uint4*>(st + side * code_bytes + r * a.row_bytes + off);
-            const long long row = s_dst[s][r];
-            if (row >= 0) dst[j] = a.codes[side] + (size_t)row * a.row_bytes + off;
+      const int q = k % kLookAhead;
+      if (k >= kLookAhead) wait(&look_empty[q], k / kLookAhead - 1);
+      // unit of round k: chunk-major over the (sequence, kv head) pairs
+      const long long u = (long long)k * gridDim.x + blockIdx.x;
+      int n = 0, h = 0;
+      if (u < a.units) {
+        const int chunk = (int)(u / segs), seg = (int)(u - (long long)chunk * segs);
+        const int b = seg / a.num_kv_heads, i = (chunk << a.log2_rows) + r;
+        h = seg - b * a.num_kv_heads;
+        // (both loads at once: entries of keep behind the kept ones are there)
+        const int p = r < a.rows && i < a.budget ? a.keep[(size_t)seg * a.budget + i] : -1;
+        n = min(a.rows, min(a.kept_lens[b], a.budget) - (chunk << a.log2_rows));
+        if (r < n) {
+          int src = -1;
+          if (p < 0 || p >= cap) atomicOr(a.err, KVQ_DEVERR_KEEP_INDEX);
+          else src = slot_of(a.block_table, b, p);
+          s_src[q][r] = src;
+          // (budget <= capacity: i is inside the table)
+          s_dst[q][r] = src >= 0 ? slot_of(a.dst_table, b, i) : -1;
+          if (r == n - 1) {
+            // ascending rows whose last is in its place all are
+            s_n[q] = a.in_place && p == i ? 0 : n;
+            s_h[q] = h;
           }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (dst[j]) *reinterpret_cast<uint4*>(dst[j]) = v[j];
       }
-      if (t < n && nf > 0) {
-        const long long row = s_dst[s][t];
-        const float* f = reinterpret_cast<const float*>(st + a.sides * code_bytes) + t;
-        if (row >= 0) {
-          for (int side = 0; side < a.sides; ++side)
-            for (int j = 0; j < a.n_scale[side]; ++j, f += a.rows)
-              a.scale[side][(size_t)row * a.n_scale[side] + j] = *f;
-          if (a.mass) a.mass[row] = *f;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&empty[s]);
+      if (n <= 0 && r == 0) s_n[q] = 0;
+      ptx::mbar_arrive(&look_full[q]);
     }
   } else if (a.in_place && lane == 0) {
     for (int k = 0; k < rounds; ++k) {
       const int s = k % S;
-      if (warp == 8) {
+      if (warp == 12) {
         // ======================================================== reporter
         // (the copies' completion is observed through the barrier; the add
         // releases it to whoever reads the full count)
-        wait(&full[s], k);
+        wait(&full[s], k / S);
         ptx::red_release_add(&a.round_count[k], 1u);
       } else {
         // ========================================================== poller

@@ -331,7 +331,7 @@ struct CompactArgs {
   unsigned int* round_count;   // [ceil(units / grid)], zero (in place)
   unsigned int* err;
 };
-constexpr int kCompactThreads = 320;
+constexpr int kCompactThreads = 448;
 constexpr int kCompactRows = 128;    // most rows of a unit
 constexpr int kCompactStages = 8;    // most ring stages
 cudaError_t launch_evict_compact(const CompactArgs& a, int grid, size_t smem, cudaStream_t stream);
