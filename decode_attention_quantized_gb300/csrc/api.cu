@@ -1358,6 +1358,7 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
   while (cluster < 16 && (rows > kHeld * cluster || (segs * cluster < dev->sms && rows / (2 * cluster) >= 2048)))
     cluster *= 2;
   if (segs * cluster > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
+  a.spread = segs * cluster <= 2 * dev->sms;
   return from_cuda(launch_evict_select(a, cluster, reinterpret_cast<cudaStream_t>(stream)));
 }
 

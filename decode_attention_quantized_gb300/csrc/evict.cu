@@ -13,35 +13,40 @@ namespace {
 // index order: a radix select of the threshold (the weight as an ordered
 // 32-bit key, four digits of 8 bits from the top, a histogram of the keys that
 // still match), then one ordered pass that writes every row above the
-// threshold and the first rows equal to it.
+// threshold and the first rows equal to it.  A digit whose matching keys are
+// all kept ends the search (24 bits tell most weights apart).
 //
 // A cluster of CTAs holds one (sequence, kv head): each warp reads a
 // contiguous stretch of the weights from global memory once and keeps it in
 // registers, so the passes touch no memory but the histogram.  Weights of one
 // head share a few exponents and may all be equal, so a histogram has a column
 // per lane (bank = lane): no two lanes of a warp ever meet, whatever the
-// values (with one 2048-bin histogram a CTA and its collisions the select of
-// 4 x 262,144 rows took 118 us, that of 512 heads of up to 131,072 rows
-// 1356 us).  The columns' sums meet through the cluster's shared memory, where
+// values.  The columns' sums meet through the cluster's shared memory, where
 // every CTA adds them up for itself: one cluster barrier a digit.  Integer
 // adds: their order cannot show.
+//
+// Bound by instructions and the latency of the passes, not by HBM (4 bytes a
+// row).  One 2048-bin histogram with its collisions took 118 us for 4 heads of
+// 262,144 rows (1356 us for 512 heads of up to 131,072 rows); 12-bit digits in
+// four copies 137 us, most of it in summing 4096 bins over 16 CTAs.
 
 constexpr int kSelWarps = kSelThreads / 32;
 
-// Ascending keys of ascending weights: -0 as +0, NaN below everything.
+// Ascending keys of ascending weights: -0 as +0, NaN (1) below everything; 0 is
+// no row's.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 0u;
   const uint32_t u = __float_as_uint(f + 0.0f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+  return f == f ? k : 1u;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectArgs a) {
-  __shared__ uint32_t hist[256 * 32];     // [bin][lane]
-  __shared__ uint32_t total[2][256];      // this CTA's counts of a digit (two passes' worth)
-  __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps], s_scan[8], s_digit[2], s_cta[2];
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(const SelectArgs a) {
+  __shared__ __align__(16) uint32_t hist[257 * 32];  // [bin][lane]; bin 256: keys that no longer match
+  __shared__ uint32_t total[2][256];                 // this CTA's counts of a digit (two passes' worth)
+  __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps], s_scan[8], s_digit[3], s_cta[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t cs = ptx::cluster_size(), rank = ptx::cluster_rank();
-  const int seg = (int)(blockIdx.x / cs);
+  const int cs = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
+  const int seg = (int)(blockIdx.x / (unsigned)cs);
   const int b = seg / a.num_kv_heads, h = seg - b * a.num_kv_heads;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -56,83 +61,100 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   const int need_all = a.budget - a.sinks - a.recent;
   const bool whole = L <= a.budget;
   if (whole || need_all == 0) {
-    for (int i = (int)rank * kSelThreads + tid; i < a.budget; i += (int)cs * kSelThreads)
+    for (int i = rank * kSelThreads + tid; i < a.budget; i += cs * kSelThreads)
       keep[i] = i >= n ? -1 : (whole || i < a.sinks ? i : L - a.budget + i);
     return;
   }
-  for (int i = (int)rank * kSelThreads + tid; i < a.sinks + a.recent; i += (int)cs * kSelThreads) {
+  for (int i = rank * kSelThreads + tid; i < a.sinks + a.recent; i += cs * kSelThreads) {
     if (i < a.sinks) keep[i] = i;
     else keep[need_all + i] = L - a.recent + (i - a.sinks);
   }
 
-  // this warp's stretch of the M rows between the ends: [w0, w0 + m), the
-  // stretches in (CTA, warp) order
+  // The M rows between the ends, in runs of 32 from a multiple of 32 on (so
+  // that a run meets one page, or two of 16 rows), go to as many CTAs as hold
+  // them in registers, or to all of the cluster when SMs are free; the others
+  // leave (a cluster barrier does not wait for CTAs that have left).
   const int M = L - a.sinks - a.recent;
-  const int warps = (int)cs * kSelWarps;
-  const int stretch = ((M + warps - 1) / warps + 31) & ~31;
-  const long long w0l = (long long)((int)rank * kSelWarps + warp) * stretch;
-  const int w0 = (int)(w0l < M ? w0l : M);
-  const int m = min(M, w0 + stretch) - w0;
+  const int first = a.sinks & ~31;
+  const int runs = (L - a.recent - first + 31) >> 5;
+  constexpr int kHeld = kSelWarps * kSelKeys;  // runs that a CTA holds
+  const int ctas = a.spread ? cs : min(cs, (runs + kHeld - 1) / kHeld);
+  if (rank >= ctas) return;
+  // this warp's runs: [r0, r0 + m), the warps in (CTA, warp) order
+  const int per = (runs + ctas * kSelWarps - 1) / (ctas * kSelWarps);
+  const int r0 = min(runs, (rank * kSelWarps + warp) * per);
+  const int m = min(runs, r0 + per) - r0;
+  const int pos0 = first + r0 * 32 + lane;  // this lane's row of run 0
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks_per_seq;
+  const float* head = a.mass + ((size_t)h << a.log2_bs);
+  const size_t page = (size_t)a.num_kv_heads << a.log2_bs;
   bool bad = false;
-  auto load = [&](int i) -> uint32_t {  // row w0 + i; branch-free, so that loads run ahead
-    const int pos = a.sinks + w0 + i;
+  // key of this lane's row of run j (0 outside the M rows); branch-free, so
+  // that loads run ahead
+  auto load = [&](int j) -> uint32_t {
+    int pos = pos0 + j * 32;
+    const bool in = (unsigned)(pos - a.sinks) < (unsigned)M;
+    pos = in ? pos : a.sinks;
     const int id = bt[pos >> a.log2_bs];
     const bool fine = (unsigned)id < (unsigned)a.num_blocks;
     bad = bad || !fine;
-    const float* p = a.mass + (fine ? ((size_t)id * a.num_kv_heads + h) * a.block_size + (pos & (a.block_size - 1)) : 0);
-    const uint32_t k = order_key(*p);
-    return fine ? k : 0u;
+    const uint32_t k = order_key(head[(fine ? (size_t)id : 0) * page + (pos & (a.block_size - 1))]);
+    return in ? (fine ? k : 1u) : 0u;
   };
-  // the first kSelKeys x 32 rows of the stretch in registers, a longer
-  // stretch's rest read again in each pass
+  // the first kSelKeys runs in registers, the rest read again in each pass
   uint32_t key[kSelKeys];
 #pragma unroll
-  for (int j = 0; j < kSelKeys; ++j) key[j] = 0u;
-#pragma unroll
   for (int j0 = 0; j0 < kSelKeys; j0 += 8) {
-    if (j0 * 32 < m) {
 #pragma unroll
-      for (int j = j0; j < j0 + 8; ++j) {
-        const int i = min(j * 32 + lane, m - 1);
-        key[j] = load(i);
-      }
+    for (int j = j0; j < j0 + 8; ++j) key[j] = 0u;
+    if (j0 < m) {
+#pragma unroll
+      for (int j = j0; j < j0 + 8; ++j) key[j] = load(j < m ? j : kSelKeys * kHeld);
     }
   }
-  // f(index in the stretch, key) for each of this lane's rows
+  // f(run, key) for this warp's runs; keys of 0 among them (rows outside the M,
+  // runs past the last of a group of eight) are below every row's: they never
+  // reach the threshold, whose digits are found from the top
   auto each = [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < kSelKeys; ++j) {
-      if (j * 32 < m) {
-        if (j * 32 + lane < m) f(key[j]);
+    for (int j0 = 0; j0 < kSelKeys; j0 += 8) {
+      if (j0 < m) {
+#pragma unroll
+        for (int j = j0; j < j0 + 8; ++j) f(j, key[j]);
       }
     }
-    for (int i = kSelKeys * 32 + lane; i < m; i += 32) f(load(i));
+    for (int j = kSelKeys; j < m; ++j) f(j, load(j));
   };
 
   uint32_t prefix = 0;
   int need = need_all;
+  uint32_t T = 0;  // rows above it stay, and the first `need` equal to it
+  uint32_t* my_hist = hist + lane;
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     for (int i = tid; i < 256 * 32 / 4; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    if (pass == 0)
-      each([&](uint32_t k) { atomicAdd(&hist[(k >> 24) * 32 + lane], 1u); });
-    else
-      each([&](uint32_t k) {
-        if ((k >> shift) >> 8 == prefix) atomicAdd(&hist[((k >> shift) & 255u) * 32 + lane], 1u);
+    if (pass == 0) {
+      each([&](int, uint32_t k) { atomicAdd(&my_hist[(k >> 24) * 32], 1u); });
+    } else {
+      each([&](int, uint32_t k) {
+        const uint32_t d = min((k >> shift) - (prefix << 8), 256u);
+        atomicAdd(&my_hist[d * 32], 1u);
       });
+    }
     __syncthreads();
     {
-      // two threads a bin, sixteen columns each, starting apart by bin so that
-      // a warp's lanes read different banks
-      const int bin = tid >> 1, c0 = (tid & 1) * 16;
+      // kSelThreads / 256 threads a bin, starting apart by bin so that a warp's
+      // lanes read different banks
+      constexpr int kPer = kSelThreads / 256, kCols = 32 / kPer;
+      const int bin = tid / kPer, c0 = (tid % kPer) * kCols;
       uint32_t s = 0;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s += hist[bin * 32 + c0 + ((j + bin) & 15)];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      if ((tid & 1) == 0) total[pass & 1][bin] = s;
+      for (int j = 0; j < kCols; ++j) s += hist[bin * 32 + c0 + ((j + bin) & (kCols - 1))];
+#pragma unroll
+      for (int o = 1; o < kPer; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (tid % kPer == 0) total[pass & 1][bin] = s;
     }
     ptx::cluster_sync();
     // the cluster's counts, highest bin first, and the scan that finds the digit
@@ -140,10 +162,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       const int bin = 255 - tid;
       const uint32_t at = ptx::smem_u32(&total[pass & 1][bin]);
       uint32_t cnt = 0;
-      for (uint32_t r = 0; r < cs; r += 4) {
+      for (int r = 0; r < ctas; r += 4) {
         uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = r + j < cs ? ptx::ld_cluster_u32(at, r + j) : 0u;
+        for (int j = 0; j < 4; ++j) v[j] = r + j < ctas ? ptx::ld_cluster_u32(at, (uint32_t)(r + j)) : 0u;
         cnt += (v[0] + v[1]) + (v[2] + v[3]);
       }
       uint32_t incl = cnt;
@@ -159,26 +181,30 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
       if (before < (uint32_t)need && before + cnt >= (uint32_t)need) {
         s_digit[0] = (uint32_t)bin;
         s_digit[1] = before;
+        s_digit[2] = cnt;
       }
     }
     __syncthreads();
     prefix = (prefix << 8) | s_digit[0];
     need -= (int)s_digit[1];
+    T = prefix << shift;
+    if ((int)s_digit[2] == need && T > 0) {
+      // every key with this prefix stays (none of them at 0: then all M would)
+      T -= 1;
+      need = 0;
+      break;
+    }
   }
   if (bad) atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
 
   // ---- ordered output
-  const uint32_t T = prefix;  // `need` rows equal to it stay, the lowest
   uint32_t gt = 0, eq = 0;
-  each([&](uint32_t k) {
+  each([&](int, uint32_t k) {
     gt += k > T;
     eq += k == T;
   });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     s_gt[warp] = gt;
     s_eq[warp] = eq;
@@ -195,7 +221,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
   }
   ptx::cluster_sync();
   uint32_t bg = 0, be = 0;  // rows above / equal before this warp's stretch
-  if (lane < (int)rank) {
+  if (lane < rank) {
     bg = ptx::ld_cluster_u32(ptx::smem_u32(&s_cta[0]), (uint32_t)lane);
     be = ptx::ld_cluster_u32(ptx::smem_u32(&s_cta[1]), (uint32_t)lane);
   }
@@ -203,25 +229,25 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
     bg += s_gt[lane];
     be += s_eq[lane];
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    bg += __shfl_xor_sync(0xffffffffu, bg, o);
-    be += __shfl_xor_sync(0xffffffffu, be, o);
-  }
+  bg = __reduce_add_sync(0xffffffffu, bg);
+  be = __reduce_add_sync(0xffffffffu, be);
   const uint32_t below = (1u << lane) - 1u;
-  auto put = [&](int i0, uint32_t k) {  // rows i0 + lane of the stretch, whole warp
-    const bool in = i0 + lane < m;
-    const bool is_gt = in && k > T, is_eq = in && k == T;
-    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
-    const uint32_t g = bg + __popc(mg & below), e = be + __popc(me & below);
-    if (is_gt || (is_eq && e < (uint32_t)need)) keep[a.sinks + g + min(e, (uint32_t)need)] = a.sinks + w0 + i0 + lane;
-    bg += __popc(mg);
-    be += __popc(me);
-  };
-#pragma unroll
-  for (int j = 0; j < kSelKeys; ++j)
-    if (j * 32 < m) put(j * 32, key[j]);
-  for (int i0 = kSelKeys * 32; i0 < m; i0 += 32) put(i0, load(min(i0 + lane, m - 1)));
+  int32_t* mid = keep + a.sinks;
+  if (need == 0) {
+    each([&](int j, uint32_t k) {
+      const uint32_t mg = __ballot_sync(0xffffffffu, k > T);
+      if (k > T) mid[bg + __popc(mg & below)] = pos0 + j * 32;
+      bg += __popc(mg);
+    });
+  } else {
+    each([&](int j, uint32_t k) {
+      const uint32_t mg = __ballot_sync(0xffffffffu, k > T), me = __ballot_sync(0xffffffffu, k == T);
+      const uint32_t g = bg + __popc(mg & below), e = be + __popc(me & below);
+      if (k > T || (k == T && e < (uint32_t)need)) mid[g + min(e, (uint32_t)need)] = pos0 + j * 32;
+      bg += __popc(mg);
+      be += __popc(me);
+    });
+  }
   ptx::cluster_sync();  // no CTA leaves while another reads its counts
 }
 

@@ -308,6 +308,7 @@ struct SelectArgs {
   int32_t* kept_lens;          // [B]
   int batch, num_kv_heads, max_blocks_per_seq, num_blocks, block_size, log2_bs, lim;
   int budget, sinks, recent;
+  int spread;                  // 1: use every CTA of the cluster (SMs are free)
   unsigned int* err;
 };
 constexpr int kSelThreads = 512;
