@@ -613,6 +613,10 @@ struct MaskCall {
   const int32_t* key_begin;
   const int32_t* key_end;
   bool split;  // the Q operand in two parts
+  // where the query-tile kernel writes the units that it finishes itself
+  void* out;
+  float* lse_out;
+  const float* head_sink;
 };
 
 PlanKind plan_kind(const MaskCall* m) { return !m ? kPlanDecode : (m->split ? kPlanMaskedSplit : kPlanMasked); }
@@ -693,6 +697,10 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
     a.slopes = mask->slopes;
     a.key_begin = mask->key_begin;
     a.key_end = mask->key_end;
+    a.out = static_cast<uint16_t*>(mask->out);
+    a.lse_out = mask->lse_out;
+    a.head_sink = mask->head_sink;
+    a.out_dim = cache->v_head_size;
   }
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -820,6 +828,7 @@ kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params,
     a.key_begin = mask->key_begin;
     a.key_end = mask->key_end;
     a.window = params->window;
+    a.direct = qt ? 1 : 0;
     return from_cuda(launch_combine_masked(a, reinterpret_cast<cudaStream_t>(stream), warp_rows));
   }
   return from_cuda(launch_combine(a, reinterpret_cast<cudaStream_t>(stream), warp_rows));
@@ -1188,7 +1197,7 @@ KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_pa
     return s;
   char* ws = static_cast<char*>(workspace) + head;
   MaskCall mc{table, mask ? mask->slopes : nullptr, mask ? mask->key_begin : nullptr, mask ? mask->key_end : nullptr,
-              shape.split};
+              shape.split, out, lse_out, head_sink};
   for (long long v0 = 0; v0 < shape.groups; v0 += kMaxBatch) {
     const long long left = shape.groups - v0;
     const kvq_decode_params v = masked_params(params, shape, left < kMaxBatch ? left : kMaxBatch);

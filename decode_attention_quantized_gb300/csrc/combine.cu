@@ -45,6 +45,16 @@ __device__ __forceinline__ CombineRow combine_row(const CombineArgs& a, int row_
   return c;
 }
 
+// Whether the row's segment is one piece (the split plan, see the kernels).
+__device__ __forceinline__ bool one_piece(const CombineArgs& a, const CombineRow& c) {
+  const int W = a.plan[0], gap = a.plan[2];
+  const int* pre = a.plan + 4;
+  const int nb = pre[c.b + 1] - pre[c.b];
+  const long long at = (long long)pre[c.b] * a.num_kv_heads + (long long)c.h * nb +
+                       (long long)gap * (c.b * a.num_kv_heads + c.h);
+  return nb > 0 && at / W == (at + nb - 1) / W;
+}
+
 // The bias at a masked row's anchor distance, which its partials leave out of
 // the scores (score_rule.cuh), in natural-log units.
 __device__ __forceinline__ float anchor_bias(const CombineArgs& a, const CombineRow& c) {
@@ -125,6 +135,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const CombineRow row = combine_row<MASK>(a, (int)blockIdx.x);
   if (MASK && !row.live) return;  // the whole CTA
+  if (MASK && a.direct && one_piece(a, row)) return;
   const int b = row.b, h = row.h, r = row.r;
 
   // pieces of segment s = b * Hkv + h are the CTAs whose cost ranges [x W,
@@ -213,6 +224,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_rows_kernel(const 
   if (row_ll >= (long long)a.batch * a.q_tokens * a.num_q_heads) return;
   const CombineRow row = combine_row<MASK>(a, (int)row_ll);
   if (MASK && !row.live) return;  // the whole warp
+  if (MASK && a.direct && one_piece(a, row)) return;
   const int b = row.b, h = row.h, r = row.r;
   const int W = a.plan[0], c = a.plan[2];
   const int* pre = a.plan + 4;

@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(288, MINB)
   // plan, the first block ids and the Q prologue overlap that grid's tail.
   // Without them build_slice waits first.
   const Slice<kTile, MASK> sp = build_slice<kTile, MASK>(a, pl_pre, pl_misc);
+  using Order = TileOrder<kTile, MASK>;
   const int t_begin = sp.t_begin, t_end = sp.t_end;
   auto piece = [&](int gt, int& b, int& h, int& k0, int& k1, int& L, int& slot, int& next) {
     sp.piece(a, gt, b, h, k0, k1, L, slot, next);
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(288, MINB)
   // =============================================================== producer
   if (warp == n_cw) {
     if constexpr (MASK)
-      produce_lanes<Gm>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+      produce_lanes<Gm, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
     else
       produce<Gm, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
     return;
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(288, MINB)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.0f;
 
-      for (int key0 = k0; key0 < k1; key0 += kTile, ++it, rp.next(a.stages)) {
+      for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it, rp.next(a.stages)) {
         const int stage = (int)rp.stage;
         if (ok) {
           ok = ptx::mbar_wait_bounded_inl(&bar_full[stage], rp.phase);
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(288, MINB)
 #pragma unroll
     for (int mt = 0; mt < Gm::NMT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.0f;
 
-    for (int key0 = k0; key0 < k1; key0 += kTile, ++it, rp.next(a.stages)) {
+    for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it, rp.next(a.stages)) {
       // (the head_dim 128 group-scale instances keep the division: with the
       // counter their code ran at half speed)
       constexpr bool kDiv = GRP && D < 256;

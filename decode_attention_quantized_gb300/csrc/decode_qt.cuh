@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
   using C = QtCfg<DT, D, SPLIT && !STACK>;
   using Gm = typename C::Gm;
   constexpr int KT = C::KT;
+  using Order = TileOrder<KT, MASK>;
   constexpr int kDqK = 4, kDqV = 8, kProducer = 12, kMma = 13, kMmaPv = 14;
   constexpr int NSB = C::NSB;
   constexpr float kLog2e = 1.4426950408889634f;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
   if (warp == kProducer) {
     // ============================================================ producer
     if constexpr (MASK)
-      produce_lanes<Gm>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
+      produce_lanes<Gm, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
     else
       produce<Gm, false>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
   } else if (warp >= kDqK && warp < kDqV + 4) {
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         }
         return false;
       };
-      for (int key0 = k0; key0 < k1; key0 += KT, ++it, rp.next(a.stages)) {
+      for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it, rp.next(a.stages)) {
         const uint32_t stage = rp.stage;
         const uint32_t buf = it & 1;
         wait(&bar_full[stage], rp.phase);
@@ -316,8 +317,8 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next, ++pc) {
       int b, h, k0, k1, L, u;
       sp.piece(a, gt, b, h, k0, k1, L, u, next);
-      for (int key0 = k0; key0 < k1; key0 += KT, ++it) {
-        const bool first = key0 == k0;
+      for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it) {
+        const bool first = key0 == Order::first(k0, k1);
         const uint32_t buf = it & 1;
         if (qk_warp) {
           const uint32_t sb = it % NSB;
@@ -375,13 +376,63 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
     // Epilogue of a piece: O out of TMEM 16 columns at a time, normalized,
     // to the workspace with the base-2 log-sum-exp.
-    auto epilogue = [&](int u, uint32_t last, float mu, float l, int F, bool valid) {
+    // A masked unit of one piece (`whole`) is finished here instead: the head
+    // sink, the static V scale and the rounding to bf16, as in the combine.
+    auto epilogue = [&](int u, uint32_t last, float mu, float l, int F, bool valid, bool whole, int h, size_t tok,
+                        const dev::RowRule& ru) {
       wait(&b_pv[last & 1], (last >> 1) & 1);
       if (pad_warp || second) return;
       ptx::tc_fence_after();
       float to_true = v_row ? dev::pow2i(F) : 1.0f;
       if constexpr (DT == KVQ_FP8_E4M3) to_true *= 256.0f;
-      const float inv = l > 0.0f ? to_true / l : 0.0f;
+      float inv = l > 0.0f ? to_true / l : 0.0f;
+      if constexpr (MASK) {
+        if (whole) {
+          const int hq = h * G + (r - t_row * G);
+          float lse = -INFINITY;
+          if (l > 0.0f) {
+            lse = (mu + ptx::fast_log2(l)) * 0.69314718055994530942f;
+            if (a.slopes && valid) lse -= a.slopes[hq] * (float)ru.d0;
+            if (a.head_sink && valid) inv /= 1.0f + expf(a.head_sink[hq] - lse);
+          }
+          if (a.v_mode == KVQ_SCALE_PER_TENSOR) inv *= a.v_scale[0];
+          const size_t row = tok * Hq + hq;
+          if (valid && a.lse_out) a.lse_out[row] = lse;
+          const float* vs = a.v_mode == KVQ_SCALE_PER_CHANNEL ? a.v_scale + (size_t)h * D : nullptr;
+          uint16_t* dst = a.out + row * a.out_dim;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            float o[16], x[16];
+            dev::tmem_ld_cols<16>(t_lane + C::O_COL + c0, o);
+            if (!valid || c0 >= a.out_dim) continue;
+            if constexpr (DT == KVQ_INT4) {
+#pragma unroll
+              for (int g8 = 0; g8 < 2; ++g8)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                  const float cf = (m & 1) ? dev::odd_channel_factor<DT>() : 1.0f;
+                  x[8 * g8 + m] = o[8 * g8 + 2 * m] * inv * cf;
+                  x[8 * g8 + m + 4] = o[8 * g8 + 2 * m + 1] * inv * cf;
+                }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = o[i] * inv;
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 s = vs ? *reinterpret_cast<const float2*>(vs + c0 + 2 * i) : make_float2(1.0f, 1.0f);
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * i] * s.x, x[2 * i + 1] * s.y);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            // (out_dim is a multiple of 8)
+            *reinterpret_cast<uint4*>(dst + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c0 + 8 < a.out_dim) *reinterpret_cast<uint4*>(dst + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          ptx::tc_fence_before();
+          return;
+        }
+      }
       if (valid) a.part_lse[(size_t)u * rows + r] = l > 0.0f ? mu + ptx::fast_log2(l) : -INFINITY;
       float* dst = a.part_o + ((size_t)u * rows + r) * D;
 #pragma unroll 1
@@ -413,7 +464,10 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     uint32_t it = 0;
     int pc = 0;
     int e_u = 0, e_F = 0;  // the previous piece, for its epilogue
-    bool e_valid = false;
+    bool e_valid = false, e_whole = false;
+    int e_h = 0;
+    size_t e_tok = 0;
+    dev::RowRule e_ru{};
     uint32_t e_last = 0;
     float e_mu = 0.0f, e_l = 0.0f;
     float alpha = 1.0f;
@@ -557,15 +611,15 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         // the previous piece's tiles may have run while the preceding grid
         // finished; the workspace is written only after it
         ptx::griddep_wait();
-        epilogue(e_u, e_last, e_mu, e_l, e_F, e_valid);
+        epilogue(e_u, e_last, e_mu, e_l, e_F, e_valid, e_whole, e_h, e_tok, e_ru);
       }
       if (!more) break;
 
       float mu = -INFINITY;         // reference maximum of this row (log2 units)
       float l0 = 0.0f, l1 = 0.0f;   // its weight sum, in two halves (even and odd keys)
       int F = -126;                 // V-scale normaliser exponent
-      for (int key0 = k0; key0 < k1; key0 += KT, ++it) {
-        const bool first = key0 == k0;
+      for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it) {
+        const bool first = key0 == Order::first(k0, k1);
         const uint32_t buf = it & 1, sb = it % NSB;
         wait(&b_qk[sb], (it / NSB) & 1);
         if (pad_warp) {
@@ -623,7 +677,37 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
         // logits in log2 units: y = S * k_scale * alpha (softcapped), masked
         // keys -inf; the products two at a time (f32x2)
-        if (k_row) {
+        // (masked, under a bias: b0 + sg k for key key0 + k where distances are
+        // linear over the tile, one integer base per tile and exact steps from
+        // every sixteenth key on; folded into the products when no cap follows)
+        float sg = 0.0f, b0 = 0.0f;
+        bool folded = false;
+        if constexpr (MASK) {
+          if (a.slopes && (key0 + KT - 1 <= ru.pos || key0 >= ru.pos)) {
+            sg = key0 >= ru.pos ? ru.ns : -ru.ns;
+            b0 = ru.ns * (float)(abs(ru.pos - key0) - ru.d0);
+            folded = softcap <= 0.0f;
+          }
+        }
+        if (MASK && folded) {
+          if (k_row) wait(&b_ksc[it & 3], (it >> 2) & 1);
+          const float* ksc = ksb + (it & 3) * KT;
+          const float sg2 = 2.0f * sg;
+#pragma unroll
+          for (int k = 0; k < KT; k += 16) {
+            float p0 = fmaf(sg, (float)k, b0), p1 = fmaf(sg, (float)(k + 1), b0);
+#pragma unroll
+            for (int j = k; j < k + 16; j += 2) {
+              float a0 = alpha, a1 = alpha;
+              if (k_row) {
+                const float2 s2 = *reinterpret_cast<const float2*>(ksc + j);
+                ptx::mul_x2(a0, a1, s2.x, s2.y, alpha, alpha);
+              }
+              ptx::fma_x2(y[j], y[j + 1], y[j], y[j + 1], a0, a1, p0, p1);
+              if (j < k + 14) ptx::add_x2(p0, p1, p0, p1, sg2, sg2);
+            }
+          }
+        } else if (k_row) {
           wait(&b_ksc[it & 3], (it >> 2) & 1);
           const float* ksc = ksb + (it & 3) * KT;
           const float am = softcap > 0.0f ? 1.0f : alpha;
@@ -660,12 +744,9 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           }
         }
         if constexpr (MASK) {
-          if (a.slopes) {
-            // |pos - key| - d0 of the tile's keys: one integer base per tile,
-            // then exact small steps (the tile that holds pos folds at it)
+          if (a.slopes && !folded) {
+            // after a cap, or in the tile that holds pos (distances fold at it)
             if (key0 + KT - 1 <= ru.pos || key0 >= ru.pos) {
-              const float sg = key0 >= ru.pos ? ru.ns : -ru.ns;
-              const float b0 = ru.ns * (float)(abs(ru.pos - key0) - ru.d0);
 #pragma unroll
               for (int k = 0; k < KT; ++k) y[k] += fmaf(sg, (float)k, b0);
             } else {
@@ -748,6 +829,12 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
       }
       e_u = u;
       e_valid = valid;
+      if constexpr (MASK) {
+        e_whole = k0 == (a.vseq[b].lo & ~(KT - 1)) && k1 == L;
+        e_h = h;
+        e_tok = (size_t)a.vseq[b].tok0 + t_row;
+        e_ru = ru;
+      }
       e_last = it - 1;
       e_mu = mu;
       e_l = l0 + l1;

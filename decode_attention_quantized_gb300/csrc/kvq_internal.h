@@ -103,6 +103,12 @@ struct DecodeArgs {
   const float* slopes;        // [Hq] or null
   const int32_t* key_begin;   // [tokens] or null
   const int32_t* key_end;     // [tokens] or null
+  // masked query-tile kernel: a unit that one CTA attends whole is finished
+  // there, and the combine leaves its rows alone
+  uint16_t* out;              // bf16 bits [tokens, Hq, out_dim]
+  float* lse_out;             // [tokens, Hq] or null
+  const float* head_sink;     // [Hq] or null
+  int out_dim;
 };
 
 struct CombineArgs {
@@ -122,6 +128,7 @@ struct CombineArgs {
   const int32_t* key_begin;
   const int32_t* key_end;
   int window;
+  int direct;  // 1: rows of one piece were finished by the attention kernel
 };
 
 // Writes the virtual sequences of a masked call: sequence b's tokens in groups
