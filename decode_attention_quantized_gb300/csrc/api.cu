@@ -852,11 +852,15 @@ kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params
 
 // A masked call's groups: T tokens of a sequence's C at a time, n groups per
 // sequence, the last one shorter.  The query-tile kernel takes as many tokens
-// as fill its 128 rows when that gives at least 64 rows (the rule kvq_prefill
-// uses); otherwise the mma.sync kernel takes up to 8 (head_dim 576: up to its
-// 48 rows).  A two-part Q operand (split: a per-channel K scale whose call
-// wants the lse) leaves the tile 64 rows at head_dim 256; G times a whole
-// number of tokens fills at least 56 of them.
+// as fill its 128 rows when that gives 17 rows or more; otherwise the mma.sync
+// kernel takes up to 8 tokens (head_dim 576: up to its 48 rows).  4 x 32,768
+// keys, mma.sync against the tile: head_dim 256 int8 12 rows 89 / 108 us, 18
+// rows 129 / 109, 48 rows 170 / 110; head_dim 128 int8 16 rows 107 / 138, 24
+// rows 181 / 138, 56 rows 310 / 137.  Under a softcap, whose tanh one warp
+// computes for 32 rows there, from 64 rows on (fp8 32 rows 179 / 257).  A
+// two-part Q operand (split: a per-channel K scale whose call wants the lse)
+// leaves the tile 64 rows at head_dim 256; G times a whole number of tokens
+// fills at least 56 of them.
 struct MaskShape {
   int T, n;
   bool qt, split;
@@ -873,7 +877,8 @@ kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse
   s.split = lse && c->k_mode == KVQ_SCALE_PER_CHANNEL;
   const int tile = s.split && c->head_dim == 256 ? kQtRows / 2 : kQtRows;
   s.T = tile / G < C ? tile / G : C;
-  s.qt = qt_ok(c, p) && s.T * G >= (tile == kQtRows ? 64 : 56);
+  const int least = p->softcap > 0.0f ? (tile == kQtRows ? 64 : 56) : 17;
+  s.qt = qt_ok(c, p) && s.T * G >= least;
   if (!s.qt) {
     const int most = c->head_dim == 576 && 48 / G < 8 ? 48 / G : 8;
     s.T = most < C ? most : C;

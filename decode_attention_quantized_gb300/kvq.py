@@ -355,28 +355,37 @@ def decode_step(cache: QuantizedPagedCache, params: DecodeParams, q, block_table
 # score rules (distance bias, key intervals) and eviction
 # ---------------------------------------------------------------------------
 
-def _need(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, device, optional: bool = False):
+def _need(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, dev: int, optional: bool = False):
     """The tensor's type, shape, order and device are what the C call takes for
     granted; returns its device pointer."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is missing")
-    if t.dtype is not dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: needs a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous {dtype} tensor of shape {shape} on cuda:{dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ' (not contiguous)'}")
     return t.data_ptr()
 
 
-def _current(device: torch.device):
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, not on the current CUDA device")
+def _current(t: torch.Tensor) -> int:
+    """The index of t's device, which has to be the current CUDA device."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, not on the current CUDA device")
+    return dev
 
 
-def _workspace(workspace: torch.Tensor, device):
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: needs a contiguous tensor on {device}")
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; None: the current one of device `dev` (read without
+    building a Stream object, which takes 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _workspace(workspace: torch.Tensor, dev: int):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs a contiguous tensor on cuda:{dev}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -390,11 +399,11 @@ class ScoreMask:
     key_begin: Optional[torch.Tensor] = None
     key_end: Optional[torch.Tensor] = None
 
-    def desc(self, params: DecodeParams, device) -> ScoreMaskDesc:
+    def desc(self, params: DecodeParams, dev: int) -> ScoreMaskDesc:
         per_token = (params.batch, params.q_tokens)
-        return ScoreMaskDesc(_need("slopes", self.slopes, torch.float32, (params.num_q_heads,), device, True),
-                             _need("key_begin", self.key_begin, torch.int32, per_token, device, True),
-                             _need("key_end", self.key_end, torch.int32, per_token, device, True))
+        return ScoreMaskDesc(_need("slopes", self.slopes, torch.float32, (params.num_q_heads,), dev, True),
+                             _need("key_begin", self.key_begin, torch.int32, per_token, dev, True),
+                             _need("key_end", self.key_end, torch.int32, per_token, dev, True))
 
 
 def kvq_attend_masked_workspace_size(cache: QuantizedPagedCache, params: DecodeParams) -> int:
@@ -409,8 +418,7 @@ def kvq_attend_masked(cache: QuantizedPagedCache, params: DecodeParams, mask: Op
                       out: torch.Tensor, lse_out: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
     """q bf16 [B, C, Hq, D], out bf16 [B, C, Hq, out_dim] with C = params.q_tokens
     >= 1; lse_out fp32 [B, C, Hq] or None; mask None: causal, no bias."""
-    dev, B, C, Hq = cache.k_codes.device, params.batch, params.q_tokens, params.num_q_heads
-    _current(dev)
+    dev, B, C, Hq = _current(cache.k_codes), params.batch, params.q_tokens, params.num_q_heads
     d = cache.desc()
     m = None if mask is None else ctypes.byref(mask.desc(params, dev))
     ws, nbytes = _workspace(workspace, dev)
@@ -420,7 +428,7 @@ def kvq_attend_masked(cache: QuantizedPagedCache, params: DecodeParams, mask: Op
         _need("seq_lens", seq_lens, torch.int32, (B,), dev),
         _need("head_sink", head_sink, torch.float32, (Hq,), dev, True),
         _need("out", out, torch.bfloat16, (B, C, Hq, cache.out_dim), dev),
-        _need("lse_out", lse_out, torch.float32, (B, C, Hq), dev, True), ws, nbytes, _stream(stream)))
+        _need("lse_out", lse_out, torch.float32, (B, C, Hq), dev, True), ws, nbytes, _raw_stream(stream, dev)))
 
 
 def kvq_key_mass_workspace_size(cache: QuantizedPagedCache, params: DecodeParams) -> int:
@@ -436,8 +444,7 @@ def kvq_key_mass(cache: QuantizedPagedCache, params: DecodeParams, mask: Optiona
     """Adds the attention weight of this call's query tokens to mass fp32
     [num_blocks, Hkv, block_size]; lse fp32 [B, C, Hq] from the attention call.
     fresh: trailing positions that held no weight before (None: the C tokens)."""
-    dev, B, C, Hq = cache.k_codes.device, params.batch, params.q_tokens, params.num_q_heads
-    _current(dev)
+    dev, B, C, Hq = _current(cache.k_codes), params.batch, params.q_tokens, params.num_q_heads
     d = cache.desc()
     m = None if mask is None else ctypes.byref(mask.desc(params, dev))
     ws, nbytes = _workspace(workspace, dev)
@@ -447,7 +454,7 @@ def kvq_key_mass(cache: QuantizedPagedCache, params: DecodeParams, mask: Optiona
         _need("seq_lens", seq_lens, torch.int32, (B,), dev), _need("lse", lse, torch.float32, (B, C, Hq), dev),
         float(decay), C if fresh is None else int(fresh),
         _need("mass", mass, torch.float32, (cache.num_blocks, cache.num_kv_heads, cache.block_size), dev), ws, nbytes,
-        _stream(stream)))
+        _raw_stream(stream, dev)))
 
 
 def make_evict_params(batch, max_blocks_per_seq, budget, *, num_blocks, block_size, num_kv_heads, sinks=0, recent=0,
@@ -461,15 +468,14 @@ def make_evict_params(batch, max_blocks_per_seq, budget, *, num_blocks, block_si
 def kvq_evict_select(params: EvictParams, mass: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                      keep: torch.Tensor, kept_lens: torch.Tensor, stream=None):
     """keep int32 [B, Hkv, budget] (ascending rows, then -1), kept_lens int32 [B]."""
-    dev, B = mass.device, params.batch
-    _current(dev)
+    dev, B = _current(mass), params.batch
     _check("kvq_evict_select", load().kvq_evict_select(
         ctypes.byref(params),
         _need("mass", mass, torch.float32, (params.num_blocks, params.num_kv_heads, params.block_size), dev),
         _need("block_table", block_table, torch.int32, (B, params.max_blocks_per_seq), dev),
         _need("seq_lens", seq_lens, torch.int32, (B,), dev),
         _need("keep", keep, torch.int32, (B, params.num_kv_heads, params.budget), dev),
-        _need("kept_lens", kept_lens, torch.int32, (B,), dev), _stream(stream)))
+        _need("kept_lens", kept_lens, torch.int32, (B,), dev), _raw_stream(stream, dev)))
 
 
 def kvq_evict_compact_workspace_size(cache: QuantizedPagedCache, params: EvictParams) -> int:
@@ -484,8 +490,7 @@ def kvq_evict_compact(cache: QuantizedPagedCache, params: EvictParams, block_tab
                       mass: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
     """Moves the kept rows (codes, row scales, mass) to the front of the pages of
     block_table (dst_table None or block_table), or into dst_table's pages."""
-    dev, B = cache.k_codes.device, params.batch
-    _current(dev)
+    dev, B = _current(cache.k_codes), params.batch
     d = cache.desc()
     ws, nbytes = _workspace(workspace, dev)
     table = (B, params.max_blocks_per_seq)
@@ -495,7 +500,7 @@ def kvq_evict_compact(cache: QuantizedPagedCache, params: EvictParams, block_tab
         _need("keep", keep, torch.int32, (B, params.num_kv_heads, params.budget), dev),
         _need("kept_lens", kept_lens, torch.int32, (B,), dev),
         _need("mass", mass, torch.float32, (cache.num_blocks, cache.num_kv_heads, cache.block_size), dev, True),
-        ws, nbytes, _stream(stream)))
+        ws, nbytes, _raw_stream(stream, dev)))
 
 
 @dataclass

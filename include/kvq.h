@@ -371,9 +371,9 @@ typedef struct {
  * Arguments and results as in kvq_prefill; mask may be NULL (causal, no
  * bias).  Sequences are cut into groups of tokens; keys that no token of a
  * group sees are not read.  With head_dim 128 or 256, no group-wise scales,
- * KVQ_DECODE_NO_TCGEN05 unset and groups of at least 64 query rows per kv
- * head, the groups are tiles of up to 128 rows on tcgen05 MMAs; otherwise of
- * up to 8 tokens on the mma.sync kernel.  KVQ_DECODE_EARLY_INPUTS and
+ * KVQ_DECODE_NO_TCGEN05 unset and more than 16 query rows per kv head (64 or
+ * more under a softcap), the groups are tiles of up to 128 rows on tcgen05
+ * MMAs; otherwise of up to 8 tokens on the mma.sync kernel.  KVQ_DECODE_EARLY_INPUTS and
  * KVQ_DECODE_EARLY_CACHE have no effect here.  lse_out is fp32-accurate: with
  * a per-channel K scale the query operand is then carried in two f16 parts,
  * which costs time (a prompt's tiles about half as much again at head_dim 128
