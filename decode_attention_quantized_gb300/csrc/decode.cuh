@@ -120,6 +120,22 @@ __device__ __forceinline__ float tanh_fast(float x) {
   return 1.0f - __fdividef(2.0f, ptx::fast_exp2(x * 2.8853900817779268f) + 1.0f);
 }
 
+// tanh(x) to 2e-7 of its value: for |x| <= 0.6 (a logit up to 30 under a cap
+// of 50) x P(x^2), P a Chebyshev interpolant of tanh(sqrt t) / sqrt t on
+// [0, 0.36] (1.1e-7 with its fp32 evaluation), else tanhf.  Where a cap's error
+// shows in fp32 results: 50 * tanh_fast would be 2e-5 off in a logit.
+__device__ __forceinline__ float tanh_near(float x) {
+  const float t = x * x;
+  if (t > 0.36f || !(t == t)) return tanhf(x);
+  float p = -0.00585642785f;
+  p = fmaf(p, t, 0.0207574754f);
+  p = fmaf(p, t, -0.0537699218f);
+  p = fmaf(p, t, 0.133317047f);
+  p = fmaf(p, t, -0.33333284f);
+  p = fmaf(p, t, 0.999999998f);
+  return p * x;
+}
+
 // Exact e4m3x2 -> f16x2 (hardware conversion; the low byte goes to the low
 // half).  Used for K only: a stale e4m3 NaN byte under a masked key can then
 // only poison that key's own score, which the mask replaces.

@@ -327,16 +327,18 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           if (it >= NSB) wait(&b_sfree[sb], ((it - NSB) / NSB) & 1);  // the softmax has read that S buffer
           __syncwarp();
           ptx::tc_fence_after();
-#pragma unroll 1
-          for (int sl = 0; sl < D / 64; ++sl)
-            ptx::mma_f16_ts_x4(tmem + C::S_COL + KT * sb, tmem + C::Q_COL + 32 * sl, 8,
-                               k_lo + ((buf * C::TILE + sl * C::SLAB) >> 4), d_hi, idesc_qk, sl > 0 ? 1u : 0u);
           if constexpr (SPLIT && !STACK) {
+            // the small part first: less is rounded
 #pragma unroll 1
             for (int sl = 0; sl < D / 64; ++sl)
               ptx::mma_f16_ts_x4(tmem + C::S_COL + KT * sb, tmem + C::QL_COL + 32 * sl, 8,
-                                 k_lo + ((buf * C::TILE + sl * C::SLAB) >> 4), d_hi, idesc_qk, 1u);
+                                 k_lo + ((buf * C::TILE + sl * C::SLAB) >> 4), d_hi, idesc_qk, sl > 0 ? 1u : 0u);
           }
+#pragma unroll 1
+          for (int sl = 0; sl < D / 64; ++sl)
+            ptx::mma_f16_ts_x4(tmem + C::S_COL + KT * sb, tmem + C::Q_COL + 32 * sl, 8,
+                               k_lo + ((buf * C::TILE + sl * C::SLAB) >> 4), d_hi, idesc_qk,
+                               sl > 0 || (SPLIT && !STACK) ? 1u : 0u);
           ptx::mma_commit(&b_qk[sb]);
           ptx::mma_commit(&b_kfree[buf]);
         } else {

@@ -13,7 +13,7 @@
 // The result is fp32 and has to agree with fp32 scores: codes are exact in
 // f16 and so are bf16 queries, but a query with a per-channel K scale folded in
 // is not; there the operand is split into two f16 values (two MMAs).  The cap
-// takes tanhf, whose error is relative (50 * tanh(x / 50) from 1 - 2 / (e^2x +
+// takes a tanh of small relative error (50 * tanh(x / 50) from 1 - 2 / (e^2x +
 // 1) would be 2e-5 off).
 #pragma once
 
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
               float s = GRP ? gx[GRP ? nt : 0][e] : acc[nt][e];
               if constexpr (NT == 1 && !GRP) s += odd[e];
               float x = s * r.alpha * (e2 ? ksb : ksa);
-              if (softcap > 0.0f) x = cap_l2 * tanhf(x);
+              if (softcap > 0.0f) x = cap_l2 * dev::tanh_near(x);
               if (a.slopes) x = fmaf(r.ns, (float)(abs(r.pos - key) - r.d0), x);
               const float p = key >= r.begin && key < r.end ? ptx::fast_exp2(x - r.c) : 0.0f;
               if (e2) sum_b += p; else sum_a += p;

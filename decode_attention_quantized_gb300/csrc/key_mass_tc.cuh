@@ -34,7 +34,10 @@ struct __align__(16) MassTcRule {
   int begin, end, pos, d0;
 };
 
-template <int DT, int D, bool SPLIT>
+// CAP: a softcap (in instances of its own: fourteen warps share the instruction
+// caches, and everything that made the weight loop's code larger -- the cap
+// beside it, prefetching or unrolling over more columns -- cost 10 to 25%).
+template <int DT, int D, bool SPLIT, bool CAP>
 __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
     key_mass_tc_kernel(const __grid_constant__ CUtensorMap tmk, const DecodeArgs a, const MassArgs ms, const int NR) {
   using Gm = Geo<DT, D, kTcKeys>;
@@ -169,11 +172,11 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         ptx::tc_fence_after();
         const uint32_t s_col = tmem + S_COL + 128 * buf, k_col = tmem + K_COL + (D / 2) * buf;
 #pragma unroll 1
-        for (int p = 0; p < (SPLIT ? 2 : 1); ++p) {
+        for (int p = SPLIT ? 1 : 0; p >= 0; --p) {  // the small part first: less is rounded
 #pragma unroll 1
           for (int sl = 0; sl < D / 64; ++sl)
             ptx::mma_f16_ts_x4(s_col, k_col + 32 * sl, 8, q_lo + p * part + sl * slab, d_hi, idesc,
-                               sl + p > 0 ? 1u : 0u);
+                               sl > 0 || (SPLIT && p == 0) ? 1u : 0u);
         }
         ptx::mma_commit(&b_s[buf]);
       }
@@ -365,11 +368,18 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
           float y[16];
           dev::tmem_ld_cols<16>(t_s + 128 * buf + c0, y);
-          if (fast && softcap <= 0.0f) {
+          if (fast) {
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float4 ac = *reinterpret_cast<const float4*>(r_ac + c0 + i);
-              float x0 = fmaf(y[i] * ks, ac.x, -ac.y), x1 = fmaf(y[i + 1] * ks, ac.z, -ac.w);
+              float x0, x1;
+              if constexpr (CAP) {
+                x0 = fmaf(cap_l2, dev::tanh_near(y[i] * ks * ac.x), -ac.y);
+                x1 = fmaf(cap_l2, dev::tanh_near(y[i + 1] * ks * ac.z), -ac.w);
+              } else {
+                x0 = fmaf(y[i] * ks, ac.x, -ac.y);
+                x1 = fmaf(y[i + 1] * ks, ac.z, -ac.w);
+              }
               if (bias) {
                 const float4 ne = *reinterpret_cast<const float4*>(r_ne + c0 + i);
                 x0 = fmaf(ne.x, ne.y - kf, x0);
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
               const float2 ac = r_ac[c0 + i], ne = r_ne[c0 + i];
               const MassTcRule ru = r_rule[c0 + i];
               float x = y[i] * ks * ac.x;
-              if (softcap > 0.0f) x = cap_l2 * tanhf(x);
+              if constexpr (CAP) x = cap_l2 * dev::tanh_near(x);
               if (bias) x = fmaf(ne.x, (float)(abs(ru.pos - key) - ru.d0), x);
               s0 += key >= ru.begin && key < ru.end ? ptx::fast_exp2(x - ac.y) : 0.0f;
             }
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
   }
 }
 
-template <int DT, int D, bool SPLIT>
+template <int DT, int D, bool SPLIT, bool CAP>
 cudaError_t launch_key_mass_tc_d(const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m, int nr, int grid,
                                  size_t smem, cudaStream_t stream) {
   static int smem_set[64] = {};
@@ -421,24 +431,29 @@ cudaError_t launch_key_mass_tc_d(const CUtensorMap& tk, const DecodeArgs& a, con
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(key_mass_tc_kernel<DT, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(key_mass_tc_kernel<DT, D, SPLIT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     smem_set[dev] = (int)smem;
   }
-  return launch_pdl(key_mass_tc_kernel<DT, D, SPLIT>, grid, kMassTcWarps * 32, smem, stream, tk, a, m, nr);
+  return launch_pdl(key_mass_tc_kernel<DT, D, SPLIT, CAP>, grid, kMassTcWarps * 32, smem, stream, tk, a, m, nr);
 }
 
 // head_dim 128 or 256, any K scale mode but PER_GROUP.
 template <int DT>
 cudaError_t dispatch_key_mass_tc(int head_dim, const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m, int nr,
                                  int grid, size_t smem, cudaStream_t stream) {
-  const bool split = a.k_mode == KVQ_SCALE_PER_CHANNEL;
-  if (head_dim == 256)
-    return split ? launch_key_mass_tc_d<DT, 256, true>(tk, a, m, nr, grid, smem, stream)
-                 : launch_key_mass_tc_d<DT, 256, false>(tk, a, m, nr, grid, smem, stream);
-  if (head_dim == 128)
-    return split ? launch_key_mass_tc_d<DT, 128, true>(tk, a, m, nr, grid, smem, stream)
-                 : launch_key_mass_tc_d<DT, 128, false>(tk, a, m, nr, grid, smem, stream);
+  const bool split = a.k_mode == KVQ_SCALE_PER_CHANNEL, cap = a.softcap > 0.0f;
+  auto go = [&](auto dtag, auto stag) -> cudaError_t {
+    constexpr int d = decltype(dtag)::value;
+    constexpr bool s = decltype(stag)::value;
+    return cap ? launch_key_mass_tc_d<DT, d, s, true>(tk, a, m, nr, grid, smem, stream)
+               : launch_key_mass_tc_d<DT, d, s, false>(tk, a, m, nr, grid, smem, stream);
+  };
+  auto by_split = [&](auto dtag) -> cudaError_t {
+    return split ? go(dtag, std::true_type{}) : go(dtag, std::false_type{});
+  };
+  if (head_dim == 256) return by_split(std::integral_constant<int, 256>{});
+  if (head_dim == 128) return by_split(std::integral_constant<int, 128>{});
   return cudaErrorInvalidValue;
 }
 
