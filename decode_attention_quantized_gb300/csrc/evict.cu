@@ -109,7 +109,10 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     for (int j = j0; j < j0 + 8; ++j) key[j] = 0u;
     if (j0 < m) {
 #pragma unroll
-      for (int j = j0; j < j0 + 8; ++j) key[j] = load(j < m ? j : kSelKeys * kHeld);
+      for (int j = j0; j < j0 + 8; ++j) {
+        const uint32_t k = load(min(j, m - 1));
+        key[j] = j < m ? k : 0u;
+      }
     }
   }
   // f(run, key) for this warp's runs; keys of 0 among them (rows outside the M,

@@ -137,6 +137,51 @@ def test_mass_is_reproducible_and_captured(kvq):
     assert torch.equal(m1, m2)
 
 
+@pytest.mark.parametrize("c", [12, 40])
+def test_mass_of_sequences_shorter_than_the_chunk(kvq, c):
+    case = ref.Case(lens=(3, 0, 11, 90), c=c, d=128)
+    cache = ref.Cache(case)
+    s = slopes_of(8)
+    lse = ref.attend(cache, s)[1]
+    mass = random_mass(cache)
+    check_mass(mass_call(kvq, cache, lse, mass, 0.75, slopes=s), cache, lse, mass, 0.75, c, s)
+
+
+@pytest.mark.parametrize("name", ["int8 row d128", "fp8 row", "int4 group", "int8 row d256 g6", "latent d576"])
+@pytest.mark.parametrize("c", [1, 24])
+def test_mass_beside_junk(kvq, name, c):
+    """Rows that no token sees hold NaN scales and codes: they decay, and
+    nothing of them reaches the others."""
+    case = dataclasses.replace(CASES[name], c=c, lens=(200,), seed=4)
+    cache = ref.Cache(case)
+    begin = np.full((1, c), 70, np.int32)
+    end = np.full((1, c), 150, np.int32)
+    lse = ref.attend(cache, None, begin, end)[1]
+    mass = random_mass(cache)
+    want, tol = ref.key_mass(cache, lse.astype(np.float32), mass, 0.5, 0, None, begin, end)
+    blk, row = cache.rows(0)
+    bad = np.r_[0:70, 150:200]
+    if case.dtype == FP8:
+        cache.k_codes[blk[bad], :, row[bad]] = 0x7F
+    if cache.k_scale.ndim >= 3:
+        cache.k_scale[blk[bad], :, row[bad]] = np.nan
+    got = mass_call(kvq, cache, lse, mass, 0.5, 0, None, begin, end)
+    assert (np.abs(got - want)[blk, :, row] <= tol[blk, :, row]).all()
+
+
+@pytest.mark.parametrize("hq,hkv,c", [(7, 1, 3), (10, 2, 30), (9, 3, 50), (8, 1, 16), (8, 1, 17), (6, 1, 22)])
+def test_mass_group_sizes(kvq, hq, hkv, c):
+    """Row counts around the kernels' tiles (8, 16, 32, 64, 128 rows), one launch
+    and several, with and without the tensor-memory kernel."""
+    for d, km in ((128, ROW), (256, CHANNEL), (64, TENSOR)):
+        case = ref.Case(d=d, km=km, vm=km, hq=hq, hkv=hkv, c=c, lens=(300, 77), seed=hq)
+        cache = ref.Cache(case)
+        s = slopes_of(hq, -0.02)
+        lse = ref.attend(cache, s)[1]
+        mass = random_mass(cache)
+        check_mass(mass_call(kvq, cache, lse, mass, 0.9, slopes=s), cache, lse, mass, 0.9, c, s)
+
+
 # -------------------------------------------------------------------- select
 
 def pages(lens, bs, seed, slack=2, width=None):
@@ -340,6 +385,52 @@ def test_compact_is_captured(kvq):
         torch.cuda.synchronize()
         assert torch.equal(g.k_codes, want)
     assert kvq.kvq_get_device_error() == 0
+
+
+# ----------------------------------------------------- caches beyond 4 GB
+
+def test_pages_beyond_four_gigabytes(kvq):
+    """The same rows in pages behind the first 4 GB of a 5 GB pool and in a small
+    pool: attention, weights, selection and moves agree bit for bit."""
+    nb, bs, hkv, d, far = 20480, 256, 8, 128, 20000
+    L, n_pages, budget = 1500, 6, 600
+    r = np.random.default_rng(1)
+    small = kvq.QuantizedPagedCache(INT8, ROW, ROW, 8, bs, hkv, d)
+    big = kvq.QuantizedPagedCache(INT8, ROW, ROW, nb, bs, hkv, d)
+    assert big.k_codes[:far].numel() > 4 << 30
+    kv = [torch.from_numpy(r.standard_normal((L, hkv, d)).astype(np.float32)).to(torch.bfloat16).cuda() for _ in "kv"]
+    order = r.permutation(n_pages).astype(np.int32)
+    outs = []
+    for g, first in ((small, 0), (big, far)):
+        pages = order + first
+        slots = pages[np.arange(L) // bs].astype(np.int64) * bs + np.arange(L) % bs
+        kvq.kvq_append(g, kv[0], kv[1], dev(slots))
+        table = dev(pages[None])
+        lens = dev(np.array([L], np.int32))
+        res = []
+        for c in (1, 40):
+            p = kvq.make_params(1, 16, c, n_pages)
+            q = torch.from_numpy(np.random.default_rng(c).standard_normal((1, c, 16, d)).astype(np.float32))
+            q = q.to(torch.bfloat16).cuda()
+            ws = torch.zeros(max(kvq.kvq_attend_masked_workspace_size(g, p), kvq.kvq_key_mass_workspace_size(g, p)) // 4,
+                             dtype=torch.int32, device="cuda")
+            out = torch.zeros((1, c, 16, d), dtype=torch.bfloat16, device="cuda")
+            lse = torch.zeros((1, c, 16), device="cuda")
+            rule = kvq.ScoreMask(slopes=dev(np.array(slopes_of(16), np.float32)))
+            kvq.kvq_attend_masked(g, p, rule, q, table, lens, None, out, lse, ws)
+            mass = torch.zeros((g.num_blocks, hkv, bs), device="cuda")
+            kvq.kvq_key_mass(g, p, rule, q, table, lens, lse, mass, ws)
+            res += [out, lse, mass[first:first + n_pages].clone()]
+        ep = kvq.make_evict_params(1, n_pages, budget, num_blocks=g.num_blocks, block_size=bs, num_kv_heads=hkv,
+                                   recent=50)
+        b = kvq.alloc_evict_buffers(g, ep)
+        kvq.evict_step(g, ep, table, lens, mass, b)
+        res += [b.keep, b.kept_lens, mass[first:first + n_pages].clone()]
+        res += [t[first:first + n_pages].clone() for t in (g.k_codes, g.v_codes, g.k_scale, g.v_scale)]
+        outs.append(res)
+    assert kvq.kvq_get_device_error() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------ together

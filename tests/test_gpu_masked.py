@@ -367,3 +367,91 @@ def test_refuses_wrong_tensors(kvq):
     with pytest.raises(kvq.KvqError) as e:
         kvq.kvq_attend_masked(g, p, None, q, table, lens, None, out, None, ws[:16])
     assert e.value.status == 3
+
+
+def test_many_tiles_take_several_launches(kvq):
+    """More tiles of 128 rows than one launch holds: 16,500 tokens of 8 heads,
+    checked at the launches' seam, in split and in whole units."""
+    C, L = 16500, 16700
+    case = ref.Case(d=128, hq=8, hkv=1, lens=(L,), c=C, bs=256)
+    cache = ref.Cache(case)
+    pos = np.arange(L - C, L)
+    begin = np.maximum(0, pos - 300).astype(np.int32)[None]
+    begin[0, 5000:5100] = 0
+    s = slopes_of(8)
+    sink = np.linspace(-1, 1, 8)
+    out, lse = run(kvq, cache, s, begin, sink=sink)
+    for t in (0, 1, 4999, 5050, 16383, 16384, 16385, 16399, 16400, 16499):
+        lo, hi, p = ref.visible(case, 0, t, begin, None)
+        k, v = cache.values(0, 0, "k")[lo:hi], cache.values(0, 0, "v")[lo:hi]
+        f16c = 2.0 ** -24 * (hi - lo) * cache.largest(0, 0, lo, hi)
+        for h in range(8):
+            x = k @ cache.q[0, t, h].astype(float) * case.scale - s[h] * np.abs(p - np.arange(lo, hi))
+            w = np.exp(x - x.max())
+            l = x.max() + np.log(w.sum())
+            assert abs(lse[0, t, h] - l) <= 2.0 ** -14
+            w = w / w.sum() / (1 + np.exp(sink[h] - l))
+            tol = 2.0 ** -8 * np.abs(w @ v) + (2.0 ** -10 + 2.0 ** -14) * (w @ np.abs(v)) + f16c
+            assert (np.abs(out[0, t, h] - w @ v) <= tol).all()
+
+
+@pytest.mark.parametrize("hq,hkv", [(7, 1), (10, 2), (3, 3), (9, 3), (20, 4)])
+@pytest.mark.parametrize("c", [1, 5, 40])
+@pytest.mark.parametrize("km", [ROW, CHANNEL])
+def test_group_sizes(kvq, hq, hkv, c, km):
+    """Groups of 1, 3, 5 and 7 query heads, whose tiles end inside 128 rows."""
+    for d in (128, 256):
+        case = ref.Case(d=d, km=km, vm=km, hq=hq, hkv=hkv, c=c, lens=(150, 77), seed=hq)
+        cache = ref.Cache(case)
+        s = slopes_of(hq, -0.05)
+        begin, end = documents(case, (60, 111))
+        check(cache, run(kvq, cache, s, begin, end), s, begin, end)
+
+
+@pytest.mark.parametrize("dtype", [INT8, FP8, INT4])
+@pytest.mark.parametrize("d,c,hq,hkv", [(64, 4, 4, 1), (128, 3, 8, 4), (128, 6, 8, 2), (128, 40, 8, 2), (256, 2, 8, 2),
+                                        (256, 8, 12, 2), (256, 50, 12, 2), (576, 2, 8, 1), (576, 9, 8, 1)])
+def test_lse_of_a_per_channel_scale(kvq, dtype, d, c, hq, hkv):
+    """lse is fp32-accurate with a per-channel K scale too: the two-part operand
+    leaves 2^-22 of sum |q k| (2^-11 with one part), on every layout; without an
+    lse the one-part kernels give the same output within its bound."""
+    if d == 576 and dtype == INT4:
+        pytest.skip("576-channel rows are 8-bit")
+    case = ref.Case(dtype=dtype, km=CHANNEL, vm=CHANNEL, d=d, c=c, hq=hq, hkv=hkv, lens=(130, 64), latent=d == 576,
+                    dv=512 if d == 576 else 0)
+    cache = ref.Cache(case)
+    s = [0.5] * hq  # steep: few keys carry a row, so their errors do not average out
+    out, lse = run(kvq, cache, s)
+    r_out, r_lse, absv, f16, size = ref.attend(cache, s)
+    # 2^-22 of the operand, 64 fp32 accumulations (2^-18 of their size), and a
+    # few roundings of the result
+    assert (np.abs(lse - r_lse) <= 2.0 ** -17 * size + 2.0 ** -20 * (1 + np.abs(r_lse))).all()
+    check(cache, (out, lse), s)
+    g = gpu_cache(kvq, cache)
+    p = kvq.make_params(2, hq, c, cache.width)
+    ws = torch.zeros(kvq.kvq_attend_masked_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+    o2 = torch.zeros((2, c, hq, g.out_dim), dtype=torch.bfloat16, device="cuda")
+    kvq.kvq_attend_masked(g, p, kvq.ScoreMask(slopes=dev(np.array(s, np.float32))), dev(cache.q).to(torch.bfloat16),
+                          dev(cache.table), dev(np.array(case.lens, np.int32)), None, o2, None, ws)
+    check(cache, (o2.double().cpu().numpy(), lse), s)
+
+
+@pytest.mark.parametrize("c", [1, 40])
+def test_tcgen05_off_and_bounds(kvq, c):
+    """KVQ_DECODE_NO_TCGEN05 takes the mma.sync kernel; a max_seq_len below the
+    capacity bounds the plan; the early-read flags change nothing."""
+    case = ref.Case(d=128, c=c, lens=(201, 130))
+    cache = ref.Cache(case, width=40)
+    s = slopes_of(8)
+    check(cache, run(kvq, cache, s, flags=kvq.DECODE_NO_TCGEN05), s)
+    a = run(kvq, cache, s)
+    b = run(kvq, cache, s, flags=kvq.DECODE_EARLY_INPUTS | kvq.DECODE_EARLY_CACHE)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    g = gpu_cache(kvq, cache)
+    p = kvq.make_params(2, 8, c, cache.width, max_seq_len=201)
+    ws = guarded(torch.zeros(kvq.kvq_attend_masked_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda"), "ws")
+    out, lse = torch.zeros((2, c, 8, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, c, 8), device="cuda")
+    kvq.kvq_attend_masked(g, p, kvq.ScoreMask(slopes=dev(np.array(s, np.float32))), dev(cache.q).to(torch.bfloat16),
+                          dev(cache.table), dev(np.array(case.lens, np.int32)), None, out, lse, ws)
+    check(cache, (out.double().cpu().numpy(), lse.double().cpu().numpy()), s)
+    assert kvq.kvq_get_device_error() == 0
