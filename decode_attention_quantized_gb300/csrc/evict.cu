@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Co
         n = min(a.rows, min(a.kept_lens[b], a.budget) - (chunk << a.log2_rows));
         if (r < n) {
           int src = -1;
-          if (p < 0 || p >= cap) atomicOr(a.err, KVQ_DEVERR_KEEP_INDEX);
+          // (in place, a row from before its destination may be gone)
+          if (p < (a.in_place ? i : 0) || p >= cap) atomicOr(a.err, KVQ_DEVERR_KEEP_INDEX);
           else src = slot_of(a.block_table, b, p);
           s_src[q][r] = src;
           // (budget <= capacity: i is inside the table)

@@ -272,9 +272,9 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
             }
             float qm = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) qm = fmaxf(qm, fabsf(qv[j]));
+            for (int j = 0; j < 8; ++j) qm = ptx::max_nan(qm, fabsf(qv[j]));
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, o));
+            for (int o = 1; o < LPR; o <<= 1) qm = ptx::max_nan(qm, __shfl_xor_sync(0xffffffffu, qm, o));
             const int eq = qm > 0.0f ? min(126, max(-126, dev::ceil_log2(qm))) : 0;
             const float sq = dev::pow2i(-eq);
             uint32_t w[4], lo[4];
@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
               if constexpr (SPLIT) *reinterpret_cast<uint4*>(dst + q_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
               if (cl == 0) {
                 const int e = ek + eq, e1 = e / 2;
-                r_ac[r].x = fminf(fac * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f);
+                const float al = fminf(fac * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f);
+                // (a row with an infinity or a NaN is marked: see below)
+                r_ac[r].x = qm <= 3.4028234e38f ? al : __uint_as_float(0x7FC00000u);
               }
             }
           }
@@ -310,8 +312,15 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
       ptx::named_bar_sync(5, 256);  // the logit factors are visible
       if (tid < NR) {
         // a row that is padding, sees nothing or has no weight: factor 0 and
-        // log-sum-exp +inf give it a weight of exactly 0 everywhere
-        if (!live) r_ac[tid].x = 0.0f;
+        // log-sum-exp +inf give it a weight of exactly 0 everywhere.  Times 0
+        // its scores may still be NaN, when its query holds an infinity or a
+        // NaN: an interval that ends at 0 then keeps every tile of the piece
+        // on the slow path, which selects by the rules.
+        if (!live) {
+          const float al = r_ac[tid].x;
+          if (al != al) ru.begin = -1;
+          r_ac[tid].x = 0.0f;
+        }
         r_ac[tid].y = ac.y;
         r_ne[tid] = ne;
         r_rule[tid] = ru;

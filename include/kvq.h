@@ -102,7 +102,8 @@ typedef enum {
 #define KVQ_DEVERR_SEQ_LEN 0x4u   /* decode: seq_len < 0, > capacity, or > max_seq_len */
 #define KVQ_DEVERR_TIMEOUT 0x8u   /* a bounded pipeline wait gave up */
 #define KVQ_DEVERR_POSITION 0x10u /* norm/RoPE prologue: position outside [0, max_position) */
-#define KVQ_DEVERR_KEEP_INDEX 0x20u /* kvq_evict_compact: a kept row outside [0, capacity) */
+#define KVQ_DEVERR_KEEP_INDEX 0x20u /* kvq_evict_compact: a kept row outside [0, capacity), or in
+                                       * place before its destination */
 
 /* Cache layouts (PR #29912, kv_cache_layout and v_head_size): SEPARATE K and V
  * caches, or LATENT (absorbed MLA): one cache whose rows serve as K, and whose
@@ -451,8 +452,9 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
  * are free for other use.  Otherwise dst_table [B, max_blocks_per_seq] names
  * other pages, none of which is a source page of this call: for sequences
  * whose pages are shared, which in-place moves would change for everyone.
- * A kept row outside the capacity sets KVQ_DEVERR_KEEP_INDEX and is not
- * moved (its destination's contents are unspecified).
+ * A kept row outside the capacity, or in place one with keep[i] < i, sets
+ * KVQ_DEVERR_KEEP_INDEX and is not moved (its destination's contents are
+ * unspecified).
  * K is moved as it was written: with rotary positions it keeps the rotation
  * of its first position.
  * In place the kernel's blocks wait for one another (a cooperative launch with

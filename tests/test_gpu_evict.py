@@ -526,3 +526,55 @@ def test_refuses_wrong_tensors(kvq):
     other = kvq.make_evict_params(1, cache.width, 20, num_blocks=cache.nb + 1, block_size=16, num_kv_heads=2)
     with pytest.raises(kvq.KvqError):
         kvq.kvq_evict_compact(g, other, table, None, keep, lens.clone(), None, ws)
+
+
+# ------------------------------------------------- padding with odd contents
+
+@pytest.mark.parametrize("name", ["int8 row d128", "fp8 tensor cap", "int4 channel d256", "int8 row d256 g6",
+                                  "int8 channel d64", "int8 group k, row v", "latent d576"])
+@pytest.mark.parametrize("c", [1, 3, 12, 40, 130])
+@pytest.mark.parametrize("junk", [np.nan, np.inf])
+def test_padding_tokens_may_hold_anything(kvq, name, c, junk):
+    """A padded batch: the queries of tokens that see nothing hold NaN or
+    infinities, which reach neither the other tokens' rows nor the keys."""
+    case = dataclasses.replace(CASES[name], c=c, seed=c, lens=(max(c, 333), max(c, 150), 150 + c))
+    cache = ref.Cache(case)
+    s = slopes_of(case.hq)
+    end = np.stack([L - c + np.arange(c) + 1 for L in case.lens]).astype(np.int32)
+    end[0, ::2] = 0         # every second token
+    end[1] = -1             # a whole sequence
+    end[2, c // 2:] = 5     # the tail, by an interval that ends before it begins
+    begin = np.zeros_like(end)
+    begin[2, c // 2:] = 9
+    r_lse = ref.attend(cache, s, begin, end)[1]
+    mass = random_mass(cache)
+    clean = cache.q.copy()
+    dead = end <= begin
+    cache.q[dead] = junk
+    cache.q[dead, :, ::3] = 1.0
+    got = run(kvq, cache, s, begin, end)
+    m = mass_call(kvq, cache, r_lse, mass, 0.5, c, s, begin, end)
+    cache.q = clean  # the plain forms see the queries without the junk
+    check(cache, got, s, begin, end)
+    check_mass(m, cache, r_lse, mass, 0.5, c, s, begin, end)
+
+
+@pytest.mark.parametrize("last,err", [(59, 0), (18, 1), (0, 1)])
+def test_compact_refuses_rows_from_before(kvq, last, err):
+    """In place a kept row from before its destination (here row 19's) is flagged
+    and not moved; the same row twice is copied twice."""
+    case = ref.Case(lens=(100,), hkv=1, hq=4)
+    cache = ref.Cache(case)
+    keep = np.arange(40, 60).astype(np.int32).reshape(1, 1, 20)
+    keep[0, 0, 4] = keep[0, 0, 3]
+    keep[0, 0, 19] = last
+    g = gpu_cache(kvq, cache)
+    p = kvq.make_evict_params(1, cache.width, 20, num_blocks=cache.nb, block_size=16, num_kv_heads=1)
+    ws = torch.zeros(kvq.kvq_evict_compact_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+    kvq.kvq_evict_compact(g, p, dev(cache.table), None, dev(keep), dev(np.array([20], np.int32)), None, ws)
+    assert kvq.kvq_get_device_error() == (kvq.DEVERR_KEEP_INDEX if err else 0)
+    got = g.k_codes.cpu().numpy()
+    for i in range(19 if err else 20):
+        src = keep[0, 0, i]
+        assert np.array_equal(got[cache.table[0, i // 16], 0, i % 16],
+                              cache.k_codes[cache.table[0, src // 16], 0, src % 16])
