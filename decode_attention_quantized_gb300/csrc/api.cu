@@ -872,7 +872,7 @@ kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse
   if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
   const int C = p->q_tokens, G = p->num_q_heads / c->num_kv_heads;
   if (G > 8 || p->batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
-  if ((long long)p->batch * C > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)(p->batch > 1 ? p->batch : 1) * C > (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
   MaskShape s{};
   s.split = lse && c->k_mode == KVQ_SCALE_PER_CHANNEL;
   const int tile = s.split && c->head_dim == 256 ? kQtRows / 2 : kQtRows;
@@ -957,7 +957,7 @@ kvq_status mass_shape(const kvq_cache* c, const kvq_decode_params* p, MassShape*
   if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
   const int C = p->q_tokens, G = p->num_q_heads / c->num_kv_heads;
   if (G > 8 || p->batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
-  if ((long long)p->batch * C > (1LL << 31) - 1) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)(p->batch > 1 ? p->batch : 1) * C > (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
   MassShape s{};
   const bool tc = mass_tc_ok(c, p, C < kMassTcRows ? C * G : kMassTcRows);
   const int most = (c->head_dim == 576 ? 32 : (tc ? kMassTcRows : 64)) / G;
@@ -1034,6 +1034,21 @@ kvq_status compact_plan(const kvq_cache* c, const kvq_evict_params* p, bool mass
 }
 
 }  // namespace
+
+cudaError_t raise_smem_limit(const void* kernel, std::atomic<int> (&smem_set)[64], size_t smem) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (smem_set[dev].load(std::memory_order_acquire) >= (int)smem) return cudaSuccess;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  if (smem_set[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) smem_set[dev].store((int)smem, std::memory_order_release);
+  return e;
+}
+
 }  // namespace kvq
 
 using namespace kvq;
@@ -1191,6 +1206,12 @@ KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_pa
   if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256) ||
       !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)) || (head_sink && !aligned(head_sink, 4)))
     return KVQ_ERR_INVALID_ARG;
+  {
+    // some rows are finished while others' queries are still to be read
+    const uint64_t rows = (uint64_t)params->batch * params->q_tokens * params->num_q_heads;
+    const uint64_t q0 = reinterpret_cast<uint64_t>(q), o0 = reinterpret_cast<uint64_t>(out);
+    if (q0 < o0 + rows * cache->v_head_size * 2 && o0 < q0 + rows * cache->head_dim * 2) return KVQ_ERR_INVALID_ARG;
+  }
   size_t head = 0, need = 0;
   if (kvq_status s = masked_workspace(cache, params, shape, &head, &need)) return s;
   if (workspace_bytes < need) return KVQ_ERR_WORKSPACE_TOO_SMALL;

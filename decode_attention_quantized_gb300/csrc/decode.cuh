@@ -1357,18 +1357,8 @@ __global__ void __launch_bounds__(288, MINB)
 // query for a small plan cannot undercut a larger plan launched later.
 template <int DT, int D, int MINB, int NT, int GS, int RULE>
 cudaError_t ensure_smem(size_t smem) {
-  static int smem_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(decode_kernel<DT, D, MINB, NT, GS, RULE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-    if (e != cudaSuccess) return e;
-    smem_set[dev] = (int)smem;
-  }
-  return cudaSuccess;
+  static std::atomic<int> smem_set[64];
+  return raise_smem_limit(reinterpret_cast<const void*>(decode_kernel<DT, D, MINB, NT, GS, RULE>), smem_set, smem);
 }
 
 template <int DT, int D, int MINB, int NT, int GS, int RULE>

@@ -970,16 +970,9 @@ __global__ void __launch_bounds__(kTcWarps * 32, 1)
 template <int DT, int D, int NR, bool GRP>
 cudaError_t launch_decode_tc_d(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid,
                                size_t smem, cudaStream_t stream) {
-  static int smem_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(decode_tc_kernel<DT, D, NR, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    smem_set[dev] = (int)smem;
-  }
+  static std::atomic<int> smem_set[64];
+  const void* kernel = reinterpret_cast<const void*>(decode_tc_kernel<DT, D, NR, GRP>);
+  if (cudaError_t e = raise_smem_limit(kernel, smem_set, smem)) return e;
   return launch_pdl(decode_tc_kernel<DT, D, NR, GRP>, grid, kTcWarps * 32, smem, stream, tk, tv, a);
 }
 

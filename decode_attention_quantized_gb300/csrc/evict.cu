@@ -495,17 +495,8 @@ cudaError_t launch_evict_select(const SelectArgs& a, int cluster, cudaStream_t s
 
 namespace {
 cudaError_t compact_smem_limit(size_t smem) {
-  static int smem_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(evict_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    smem_set[dev] = (int)smem;
-  }
-  return cudaSuccess;
+  static std::atomic<int> smem_set[64];
+  return raise_smem_limit(reinterpret_cast<const void*>(evict_compact_kernel), smem_set, smem);
 }
 }  // namespace
 

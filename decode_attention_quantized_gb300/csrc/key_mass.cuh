@@ -282,17 +282,9 @@ __global__ void __launch_bounds__(kMassThreads, NT == 1 && D <= 256 ? (SPLIT ? 3
 template <int DT, int D, int NT, bool SPLIT, bool GRP>
 cudaError_t key_mass_d(const CUtensorMap* tk, const DecodeArgs* a, const MassArgs* m, int grid, size_t smem,
                        cudaStream_t stream, int* blocks_per_sm) {
-  static int smem_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(key_mass_kernel<DT, D, NT, SPLIT, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-    if (e != cudaSuccess) return e;
-    smem_set[dev] = (int)smem;
-  }
+  static std::atomic<int> smem_set[64];
+  const void* kernel = reinterpret_cast<const void*>(key_mass_kernel<DT, D, NT, SPLIT, GRP>);
+  if (cudaError_t e = raise_smem_limit(kernel, smem_set, smem)) return e;
   if (blocks_per_sm)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, key_mass_kernel<DT, D, NT, SPLIT, GRP>,
                                                          kMassThreads, smem);

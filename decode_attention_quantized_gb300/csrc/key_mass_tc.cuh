@@ -434,16 +434,9 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
 template <int DT, int D, bool SPLIT, bool CAP>
 cudaError_t launch_key_mass_tc_d(const CUtensorMap& tk, const DecodeArgs& a, const MassArgs& m, int nr, int grid,
                                  size_t smem, cudaStream_t stream) {
-  static int smem_set[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (smem_set[dev] < (int)smem) {
-    e = cudaFuncSetAttribute(key_mass_tc_kernel<DT, D, SPLIT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    smem_set[dev] = (int)smem;
-  }
+  static std::atomic<int> smem_set[64];
+  const void* kernel = reinterpret_cast<const void*>(key_mass_tc_kernel<DT, D, SPLIT, CAP>);
+  if (cudaError_t e = raise_smem_limit(kernel, smem_set, smem)) return e;
   return launch_pdl(key_mass_tc_kernel<DT, D, SPLIT, CAP>, grid, kMassTcWarps * 32, smem, stream, tk, a, m, nr);
 }
 

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -210,6 +211,11 @@ __host__ __device__ constexpr QtSmem qt_smem_layout(int head_dim, int stages, in
   s.total = s.slot + 16;
   return s;
 }
+
+// Raises (never lowers) a kernel's dynamic shared-memory limit on the current
+// device; smem_set holds what it was raised to.  Of two threads that raise it
+// at once the larger limit stays.
+cudaError_t raise_smem_limit(const void* kernel, std::atomic<int> (&smem_set)[64], size_t smem);
 
 // Launches a kernel with programmatic stream serialization: it may start while
 // the previous kernel on the stream finishes, and every kvq kernel waits

@@ -379,7 +379,7 @@ typedef struct {
  * a per-channel K scale the query operand is then carried in two f16 parts,
  * which costs time (a prompt's tiles about half as much again at head_dim 128
  * and twice at 256); lse_out NULL leaves that out.  batch <= 1024;
- * batch * C < 2^31.  workspace: at least
+ * batch * C <= 2^30.  out must not overlap q.  workspace: at least
  * kvq_attend_masked_workspace_size bytes, 256-byte aligned; it belongs to
  * this call until the call's kernels have run. */
 KVQ_API kvq_status kvq_attend_masked_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,

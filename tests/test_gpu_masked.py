@@ -455,3 +455,76 @@ def test_tcgen05_off_and_bounds(kvq, c):
                           dev(cache.table), dev(np.array(case.lens, np.int32)), None, out, lse, ws)
     check(cache, (out.double().cpu().numpy(), lse.double().cpu().numpy()), s)
     assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("d,c,km", [(64, 1, ROW), (128, 4, CHANNEL), (128, 40, ROW), (256, 50, CHANNEL), (256, 70, ROW)])
+def test_captured_and_on_two_streams(kvq, d, c, km):
+    """Two calls with workspaces of their own, on two streams at once and
+    captured into graphs that replay on two streams: the same bits as one call
+    at a time."""
+    calls = []
+    for seed in (1, 2):
+        case = ref.Case(d=d, km=km, vm=km, c=c, lens=(900, 150, 411), seed=seed)
+        cache = ref.Cache(case)
+        s = slopes_of(8)
+        want = run(kvq, cache, s)
+        check(cache, want, s)
+        g = gpu_cache(kvq, cache)
+        p = kvq.make_params(3, 8, c, cache.width)
+        ws = torch.zeros(kvq.kvq_attend_masked_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+        out = torch.zeros((3, c, 8, d), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((3, c, 8), device="cuda")
+        args = (g, p, kvq.ScoreMask(slopes=dev(np.array(s, np.float32))), dev(cache.q).to(torch.bfloat16),
+                dev(cache.table), dev(np.array(case.lens, np.int32)), None, out, lse, ws)
+        calls.append((args, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def same():
+        torch.cuda.synchronize()
+        for args, want, _ in calls:
+            assert np.array_equal(args[7].double().cpu().numpy(), want[0])
+            assert np.array_equal(args[8].double().cpu().numpy(), want[1])
+            args[7].zero_()
+            args[8].zero_()
+        torch.cuda.synchronize()
+
+    for _ in range(4):
+        for args, _, st in calls:
+            kvq.kvq_attend_masked(*args, stream=st)
+    same()
+    graphs = []
+    for args, _, st in calls:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            kvq.kvq_attend_masked(*args)
+        graphs.append((gr, st))
+    for _ in range(4):
+        for gr, st in graphs:
+            with torch.cuda.stream(st):
+                gr.replay()
+    same()
+    assert kvq.kvq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("d,c", [(64, 1), (128, 40), (256, 3)])
+def test_bad_pages_and_lengths_are_flagged(kvq, d, c):
+    """A block id outside the pool, or a length outside the capacity, sets the
+    device error; the other sequences' rows are right."""
+    case = ref.Case(d=d, c=c, lens=(100, 90, 170))
+    cache = ref.Cache(case)
+    want = run(kvq, cache)
+    good = cache.table.copy()
+    g = gpu_cache(kvq, cache)
+    for bad in (cache.nb, -1, 2 ** 31 - 1):
+        table = good.copy()
+        table[1, 2] = bad
+        for lens, err in (((100, 90, 170), kvq.DEVERR_BLOCK_ID), ((100, -3, 170), kvq.DEVERR_SEQ_LEN)):
+            p = kvq.make_params(3, 8, c, cache.width)
+            ws = torch.zeros(kvq.kvq_attend_masked_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+            out = torch.zeros((3, c, 8, d), dtype=torch.bfloat16, device="cuda")
+            lse = torch.zeros((3, c, 8), device="cuda")
+            kvq.kvq_attend_masked(g, p, None, dev(cache.q).to(torch.bfloat16), dev(table),
+                                  dev(np.array(lens, np.int32)), None, out, lse, ws)
+            assert kvq.kvq_get_device_error() == err
+            o = out.double().cpu().numpy()
+            assert np.allclose(o[[0, 2]], want[0][[0, 2]], rtol=2.0 ** -7, atol=2.0 ** -7)

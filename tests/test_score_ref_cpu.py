@@ -166,3 +166,21 @@ def test_evict_refuses_pointers(kvq):
     for other in (dict(num_blocks=9), dict(block_size=32, num_blocks=4), dict(num_kv_heads=1)):
         o = cache_desc(kvq, **other)
         assert lib.kvq_evict_compact(ctypes.byref(o), ctypes.byref(p), *m, 1 << 40, None) == 1
+
+
+def test_masked_and_mass_refuse_token_counts_that_overflow(kvq):
+    lib, c = kvq.load(), cache_desc(kvq)
+    n = ctypes.c_size_t(0)
+    for batch, tokens in ((0, 2 ** 31 - 1), (1, 2 ** 31 - 1), (1, 2 ** 30 + 1), (1024, 2 ** 20 + 1)):
+        p = params(kvq, batch=batch, q_tokens=tokens)
+        a = [ctypes.byref(c), ctypes.byref(p)]
+        assert lib.kvq_attend_masked_workspace_size(*a, ctypes.byref(n)) == 2
+        assert lib.kvq_key_mass_workspace_size(*a, ctypes.byref(n)) == 2
+
+
+def test_masked_refuses_an_output_over_the_queries(kvq):
+    lib, c, p = kvq.load(), cache_desc(kvq), params(kvq)
+    size = 2 * 5 * 8 * c.head_dim * 2
+    for out in (FAKE, FAKE + 16, FAKE + size - 16, FAKE - size + 16):
+        assert lib.kvq_attend_masked(ctypes.byref(c), ctypes.byref(p), None, FAKE, FAKE, FAKE, None, out, None, FAKE,
+                                     1 << 40, None) == 1
