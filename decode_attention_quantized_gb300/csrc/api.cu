@@ -992,6 +992,7 @@ kvq_status check_evict(const kvq_evict_params* p) {
   if (cap > (1LL << 30)) return KVQ_ERR_INVALID_ARG;
   if (p->budget > cap) return KVQ_ERR_INVALID_ARG;
   if ((long long)p->batch * p->num_kv_heads > (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)p->num_kv_heads * p->block_size > (1LL << 29)) return KVQ_ERR_UNSUPPORTED;  // a page's weights: 2 GB
   return KVQ_OK;
 }
 
@@ -1384,6 +1385,9 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
   a.sinks = params->sinks;
   a.recent = params->recent;
   a.err = dev->err;
+  // many heads
+  if ((long long)a.batch * a.num_kv_heads >= dev->sms && select_many_smem(a.lim) <= 110 * 1024 && aligned(mass, 16))
+    return from_cuda(launch_evict_select_many(a, reinterpret_cast<cudaStream_t>(stream)));
   // a CTA keeps 16,384 rows in registers: as many CTAs (up to 16) as hold the
   // longest head, more while SMs are free and each still has 2048 rows
   const long long segs = (long long)params->batch * params->num_kv_heads;

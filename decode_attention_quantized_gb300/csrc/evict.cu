@@ -40,6 +40,35 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return f == f ? k : 1u;
 }
 
+// What both kernels begin with: the lengths, and the rows that stay whatever
+// their weight (t of `threads` threads of the head).  False: there are no
+// others to choose.
+struct SelectHead {
+  int L, need;  // rows, and how many of those between the ends stay
+};
+__device__ __forceinline__ bool select_ends(const SelectArgs& a, int b, int h, int t, int threads, SelectHead& hd) {
+  const int raw = a.seq_lens[b];
+  const int L = raw < 0 ? 0 : (raw > a.lim ? a.lim : raw);
+  if (raw != L && h == 0 && t == 0) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
+  int32_t* keep = a.keep + (size_t)(b * a.num_kv_heads + h) * a.budget;
+  const int n = min(L, a.budget);
+  if (h == 0 && t == 0) a.kept_lens[b] = n;
+  // everything stays, or only the protected ends do
+  const int need = a.budget - a.sinks - a.recent;
+  const bool whole = L <= a.budget;
+  if (whole || need == 0) {
+    for (int i = t; i < a.budget; i += threads) keep[i] = i >= n ? -1 : (whole || i < a.sinks ? i : L - a.budget + i);
+    return false;
+  }
+  for (int i = t; i < a.sinks + a.recent; i += threads) {
+    if (i < a.sinks) keep[i] = i;
+    else keep[need + i] = L - a.recent + (i - a.sinks);
+  }
+  hd.L = L;
+  hd.need = need;
+  return true;
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(const SelectArgs a) {
   __shared__ __align__(16) uint32_t hist[257 * 32];  // [bin][lane]; bin 256: keys that no longer match
   __shared__ uint32_t total[2][256];                 // this CTA's counts of a digit (two passes' worth)
@@ -51,24 +80,10 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  const int raw = a.seq_lens[b];
-  const int L = raw < 0 ? 0 : (raw > a.lim ? a.lim : raw);
-  if (raw != L && h == 0 && rank == 0 && tid == 0) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
+  SelectHead hd;
+  if (!select_ends(a, b, h, rank * kSelThreads + tid, cs * kSelThreads, hd)) return;  // (the whole cluster)
+  const int L = hd.L, need_all = hd.need;
   int32_t* keep = a.keep + (size_t)seg * a.budget;
-  const int n = min(L, a.budget);
-  if (h == 0 && rank == 0 && tid == 0) a.kept_lens[b] = n;
-  // everything stays, or only the protected ends do (the whole cluster agrees)
-  const int need_all = a.budget - a.sinks - a.recent;
-  const bool whole = L <= a.budget;
-  if (whole || need_all == 0) {
-    for (int i = rank * kSelThreads + tid; i < a.budget; i += cs * kSelThreads)
-      keep[i] = i >= n ? -1 : (whole || i < a.sinks ? i : L - a.budget + i);
-    return;
-  }
-  for (int i = rank * kSelThreads + tid; i < a.sinks + a.recent; i += cs * kSelThreads) {
-    if (i < a.sinks) keep[i] = i;
-    else keep[need_all + i] = L - a.recent + (i - a.sinks);
-  }
 
   // The M rows between the ends, in runs of 32 from a multiple of 32 on (so
   // that a run meets one page, or two of 16 rows), go to as many CTAs as hold
@@ -252,6 +267,395 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     });
   }
   ptx::cluster_sync();  // no CTA leaves while another reads its counts
+}
+
+// -------------------------------------------------------- select, many heads
+//
+// With a head or more per SM one CTA takes a head and reads its weights once:
+//   1. a sample of 4096 rows, evenly spread, brackets the threshold: two ranks
+//      three standard deviations to either side of the wanted one, to 16 bits;
+//   2. one pass over the weights (16 bytes a lane) marks the rows above the
+//      bracket and those inside it, a bit each: two compares and two votes a
+//      row, nothing else;
+//   3. the weights of the rows inside are read again into a list, whose radix
+//      select by key and then by row (the lower row first), digits of 8 bits,
+//      adds its rows to the bits of the rows above;
+//   4. the bits give the rows in order.
+// Exact whatever the sample was: when the wanted rank turns out not to lie in
+// the bracket, or the list overflows (thousands of rows of nearly the same
+// weight), the head goes through the digits of the kernel above, reading its
+// weights again for each (from L2).  512 heads of up to 131,072 rows: @@ us
+// (276 with the clusters above, whose loads, digit passes, counts and output
+// took 107, 62, 70 and 38 us of it).
+constexpr int kManyThreads = kSelThreads, kManyWarps = kManyThreads / 32;
+constexpr int kManySample = 8;                              // samples a thread
+constexpr int kManySamples = kManySample * kManyThreads;
+constexpr int kManyList = 6144;                             // rows inside the bracket
+static_assert(2 * kManyList >= 257 * 32, "the digits' columns take the list's place");
+
+// The digit of the need-th largest key from a digit's counts (every warp for
+// itself, eight bins a lane from the highest on).
+__device__ __forceinline__ void find_digit(const uint32_t* bins, uint32_t need, int lane, uint32_t& digit,
+                                           uint32_t& same, uint32_t& before) {
+  uint32_t cnt[8], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += cnt[i] = bins[255 - (8 * lane + i)];
+  uint32_t above = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
+    if (lane >= o) above += y;
+  }
+  const int owner = max(0, __ffs(__ballot_sync(0xffffffffu, above >= need)) - 1);
+  above -= sum;
+  uint32_t d = 0, c = 0;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (!found) {
+      if (above + cnt[i] >= need) {
+        found = true;
+        d = 255u - (8 * lane + i);
+        c = cnt[i];
+      } else {
+        above += cnt[i];
+      }
+    }
+  }
+  digit = __shfl_sync(0xffffffffu, d, owner);
+  same = __shfl_sync(0xffffffffu, c, owner);
+  before = __shfl_sync(0xffffffffu, above, owner);
+}
+
+__global__ void __launch_bounds__(kManyThreads, 2) evict_select_many_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint32_t many_smem[];
+  uint32_t* lkey = many_smem;         // [kManyList] keys inside the bracket, less its lower end
+  uint32_t* lrow = lkey + kManyList;  // [kManyList] their rows, from `first` on
+  uint32_t* hist = many_smem;         // [257][32] a digit's counts, a column a lane
+  // [blocks][2][4] a block of 128 rows: the rows that stay, then those inside
+  // the bracket; bit l of word c is row 4 l + c
+  uint32_t* mask = lrow + kManyList;
+  __shared__ uint32_t bins[2][256];
+  __shared__ uint32_t s_list, s_above, s_valid, s_warp[kManyWarps], s_equal[kManyWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int seg = (int)blockIdx.x, b = seg / a.num_kv_heads, h = seg - b * a.num_kv_heads;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  SelectHead hd;
+  if (!select_ends(a, b, h, tid, kManyThreads, hd)) return;
+  const int L = hd.L;
+  const int M = L - a.sinks - a.recent, first = a.sinks & ~31, runs = (L - a.recent - first + 31) >> 5;
+  const int32_t* bt = a.block_table + (size_t)b * a.max_blocks_per_seq;
+  const char* head = reinterpret_cast<const char*>(a.mass + ((size_t)h << a.log2_bs));
+  const uint32_t page_bytes = 4u * ((uint32_t)a.num_kv_heads << a.log2_bs);  // (the host's check: below 2^32)
+  const bool two = a.log2_bs == 4;  // a run of 32 rows lies on one page, or on two of 16 rows
+  bool bad = false;
+  if (tid == 0) s_list = s_above = s_valid = 0;
+
+  // the page of run base + lane (of half a run, when two), -1: unreadable or none
+  auto look_up = [&](int base) -> int {
+    const int x = two ? 16 * lane : 32 * lane;
+    if (lane >= (two ? 16 : 8) || first + base * 32 + x >= L - a.recent) return -1;
+    const int id = bt[(first + base * 32 + x) >> a.log2_bs];
+    if ((unsigned)id < (unsigned)a.num_blocks) return id;
+    bad = true;
+    return -1;
+  };
+  // this lane's weights of the eight runs from base on
+  auto fetch = [&](int base, int ids, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int id = __shfl_sync(0xffffffffu, ids, two ? 2 * i + (lane >> 4) : i);
+      f[i] = __uint_as_float(0x7FC00000u);
+      if (id >= 0)
+        f[i] = *reinterpret_cast<const float*>(head + (uint64_t)(uint32_t)id * page_bytes +
+                                               4u * (uint32_t)((first + 32 * (base + i) + lane) & (a.block_size - 1)));
+    }
+  };
+  // f(run, key) for the runs of [r0, r1), eight at a time from r0 on, `step`
+  // apart; key 0: not one of the M rows
+  auto rows = [&](int r0, int r1, int step, auto f) {
+    if (r0 >= r1) return;
+    float now[8], next[8];
+    fetch(r0, look_up(r0), now);
+    int ids = look_up(r0 + step);
+    for (int base = r0; base < r1; base += step) {
+      fetch(base + step, ids, next);
+      ids = look_up(base + 2 * step);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = (unsigned)(first + 32 * (base + i) + lane - a.sinks) < (unsigned)M && base + i < r1;
+        f(base, i, in ? order_key(now[i]) : 0u);
+        now[i] = next[i];
+      }
+    }
+  };
+  // one digit of the need-th largest of the keys that `each` goes through
+  uint32_t* my_hist = hist + lane;
+  auto digit_of = [&](auto each, int shift, uint32_t prefix, uint32_t need, uint32_t& digit, uint32_t& same,
+                      uint32_t& before) {
+    __syncthreads();
+    for (int i = tid; i < 256 * 32 / 4; i += kManyThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    each([&](uint32_t k) {
+      const uint32_t d = shift == 24 ? k >> 24 : min((k >> shift) - (prefix << 8), 256u);
+      atomicAdd(&my_hist[d * 32], 1u);
+    });
+    __syncthreads();
+    const int bin = tid >> 1, c0 = (tid & 1) * 16;  // two threads a bin
+    uint32_t s = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s += hist[bin * 32 + c0 + ((j + bin) & 15)];
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    if ((tid & 1) == 0) bins[0][bin] = s;
+    __syncthreads();
+    find_digit(bins[0], need, lane, digit, same, before);
+  };
+
+  // key of row `row` from `first` on
+  auto key_at = [&](int row) -> uint32_t {
+    const int pos = first + row, id = bt[pos >> a.log2_bs];
+    if ((unsigned)id >= (unsigned)a.num_blocks) return 1u;
+    return order_key(*reinterpret_cast<const float*>(head + (uint64_t)(uint32_t)id * page_bytes +
+                                                     4u * (uint32_t)(pos & (a.block_size - 1))));
+  };
+
+  // ---- the bracket [lo, hi]
+  uint32_t need = (uint32_t)hd.need, lo = 1u, hi = 0xFFFFFFFFu;
+  if (M > kManyList) {
+    uint32_t smp[kManySample];
+#pragma unroll
+    for (int j = 0; j < kManySample; ++j) {
+      smp[j] = key_at(a.sinks - first + (int)(((long long)(tid + j * kManyThreads) * M) / kManySamples));
+    }
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int j = 0; j < kManySample; ++j) f(smp[j]);
+    };
+    const float r = (float)need / (float)M * kManySamples;
+    // five standard deviations to either side (one head in a million misses),
+    // fewer if the list would not hold them
+    const float sigma = sqrtf(r * fmaxf(0.0f, 1.0f - r / kManySamples));
+    const float half = fminf(5.0f * sigma + 2.0f, 0.45f * kManyList * kManySamples / (float)M);
+    const int rank_hi = (int)floorf(r - half), rank_lo = (int)ceilf(r + half);
+    uint32_t d, d2, same, before;
+    if (rank_hi >= 1) {
+      digit_of(each, 24, 0u, (uint32_t)rank_hi, d, same, before);
+      digit_of(each, 16, d, (uint32_t)rank_hi - before, d2, same, before);
+      hi = (d << 24) | (d2 << 16) | 0xFFFFu;
+    }
+    if (rank_lo <= kManySamples) {
+      digit_of(each, 24, 0u, (uint32_t)rank_lo, d, same, before);
+      digit_of(each, 16, d, (uint32_t)rank_lo - before, d2, same, before);
+      lo = max(1u, (d << 24) | (d2 << 16));
+    }
+  }
+  __syncthreads();
+
+  // ---- the pass over the weights.  Floats compare as their keys do, but for
+  // the two zeros and NaN, which the list's exact keys put right: a row above
+  // as a float is above, and a row neither above nor below the lower end is
+  // looked at again.
+  const int blocks = (L - a.recent - first + 127) >> 7;
+  {
+    auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); };
+    const float lo_f = value(lo), hi_f = value(hi);
+    constexpr int kStep = kManyWarps * 4;  // four blocks a warp at a time
+    // the page of the 16 rows from base * 128 + 16 * lane on, -1: unreadable or none
+    auto look_up16 = [&](int base) -> int {
+      const int pos = first + base * 128 + 16 * lane;
+      if (pos >= L - a.recent) return -1;
+      const int id = bt[pos >> a.log2_bs];
+      if ((unsigned)id < (unsigned)a.num_blocks) return id;
+      bad = true;
+      return -1;
+    };
+    auto fetch4 = [&](int base, int ids, float4 (&f)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int id = __shfl_sync(0xffffffffu, ids, 8 * i + (lane >> 2));
+        const float nan = __uint_as_float(0x7FC00000u);
+        f[i] = make_float4(nan, nan, nan, nan);
+        if (id >= 0)
+          f[i] = *reinterpret_cast<const float4*>(
+              head + (uint64_t)(uint32_t)id * page_bytes +
+              4u * (uint32_t)((first + 128 * (base + i) + 4 * lane) & (a.block_size - 1)));
+      }
+    };
+    float4 now[4], next[4];
+    int ids = look_up16(warp * 4);
+    if (warp * 4 < blocks) fetch4(warp * 4, ids, now);
+    ids = look_up16(warp * 4 + kStep);
+    for (int base = warp * 4; base < blocks; base += kStep) {
+      fetch4(base + kStep, ids, next);
+      ids = look_up16(base + 2 * kStep);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+        uint32_t word = 0;
+        const int row0 = first + 128 * (base + i);
+        const bool inner = row0 >= a.sinks && row0 + 128 <= L - a.recent;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool ok = inner || (unsigned)(row0 + 4 * lane + c - a.sinks) < (unsigned)M;
+          const uint32_t up = __ballot_sync(0xffffffffu, ok && x[c] > hi_f);
+          const uint32_t in = __ballot_sync(0xffffffffu, ok && !(x[c] > hi_f) && !(x[c] < lo_f));
+          if (lane == c) word = up;
+          if (lane == 4 + c) word = in;
+        }
+        if (lane < 8 && base + i < blocks) mask[(base + i) * 8 + lane] = word;
+        now[i] = next[i];
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- the list: the rows, then their keys
+  {
+    uint32_t above = 0, mine = 0;
+    for (int w = tid; w < blocks * 4; w += kManyThreads) {
+      above += __popc(mask[(w >> 2) * 8 + (w & 3)]);
+      mine += __popc(mask[(w >> 2) * 8 + 4 + (w & 3)]);
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    uint32_t at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    uint32_t start = 0;
+    if (lane == 31) {
+      start = atomicAdd(&s_list, at);
+      atomicAdd(&s_above, above);
+    }
+    at += __shfl_sync(0xffffffffu, start, 31) - mine;
+    for (int w = tid; w < blocks * 4; w += kManyThreads) {
+      for (uint32_t m = mask[(w >> 2) * 8 + 4 + (w & 3)]; m; m &= m - 1, ++at)
+        if (at < kManyList) lrow[at] = (uint32_t)((w >> 2) * 128 + 4 * (__ffs(m) - 1) + (w & 3));
+    }
+  }
+  if (tid < 256) bins[0][tid] = 0;
+  __syncthreads();
+  const uint32_t n = s_list;
+  if (n <= kManyList) {
+    uint32_t above = 0, valid = 0;
+#pragma unroll 4
+    for (uint32_t i = tid; i < n; i += kManyThreads) {
+      const uint32_t row = lrow[i], k = key_at((int)row);
+      if (k > hi) {
+        atomicOr(&mask[(row >> 7) * 8 + (row & 3u)], 1u << ((row & 127u) >> 2));
+        ++above;
+      }
+      const bool in = k - lo <= hi - lo;
+      valid += in;
+      lkey[i] = in ? k - lo : 0u;
+      if (!in) lrow[i] = 0xFFFFFFFFu;  // not one of the list's: below every entry
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    valid = __reduce_add_sync(0xffffffffu, valid);
+    if (lane == 0) {
+      atomicAdd(&s_above, above);
+      atomicAdd(&s_valid, valid);
+    }
+  }
+  __syncthreads();
+  int32_t* mid = a.keep + (size_t)seg * a.budget + a.sinks;
+  if (n <= kManyList && s_above <= need && need - s_above <= s_valid) {
+    // ---- its need-th largest, the lowest row among equals
+    need -= s_above;
+    auto entry = [&](uint32_t i) { return ((uint64_t)lkey[i] << 32) | (uint32_t)~lrow[i]; };
+    int shift = 64 - __clz((int)((hi - lo) | 1u));  // no entry has bits above
+    uint64_t pre = 0;                               // the entries of pre at `shift` and above it stay
+    const bool none = need == 0, all = need == s_valid;
+    bool open = !none && !all;
+    for (int pass = 0; open && shift > 0; ++pass) {
+      const int width = min(8, shift), low = shift - width;
+      uint32_t* cnt = bins[pass & 1];
+      if (tid < 256) bins[(pass + 1) & 1][tid] = 0;
+      for (uint32_t i = tid; i < n; i += kManyThreads) {
+        const uint64_t e = entry(i);
+        if (pass == 0 || (e >> shift) == pre) atomicAdd(&cnt[(uint32_t)(e >> low) & ((1u << width) - 1u)], 1u);
+      }
+      __syncthreads();
+      uint32_t d, same, before;
+      find_digit(cnt, need, lane, d, same, before);
+      pre = (pre << width) | d;
+      need -= before;
+      shift = low;
+      open = same > need;
+      __syncthreads();
+    }
+    if (!none) {
+      for (uint32_t i = tid; i < n; i += kManyThreads) {
+        const uint32_t row = lrow[i];
+        if (row != 0xFFFFFFFFu && (all || (entry(i) >> shift) >= pre))
+          atomicOr(&mask[(row >> 7) * 8 + (row & 3u)], 1u << ((row & 127u) >> 2));
+      }
+    }
+    __syncthreads();
+
+    // ---- the rows in order, a stretch of blocks a warp
+    const int per = (blocks + kManyWarps - 1) / kManyWarps, w0 = min(blocks, warp * per), w1 = min(blocks, w0 + per);
+    uint32_t kept = 0;
+    for (int w = 4 * w0 + lane; w < 4 * w1; w += 32) kept += __popc(mask[(w >> 2) * 8 + (w & 3)]);
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if (lane == 0) s_warp[warp] = kept;
+    __syncthreads();
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+    for (int w = w0; w < w1; ++w) {
+      const uint4 m = *reinterpret_cast<const uint4*>(mask + w * 8);
+      if ((m.x | m.y | m.z | m.w) == 0u) continue;
+      const uint32_t four = (m.x >> lane & 1u) | (m.y >> lane & 1u) << 1 | (m.z >> lane & 1u) << 2 | (m.w >> lane & 1u) << 3;
+      // rows of the lanes below
+      const uint32_t below = (1u << lane) - 1u;
+      uint32_t to = at + __popc(m.x & below) + __popc(m.y & below) + __popc(m.z & below) + __popc(m.w & below);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (four >> c & 1u) {
+          // (never more than that, unless another stream changes the weights meanwhile)
+          if (to < (uint32_t)hd.need) mid[to] = first + 128 * w + 4 * lane + c;
+          ++to;
+        }
+      at += __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+    }
+  } else {
+    // ---- digit by digit over all rows
+    auto each = [&](auto f) { rows(warp * 8, runs, kManyWarps * 8, [&](int, int, uint32_t k) { f(k); }); };
+    uint32_t T = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      uint32_t d, same, before;
+      digit_of(each, 24 - 8 * pass, T, need, d, same, before);
+      T = (T << 8) | d;
+      need -= before;
+    }
+    // the rows above T, and the first `need` equal to it, a stretch of runs a warp
+    const int per = (runs + kManyWarps - 1) / kManyWarps, w0 = min(runs, warp * per), w1 = min(runs, w0 + per);
+    uint32_t gt = 0, eq = 0;
+    rows(w0, w1, 8, [&](int, int, uint32_t k) {
+      gt += k > T;
+      eq += k == T;
+    });
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      s_warp[warp] = gt;
+      s_equal[warp] = eq;
+    }
+    __syncthreads();
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane] : 0u);
+    const uint32_t below = (1u << lane) - 1u;
+    rows(w0, w1, 8, [&](int base, int i, uint32_t k) {
+      const uint32_t up = __ballot_sync(0xffffffffu, k > T), same = __ballot_sync(0xffffffffu, k == T);
+      const uint32_t e = eq + __popc(same & below), to = gt + __popc(up & below) + min(e, need);
+      if ((k > T || (k == T && e < need)) && to < (uint32_t)hd.need) mid[to] = first + (base + i) * 32 + lane;
+      gt += __popc(up);
+      eq += __popc(same);
+    });
+  }
+  if (bad) atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
 }
 
 // ----------------------------------------------------------------- compact
@@ -491,6 +895,15 @@ cudaError_t launch_evict_select(const SelectArgs& a, int cluster, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+}
+
+size_t select_many_smem(int rows) { return (size_t)(2 * kManyList + 8 * ((rows + 127) / 128 + 1)) * 4; }
+
+cudaError_t launch_evict_select_many(const SelectArgs& a, cudaStream_t stream) {
+  static std::atomic<int> smem_set[64];
+  const size_t smem = select_many_smem(a.lim);
+  if (cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(evict_select_many_kernel), smem_set, smem)) return e;
+  return launch_pdl(evict_select_many_kernel, (unsigned)(a.batch * a.num_kv_heads), kManyThreads, smem, stream, a);
 }
 
 namespace {

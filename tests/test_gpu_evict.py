@@ -251,6 +251,75 @@ def test_select(kvq, kind, lens, budget, sinks, recent):
     check_select(kvq, masses(kind, 3, 16), lens, 16, budget, sinks, recent)
 
 
+@pytest.mark.parametrize("near", [1, 2, 511, 513, 1025, 2047, 2048, 2049, 6000])
+@pytest.mark.parametrize("kinds", [1, 7, 1 << 16])
+@pytest.mark.parametrize("neg", [False, True])
+def test_select_among_weights_of_one_upper_half(kvq, near, kinds, neg):
+    """`near` weights share the threshold's upper 16 bits (and take `kinds` lower
+    halves), with others above and below: around the number that is sorted out
+    on chip, over several CTAs, the threshold at either end and in the middle."""
+    r = np.random.default_rng(near + kinds)
+    L = 9000
+    table, nb = pages((L,), 64, 3)
+    up, down = (L - near) // 3, L - near - (L - near) // 3
+    w = np.concatenate([r.uniform(2.0, 9.0, up), r.uniform(0.0, 0.9, down)]).astype(np.float32)
+    low = (r.integers(0, kinds, near) * (65535 // max(1, kinds - 1) if kinds > 1 else 1)).astype(np.uint32)
+    w = np.concatenate([w, (np.uint32(0x3F800000) + low).view(np.float32)])
+    w = r.permutation(-w if neg else w)
+    mass = np.zeros((nb, 1, 64), np.float32)
+    j = np.arange(L)
+    mass[table[0, j // 64], 0, j % 64] = w
+    above = down if neg else up
+    for budget in sorted({above + 1, above + (near + 1) // 2, above + near}):
+        got = select_call(kvq, mass, table, (L,), nb, 64, budget, 0, 0)
+        want = ref.select(mass, table, (L,), 64, budget, 0, 0)
+        assert np.array_equal(got[0], want[0])
+    assert kvq.kvq_get_device_error() == 0
+
+
+MANY = (20000, 12001, 9000, 8300, 8193, 4097, 3000, 2047, 1024, 777, 512, 300, 100, 65, 64, 33, 31, 1, 0)
+
+
+@pytest.mark.parametrize("kind", ["weights", "equal", "few", "close", "odd"])
+@pytest.mark.parametrize("bs,budget,sinks,recent", [(16, 700, 4, 16), (64, 64, 0, 0), (256, 6000, 33, 500),
+                                                    (1024, 8192, 1, 0), (32, 40, 3, 36)])
+def test_select_of_many_heads(kvq, kind, bs, budget, sinks, recent):
+    """A head or more per SM (152 here): one pass between sampled bounds, and
+    the digits over all rows where the weights are too alike for it."""
+    check_select(kvq, masses(kind, 8, bs), MANY, bs, budget, sinks, recent)
+
+
+@pytest.mark.parametrize("what", ["sample", "ties", "steps", "tail"])
+def test_select_of_many_heads_against_the_sample(kvq, what):
+    """Weights that the evenly spread sample tells nothing about: other values
+    at the sampled rows, one value almost everywhere, a few values, and every
+    large weight in one stretch."""
+    r = np.random.default_rng(5)
+    lens, bs, hkv, budget = (20000,) * 4, 64, 40, 5000
+    table, nb = pages(lens, bs, 1)
+    mass = np.zeros((nb, hkv, bs), np.float32)
+    j = np.arange(20000)
+    for b in range(4):
+        for h in range(hkv):
+            w = r.exponential(1.0, 20000).astype(np.float32)
+            if what == "sample":
+                w[(np.arange(4096) * 20000) >> 12] = 1e6 if h % 2 else 1e-6
+            elif what == "ties":
+                w[r.random(20000) < 0.97] = 0.5 if h % 2 else 0.0
+            elif what == "steps":
+                w = np.floor(4.0 * w).astype(np.float32)
+            else:
+                w[: 20000 - budget - (h - 20) * 40] *= 1e-3
+            mass[table[b, j // bs], h, j % bs] = w
+    got = select_call(kvq, mass, table, lens, nb, bs, budget, 0, 0)
+    assert kvq.kvq_get_device_error() == 0
+    for b in range(4):
+        for h in range(hkv):
+            w = mass[table[b, j // bs], h, j % bs]
+            want = np.sort(np.lexsort((j, -w))[:budget])  # the largest, ties to the lower row
+            assert np.array_equal(got[0][b, h], want), (b, h)
+
+
 def test_select_long_and_wide(kvq):
     """Sixteen CTAs to a head; a part longer than the keys a CTA keeps on chip
     (read again from global memory); lengths far below the bound."""
