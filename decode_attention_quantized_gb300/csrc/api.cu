@@ -996,6 +996,21 @@ kvq_status check_evict(const kvq_evict_params* p) {
   return KVQ_OK;
 }
 
+// The one-pass kernel: enough long heads (against the clusters, a mixed batch's
+// heads keeping 4096 rows: 80 heads of 131,072 rows 42 / 58 us, 304 89 / 213;
+// of 32,768 rows 80 heads 25 / 23, 160 33 / 33, 304 38 / 45; of 16,384 rows,
+// 2048 kept, 512 heads 46 / 42), a bit map that leaves two CTAs to an SM,
+// 16-byte loads, and a list that holds ten standard deviations of the sample's
+// rank (512 ragged heads of up to 131,072 rows, 65,536 kept: without this 304 /
+// 167, most heads going through the digits).
+bool select_many_ok(const SelectArgs& a, int sms) {
+  const long long segs = (long long)a.batch * a.num_kv_heads;
+  const double need = a.budget - a.sinks - a.recent, rest = a.lim - need;
+  const double list = rest > 0 ? 10.0 / 64.0 * std::sqrt(need * rest) : 0.0;
+  return a.lim >= 32768 && 2 * segs >= sms && segs * a.lim >= sms * 32768LL && select_many_smem(a.lim) <= 110 * 1024 &&
+         list <= 0.9 * kManyList && aligned(a.mass, 16);
+}
+
 // Launch shape of kvq_evict_compact: units of up to 128 rows and kUnitBytes,
 // two CTAs per SM with as many ring stages as fit.
 constexpr int kUnitBytes = 32 * 1024;
@@ -1385,8 +1400,7 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
   a.sinks = params->sinks;
   a.recent = params->recent;
   a.err = dev->err;
-  // many heads
-  if ((long long)a.batch * a.num_kv_heads >= dev->sms && select_many_smem(a.lim) <= 110 * 1024 && aligned(mass, 16))
+  if (select_many_ok(a, dev->sms))
     return from_cuda(launch_evict_select_many(a, reinterpret_cast<cudaStream_t>(stream)));
   // a CTA keeps 16,384 rows in registers: as many CTAs (up to 16) as hold the
   // longest head, more while SMs are free and each still has 2048 rows

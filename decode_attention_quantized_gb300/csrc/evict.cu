@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
 
 // -------------------------------------------------------- select, many heads
 //
-// With a head or more per SM one CTA takes a head and reads its weights once:
+// With enough long heads (the rule is with the launch) one CTA takes a head and
+// reads its weights once:
 //   1. a sample of 4096 rows, evenly spread, brackets the threshold: two ranks
 //      three standard deviations to either side of the wanted one, to 16 bits;
 //   2. one pass over the weights (16 bytes a lane) marks the rows above the
@@ -284,13 +285,15 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
 // Exact whatever the sample was: when the wanted rank turns out not to lie in
 // the bracket, or the list overflows (thousands of rows of nearly the same
 // weight), the head goes through the digits of the kernel above, reading its
-// weights again for each (from L2).  512 heads of up to 131,072 rows: @@ us
+// weights again for each (from L2).  512 heads of up to 131,072 rows: 106 us
 // (276 with the clusters above, whose loads, digit passes, counts and output
-// took 107, 62, 70 and 38 us of it).
+// took 107, 62, 70 and 38 us of it).  304 heads of 131,072 rows take 89: 25 the
+// sample's scattered reads and digits, 33 the pass (4.8 TB/s), 15 the list and
+// its digits, the rest launch and output.  Half the sample misses the bracket
+// often enough to lose what it saves.
 constexpr int kManyThreads = kSelThreads, kManyWarps = kManyThreads / 32;
 constexpr int kManySample = 8;                              // samples a thread
 constexpr int kManySamples = kManySample * kManyThreads;
-constexpr int kManyList = 6144;                             // rows inside the bracket
 static_assert(2 * kManyList >= 257 * 32, "the digits' columns take the list's place");
 
 // The digit of the need-th largest key from a digit's counts (every warp for
@@ -338,9 +341,28 @@ __global__ void __launch_bounds__(kManyThreads, 2) evict_select_many_kernel(cons
   __shared__ uint32_t bins[2][256];
   __shared__ uint32_t s_list, s_above, s_valid, s_warp[kManyWarps], s_equal[kManyWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seg = (int)blockIdx.x, b = seg / a.num_kv_heads, h = seg - b * a.num_kv_heads;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  // the longest sequences first: the heads that start last end the call
+  // (64 sequences of up to 131,072 rows: 115 against 134 us)
+  const int nth = (int)blockIdx.x / a.num_kv_heads, h = (int)blockIdx.x - nth * a.num_kv_heads;
+  if (a.batch <= 128) {
+    int* lens = reinterpret_cast<int*>(bins[0]);
+    const int len = tid < a.batch ? a.seq_lens[tid] : 0;
+    if (tid < a.batch) lens[tid] = len;
+    __syncthreads();
+    if (tid < a.batch) {
+      int ahead = 0;
+#pragma unroll 4
+      for (int i = 0; i < a.batch; ++i) ahead += lens[i] > len || (lens[i] == len && i < tid);
+      if (ahead == nth) s_list = (uint32_t)tid;
+    }
+  } else if (tid == 0) {
+    s_list = (uint32_t)nth;
+  }
+  __syncthreads();
+  const int b = (int)s_list, seg = b * a.num_kv_heads + h;
+  __syncthreads();
   SelectHead hd;
   if (!select_ends(a, b, h, tid, kManyThreads, hd)) return;
   const int L = hd.L;
@@ -438,16 +460,16 @@ __global__ void __launch_bounds__(kManyThreads, 2) evict_select_many_kernel(cons
     const float sigma = sqrtf(r * fmaxf(0.0f, 1.0f - r / kManySamples));
     const float half = fminf(5.0f * sigma + 2.0f, 0.45f * kManyList * kManySamples / (float)M);
     const int rank_hi = (int)floorf(r - half), rank_lo = (int)ceilf(r + half);
-    uint32_t d, d2, same, before;
+    uint32_t d, d2, same, before, e, before_lo;
+    digit_of(each, 24, 0u, (uint32_t)max(1, rank_hi), d, same, before);
+    find_digit(bins[0], (uint32_t)min(kManySamples, rank_lo), lane, e, same, before_lo);
     if (rank_hi >= 1) {
-      digit_of(each, 24, 0u, (uint32_t)rank_hi, d, same, before);
       digit_of(each, 16, d, (uint32_t)rank_hi - before, d2, same, before);
       hi = (d << 24) | (d2 << 16) | 0xFFFFu;
     }
     if (rank_lo <= kManySamples) {
-      digit_of(each, 24, 0u, (uint32_t)rank_lo, d, same, before);
-      digit_of(each, 16, d, (uint32_t)rank_lo - before, d2, same, before);
-      lo = max(1u, (d << 24) | (d2 << 16));
+      digit_of(each, 16, e, (uint32_t)rank_lo - before_lo, d2, same, before);
+      lo = max(1u, (e << 24) | (d2 << 16));
     }
   }
   __syncthreads();
@@ -603,21 +625,72 @@ __global__ void __launch_bounds__(kManyThreads, 2) evict_select_many_kernel(cons
     if (lane == 0) s_warp[warp] = kept;
     __syncthreads();
     uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0u);
-    for (int w = w0; w < w1; ++w) {
-      const uint4 m = *reinterpret_cast<const uint4*>(mask + w * 8);
-      if ((m.x | m.y | m.z | m.w) == 0u) continue;
-      const uint32_t four = (m.x >> lane & 1u) | (m.y >> lane & 1u) << 1 | (m.z >> lane & 1u) << 2 | (m.w >> lane & 1u) << 3;
-      // rows of the lanes below
-      const uint32_t below = (1u << lane) - 1u;
-      uint32_t to = at + __popc(m.x & below) + __popc(m.y & below) + __popc(m.z & below) + __popc(m.w & below);
+    if (hd.need <= 2 * kManyList && hd.need <= M / 16) {
+      // few of them: a block a lane, through shared memory in the list's place
+      // (304 heads of 131,072 rows, 4096 kept: 89 against 100 us with the
+      // stores of a lane or two each below; of 32,768 rows, 4096 kept 38
+      // against 37, 12,000 kept 41 against 35)
+      uint32_t* stage = many_smem;
+      for (int g = w0; g < w1; g += 32) {
+        uint4 m = make_uint4(0, 0, 0, 0);
+        if (g + lane < w1) m = *reinterpret_cast<const uint4*>(mask + (g + lane) * 8);
+        const uint32_t mine = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+        uint32_t to = mine;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (four >> c & 1u) {
-          // (never more than that, unless another stream changes the weights meanwhile)
-          if (to < (uint32_t)hd.need) mid[to] = first + 128 * w + 4 * lane + c;
-          ++to;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, to, o);
+          if (lane >= o) to += y;
         }
-      at += __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+        const uint32_t total = __shfl_sync(0xffffffffu, to, 31);
+        to += at - mine;
+        at += total;
+        for (uint32_t some = m.x | m.y | m.z | m.w; some; some &= some - 1) {
+          const int l = __ffs(some) - 1;
+          const uint32_t four = (m.x >> l & 1u) | (m.y >> l & 1u) << 1 | (m.z >> l & 1u) << 2 | (m.w >> l & 1u) << 3;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (four >> c & 1u) {
+              if (to < 2 * kManyList) stage[to] = (uint32_t)(first + 128 * (g + lane) + 4 * l + c);
+              ++to;
+            }
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < hd.need; i += kManyThreads) mid[i] = (int)stage[i];
+      if (bad) atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
+      return;
+    }
+    // four blocks at a time: how many of each block's rows the lanes below
+    // have, a byte a block (128 at most), from one scan
+    for (int g = w0; g < w1; g += 4) {
+      uint32_t nib[4], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 m = make_uint4(0, 0, 0, 0);
+        if (g + i < w1) m = *reinterpret_cast<const uint4*>(mask + (g + i) * 8);
+        const uint32_t x = m.x >> lane & 1u, y = m.y >> lane & 1u, z = m.z >> lane & 1u, v = m.w >> lane & 1u;
+        nib[i] = x | y << 1 | z << 2 | v << 3;
+        mine |= (x + y + z + v) << (8 * i);
+      }
+      uint32_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t total = __shfl_sync(0xffffffffu, incl, 31), below = incl - mine;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t to = at + (below >> (8 * i) & 255u);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (nib[i] >> c & 1u) {
+            // (never more than that, unless another stream changes the weights meanwhile)
+            if (to < (uint32_t)hd.need) mid[to] = first + 128 * (g + i) + 4 * lane + c;
+            ++to;
+          }
+        at += total >> (8 * i) & 255u;
+      }
     }
   } else {
     // ---- digit by digit over all rows

@@ -326,6 +326,8 @@ struct SelectArgs {
 };
 constexpr int kSelThreads = 512;
 constexpr int kSelKeys = 32;  // rows that a lane keeps in registers
+// The one-pass kernel for many heads: the rows near the threshold that it can list.
+constexpr int kManyList = 6144;
 size_t select_many_smem(int rows);
 cudaError_t launch_evict_select_many(const SelectArgs& a, cudaStream_t stream);
 cudaError_t launch_evict_select(const SelectArgs& a, int cluster, cudaStream_t stream);

@@ -436,7 +436,8 @@ typedef struct {
  * keep int32 [B, Hkv, budget]: the kept rows in ascending order, then -1.
  * kept_lens int32 [B]: min(seq_lens[b], budget), the lengths after
  * kvq_evict_compact (it may not be seq_lens itself).  An unreadable block id
- * sets KVQ_DEVERR_BLOCK_ID and ranks its rows as NaN. */
+ * sets KVQ_DEVERR_BLOCK_ID and ranks its rows as NaN.
+ * num_kv_heads * block_size <= 2^29; batch * num_kv_heads <= 2^24. */
 KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float* mass, const int32_t* block_table,
                                     const int32_t* seq_lens, int32_t* keep, int32_t* kept_lens,
                                     kvq_stream_t stream);

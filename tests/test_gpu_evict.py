@@ -207,8 +207,8 @@ def select_call(kvq, mass, table, lens, nb, bs, budget, sinks, recent, max_seq_l
     return keep.cpu().numpy(), kept.cpu().numpy()
 
 
-def check_select(kvq, mass, lens, bs, budget, sinks, recent, seed=0, **kw):
-    table, nb = pages(lens, bs, seed)
+def check_select(kvq, mass, lens, bs, budget, sinks, recent, seed=0, width=None, **kw):
+    table, nb = pages(lens, bs, seed, width=width)
     full = mass(nb)
     got = select_call(kvq, full, table, lens, nb, bs, budget, sinks, recent, **kw)
     assert kvq.kvq_get_device_error() == 0
@@ -284,9 +284,10 @@ MANY = (20000, 12001, 9000, 8300, 8193, 4097, 3000, 2047, 1024, 777, 512, 300, 1
 @pytest.mark.parametrize("bs,budget,sinks,recent", [(16, 700, 4, 16), (64, 64, 0, 0), (256, 6000, 33, 500),
                                                     (1024, 8192, 1, 0), (32, 40, 3, 36)])
 def test_select_of_many_heads(kvq, kind, bs, budget, sinks, recent):
-    """A head or more per SM (152 here): one pass between sampled bounds, and
-    the digits over all rows where the weights are too alike for it."""
-    check_select(kvq, masses(kind, 8, bs), MANY, bs, budget, sinks, recent)
+    """A head or more per SM (152 here) of up to 40,960 rows: one pass between
+    sampled bounds, and the digits over all rows where the weights are too alike
+    for it."""
+    check_select(kvq, masses(kind, 8, bs), MANY, bs, budget, sinks, recent, width=40960 // bs)
 
 
 @pytest.mark.parametrize("what", ["sample", "ties", "steps", "tail"])
@@ -296,7 +297,7 @@ def test_select_of_many_heads_against_the_sample(kvq, what):
     large weight in one stretch."""
     r = np.random.default_rng(5)
     lens, bs, hkv, budget = (20000,) * 4, 64, 40, 5000
-    table, nb = pages(lens, bs, 1)
+    table, nb = pages(lens, bs, 1, width=640)
     mass = np.zeros((nb, hkv, bs), np.float32)
     j = np.arange(20000)
     for b in range(4):

@@ -178,6 +178,14 @@ def test_masked_and_mass_refuse_token_counts_that_overflow(kvq):
         assert lib.kvq_key_mass_workspace_size(*a, ctypes.byref(n)) == 2
 
 
+def test_evict_refuses_shapes_that_overflow(kvq):
+    lib = kvq.load()
+    for d in (dict(num_kv_heads=2 ** 14, block_size=2 ** 16), dict(batch=2 ** 20, num_kv_heads=32)):
+        p = kvq.EvictParams(**{**dict(batch=2, max_blocks_per_seq=4, max_seq_len=0, num_blocks=8, block_size=16,
+                                      num_kv_heads=2, budget=32, sinks=0, recent=0), **d})
+        assert lib.kvq_evict_select(ctypes.byref(p), FAKE, FAKE, FAKE, FAKE, FAKE + 4, None) == 2
+
+
 def test_masked_refuses_an_output_over_the_queries(kvq):
     lib, c, p = kvq.load(), cache_desc(kvq), params(kvq)
     size = 2 * 5 * 8 * c.head_dim * 2
