@@ -648,3 +648,54 @@ def test_compact_refuses_rows_from_before(kvq, last, err):
         src = keep[0, 0, i]
         assert np.array_equal(got[cache.table[0, i // 16], 0, i % 16],
                               cache.k_codes[cache.table[0, src // 16], 0, src % 16])
+
+
+def test_select_of_many_heads_bad_pages_alignment_and_capture(kvq):
+    """A page outside the pool is flagged and its rows rank last; weights at an
+    address that 16-byte loads cannot take give the same rows, as do a call on
+    another stream and a replayed one."""
+    r = np.random.default_rng(9)
+    B, hkv, bs, L, budget = 20, 8, 64, 33000, 900
+    table, nb = pages((L,) * B, bs, 2)
+    w = r.exponential(1.0, (nb, hkv, bs)).astype(np.float32)
+    p = kvq.make_evict_params(B, table.shape[1], budget, num_blocks=nb, block_size=bs, num_kv_heads=hkv, sinks=5,
+                              recent=40)
+    lens, tbl = dev(np.full(B, L, np.int32)), dev(table)
+    aligned = dev(w)
+    shifted = torch.zeros(w.size + 1, device="cuda")[1:].view(w.shape)
+    shifted.copy_(aligned)
+    keep = torch.full((B, hkv, budget), -9, dtype=torch.int32, device="cuda")
+    kept = torch.full((B,), -9, dtype=torch.int32, device="cuda")
+    kvq.kvq_evict_select(p, aligned, tbl, lens, keep, kept)
+    j = np.arange(L)
+    for b, h in ((0, 0), (7, 3), (19, 7)):
+        v = w[table[b, j // bs], h, j % bs]
+        mid = 5 + np.lexsort((j[5:-40], -v[5:-40]))[:budget - 45]
+        want = np.concatenate([np.arange(5), np.sort(mid), np.arange(L - 40, L)])
+        assert np.array_equal(keep[b, h].cpu().numpy(), want)
+    assert (kept == budget).all()
+    other = torch.zeros_like(keep)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kvq.kvq_evict_select(p, aligned, tbl, lens, other, kept, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(keep, other)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        kvq.kvq_evict_select(p, aligned, tbl, lens, other, kept)
+    other.zero_()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(keep, other)
+    kvq.kvq_evict_select(p, shifted, tbl, lens, other, kept)
+    assert torch.equal(keep, other)
+    assert kvq.kvq_get_device_error() == 0
+    # two pages of sequence 3, one outside the pool on either side
+    bad = table.copy()
+    bad[3, 100], bad[3, 200] = nb, -1
+    kvq.kvq_evict_select(p, aligned, dev(bad), lens, other, kept)
+    assert kvq.kvq_get_device_error() == kvq.DEVERR_BLOCK_ID
+    same = [b for b in range(B) if b != 3]
+    assert torch.equal(keep[same], other[same])
+    at = other[3].cpu().numpy() // bs
+    assert not np.isin(at, (100, 200)).any()
