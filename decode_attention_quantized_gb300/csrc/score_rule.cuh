@@ -32,11 +32,13 @@ __device__ __forceinline__ float rule_score(const RowRule& r, float x, int key, 
 }
 
 // tok: index of the row's token in [B, C]; hi: one past the last key loaded.
+// begin is 0 or more and end in [0, hi], so that their distances to a key or a
+// position stay inside int32 whatever the caller's int32 values are.
 __device__ __forceinline__ void row_range(const int32_t* key_begin, const int32_t* key_end, int window, size_t tok,
                                           int pos, int hi, int& begin, int& end) {
   begin = key_begin ? max(0, key_begin[tok]) : 0;
   if (window > 0 && pos >= window) begin = max(begin, pos - window + 1);
-  end = min(key_end ? key_end[tok] : pos + 1, hi);
+  end = max(0, min(key_end ? key_end[tok] : pos + 1, hi));
 }
 
 // The distance d0 of RowRule (0 for a row that sees nothing).
