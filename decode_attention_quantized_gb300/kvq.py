@@ -508,6 +508,7 @@ class EvictBuffers:
     workspace: torch.Tensor
     keep: torch.Tensor
     kept_lens: torch.Tensor
+    other_lens: Optional[torch.Tensor] = None  # the new lengths when kept_lens are the old ones (evict_step)
 
 
 def alloc_evict_buffers(cache: QuantizedPagedCache, params: EvictParams) -> EvictBuffers:
@@ -516,12 +517,21 @@ def alloc_evict_buffers(cache: QuantizedPagedCache, params: EvictParams) -> Evic
     return EvictBuffers(
         torch.empty(kvq_evict_compact_workspace_size(cache, params) // 4 + 64, dtype=torch.int32, device=dev),
         torch.empty((params.batch, params.num_kv_heads, params.budget), dtype=torch.int32, device=dev),
+        torch.empty((params.batch,), dtype=torch.int32, device=dev),
         torch.empty((params.batch,), dtype=torch.int32, device=dev))
 
 
 def evict_step(cache: QuantizedPagedCache, params: EvictParams, block_table: torch.Tensor, seq_lens: torch.Tensor,
                mass: torch.Tensor, bufs: EvictBuffers, dst_table: Optional[torch.Tensor] = None, stream=None):
-    """kvq_evict_select followed by kvq_evict_compact; returns the new lengths."""
-    kvq_evict_select(params, mass, block_table, seq_lens, bufs.keep, bufs.kept_lens, stream)
-    kvq_evict_compact(cache, params, block_table, dst_table, bufs.keep, bufs.kept_lens, mass, bufs.workspace, stream)
-    return bufs.kept_lens
+    """kvq_evict_select followed by kvq_evict_compact; returns the new lengths:
+    bufs.kept_lens, or bufs.other_lens when seq_lens is bufs.kept_lens, so that
+    what one step returned may be the next step's seq_lens.  seq_lens is left as
+    it was; the next step overwrites the returned tensor unless it is given it."""
+    kept = bufs.kept_lens
+    if seq_lens.data_ptr() == kept.data_ptr():
+        if bufs.other_lens is None:
+            bufs.other_lens = torch.empty_like(kept)
+        kept = bufs.other_lens
+    kvq_evict_select(params, mass, block_table, seq_lens, bufs.keep, kept, stream)
+    kvq_evict_compact(cache, params, block_table, dst_table, bufs.keep, kept, mass, bufs.workspace, stream)
+    return kept

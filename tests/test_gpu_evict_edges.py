@@ -1,0 +1,54 @@
+"""Evictions as a serving loop runs them, against the plain forms of score_ref."""
+import numpy as np
+import pytest
+import torch
+
+import score_ref as ref
+from test_gpu_masked import dev
+
+pytestmark = pytest.mark.gpu
+
+INT8, ROW = ref.INT8, ref.ROW
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from decode_attention_quantized_gb300 import kvq
+    kvq.load()
+    return kvq
+
+
+@pytest.mark.parametrize("add", ["in place", "out of place", "none"])
+def test_lengths_stay_on_the_device(kvq, add):
+    """seq_lens = evict_step(...) step after step with the same buffers: the
+    returned lengths are the next step's argument, as they are, advanced in
+    place, or through a new tensor."""
+    hkv, d, bs, budget, width, nb = 2, 64, 16, 40, 4, 10
+    r = np.random.default_rng(3)
+    table = r.permutation(nb)[:2 * width].reshape(2, width).astype(np.int32)
+    g = kvq.QuantizedPagedCache(INT8, ROW, ROW, nb, bs, hkv, d)
+    for t in (g.k_codes, g.v_codes):
+        t.copy_(dev(r.integers(0, 256, tuple(t.shape)).astype(np.uint8)))
+    ep = kvq.make_evict_params(2, width, budget, num_blocks=nb, block_size=bs, num_kv_heads=hkv, sinks=2, recent=4)
+    bufs = kvq.alloc_evict_buffers(g, ep)
+    tbl, lens = dev(table), np.array([64, 50], np.int32)
+    seq_lens = dev(lens)
+    for step in range(5):
+        mass = dev(r.exponential(0.1, (nb, hkv, bs)).astype(np.float32))
+        want, kept = ref.select(mass.cpu().numpy(), table, [int(x) for x in lens], bs, budget, 2, 4)
+        arrays = [t.cpu().numpy() for t in (g.k_codes, g.v_codes, g.k_scale, g.v_scale, mass)]
+        moved = ref.compact(arrays, table, table, want, kept, bs)
+        given = seq_lens.clone()
+        before = seq_lens
+        seq_lens = kvq.evict_step(g, ep, tbl, seq_lens, mass, bufs)
+        assert torch.equal(before, given), "the lengths that were passed changed"
+        assert np.array_equal(seq_lens.cpu().numpy(), kept)
+        assert np.array_equal(bufs.keep.cpu().numpy(), want)
+        for t, w in zip((g.k_codes, g.v_codes, g.k_scale, g.v_scale, mass), moved):
+            assert np.array_equal(t.cpu().numpy(), w)
+        lens = kept
+        if add != "none":
+            n = 9 + step
+            seq_lens = seq_lens.add_(n) if add == "in place" else seq_lens + n
+            lens = kept + np.int32(n)
+    assert kvq.kvq_get_device_error() == 0
