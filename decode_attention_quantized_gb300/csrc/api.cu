@@ -56,6 +56,11 @@ kvq_status encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Whether the n bytes at a and the m bytes at b share a byte.
+bool overlap(const void* a, uint64_t n, const void* b, uint64_t m) {
+  const uint64_t x = reinterpret_cast<uint64_t>(a), y = reinterpret_cast<uint64_t>(b);
+  return n > 0 && m > 0 && x < y + m && y < x + n;
+}
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int ilog2(int x) {
   int l = 0;
@@ -1378,8 +1383,20 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
   if (params->batch == 0) return KVQ_OK;
   if (!mass || !block_table || !seq_lens || !keep || !kept_lens) return KVQ_ERR_INVALID_ARG;
   if (!aligned(mass, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(keep, 4) ||
-      !aligned(kept_lens, 4) || kept_lens == seq_lens)
+      !aligned(kept_lens, 4))
     return KVQ_ERR_INVALID_ARG;
+  {
+    // A head's CTAs each read its length: an output that changed it between
+    // their reads would part them (some would leave while others still read
+    // their shared memory).  The weights and the table are read again, too.
+    const uint64_t lens = 4ull * params->batch, heads = (uint64_t)params->batch * params->num_kv_heads;
+    const uint64_t rows = 4 * heads * params->budget, table = lens * params->max_blocks_per_seq;
+    const uint64_t weights = 4ull * params->num_blocks * params->num_kv_heads * params->block_size;
+    if (overlap(kept_lens, lens, keep, rows)) return KVQ_ERR_INVALID_ARG;
+    for (auto [out, n] : {std::pair<const void*, uint64_t>{kept_lens, lens}, {keep, rows}})
+      if (overlap(out, n, seq_lens, lens) || overlap(out, n, block_table, table) || overlap(out, n, mass, weights))
+        return KVQ_ERR_INVALID_ARG;
+  }
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   SelectArgs a{};
@@ -1445,6 +1462,25 @@ KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_par
   if (!aligned(block_table, 4) || (dst_table && !aligned(dst_table, 4)) || !aligned(keep, 4) ||
       !aligned(kept_lens, 4) || (mass && !aligned(mass, 4)) || !aligned(workspace, 256))
     return KVQ_ERR_INVALID_ARG;
+  {
+    // what says where rows lie may not be among what is written: a unit's
+    // threads each read it
+    const uint64_t lens = 4ull * params->batch, table = lens * params->max_blocks_per_seq;
+    const uint64_t rows = lens * params->num_kv_heads * params->budget;
+    const uint64_t cells = (uint64_t)params->num_blocks * params->num_kv_heads * params->block_size;
+    const std::pair<const void*, uint64_t> reads[] = {
+        {block_table, table}, {dst_table, dst_table ? table : 0}, {keep, rows}, {kept_lens, lens}};
+    const std::pair<const void*, uint64_t> writes[] = {
+        {workspace, workspace_bytes},
+        {cache->k_codes, cells * row_bytes(cache)},
+        {cache->v_codes, cells * row_bytes(cache)},
+        {cache->k_scale, 4 * cells * scales_per_row(cache, cache->k_mode)},
+        {cache->v_scale, 4 * cells * scales_per_row(cache, cache->v_mode)},
+        {mass, mass ? 4 * cells : 0}};
+    for (auto [r, n] : reads)
+      for (auto [w, m] : writes)
+        if (overlap(r, n, w, m)) return KVQ_ERR_INVALID_ARG;
+  }
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   CompactPlan P;  // (the plan with a weight array, whether or not there is one: its workspace was asked for)

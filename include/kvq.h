@@ -435,8 +435,9 @@ typedef struct {
  * number.  A sequence of at most `budget` rows stays whole.
  * keep int32 [B, Hkv, budget]: the kept rows in ascending order, then -1.
  * kept_lens int32 [B]: min(seq_lens[b], budget), the lengths after
- * kvq_evict_compact (it may not be seq_lens itself).  An unreadable block id
- * sets KVQ_DEVERR_BLOCK_ID and ranks its rows as NaN.
+ * kvq_evict_compact.  keep and kept_lens may overlap neither one another nor
+ * an input (refused).  An unreadable block id sets KVQ_DEVERR_BLOCK_ID and
+ * ranks its rows as NaN.
  * num_kv_heads * block_size <= 2^29; batch * num_kv_heads <= 2^24. */
 KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float* mass, const int32_t* block_table,
                                     const int32_t* seq_lens, int32_t* keep, int32_t* kept_lens,
@@ -459,8 +460,9 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
  * K is moved as it was written: with rotary positions it keeps the rotation
  * of its first position.
  * In place the kernel's blocks wait for one another (a cooperative launch with
- * bounded waits; KVQ_DEVERR_TIMEOUT).  workspace: at least
- * kvq_evict_compact_workspace_size bytes, 256-byte aligned (used in place
+ * bounded waits; KVQ_DEVERR_TIMEOUT).  The tables, keep and kept_lens may not
+ * overlap the workspace, the cache's arrays or mass (refused).  workspace: at
+ * least kvq_evict_compact_workspace_size bytes, 256-byte aligned (used in place
  * only, but checked always); it belongs to this call until its kernel has
  * run. */
 KVQ_API kvq_status kvq_evict_compact_workspace_size(const kvq_cache* cache, const kvq_evict_params* params,

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import score_ref as ref
+from guard import guarded
+from test_gpu_evict import masses, pages
 from test_gpu_masked import dev
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +54,19 @@ def test_lengths_stay_on_the_device(kvq, add):
             seq_lens = seq_lens.add_(n) if add == "in place" else seq_lens + n
             lens = kept + np.int32(n)
     assert kvq.kvq_get_device_error() == 0
+
+
+def test_lengths_beside_one_another(kvq):
+    """seq_lens, kept_lens and keep in one allocation, end to end: nothing overlaps."""
+    bs, hkv, budget, lens = 16, 3, 50, (200, 17, 90)
+    table, nb = pages(lens, bs, 1)
+    mass = masses("weights", hkv, bs)(nb)
+    n = hkv * budget
+    one = guarded(torch.zeros(3 + 3 + 3 * n, dtype=torch.int32, device="cuda"), "lengths and rows")
+    one[:3].copy_(dev(np.array(lens, np.int32)))
+    p = kvq.make_evict_params(3, table.shape[1], budget, num_blocks=nb, block_size=bs, num_kv_heads=hkv)
+    keep = one[6:].view(3, hkv, budget)
+    kvq.kvq_evict_select(p, dev(mass), dev(table), one[:3], keep, one[3:6])
+    assert kvq.kvq_get_device_error() == 0
+    want = ref.select(mass, table, lens, bs, budget, 0, 0)
+    assert np.array_equal(keep.cpu().numpy(), want[0]) and np.array_equal(one[3:6].cpu().numpy(), want[1])
