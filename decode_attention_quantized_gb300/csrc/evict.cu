@@ -253,17 +253,23 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
   be = __reduce_add_sync(0xffffffffu, be);
   const uint32_t below = (1u << lane) - 1u;
   int32_t* mid = keep + a.sinks;
+  // (Runs that are read again may give other weights than the passes saw, when
+  // another stream writes them meanwhile: then more rows than need_all may be
+  // above T, or `need` have gone below 0.  No place past the head's is written.)
+  auto put = [&](uint32_t to, int j) {
+    if (to < (uint32_t)need_all) mid[to] = pos0 + j * 32;
+  };
   if (need == 0) {
     each([&](int j, uint32_t k) {
       const uint32_t mg = __ballot_sync(0xffffffffu, k > T);
-      if (k > T) mid[bg + __popc(mg & below)] = pos0 + j * 32;
+      if (k > T) put(bg + __popc(mg & below), j);
       bg += __popc(mg);
     });
   } else {
     each([&](int j, uint32_t k) {
       const uint32_t mg = __ballot_sync(0xffffffffu, k > T), me = __ballot_sync(0xffffffffu, k == T);
       const uint32_t g = bg + __popc(mg & below), e = be + __popc(me & below);
-      if (k > T || (k == T && e < (uint32_t)need)) mid[g + min(e, (uint32_t)need)] = pos0 + j * 32;
+      if (k > T || (k == T && e < (uint32_t)need)) put(g + min(e, (uint32_t)need), j);
       bg += __popc(mg);
       be += __popc(me);
     });

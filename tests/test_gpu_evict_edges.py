@@ -70,3 +70,45 @@ def test_lengths_beside_one_another(kvq):
     assert kvq.kvq_get_device_error() == 0
     want = ref.select(mass, table, lens, bs, budget, 0, 0)
     assert np.array_equal(keep.cpu().numpy(), want[0]) and np.array_equal(one[3:6].cpu().numpy(), want[1])
+
+
+def test_selection_while_the_weights_change(kvq):
+    """Heads too long to be held on chip are read again in every pass.  Weights
+    that another stream writes meanwhile make the rows in `keep` unspecified,
+    but nothing outside their places is written: not the protected rows of the
+    same head, and not what lies around keep."""
+    bs, L, budget, sinks, recent = 1024, 600_000, 150_000, 7, 90
+    table, nb = pages((L,), bs, 1)
+    r = np.random.default_rng(0)
+    kinds = [torch.from_numpy(r.exponential(1.0, (nb, 1, bs)).astype(np.float32)).cuda() for _ in range(3)]
+    kinds.append(torch.zeros((nb, 1, bs), device="cuda"))
+    kinds.append(torch.full((nb, 1, bs), 7.0, device="cuda"))
+    mass = kinds[0].clone()
+    p = kvq.make_evict_params(1, table.shape[1], budget, num_blocks=nb, block_size=bs, num_kv_heads=1, sinks=sinks,
+                              recent=recent)
+    keep = guarded(torch.full((1, 1, budget), -9, dtype=torch.int32, device="cuda"), "keep")
+    kept = guarded(torch.zeros(1, dtype=torch.int32, device="cuda"), "kept")
+    tbl, lens = dev(table), dev(np.array([L], np.int32))
+    other, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(other):
+            for k in kinds * 4:
+                mass.copy_(k)
+        with torch.cuda.stream(mine):
+            for _ in range(10):
+                kvq.kvq_evict_select(p, mass, tbl, lens, keep, kept)
+    torch.cuda.synchronize()
+    assert kvq.kvq_get_device_error() == 0
+    ends = keep[0, 0].cpu().numpy()
+    assert np.array_equal(ends[:sinks], np.arange(sinks))
+    assert np.array_equal(ends[budget - recent:], np.arange(L - recent, L))
+    mid = ends[sinks:budget - recent]
+    assert ((mid == -9) | ((mid >= sinks) & (mid < L - recent))).all()
+    # and left alone it is right again
+    mass.copy_(kinds[0])
+    kvq.kvq_evict_select(p, mass, tbl, lens, keep, kept)
+    j = np.arange(sinks, L - recent)
+    w = kinds[0].cpu().numpy()[table[0, j // bs], 0, j % bs]
+    want = np.sort(j[np.lexsort((j, -w))[:budget - sinks - recent]])
+    assert np.array_equal(keep[0, 0, sinks:budget - recent].cpu().numpy(), want)
