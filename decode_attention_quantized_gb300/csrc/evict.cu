@@ -952,15 +952,15 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Co
 }  // namespace
 
 cudaError_t launch_evict_select(const SelectArgs& a, int cluster, cudaStream_t stream) {
-  static bool wide[64] = {};  // clusters of 16 allowed on the device
+  static std::atomic<bool> wide[64];  // clusters of 16 allowed on the device (host threads may set it side by side)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!wide[dev]) {
+  if (!wide[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    wide[dev] = true;
+    wide[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = (unsigned)((long long)a.batch * a.num_kv_heads * cluster);

@@ -112,3 +112,57 @@ def test_selection_while_the_weights_change(kvq):
     w = kinds[0].cpu().numpy()[table[0, j // bs], 0, j % bs]
     want = np.sort(j[np.lexsort((j, -w))[:budget - sinks - recent]])
     assert np.array_equal(keep[0, 0, sinks:budget - recent].cpu().numpy(), want)
+
+
+FIRST_SELECTIONS = """
+import threading
+import numpy as np
+import torch
+from decode_attention_quantized_gb300 import kvq
+
+kvq.load()
+torch.cuda.init()
+n, bs, L, budget = 8, 64, 20000, 777
+nb = (L + bs - 1) // bs
+mass = torch.rand((nb, 1, bs), device="cuda")
+table = torch.randperm(nb, device="cuda", dtype=torch.int32).view(1, nb)
+lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+keep = [torch.zeros((1, 1, budget), dtype=torch.int32, device="cuda") for _ in range(n)]
+kept = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(n)]
+p = kvq.make_evict_params(1, nb, budget, num_blocks=nb, block_size=bs, num_kv_heads=1)
+torch.cuda.synchronize()
+gate, failed = threading.Barrier(n), []
+
+def call(i):
+    try:
+        torch.cuda.set_device(0)
+        s = torch.cuda.Stream()
+        gate.wait()
+        kvq.kvq_evict_select(p, mass, table, lens, keep[i], kept[i], stream=s)
+        s.synchronize()
+    except Exception as e:
+        failed.append(e)
+
+threads = [threading.Thread(target=call, args=(i,)) for i in range(n)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not failed, failed
+w = mass.cpu().numpy()[table[0].cpu().numpy()][:, 0].reshape(-1)[:L]
+want = np.sort(np.lexsort((np.arange(L), -w))[:budget])
+for k in keep:
+    assert np.array_equal(k[0, 0].cpu().numpy(), want)
+assert kvq.kvq_get_device_error() == 0
+print("first selections agree")
+"""
+
+
+def test_first_selections_of_several_threads(kvq):
+    """Host threads whose selections are a process's first ones (in a process of
+    their own) set the kernel's attributes side by side."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_SELECTIONS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first selections agree" in r.stdout, r.stderr
