@@ -120,20 +120,53 @@ __device__ __forceinline__ float tanh_fast(float x) {
   return 1.0f - __fdividef(2.0f, ptx::fast_exp2(x * 2.8853900817779268f) + 1.0f);
 }
 
-// tanh(x) to 2e-7 of its value: for |x| <= 0.6 (a logit up to 30 under a cap
-// of 50) x P(x^2), P a Chebyshev interpolant of tanh(sqrt t) / sqrt t on
-// [0, 0.36] (1.1e-7 with its fp32 evaluation), else tanhf.  Where a cap's error
-// shows in fp32 results: 50 * tanh_fast would be 2e-5 off in a logit.
+// tanh(x) to 4e-7 of its value, for the score rules' caps (the masked attention
+// and the key mass, which reads that attention's lse, give a key one score):
+// x P(x^2) / Q(x^2) on [-9, 9], where tanh is within 3e-8 of +-1 at the ends.
+// P / Q is the minimax quotient of degrees 4 and 4 to tanh(sqrt t) / sqrt t on
+// [0, 81], in relative error (2.1e-8; iteratively reweighted least squares on
+// Chebyshev nodes); its coefficients are positive, so each sum is accurate to
+// its last bits.  A cap's error shows in an fp32 lse: softcap * tanh_fast is a
+// few 1e-7 of the cap off, 2e-5 at a cap of 50.  No branch, and one slow
+// instruction in place of tanh_fast's two.  NaN stays NaN.
 __device__ __forceinline__ float tanh_near(float x) {
+  x = ptx::min_nan(ptx::max_nan(x, -9.0f), 9.0f);
   const float t = x * x;
-  if (t > 0.36f || !(t == t)) return tanhf(x);
-  float p = -0.00585642785f;
-  p = fmaf(p, t, 0.0207574754f);
-  p = fmaf(p, t, -0.0537699218f);
-  p = fmaf(p, t, 0.133317047f);
-  p = fmaf(p, t, -0.33333284f);
-  p = fmaf(p, t, 0.999999998f);
-  return p * x;
+  const float p = fmaf(fmaf(fmaf(fmaf(1.33546623e-8f, t, 2.06090826e-5f), t, 3.49558820e-3f), t, 0.133810252f), t, 1.0f);
+  const float q = fmaf(fmaf(fmaf(fmaf(7.77655885e-7f, t, 3.28563474e-4f), t, 2.58769821e-2f), t, 0.467143416f), t, 1.0f);
+  return x * p * ptx::fast_rcp(q);
+}
+
+// y = cap * tanh_near(y) for a thread's N scores: the same operations two at a
+// time (f32x2), the ends cut off only where some score passes one.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&y)[N], float cap) {
+  float big = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) big = ptx::max3(big, fabsf(y[k]), fabsf(y[k + 1]));
+  if (big > 9.0f) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) y[k] = ptx::min_nan(ptx::max_nan(y[k], -9.0f), 9.0f);
+  }
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float t0, t1, p0, p1, q0, q1;
+    auto step = [&](float& a0, float& a1, float c) { ptx::fma_x2(a0, a1, a0, a1, t0, t1, c, c); };
+    ptx::mul_x2(t0, t1, y[k], y[k + 1], y[k], y[k + 1]);
+    p0 = p1 = 1.33546623e-8f;
+    step(p0, p1, 2.06090826e-5f);
+    step(p0, p1, 3.49558820e-3f);
+    step(p0, p1, 0.133810252f);
+    step(p0, p1, 1.0f);
+    q0 = q1 = 7.77655885e-7f;
+    step(q0, q1, 3.28563474e-4f);
+    step(q0, q1, 2.58769821e-2f);
+    step(q0, q1, 0.467143416f);
+    step(q0, q1, 1.0f);
+    ptx::mul_x2(p0, p1, p0, p1, y[k], y[k + 1]);
+    ptx::mul_x2(p0, p1, p0, p1, cap, cap);
+    ptx::mul_x2(y[k], y[k + 1], p0, p1, ptx::fast_rcp(q0), ptx::fast_rcp(q1));
+  }
 }
 
 // Exact e4m3x2 -> f16x2 (hardware conversion; the low byte goes to the low
@@ -667,7 +700,10 @@ __global__ void __launch_bounds__(288, MINB)
             x[nt][3] = sacc[0][nt][3] * al[nt][1] * ksb;
             if (softcap > 0.0f) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[nt][e] = softcap * dev::tanh_fast(x[nt][e] * inv_cap) * kLog2e;
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (MASK) x[nt][e] = softcap * kLog2e * dev::tanh_near(x[nt][e] * inv_cap);
+                else x[nt][e] = softcap * dev::tanh_fast(x[nt][e] * inv_cap) * kLog2e;
+              }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -1112,7 +1148,7 @@ __global__ void __launch_bounds__(288, MINB)
         }
         if (softcap > 0.0f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = cap_l2 * dev::tanh_fast(x[e]);
+          for (int e = 0; e < 4; ++e) x[e] = cap_l2 * (MASK ? dev::tanh_near(x[e]) : dev::tanh_fast(x[e]));
         }
         // a sub-tile whose keys every query position sees (below the first
         // draft, inside every row's window) needs no mask; padding rows then

@@ -98,7 +98,9 @@ __device__ __forceinline__ uint32_t qt_chunk(uint32_t tile, int kk, int c) {
 // full: a unit then has at most 64 rows, the second parts are the operand's
 // rows 64..127, and warps 2 and 3 hand their rows of S to warps 0 and 1
 // through shared memory (as f16: 2^-11 of a 2^-12 correction).
-template <int DT, int D, int RULE>
+// CAP (masked): a softcap, in instances of its own: beside the uncapped scores its
+// code cost those 13% (2048 tokens over 16,384 int8 keys 945 -> 1073 us).
+template <int DT, int D, int RULE, bool CAP>
 __global__ void __launch_bounds__(kQtWarps * 32, 1)
     decode_qt_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const DecodeArgs a) {
@@ -362,7 +364,8 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16);
     const int G = a.group, T = a.q_tokens, Hq = a.num_q_heads, W = a.window, rows = a.rows;
     const float softcap = a.softcap;
-    const float inv_cap = softcap > 0.0f ? 1.0f / softcap : 0.0f;
+    const bool capped = MASK ? CAP : softcap > 0.0f;
+    const float inv_cap = capped ? 1.0f / softcap : 0.0f;
     // (a masked call's last group of a chunk may hold fewer tokens: its rows
     // past them are set aside per piece)
     bool valid = r < rows;
@@ -588,12 +591,13 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         ptx::tmem_wait_st();
         float base = a.sm_scale;
         if (a.k_mode == KVQ_SCALE_PER_TENSOR) base *= a.k_scale[0];
-        if (softcap <= 0.0f) base *= kLog2e;
+        if (!capped) base *= kLog2e;
         // alpha = base * 2^(ek + eq) in two exact power-of-two steps, finite
         // and > 0 (so that alpha * -inf stays -inf)
         const int e = ek + eq, e1 = e / 2;
         alpha = valid ? fmaxf(fminf(base * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1e-30f) : 1.0f;
         if constexpr (MASK) {
+          if constexpr (CAP) alpha = fminf(alpha * inv_cap, 3.4028234e38f);
           // a row with no token sees the piece's keys with no bias: finite
           // scores that feed only its own unwritten output
           ru = dev::RowRule{};
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           if (a.slopes && (key0 + KT - 1 <= ru.pos || key0 >= ru.pos)) {
             sg = key0 >= ru.pos ? ru.ns : -ru.ns;
             b0 = ru.ns * (float)(abs(ru.pos - key0) - ru.d0);
-            folded = softcap <= 0.0f;
+            folded = !CAP;
           }
         }
         if (MASK && folded) {
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         } else if (k_row) {
           wait(&b_ksc[it & 3], (it >> 2) & 1);
           const float* ksc = ksb + (it & 3) * KT;
-          const float am = softcap > 0.0f ? 1.0f : alpha;
+          const float am = MASK || !capped ? alpha : 1.0f;  // (masked: with 1 / softcap in it)
 #pragma unroll
           for (int k = 0; k < KT; k += 4) {
             const float4 s4 = *reinterpret_cast<const float4*>(ksc + k);
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
             ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], a0, a1);
             ptx::mul_x2(y[k + 2], y[k + 3], y[k + 2], y[k + 3], a2, a3);
           }
-        } else if (softcap <= 0.0f) {
+        } else if (MASK || !capped) {
 #pragma unroll
           for (int k = 0; k < KT; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
         }
@@ -731,7 +735,9 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&b_sfree[sb]);
-        if (softcap > 0.0f) {
+        if constexpr (MASK) {
+          if constexpr (CAP) dev::cap_scores<KT>(y, softcap * kLog2e);
+        } else if (softcap > 0.0f) {
           const float ac = alpha * inv_cap;
 #pragma unroll
           for (int k = 0; k < KT; ++k) y[k] = softcap * dev::tanh_fast(y[k] * ac) * kLog2e;
@@ -855,21 +861,34 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
 
 // Raises (never lowers) the kernel's dynamic shared-memory limit on the
 // current device, then launches one CTA per grid slot.
-template <int DT, int D, int RULE>
+template <int DT, int D, int RULE, bool CAP>
 cudaError_t launch_decode_qt_d(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid,
                                size_t smem, cudaStream_t stream) {
   static std::atomic<int> smem_set[64];
-  const void* kernel = reinterpret_cast<const void*>(decode_qt_kernel<DT, D, RULE>);
+  const void* kernel = reinterpret_cast<const void*>(decode_qt_kernel<DT, D, RULE, CAP>);
   if (cudaError_t e = raise_smem_limit(kernel, smem_set, smem)) return e;
-  return launch_pdl(decode_qt_kernel<DT, D, RULE>, grid, kQtWarps * 32, smem, stream, tk, tv, a);
+  return launch_pdl(decode_qt_kernel<DT, D, RULE, CAP>, grid, kQtWarps * 32, smem, stream, tk, tv, a);
 }
 
-template <int DT, int RULE = 0>
+template <int DT, int RULE = 0, bool CAP = false>
 cudaError_t dispatch_decode_qt(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                int grid, size_t smem, cudaStream_t stream) {
-  if (head_dim == 256) return launch_decode_qt_d<DT, 256, RULE>(tk, tv, a, grid, smem, stream);
-  if (head_dim == 128) return launch_decode_qt_d<DT, 128, RULE>(tk, tv, a, grid, smem, stream);
+  if (head_dim == 256) return launch_decode_qt_d<DT, 256, RULE, CAP>(tk, tv, a, grid, smem, stream);
+  if (head_dim == 128) return launch_decode_qt_d<DT, 128, RULE, CAP>(tk, tv, a, grid, smem, stream);
   return cudaErrorInvalidValue;
+}
+
+// A masked call's instances: a one-part or a two-part Q operand, with or
+// without a softcap.
+template <int DT>
+cudaError_t dispatch_qt_mask(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream) {
+  if (a.softcap > 0.0f) {
+    if (split) return dispatch_decode_qt<DT, 2, true>(head_dim, tk, tv, a, grid, smem, stream);
+    return dispatch_decode_qt<DT, 1, true>(head_dim, tk, tv, a, grid, smem, stream);
+  }
+  if (split) return dispatch_decode_qt<DT, 2, false>(head_dim, tk, tv, a, grid, smem, stream);
+  return dispatch_decode_qt<DT, 1, false>(head_dim, tk, tv, a, grid, smem, stream);
 }
 
 }  // namespace kvq

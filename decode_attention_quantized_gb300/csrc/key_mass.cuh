@@ -13,8 +13,8 @@
 // The result is fp32 and has to agree with fp32 scores: codes are exact in
 // f16 and so are bf16 queries, but a query with a per-channel K scale folded in
 // is not; there the operand is split into two f16 values (two MMAs).  The cap
-// takes a tanh of small relative error (50 * tanh(x / 50) from 1 - 2 / (e^2x +
-// 1) would be 2e-5 off).
+// takes a tanh of small relative error, the masked attention's (50 * tanh(x / 50)
+// from 1 - 2 / (e^2x + 1) would be 2e-5 off).
 #pragma once
 
 #include "decode.cuh"

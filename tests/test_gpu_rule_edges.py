@@ -1,5 +1,14 @@
 """Masked attention and key mass at the edges of what their arguments allow,
-against the 64-bit forms of score_ref."""
+against the 64-bit forms of score_ref.
+
+The lse's bound (lse_bound): a logit takes at most 64 fp32 accumulations of
+partial sums of at most `size` = sum |q k| sm_scale (2^6 * 2^-24), with a
+per-channel K scale 2^-21 of it from the two f16 parts of the operand: together
+2^-17.  A cap is below its argument and has a slope of at most 1: its own error
+is 2^-21 of its value (tanh to 4e-7) and a rounding or two of its argument
+(2^-23 of it), which the factor of 2 between 2^-17 and 2^-18 + 2^-21 leaves
+room for.  The last roundings (bias, exp2, log2, the sum of the parts) are 2^-20
+of 1, of the lse and of the largest bias that was taken out of it."""
 import dataclasses
 
 import numpy as np
@@ -8,9 +17,12 @@ import torch
 
 import score_ref as ref
 from guard import guarded
-from test_gpu_masked import CASES, check, dev, gpu_cache, run, slopes_of
+from test_gpu_masked import CASES, check, dev, documents, gpu_cache, run, slopes_of
 
 pytestmark = pytest.mark.gpu
+
+INT8, FP8, INT4 = ref.INT8, ref.FP8, ref.INT4
+TENSOR, CHANNEL = ref.TENSOR, ref.CHANNEL
 
 
 @pytest.fixture(scope="module")
@@ -18,6 +30,19 @@ def kvq():
     from decode_attention_quantized_gb300 import kvq
     kvq.load()
     return kvq
+
+
+def lse_bound(c: ref.Cache, r_lse, size, slopes=None):
+    far = 0.0 if slopes is None else max(abs(float(s)) for s in slopes) * max(c.case.lens)
+    return 2.0 ** -17 * size + 2.0 ** -20 * (1 + np.abs(r_lse) + far)
+
+
+def check_lse(c: ref.Cache, lse, slopes=None, key_begin=None, key_end=None):
+    _, r_lse, _, _, size = ref.attend(c, slopes, key_begin, key_end)
+    some = r_lse != -np.inf
+    assert (lse[~some] == -np.inf).all() and np.isfinite(lse[some]).all()
+    e = np.abs(lse[some] - r_lse[some]) / lse_bound(c, r_lse, size, slopes)[some]
+    assert e.size == 0 or e.max() <= 1.0, f"lse {e.max():.2f} times its bound"
 
 
 def mass_call(kvq, c: ref.Cache, lse, mass, decay=1.0, fresh=None, slopes=None, key_begin=None, key_end=None):
@@ -74,3 +99,54 @@ def test_mass_of_ends_far_below_zero(kvq, c, name):
     got = mass_call(kvq, cache, lse, mass, 0.5, 0, s, None, end)
     want, tol = ref.key_mass(cache, lse.astype(np.float32), mass, 0.5, 0, s, None, end)
     assert (np.abs(got - want) <= tol).all()
+
+
+# ---------------------------------------------------------------------- the cap
+
+CAPPED = {
+    "grouped d64": ref.Case(d=64, hq=4, hkv=4, lens=(130, 65), c=1),
+    "grouped d128": ref.Case(dtype=FP8, lens=(333, 100), c=3),
+    "grouped d256 group scales": ref.Case(dtype=INT4, km=ref.GROUP, vm=ref.GROUP, gs=32, d=256, lens=(150, 77), c=2),
+    "wide d256": ref.Case(d=256, hq=16, hkv=2, lens=(257, 64), c=4),
+    "wide channel d256": ref.Case(dtype=INT4, km=CHANNEL, vm=CHANNEL, d=256, hq=12, hkv=2, lens=(190, 64), c=4),
+    "wide d576": ref.Case(d=576, hq=8, hkv=1, latent=True, dv=512, lens=(99, 140), c=2),
+    "tile d128": ref.Case(dtype=FP8, lens=(333, 100), c=40),
+    "tile tensor d128": ref.Case(dtype=INT8, km=TENSOR, vm=TENSOR, lens=(130, 97), c=33),
+    "tile channel d128": ref.Case(km=CHANNEL, vm=CHANNEL, lens=(333, 100), c=40),
+    "tile channel d256": ref.Case(dtype=INT4, km=CHANNEL, vm=CHANNEL, d=256, hq=14, hkv=2, lens=(190, 70), c=50),
+    "tile d256": ref.Case(d=256, hq=6, hkv=1, lens=(190, 70), c=50),
+}
+
+
+@pytest.mark.parametrize("cap", [5.0, 500.0, 20000.0])
+@pytest.mark.parametrize("name", CAPPED)
+def test_lse_under_a_cap(kvq, name, cap):
+    """The lse is fp32-accurate under a cap of any size: the cap's own error is
+    relative to the capped logit, not to the cap.  Under a steep bias, where few
+    keys carry a row and their errors do not average out, and without one."""
+    cache = ref.Cache(dataclasses.replace(CAPPED[name], softcap=cap))
+    for s in ([0.5] * cache.case.hq, None):
+        got = run(kvq, cache, s)
+        check_lse(cache, got[1], s)
+        check(cache, got, s)
+
+
+@pytest.mark.parametrize("cap", [5.0, 500.0, 20000.0])
+@pytest.mark.parametrize("name", CAPPED)
+def test_attention_and_mass_cap_alike(kvq, name, cap):
+    """The weights that the attention's own lse gives a row's keys add up to 1:
+    the two calls give a key the same score."""
+    cache = ref.Cache(dataclasses.replace(CAPPED[name], softcap=cap))
+    case = cache.case
+    s = [0.5] * case.hq
+    lse = run(kvq, cache, s)[1]
+    got = mass_call(kvq, cache, lse, np.zeros((cache.nb, case.hkv, case.bs), np.float32), slopes=s)
+    _, r_lse, _, _, size = ref.attend(cache, s)
+    # each weight moves by what its logit and the lse are off (their bound, twice),
+    # and by 2^-20 for exp2 and the sums
+    bound = 2 * lse_bound(cache, r_lse, size, s) + 2.0 ** -20
+    for b in range(len(case.lens)):
+        blk, row = cache.rows(b)
+        for h in range(case.hkv):
+            heads = slice(h * case.group, (h + 1) * case.group)
+            assert abs(got[blk, h, row].astype(np.float64).sum() - case.c * case.group) <= bound[b, :, heads].sum()
