@@ -593,9 +593,10 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         if (a.k_mode == KVQ_SCALE_PER_TENSOR) base *= a.k_scale[0];
         if (!capped) base *= kLog2e;
         // alpha = base * 2^(ek + eq) in two exact power-of-two steps, finite
-        // and > 0 (so that alpha * -inf stays -inf)
+        // and > 0 (so that alpha * -inf stays -inf); no higher floor: large K
+        // scales make ordinary logits of small queries
         const int e = ek + eq, e1 = e / 2;
-        alpha = valid ? fmaxf(fminf(base * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1e-30f) : 1.0f;
+        alpha = valid ? fmaxf(fminf(base * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1.17549435e-38f) : 1.0f;
         if constexpr (MASK) {
           if constexpr (CAP) alpha = fminf(alpha * inv_cap, 3.4028234e38f);
           // a row with no token sees the piece's keys with no bias: finite

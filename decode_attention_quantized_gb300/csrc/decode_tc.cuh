@@ -722,9 +722,10 @@ __global__ void __launch_bounds__(kTcWarps * 32, 1)
           if (cl == 0) {
             // alpha = base * 2^(ek + eq) as two exact power-of-two steps (each
             // exponent within the normal range), finite, and > 0 so that
-            // alpha * (-inf) stays -inf
+            // alpha * (-inf) stays -inf (no higher floor: large K scales make
+            // ordinary logits of small queries)
             const int e = ek + eq, e1 = e / 2;
-            const float al = fmaxf(fminf(base * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1e-30f);
+            const float al = fmaxf(fminf(base * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1.17549435e-38f);
             const bool valid = r < rows;
             f_alpha[r] = valid ? al : 1.0f;
             i_pos[r] = valid ? L - T + dev::div_small(r, inv_g) : -1;

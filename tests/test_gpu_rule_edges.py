@@ -150,3 +150,56 @@ def test_attention_and_mass_cap_alike(kvq, name, cap):
         for h in range(case.hkv):
             heads = slice(h * case.group, (h + 1) * case.group)
             assert abs(got[blk, h, row].astype(np.float64).sum() - case.c * case.group) <= bound[b, :, heads].sum()
+
+
+# ------------------------------------------------------------ ends of the range
+
+RANGE = {
+    "int8 d128": ref.Case(lens=(333, 100)),
+    "fp8 d256": ref.Case(dtype=FP8, d=256, hq=12, hkv=2, lens=(333, 90)),
+    "int4 d256": ref.Case(dtype=INT4, d=256, hq=8, hkv=2, lens=(200, 90)),
+}
+
+
+def far_cache(case, p):
+    """K rows of about 2^p and queries of about 2^-p: ordinary logits."""
+    cache = ref.Cache(case)
+    cache.k_scale *= np.float32(2.0 ** p)
+    cache.q = ref.bf16(cache.q * np.float32(2.0 ** -p))
+    return cache
+
+
+@pytest.mark.parametrize("p", [100, 122])
+@pytest.mark.parametrize("c", [1, 40])
+@pytest.mark.parametrize("name", RANGE)
+def test_large_keys_and_small_queries(kvq, name, c, p):
+    """The logit factor of a row may be small and the K scale large: neither is
+    cut off, and no product of the two leaves fp32's range on the way."""
+    cache = far_cache(dataclasses.replace(RANGE[name], c=c), p)
+    s = slopes_of(cache.case.hq)
+    got = run(kvq, cache, s)
+    check_lse(cache, got[1], s)
+    check(cache, got, s)
+
+
+@pytest.mark.parametrize("c,call", [(8, "decode"), (2, "decode"), (40, "prefill")])
+@pytest.mark.parametrize("name", RANGE)
+def test_large_keys_and_small_queries_without_a_rule(kvq, name, c, call):
+    cache = far_cache(dataclasses.replace(RANGE[name], c=c), 100)
+    case = cache.case
+    g = gpu_cache(kvq, cache)
+    p = kvq.make_params(2, case.hq, c, cache.width)
+    q, table, lens = dev(cache.q).to(torch.bfloat16), dev(cache.table), dev(np.array(case.lens, np.int32))
+    out = torch.zeros((2, c, case.hq, case.d), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((2, c, case.hq), device="cuda")
+    if call == "decode":
+        out, lse = kvq.decode_step(g, p, q, table, lens, kvq.alloc_decode_buffers(g, p))
+    else:
+        ws = torch.zeros(kvq.kvq_prefill_workspace_size(g, p) // 4, dtype=torch.int32, device="cuda")
+        kvq.kvq_prefill(g, p, q, table, lens, None, out, lse, ws)
+    assert kvq.kvq_get_device_error() == 0
+    r_lse, size = ref.attend(cache)[1], ref.attend(cache)[4]
+    # (the tensor-memory decode sums its weights as f16, each 2^-11 off: the sum,
+    # and so the lse, by 2^-11 at most)
+    assert (np.abs(lse.double().cpu().numpy() - r_lse) <= lse_bound(cache, r_lse, size) + 2.0 ** -11).all()
+    check(cache, (out.double().cpu().numpy(), r_lse))
