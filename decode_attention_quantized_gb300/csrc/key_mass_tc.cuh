@@ -372,6 +372,8 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
         ptx::tc_fence_after();
         const bool fast = key0 >= bmax && key0 + KT <= emin && (!bias || key0 + KT - 1 <= pmin);
         const float kf = (float)(key - k0);
+        // (K scale times logit factor first: a product of codes and a large scale
+        // may leave fp32's range where the logit does not)
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 1
         for (int c0 = c_lo; c0 < c_hi; c0 += 16) {
@@ -383,11 +385,11 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
               const float4 ac = *reinterpret_cast<const float4*>(r_ac + c0 + i);
               float x0, x1;
               if constexpr (CAP) {
-                x0 = fmaf(cap_l2, dev::tanh_near(y[i] * ks * ac.x), -ac.y);
-                x1 = fmaf(cap_l2, dev::tanh_near(y[i + 1] * ks * ac.z), -ac.w);
+                x0 = fmaf(cap_l2, dev::tanh_near(y[i] * (ks * ac.x)), -ac.y);
+                x1 = fmaf(cap_l2, dev::tanh_near(y[i + 1] * (ks * ac.z)), -ac.w);
               } else {
-                x0 = fmaf(y[i] * ks, ac.x, -ac.y);
-                x1 = fmaf(y[i + 1] * ks, ac.z, -ac.w);
+                x0 = fmaf(y[i], ks * ac.x, -ac.y);
+                x1 = fmaf(y[i + 1], ks * ac.z, -ac.w);
               }
               if (bias) {
                 const float4 ne = *reinterpret_cast<const float4*>(r_ne + c0 + i);
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kMassTcWarps * 32, 1)
             for (int i = 0; i < 16; ++i) {
               const float2 ac = r_ac[c0 + i], ne = r_ne[c0 + i];
               const MassTcRule ru = r_rule[c0 + i];
-              float x = y[i] * ks * ac.x;
+              float x = y[i] * (ks * ac.x);
               if constexpr (CAP) x = cap_l2 * dev::tanh_near(x);
               if (bias) x = fmaf(ne.x, (float)(abs(ru.pos - key) - ru.d0), x);
               s0 += key >= ru.begin && key < ru.end ? ptx::fast_exp2(x - ac.y) : 0.0f;

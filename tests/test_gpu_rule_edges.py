@@ -203,3 +203,21 @@ def test_large_keys_and_small_queries_without_a_rule(kvq, name, c, call):
     # and so the lse, by 2^-11 at most)
     assert (np.abs(lse.double().cpu().numpy() - r_lse) <= lse_bound(cache, r_lse, size) + 2.0 ** -11).all()
     check(cache, (out.double().cpu().numpy(), r_lse))
+
+
+@pytest.mark.parametrize("p", [100, 122])
+@pytest.mark.parametrize("cap", [0.0, 50.0])
+@pytest.mark.parametrize("c", [1, 40])
+@pytest.mark.parametrize("name", RANGE)
+def test_mass_of_large_keys_and_small_queries(kvq, name, c, cap, p):
+    """A padding token among the rows, whose logit factor is 0."""
+    cache = far_cache(dataclasses.replace(RANGE[name], c=c, softcap=cap), p)
+    case = cache.case
+    end = np.stack([L - c + np.arange(c) + 1 for L in case.lens])
+    if c > 1:
+        end[:, 3] = 0
+    lse = ref.attend(cache, None, None, end)[1]
+    got = mass_call(kvq, cache, lse, np.zeros((cache.nb, case.hkv, case.bs), np.float32), key_end=end)
+    want, tol = ref.key_mass(cache, lse.astype(np.float32), np.zeros_like(got), 1.0, case.c, None, None, end)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all()
