@@ -399,6 +399,7 @@ KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_pa
  * s and the visible keys are those of kvq_attend_masked with the same params
  * and mask (of kvq_decode / kvq_prefill with mask NULL); lse fp32
  * [B, C, Hq] is their lse_out (before the head sink; -inf rows add nothing).
+ * For the weights beside a head sink pass log(e^lse + e^sink) in its place.
  * kvq_attend_masked's is fp32-accurate; the unmasked calls' is a few 1e-7 of a
  * softcap off, and kvq_decode's with 17 or more query rows per kv head up to
  * 2^-11 (weights summed as f16), which the weights of the row then show.

@@ -1,11 +1,12 @@
-"""Evictions as a serving loop runs them, against the plain forms of score_ref."""
+"""Evictions as a serving loop runs them, and selections at the edges of what
+the arguments allow, against the plain forms of score_ref."""
 import numpy as np
 import pytest
 import torch
 
 import score_ref as ref
 from guard import guarded
-from test_gpu_evict import masses, pages
+from test_gpu_evict import masses, pages, select_call
 from test_gpu_masked import dev
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +167,30 @@ def test_first_selections_of_several_threads(kvq):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_SELECTIONS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "first selections agree" in r.stdout, r.stderr
+
+
+@pytest.mark.parametrize("batch", [129, 200])
+def test_select_of_many_sequences(kvq, batch):
+    """More than 128 sequences of unequal lengths in the one-pass selection
+    (capacity of 40,960 rows, a head or more per SM): heads in batch order."""
+    bs, hkv, budget, sinks, recent = 256, 2, 700, 3, 20
+    r = np.random.default_rng(batch)
+    lens = [int(x) for x in np.exp(r.uniform(np.log(2), np.log(9000), batch))]
+    lens[5], lens[batch - 1], lens[77], lens[3] = 40960, 33000, 0, 700
+    table, nb = pages(lens, bs, 2, width=160)
+    mass = masses("weights", hkv, bs, 4)(nb)
+    keep, kept = select_call(kvq, mass, table, lens, nb, bs, budget, sinks, recent)
+    assert kvq.kvq_get_device_error() == 0
+    assert np.array_equal(kept, np.minimum(lens, budget))
+    for b, L in enumerate(lens):
+        j = np.arange(L)
+        for h in range(hkv):
+            want = np.full(budget, -1, np.int32)
+            if L <= budget:
+                want[:L] = j
+            else:
+                mid = np.arange(sinks, L - recent)
+                w = mass[table[b, mid // bs], h, mid % bs]
+                rows = mid[np.lexsort((mid, -w))[:budget - sinks - recent]]
+                want[:] = np.sort(np.concatenate([j[:sinks], rows, j[L - recent:]]))
+            assert np.array_equal(keep[b, h], want), (b, h)

@@ -221,3 +221,52 @@ def test_mass_of_large_keys_and_small_queries(kvq, name, c, cap, p):
     want, tol = ref.key_mass(cache, lse.astype(np.float32), np.zeros_like(got), 1.0, case.c, None, None, end)
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= tol).all()
+
+
+# --------------------------------------------------- lse of a per-channel scale
+
+@pytest.mark.parametrize("dtype", [INT8, FP8, INT4])
+@pytest.mark.parametrize("d,c,hq,hkv", [(64, 5, 7, 1), (128, 1, 10, 2), (128, 40, 7, 1), (128, 40, 9, 3),
+                                        (256, 5, 10, 2), (256, 20, 7, 1), (256, 40, 20, 4), (256, 70, 3, 1),
+                                        (576, 3, 7, 1)])
+@pytest.mark.parametrize("sign", [0.5, -0.5])
+def test_lse_of_a_per_channel_scale_under_a_rule(kvq, dtype, d, c, hq, hkv, sign):
+    """The two-part operand with odd groups, documents, prefixes, biases of both
+    signs and a sink: an f16 operand of one part would be 2^-11 of sum |q k| off."""
+    if d == 576 and dtype == INT4:
+        pytest.skip("576-channel rows are 8-bit")
+    case = ref.Case(dtype=dtype, km=CHANNEL, vm=CHANNEL, d=d, c=c, hq=hq, hkv=hkv, lens=(160, max(c, 64)),
+                    latent=d == 576, dv=512 if d == 576 else 0)
+    cache = ref.Cache(case)
+    begin, end = documents(case, (13, 40, 64, 90))
+    end[1] = np.maximum(end[1], 30)  # a prefix, seen in both directions
+    begin[1] = np.minimum(begin[1], 8)
+    end[0, ::7] = 0
+    s = [sign] * hq
+    sink = np.linspace(-2.0, 2.0, hq)
+    got = run(kvq, cache, s, begin, end, sink)
+    check_lse(cache, got[1], s, begin, end)
+    check(cache, got, s, begin, end, sink)
+
+
+# -------------------------------------------------------------------- head sinks
+
+@pytest.mark.parametrize("name", ["int8 row d128", "fp8 tensor cap", "int4 channel d256"])
+@pytest.mark.parametrize("c", [1, 40])
+def test_mass_beside_a_sink(kvq, name, c):
+    """With a head sink the attention's weights are e^(s - log(e^lse + e^sink)):
+    kvq_key_mass takes that logarithm in the lse's place."""
+    case = dataclasses.replace(CASES[name], c=c, lens=(130, max(c, 64)))
+    cache = ref.Cache(case)
+    sink = np.linspace(-1.0, 3.0, case.hq)
+    lse = ref.attend(cache)[1]
+    both = np.logaddexp(lse, sink)
+    zero = np.zeros((cache.nb, case.hkv, case.bs), np.float32)
+    got = mass_call(kvq, cache, both, zero)
+    want, tol = ref.key_mass(cache, both.astype(np.float32), zero, 1.0, c)
+    assert (np.abs(got - want) <= tol).all()
+    for b, L in enumerate(case.lens):
+        blk, row = cache.rows(b)
+        total = got[blk, :, row].astype(np.float64).sum()
+        share = (1.0 / (1.0 + np.exp(sink - lse[b]))).sum()  # what the sink leaves of each row
+        assert abs(total - share) <= tol[blk, :, row].sum() + 2.0 ** -22 * case.c * case.hq * (1 + np.abs(both).max())
