@@ -1416,6 +1416,7 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
   a.budget = params->budget;
   a.sinks = params->sinks;
   a.recent = params->recent;
+  a.need = params->budget - params->sinks - params->recent;
   a.err = dev->err;
   if (select_many_ok(a, dev->sms))
     return from_cuda(launch_evict_select_many(a, reinterpret_cast<cudaStream_t>(stream)));

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
 
   SelectHead hd;
   if (!select_ends(a, b, h, rank * kSelThreads + tid, cs * kSelThreads, hd)) return;  // (the whole cluster)
-  const int L = hd.L, need_all = hd.need;
+  const int L = hd.L;
   int32_t* keep = a.keep + (size_t)seg * a.budget;
 
   // The M rows between the ends, in runs of 32 from a multiple of 32 on (so
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
   // f(run, key) for this warp's runs; keys of 0 among them (rows outside the M,
   // runs past the last of a group of eight) are below every row's: they never
   // reach the threshold, whose digits are found from the top
-  auto each = [&](auto f) {
+  auto each_held = [&](auto f) {
 #pragma unroll
     for (int j0 = 0; j0 < kSelKeys; j0 += 8) {
       if (j0 < m) {
@@ -143,11 +143,14 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
         for (int j = j0; j < j0 + 8; ++j) f(j, key[j]);
       }
     }
+  };
+  auto each = [&](auto f) {
+    each_held(f);
     for (int j = kSelKeys; j < m; ++j) f(j, load(j));
   };
 
   uint32_t prefix = 0;
-  int need = need_all;
+  int need = hd.need;
   uint32_t T = 0;  // rows above it stay, and the first `need` equal to it
   uint32_t* my_hist = hist + lane;
 #pragma unroll 1
@@ -253,26 +256,35 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
   be = __reduce_add_sync(0xffffffffu, be);
   const uint32_t below = (1u << lane) - 1u;
   int32_t* mid = keep + a.sinks;
-  // (Runs that are read again may give other weights than the passes saw, when
-  // another stream writes them meanwhile: then more rows than need_all may be
-  // above T, or `need` have gone below 0.  No place past the head's is written.)
-  auto put = [&](uint32_t to, int j) {
-    if (to < (uint32_t)need_all) mid[to] = pos0 + j * 32;
-  };
-  if (need == 0) {
-    each([&](int j, uint32_t k) {
-      const uint32_t mg = __ballot_sync(0xffffffffu, k > T);
-      if (k > T) put(bg + __popc(mg & below), j);
-      bg += __popc(mg);
-    });
-  } else {
-    each([&](int j, uint32_t k) {
-      const uint32_t mg = __ballot_sync(0xffffffffu, k > T), me = __ballot_sync(0xffffffffu, k == T);
-      const uint32_t g = bg + __popc(mg & below), e = be + __popc(me & below);
-      if (k > T || (k == T && e < (uint32_t)need)) put(g + min(e, (uint32_t)need), j);
+  // Runs that are read again may give other weights in each pass, when another
+  // stream writes them meanwhile: then more than a.need rows may have been
+  // counted, or `need` have gone below 0.  A warp whose rows would end past the
+  // head's places writes none, and the runs that are read once more are bounded
+  // store by store (all of them so: 6% of a call whose rows are all held).
+  if (bg + gt + min(be + eq, (uint32_t)need) <= (uint32_t)a.need) {
+    if (need == 0) {
+      each_held([&](int j, uint32_t k) {
+        const uint32_t mg = __ballot_sync(0xffffffffu, k > T);
+        if (k > T) mid[bg + __popc(mg & below)] = pos0 + j * 32;
+        bg += __popc(mg);
+      });
+    } else {
+      each_held([&](int j, uint32_t k) {
+        const uint32_t mg = __ballot_sync(0xffffffffu, k > T), me = __ballot_sync(0xffffffffu, k == T);
+        const uint32_t g = bg + __popc(mg & below), e = be + __popc(me & below);
+        if (k > T || (k == T && e < (uint32_t)need)) mid[g + min(e, (uint32_t)need)] = pos0 + j * 32;
+        bg += __popc(mg);
+        be += __popc(me);
+      });
+    }
+#pragma unroll 8
+    for (int j = kSelKeys; j < m; ++j) {
+      const uint32_t k = load(j), mg = __ballot_sync(0xffffffffu, k > T), me = __ballot_sync(0xffffffffu, k == T);
+      const uint32_t e = be + __popc(me & below), to = bg + __popc(mg & below) + min(e, (uint32_t)need);
+      if ((k > T || (k == T && e < (uint32_t)need)) && to < (uint32_t)a.need) mid[to] = pos0 + j * 32;
       bg += __popc(mg);
       be += __popc(me);
-    });
+    }
   }
   ptx::cluster_sync();  // no CTA leaves while another reads its counts
 }

@@ -321,6 +321,7 @@ struct SelectArgs {
   int32_t* kept_lens;          // [B]
   int batch, num_kv_heads, max_blocks_per_seq, num_blocks, block_size, log2_bs, lim;
   int budget, sinks, recent;
+  int need;                    // budget - sinks - recent: rows chosen by weight
   int spread;                  // 1: use every CTA of the cluster (SMs are free)
   unsigned int* err;
 };
