@@ -861,11 +861,12 @@ kvq_status decode_workspace_size(const kvq_cache* cache, const kvq_decode_params
 // kernel takes up to 8 tokens (head_dim 576: up to its 48 rows).  4 x 32,768
 // keys, mma.sync against the tile: head_dim 256 int8 12 rows 89 / 108 us, 18
 // rows 129 / 109, 48 rows 170 / 110; head_dim 128 int8 16 rows 107 / 138, 24
-// rows 181 / 138, 56 rows 310 / 137.  Under a softcap, whose tanh one warp
-// computes for 32 rows there, from 64 rows on (fp8 32 rows 179 / 257).  A
-// two-part Q operand (split: a per-channel K scale whose call wants the lse)
-// leaves the tile 64 rows at head_dim 256; G times a whole number of tokens
-// fills at least 56 of them.
+// rows 181 / 138, 56 rows 310 / 137.  Under a softcap, which one warp computes
+// for 32 rows there, from 64 rows on (fp8 head_dim 128 32 rows 183 / 232, int8
+// per-channel 197 / 244, int4 head_dim 256 24 rows 157 / 175).  A two-part Q
+// operand (split: a per-channel K scale whose call wants the lse) leaves the
+// tile 64 rows at head_dim 256, of which G times a whole number of tokens fills
+// at least 56: there 56 rows are enough.
 struct MaskShape {
   int T, n;
   bool qt, split;
@@ -1007,7 +1008,8 @@ kvq_status check_evict(const kvq_evict_params* p) {
 // 2048 kept, 512 heads 46 / 42), a bit map that leaves two CTAs to an SM,
 // 16-byte loads, and a list that holds ten standard deviations of the sample's
 // rank (512 ragged heads of up to 131,072 rows, 65,536 kept: without this 304 /
-// 167, most heads going through the digits).
+// 167, most heads going through the digits).  Weights that are nearly all equal
+// go through the digits whatever the rule says (figures at the kernel).
 bool select_many_ok(const SelectArgs& a, int sms) {
   const long long segs = (long long)a.batch * a.num_kv_heads;
   const double need = a.budget - a.sinks - a.recent, rest = a.lim - need;

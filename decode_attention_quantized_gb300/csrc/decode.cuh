@@ -1460,7 +1460,10 @@ cudaError_t dispatch_decode(int head_dim, int nt, const CUtensorMap* tk, const C
     case 256: return by_nt(std::integral_constant<int, 256>{});
     case 576:
       if constexpr (DT != KVQ_INT4) {
-        if (nt == 1) return go(KernelCfg<576, (RULE > 0) ? 1 : 2, 1>{});  // two CTAs per SM (96 registers)
+        // two CTAs per SM (96 registers); with a score rule one, whose rows need
+        // more: 131,072 keys of one sequence 60 us against 100 with two, 32 x
+        // 4096 fp8 keys 54 / 64, 8 x 32,768 int8 keys 95 / 74, fp8 87 / 85
+        if (nt == 1) return go(KernelCfg<576, (RULE > 0) ? 1 : 2, 1>{});
         if (nt == 2) return go(KernelCfg<576, 1, 2>{});
         if (nt == 3) return go(KernelCfg<576, 1, 3>{});
       }

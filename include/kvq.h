@@ -356,10 +356,13 @@ KVQ_API kvq_status kvq_prefill(const kvq_cache* cache, const kvq_decode_params* 
  *                  rows are zero and their lse is -inf
  * The logit of query head h and key j is softcap(sm_scale <q, k_j>) -
  * slopes[h] * |pos - j| (the bias comes after the cap and is not capped).
- * Positions and distances count cache rows: after an eviction they are those
- * of the rows that were kept.  The reference's pages name neither; the rules
- * are the usual ones of models with linear distance biases, packed documents
- * and bidirectional prefixes. */
+ * Positions and distances count cache rows.  After kvq_evict_compact they are
+ * those of the rows that were kept, and every kv head kept its own: a distance
+ * shrinks by the evicted rows between query and key, and key_begin, key_end and
+ * window cut other tokens in each head.  Only the rows that sinks and recent
+ * protect lie at the same places in all of them.  The reference's pages name
+ * neither rule; both are the usual ones of models with linear distance biases,
+ * packed documents and bidirectional prefixes. */
 typedef struct {
   const float* slopes;      /* fp32 [Hq] (device; finite, any sign), or NULL: no bias */
   const int32_t* key_begin; /* int32 [B, C] (device; any values), or NULL */
@@ -372,9 +375,11 @@ typedef struct {
  * Arguments and results as in kvq_prefill; mask may be NULL (causal, no
  * bias).  Sequences are cut into groups of tokens; keys that no token of a
  * group sees are not read.  With head_dim 128 or 256, no group-wise scales,
- * KVQ_DECODE_NO_TCGEN05 unset and more than 16 query rows per kv head (64 or
- * more under a softcap), the groups are tiles of up to 128 rows on tcgen05
- * MMAs; otherwise of up to 8 tokens on the mma.sync kernel.  KVQ_DECODE_EARLY_INPUTS and
+ * KVQ_DECODE_NO_TCGEN05 unset and more than 16 query rows per kv head, the
+ * groups are tiles of up to 128 rows on tcgen05 MMAs; otherwise of up to 8
+ * tokens on the mma.sync kernel.  (Under a softcap tiles from 64 rows on; with
+ * a per-channel K scale, an lse_out and head_dim 256 tiles have up to 64 rows,
+ * from 56 on under a softcap.)  KVQ_DECODE_EARLY_INPUTS and
  * KVQ_DECODE_EARLY_CACHE have no effect here.  lse_out is fp32-accurate: with
  * a per-channel K scale the query operand is then carried in two f16 parts,
  * which costs time (a prompt's tiles about half as much again at head_dim 128
