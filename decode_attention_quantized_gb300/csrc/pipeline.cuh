@@ -401,7 +401,9 @@ struct TileOrder {
 // segment's page a tile ahead, and the lanes issue their copies side by side
 // under one expect-tx arrival of the stage's bytes.  (With lane 0 alone
 // working through the segments, a stage of 128 keys took it 2000 to 3400
-// clocks, about 850 a segment, and one CTA per SM waited for that.)
+// clocks, about 850 a segment, and one CTA per SM waited for that.)  Rows of a
+// stage that are not loaded hold whatever was there, like rows that no token
+// sees.
 // DESC: a piece's tiles from its last to its first (TileOrder).
 template <class Gm, bool DESC = false>
 __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& sp, const CUtensorMap* tmk,
@@ -449,7 +451,9 @@ __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& 
         if (!ok) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      bool load = mine && key < k1 && ok;  // nothing is loaded after a timeout
+      // (nothing is loaded after a timeout, nor from pages that end before the
+      // first key some token sees: they may have left the table)
+      bool load = mine && key < k1 && key + seg_rows > vs.lo && ok;
       if (load && (id < 0 || id >= a.num_blocks)) {
         atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
         load = false;

@@ -373,8 +373,10 @@ typedef struct {
  * sequence under a score rule: one call for a decode step (C = 1, or 1 +
  * drafts) and for a prompt's chunk (any C, not only multiples of a tile).
  * Arguments and results as in kvq_prefill; mask may be NULL (causal, no
- * bias).  Sequences are cut into groups of tokens; keys that no token of a
- * group sees are not read.  With head_dim 128 or 256, no group-wise scales,
+ * bias).  Sequences are cut into groups of tokens; of a group's keys those
+ * before the first and behind the last that some token of it sees are not read,
+ * and their pages need not be in the table.  (Those between are read, seen or
+ * not.)  With head_dim 128 or 256, no group-wise scales,
  * KVQ_DECODE_NO_TCGEN05 unset and more than 16 query rows per kv head, the
  * groups are tiles of up to 128 rows on tcgen05 MMAs; otherwise of up to 8
  * tokens on the mma.sync kernel.  (Under a softcap tiles from 64 rows on; with

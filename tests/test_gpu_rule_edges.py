@@ -270,3 +270,27 @@ def test_mass_beside_a_sink(kvq, name, c):
         total = got[blk, :, row].astype(np.float64).sum()
         share = (1.0 / (1.0 + np.exp(sink - lse[b]))).sum()  # what the sink leaves of each row
         assert abs(total - share) <= tol[blk, :, row].sum() + 2.0 ** -22 * case.c * case.hq * (1 + np.abs(both).max())
+
+
+# ------------------------------------------------------------- freed pages
+
+@pytest.mark.parametrize("name,c", [("int8 row d128", 1), ("fp8 row", 5), ("int8 row d256 g6", 40), ("fp8 row", 40),
+                                    ("int4 channel d256", 40), ("latent d576", 3), ("int8 channel d64", 6)])
+@pytest.mark.parametrize("how", ["window", "documents"])
+def test_pages_before_every_key_that_is_seen(kvq, name, c, how):
+    """Pages whose rows lie wholly before the first key that a token sees, down to
+    the last one, may have left the table: they are neither read nor flagged."""
+    case = dataclasses.replace(CASES[name], c=c, bs=16, lens=(250, 241), window=30 if how == "window" else 0)
+    cache = ref.Cache(case)
+    begin = None
+    if how == "documents":
+        begin = np.array([[L - c - 30] * c for L in case.lens], np.int32)
+    want = ref.attend(cache, None, begin)
+    for b, L in enumerate(case.lens):
+        first = L - c + 1 - 30 if how == "window" else L - c - 30
+        cache.table[b, :first // 16] = -1
+    g = gpu_cache(kvq, cache)
+    got = run(kvq, cache, None, begin, gcache=g)
+    assert (np.abs(got[1] - want[1]) <= lse_bound(cache, want[1], want[4]) + 2.0 ** -15).all()
+    tol = 2.0 ** -8 * np.abs(want[0]) + want[3] + 2 * (2.0 ** -11 * want[4] + 2.0 ** -15)[..., None] * want[2] + 1e-30
+    assert (np.abs(got[0] - want[0]) <= tol).all()
