@@ -1465,30 +1465,28 @@ KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_par
   if (!aligned(block_table, 4) || (dst_table && !aligned(dst_table, 4)) || !aligned(keep, 4) ||
       !aligned(kept_lens, 4) || (mass && !aligned(mass, 4)) || !aligned(workspace, 256))
     return KVQ_ERR_INVALID_ARG;
+  const uint64_t lens = 4ull * params->batch, table = lens * params->max_blocks_per_seq;
+  const uint64_t rows = lens * params->num_kv_heads * params->budget;
+  // what says where rows lie may not be among what is written: a unit's
+  // threads each read it
+  auto writes_rows = [&](const void* to, uint64_t n) {
+    return overlap(block_table, table, to, n) || overlap(dst_table, dst_table ? table : 0, to, n) ||
+           overlap(keep, rows, to, n) || overlap(kept_lens, lens, to, n);
+  };
   {
-    // what says where rows lie may not be among what is written: a unit's
-    // threads each read it
-    const uint64_t lens = 4ull * params->batch, table = lens * params->max_blocks_per_seq;
-    const uint64_t rows = lens * params->num_kv_heads * params->budget;
     const uint64_t cells = (uint64_t)params->num_blocks * params->num_kv_heads * params->block_size;
-    const std::pair<const void*, uint64_t> reads[] = {
-        {block_table, table}, {dst_table, dst_table ? table : 0}, {keep, rows}, {kept_lens, lens}};
-    const std::pair<const void*, uint64_t> writes[] = {
-        {workspace, workspace_bytes},
-        {cache->k_codes, cells * row_bytes(cache)},
-        {cache->v_codes, cells * row_bytes(cache)},
-        {cache->k_scale, 4 * cells * scales_per_row(cache, cache->k_mode)},
-        {cache->v_scale, 4 * cells * scales_per_row(cache, cache->v_mode)},
-        {mass, mass ? 4 * cells : 0}};
-    for (auto [r, n] : reads)
-      for (auto [w, m] : writes)
-        if (overlap(r, n, w, m)) return KVQ_ERR_INVALID_ARG;
+    if (writes_rows(cache->k_codes, cells * row_bytes(cache)) || writes_rows(cache->v_codes, cells * row_bytes(cache)) ||
+        writes_rows(cache->k_scale, 4 * cells * scales_per_row(cache, cache->k_mode)) ||
+        writes_rows(cache->v_scale, 4 * cells * scales_per_row(cache, cache->v_mode)) ||
+        writes_rows(mass, mass ? 4 * cells : 0))
+      return KVQ_ERR_INVALID_ARG;
   }
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
   CompactPlan P;  // (the plan with a weight array, whether or not there is one: its workspace was asked for)
   if (kvq_status s = compact_plan(cache, params, true, *dev, &P)) return s;
   if (workspace_bytes < P.ws) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  if (writes_rows(workspace, P.ws)) return KVQ_ERR_INVALID_ARG;
   CompactArgs a{};
   a.block_table = block_table;
   a.in_place = !dst_table || dst_table == block_table;

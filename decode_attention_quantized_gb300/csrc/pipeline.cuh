@@ -404,8 +404,11 @@ struct TileOrder {
 // clocks, about 850 a segment, and one CTA per SM waited for that.)  Rows of a
 // stage that are not loaded hold whatever was there, like rows that no token
 // sees.
-// DESC: a piece's tiles from its last to its first (TileOrder).
-template <class Gm, bool DESC = false>
+// ATTEND: the attention kernels, a piece's tiles from its last to its first
+// (TileOrder), and nothing from pages that end before the first key some token
+// sees (they may have left the table).  The key-mass kernels write to every
+// key's place and flag each unreadable id.
+template <class Gm, bool ATTEND = false>
 __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& sp, const CUtensorMap* tmk,
                               const CUtensorMap* tmv, uint8_t* ring, uint64_t* bar_full, uint64_t* bar_empty,
                               const int* pl_pre, const int* pl_misc) {
@@ -430,7 +433,7 @@ __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& 
     sp.piece(a, gt, b, h, k0, k1, L, slot, next);
     const VSeq vs = a.vseq[b];
     const int32_t* bt = a.block_table + (size_t)vs.brow * a.max_blocks_per_seq;
-    using Order = TileOrder<KT, DESC>;
+    using Order = TileOrder<KT, ATTEND>;
     const int key_first = Order::first(k0, k1) + my_row;
     int id_next = mine && key_first < k1 ? bt[key_first >> a.log2_bs] : -1;
     if (gt != sp.t_begin) {
@@ -451,9 +454,7 @@ __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& 
         if (!ok) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      // (nothing is loaded after a timeout, nor from pages that end before the
-      // first key some token sees: they may have left the table)
-      bool load = mine && key < k1 && key + seg_rows > vs.lo && ok;
+      bool load = mine && key < k1 && (!ATTEND || key + seg_rows > vs.lo) && ok;  // nothing is loaded after a timeout
       if (load && (id < 0 || id >= a.num_blocks)) {
         atomicOr(a.err, KVQ_DEVERR_BLOCK_ID);
         load = false;

@@ -382,11 +382,12 @@ typedef struct {
  * tokens on the mma.sync kernel.  (Under a softcap tiles from 64 rows on; with
  * a per-channel K scale, an lse_out and head_dim 256 tiles have up to 64 rows,
  * from 56 on under a softcap.)  KVQ_DECODE_EARLY_INPUTS and
- * KVQ_DECODE_EARLY_CACHE have no effect here.  lse_out is fp32-accurate: with
- * a per-channel K scale the query operand is then carried in two f16 parts,
- * which costs time (a prompt's tiles about half as much again at head_dim 128
- * and twice at 256); lse_out NULL leaves that out.  batch <= 1024;
- * batch * C <= 2^30.  out must not overlap q.  workspace: at least
+ * KVQ_DECODE_EARLY_CACHE have no effect here.  lse_out is fp32-accurate (on the
+ * tiles a bias counts to 2^-14 of its slope): with a per-channel K scale the
+ * query operand is then carried in two f16 parts, which costs time (a prompt's
+ * tiles about half as much again at head_dim 128 and twice at 256); lse_out NULL
+ * leaves that out.  batch <= 1024; batch * C <= 2^30.  out must not overlap q.
+ * workspace: at least
  * kvq_attend_masked_workspace_size bytes, 256-byte aligned; it belongs to
  * this call until the call's kernels have run. */
 KVQ_API kvq_status kvq_attend_masked_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
@@ -416,7 +417,9 @@ KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_pa
  * decay in [0, 1]: 1 sums, 0 overwrites (mass is then not read).  The scores
  * are fp32-accurate (a folded per-channel K scale enters as two f16 parts).
  * Each key is written by one thread in a fixed order: repeated calls give the
- * same bits.  A page must not be shared by two sequences of the call.
+ * same bits.  A page must not be shared by two sequences of the call.  Every
+ * page of [0, seq_lens[b]) is needed: an unreadable block id sets
+ * KVQ_DEVERR_BLOCK_ID, and its keys keep what they held.
  * workspace: at least kvq_key_mass_workspace_size bytes, 256-byte aligned; it
  * belongs to this call until the call's kernels have run. */
 KVQ_API kvq_status kvq_key_mass_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
@@ -472,7 +475,8 @@ KVQ_API kvq_status kvq_evict_select(const kvq_evict_params* params, const float*
  * of its first position.
  * In place the kernel's blocks wait for one another (a cooperative launch with
  * bounded waits; KVQ_DEVERR_TIMEOUT).  The tables, keep and kept_lens may not
- * overlap the workspace, the cache's arrays or mass (refused).  workspace: at
+ * overlap the cache's arrays, mass or the part of the workspace that is needed
+ * (refused).  workspace: at
  * least kvq_evict_compact_workspace_size bytes, 256-byte aligned (used in place
  * only, but checked always); it belongs to this call until its kernel has
  * run. */

@@ -73,6 +73,29 @@ def test_lengths_beside_one_another(kvq):
     assert np.array_equal(keep.cpu().numpy(), want[0]) and np.array_equal(one[3:6].cpu().numpy(), want[1])
 
 
+def test_rows_in_the_workspace_are_refused(kvq):
+    """The rows' places may not lie in the part of the workspace that a call uses;
+    behind it, in the same allocation, they may."""
+    bs, hkv, d, budget, lens = 16, 2, 64, 24, (60, 33)
+    g = kvq.QuantizedPagedCache(INT8, ROW, ROW, 10, bs, hkv, d)
+    p = kvq.make_evict_params(2, 4, budget, num_blocks=10, block_size=bs, num_kv_heads=hkv)
+    n = kvq.kvq_evict_compact_workspace_size(g, p) // 4
+    arena = torch.zeros(n + 4 * 64, dtype=torch.int32, device="cuda")
+    table = dev(np.arange(8, dtype=np.int32).reshape(2, 4))
+    mass = torch.rand((10, hkv, bs), device="cuda")
+    for at in (n, n - 1, 0):
+        kept = arena[at:at + 2]
+        keep = torch.zeros((2, hkv, budget), dtype=torch.int32, device="cuda")
+        kvq.kvq_evict_select(p, mass, table, dev(np.array(lens, np.int32)), keep, kept)
+        if at == n:
+            kvq.kvq_evict_compact(g, p, table, None, keep, kept, mass, arena)
+            assert kept.tolist() == [budget, budget]
+        else:
+            with pytest.raises(kvq.KvqError):
+                kvq.kvq_evict_compact(g, p, table, None, keep, kept, mass, arena)
+    assert kvq.kvq_get_device_error() == 0
+
+
 def test_selection_while_the_weights_change(kvq):
     """Heads too long to be held on chip are read again in every pass.  Weights
     that another stream writes meanwhile make the rows in `keep` unspecified,

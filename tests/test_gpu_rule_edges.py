@@ -294,3 +294,45 @@ def test_pages_before_every_key_that_is_seen(kvq, name, c, how):
     assert (np.abs(got[1] - want[1]) <= lse_bound(cache, want[1], want[4]) + 2.0 ** -15).all()
     tol = 2.0 ** -8 * np.abs(want[0]) + want[3] + 2 * (2.0 ** -11 * want[4] + 2.0 ** -15)[..., None] * want[2] + 1e-30
     assert (np.abs(got[0] - want[0]) <= tol).all()
+
+
+# ------------------------------------------------------------------ steep biases
+
+@pytest.mark.parametrize("slope", [0.25, 30.0, 1000.0])
+@pytest.mark.parametrize("d,km,c,hq,hkv,cap", [(128, ref.ROW, 1, 8, 2, 0.0), (128, ref.ROW, 70, 8, 2, 0.0),
+                                               (256, CHANNEL, 70, 6, 1, 0.0), (256, ref.ROW, 70, 6, 1, 30.0),
+                                               (64, ref.ROW, 5, 4, 1, 0.0), (256, ref.ROW, 4, 16, 2, 0.0)])
+def test_steep_biases(kvq, slope, d, km, c, hq, hkv, cap):
+    """A bias is slope times distance to a rounding or two of itself; in the tile
+    kernel to 2^-14 of the slope.  (Some tokens sit on the last key of a tile,
+    some see no key near.)"""
+    case = ref.Case(d=d, km=km, vm=km, c=c, hq=hq, hkv=hkv, lens=(192, 230), softcap=cap)
+    cache = ref.Cache(case)
+    pos = np.stack([L - c + np.arange(c) for L in case.lens])
+    end = pos + 1
+    end[:, ::3] -= 5
+    s = [slope] * hq
+    lse = run(kvq, cache, s, None, end)[1]
+    _, r_lse, _, _, size = ref.attend(cache, s, None, end)
+    # (slope times an integer below 2^24 is rounded once where the anchor's bias
+    # goes back into the lse; that is in 2^-20 of the lse.  The tile kernel takes
+    # up to 63 slopes a tile from a rounded base in at most 8 rounded steps: 9
+    # times half an ulp, 2^-24 of 64 slopes, is below 2^-14 of the slope)
+    tile = d >= 128 and c * (hq // hkv) > 16
+    bound = 2.0 ** -17 * size + 2.0 ** -20 * (1 + np.abs(r_lse)) + (2.0 ** -14 * slope if tile else 0.0)
+    assert (np.abs(lse - r_lse) <= bound).all()
+
+
+# ------------------------------------------------------------ mixed scale modes
+
+@pytest.mark.parametrize("km,vm", [(CHANNEL, ref.GROUP), (ref.GROUP, CHANNEL), (ref.ROW, ref.GROUP), (CHANNEL, ref.ROW)])
+@pytest.mark.parametrize("d,c,hq,hkv", [(128, 1, 8, 2), (128, 9, 7, 1), (256, 20, 6, 3), (64, 3, 4, 4)])
+def test_scale_modes_of_two_kinds(kvq, km, vm, d, c, hq, hkv):
+    """K and V of different modes, with and without the two-part operand."""
+    case = ref.Case(dtype=INT4, km=km, vm=vm, gs=32, d=d, c=c, hq=hq, hkv=hkv, lens=(140, max(c, 33)))
+    cache = ref.Cache(case)
+    begin, end = documents(case, (13, 40, 90))
+    s = slopes_of(hq, -1.0)
+    got = run(kvq, cache, s, begin, end)
+    check_lse(cache, got[1], s, begin, end)
+    check(cache, got, s, begin, end)
