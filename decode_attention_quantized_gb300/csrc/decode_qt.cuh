@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         } else if (k_row) {
           wait(&b_ksc[it & 3], (it >> 2) & 1);
           const float* ksc = ksb + (it & 3) * KT;
-          const float am = MASK || !capped ? alpha : 1.0f;  // (masked: with 1 / softcap in it)
+          const float am = CAP || softcap <= 0.0f ? alpha : 1.0f;  // (CAP: with 1 / softcap in it)
 #pragma unroll
           for (int k = 0; k < KT; k += 4) {
             const float4 s4 = *reinterpret_cast<const float4*>(ksc + k);
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
             ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], a0, a1);
             ptx::mul_x2(y[k + 2], y[k + 3], y[k + 2], y[k + 3], a2, a3);
           }
-        } else if (MASK || !capped) {
+        } else if (CAP || softcap <= 0.0f) {
 #pragma unroll
           for (int k = 0; k < KT; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
         }
