@@ -685,8 +685,11 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         // logits in log2 units: y = S * k_scale * alpha (softcapped), masked
         // keys -inf; the products two at a time (f32x2)
         // (masked, under a bias: b0 + sg k for key key0 + k where distances are
-        // linear over the tile, one integer base per tile and exact steps from
-        // every sixteenth key on; folded into the products when no cap follows)
+        // linear over the tile, one integer base per tile and steps of the slope
+        // from every sixteenth key on: 2^-14 of a slope off at most, and folded
+        // into the products when no cap follows.  Integer distances that meet
+        // the slope last are off by a rounding only, and took a biased
+        // per-channel prompt from 452 to 546 us)
         float sg = 0.0f, b0 = 0.0f;
         bool folded = false;
         if constexpr (MASK) {

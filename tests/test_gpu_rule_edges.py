@@ -336,3 +336,19 @@ def test_scale_modes_of_two_kinds(kvq, km, vm, d, c, hq, hkv):
     got = run(kvq, cache, s, begin, end)
     check_lse(cache, got[1], s, begin, end)
     check(cache, got, s, begin, end)
+
+
+# ------------------------------------------------------------------- repetition
+
+@pytest.mark.parametrize("name,c", [("int8 row d128", 1), ("fp8 tensor cap", 8), ("fp8 row", 40),
+                                    ("int4 channel d256", 40), ("int8 row d256 g6", 90), ("latent d576", 3)])
+def test_repeated_calls_give_the_same_bits(kvq, name, c):
+    case = dataclasses.replace(CASES[name], c=c, lens=(1500, 700, max(c, 97)))
+    cache = ref.Cache(case)
+    g = gpu_cache(kvq, cache)
+    s = slopes_of(case.hq)
+    begin, end = documents(case, (13, 400, 900))
+    first = run(kvq, cache, s, begin, end, gcache=g)
+    for _ in range(4):
+        again = run(kvq, cache, s, begin, end, gcache=g)
+        assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
