@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "kvq_internal.h"
 
@@ -60,6 +61,17 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool overlap(const void* a, uint64_t n, const void* b, uint64_t m) {
   const uint64_t x = reinterpret_cast<uint64_t>(a), y = reinterpret_cast<uint64_t>(b);
   return n > 0 && m > 0 && x < y + m && y < x + n;
+}
+// Whether no output shares a byte with an input or another output.
+template <size_t N, size_t M>
+bool disjoint(const std::pair<const void*, uint64_t> (&in)[N], const std::pair<const void*, uint64_t> (&out)[M]) {
+  for (size_t i = 0; i < M; ++i) {
+    for (const auto& x : in)
+      if (overlap(out[i].first, out[i].second, x.first, x.second)) return false;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i].first, out[i].second, out[j].first, out[j].second)) return false;
+  }
+  return true;
 }
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int ilog2(int x) {
@@ -199,7 +211,18 @@ size_t fixed_smem(const kvq_cache* c, int row_groups, int key_warps, int nt, int
 // wide), or -group_size for the grouped layout with per-group scales.
 int kernel_nt(const kvq_cache* c, const Plan& P) { return any_group(c) ? -c->group_size : P.nt; }
 
-cudaError_t occupancy(const kvq_cache* c, int nt, int threads, size_t smem, bool mask, bool split, int* n) {
+// The mma.sync kernel's dispatch for draft trees.
+auto tree_kernel(const kvq_cache* c, bool split) {
+  switch (c->dtype) {
+    case KVQ_INT8: return split ? dispatch_decode_tree_split_int8 : dispatch_decode_tree_int8;
+    case KVQ_FP8_E4M3: return split ? dispatch_decode_tree_split_fp8 : dispatch_decode_tree_fp8;
+    default: return split ? dispatch_decode_tree_split_int4 : dispatch_decode_tree_int4;
+  }
+}
+
+cudaError_t occupancy(const kvq_cache* c, int nt, int threads, size_t smem, bool mask, bool split, bool tree,
+                      int* n) {
+  if (tree) return tree_kernel(c, split)(c->head_dim, nt, nullptr, nullptr, nullptr, 0, threads, smem, nullptr, n);
   if (mask) {
     switch (c->dtype) {
       case KVQ_INT8: return occupancy_decode_mask_int8(c->head_dim, nt, split, threads, smem, n);
@@ -371,12 +394,13 @@ kvq_status make_plan_mass(const kvq_cache* c, const kvq_decode_params* p, const 
 // Which kernels a plan is for: the attention kernels, their masked instances
 // (no tensor-memory layout of keys as MMA rows there; Split: a two-part Q
 // operand), the key-mass kernel.
-enum PlanKind { kPlanDecode = 0, kPlanMasked = 1, kPlanMass = 2, kPlanMaskedSplit = 3 };
+enum PlanKind { kPlanDecode = 0, kPlanMasked = 1, kPlanMass = 2, kPlanMaskedSplit = 3, kPlanTree = 4, kPlanTreeSplit = 5 };
 
 kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool qt,
                               PlanKind kind, Plan* out) {
   if (kind == kPlanMass) return make_plan_mass(c, p, dev, out);
-  const bool split = kind == kPlanMaskedSplit, mask = kind == kPlanMasked || split;
+  const bool split = kind == kPlanMaskedSplit || kind == kPlanTreeSplit;
+  const bool tree = kind == kPlanTree || kind == kPlanTreeSplit, mask = kind == kPlanMasked || split || tree;
   Plan P{};
   const int G = p->num_q_heads / c->num_kv_heads;
   P.rows = G * p->q_tokens;
@@ -441,7 +465,7 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
     stages = stages > kMaxStages ? kMaxStages : stages;
     const size_t smem = fixed_smem(c, P.row_groups, P.key_warps, P.nt, B, stages, mask, split) + (size_t)stages * stride;
     int n = 0;
-    if (occupancy(c, kernel_nt(c, P), P.threads, smem, mask, split, &n) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (occupancy(c, kernel_nt(c, P), P.threads, smem, mask, split, tree, &n) != cudaSuccess) return KVQ_ERR_CUDA;
     if (n >= target) {
       occ = target;
       P.stages = stages;
@@ -618,13 +642,18 @@ struct MaskCall {
   const int32_t* key_begin;
   const int32_t* key_end;
   bool split;  // the Q operand in two parts
+  const uint32_t* tree_bits;  // draft trees; else null
+  int tree_words;
   // where the query-tile kernel writes the units that it finishes itself
   void* out;
   float* lse_out;
   const float* head_sink;
 };
 
-PlanKind plan_kind(const MaskCall* m) { return !m ? kPlanDecode : (m->split ? kPlanMaskedSplit : kPlanMasked); }
+PlanKind masked_kind(bool split, bool tree) {
+  return tree ? (split ? kPlanTreeSplit : kPlanTree) : (split ? kPlanMaskedSplit : kPlanMasked);
+}
+PlanKind plan_kind(const MaskCall* m) { return !m ? kPlanDecode : masked_kind(m->split, m->tree_bits != nullptr); }
 
 // kvq_decode with the block-table row of sequence b at b / bt_div.  With
 // early_reads 1, q, the block table, seq_lens and the static scales are read
@@ -702,6 +731,8 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
     a.slopes = mask->slopes;
     a.key_begin = mask->key_begin;
     a.key_end = mask->key_end;
+    a.tree_bits = mask->tree_bits;
+    a.tree_words = mask->tree_words;
     a.out = static_cast<uint16_t*>(mask->out);
     a.lse_out = mask->lse_out;
     a.head_sink = mask->head_sink;
@@ -710,7 +741,16 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (mask && P.qt) {
+  if (mask && mask->tree_bits && P.qt) {
+    switch (cache->dtype) {
+      case KVQ_INT8: e = launch_qt_tree_int8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_qt_tree_fp8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      default: e = launch_qt_tree_int4(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+    }
+  } else if (mask && mask->tree_bits) {
+    e = tree_kernel(cache, mask->split)(cache->head_dim, kernel_nt(cache, P), &tk, &tv, &a, P.grid, P.threads, P.smem, st,
+                                        nullptr);
+  } else if (mask && P.qt) {
     switch (cache->dtype) {
       case KVQ_INT8: e = launch_qt_mask_int8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
       case KVQ_FP8_E4M3: e = launch_qt_mask_fp8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
@@ -905,17 +945,26 @@ kvq_decode_params masked_params(const kvq_decode_params* p, const MaskShape& s, 
   return v;
 }
 
+int tree_words(const kvq_decode_params* p) { return (p->q_tokens + 31) / 32; }
+// begin, end and bits of every node.
+size_t tree_bytes(const kvq_decode_params* p) {
+  const size_t nodes = (size_t)p->batch * p->q_tokens;
+  return 2 * align256(4 * nodes) + align256(4 * nodes * tree_words(p));
+}
+
 // Launches of at most kMaxBatch groups follow one another on the stream and
 // share the split workspace behind the table of groups.
-kvq_status masked_workspace(const kvq_cache* c, const kvq_decode_params* p, const MaskShape& s, size_t* head,
-                            size_t* total) {
-  *head = align256((size_t)s.groups * sizeof(VSeq));
+// tree: the nodes' intervals and bits stand there too.
+kvq_status masked_workspace(const kvq_cache* c, const kvq_decode_params* p, const MaskShape& s, bool tree,
+                            size_t* head, size_t* total) {
+  *head = align256((size_t)s.groups * sizeof(VSeq)) + (tree ? tree_bytes(p) : 0);
   size_t most = 0;
   const long long last = s.groups % kMaxBatch;
   for (long long count : {s.groups >= kMaxBatch ? (long long)kMaxBatch : last, last}) {
     const kvq_decode_params v = masked_params(p, s, count);
     size_t ws = 0;
-    if (kvq_status st = decode_workspace_size(c, &v, s.qt, &ws, s.split ? kPlanMaskedSplit : kPlanMasked)) return st;
+    if (kvq_status st = decode_workspace_size(c, &v, s.qt, &ws, masked_kind(s.split, tree)))
+      return st;
     most = ws > most ? ws : most;
   }
   *total = *head + most;
@@ -1016,6 +1065,147 @@ bool select_many_ok(const SelectArgs& a, int sms) {
   const double list = rest > 0 ? 10.0 / 64.0 * std::sqrt(need * rest) : 0.0;
   return a.lim >= 32768 && 2 * segs >= sms && segs * a.lim >= sms * 32768LL && select_many_smem(a.lim) <= 110 * 1024 &&
          list <= 0.9 * kManyList && aligned(a.mass, 16);
+}
+
+// Host checks of a prompt's shapes.
+kvq_status check_prompt(const kvq_prompt_params* p) {
+  if (!p || p->batch < 0 || p->total_tokens < 0 || p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->max_seq_len < 0 ||
+      p->window < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (p->num_q_heads % p->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(p->sm_scale) || !std::isfinite(p->softcap) || p->softcap < 0.0f) return KVQ_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return KVQ_ERR_UNSUPPORTED;
+  if (p->num_q_heads / p->num_kv_heads > 8 || p->batch > kMaxBatch || p->num_q_heads > 65536) return KVQ_ERR_UNSUPPORTED;
+  const long long dense[3] = {(long long)p->num_q_heads * p->head_dim, (long long)p->num_kv_heads * p->head_dim,
+                              (long long)p->num_kv_heads * p->head_dim};
+  const int32_t stride[3] = {p->q_stride, p->k_stride, p->v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] != 0 && (stride[i] < dense[i] || stride[i] % 8 != 0)) return KVQ_ERR_INVALID_ARG;
+  // the work units (at least 16 tokens of a sequence and kv head) index with int
+  if (((long long)p->total_tokens / 16 + kMaxBatch) * p->num_kv_heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+// (the table of work units)
+size_t prompt_workspace(const kvq_prompt_params* p) { return align256((size_t)(4 * p->batch + 8) * 4); }
+
+// (a NULL parents array is a host-side mistake whatever the batch)
+kvq_status check_tree(const kvq_decode_params* p, const kvq_tree* t) {
+  if (!t || !t->parents || !aligned(t->parents, 4) || (t->num_nodes && !aligned(t->num_nodes, 4)))
+    return KVQ_ERR_INVALID_ARG;
+  return p->q_tokens > KVQ_MAX_TREE_NODES ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
+}
+
+// kvq_attend_masked and kvq_attend_tree: a call's groups, prepared by a kernel
+// of their own, in launches of the masked kernels.
+kvq_status attend_groups_workspace(const kvq_cache* cache, const kvq_decode_params* params, bool tree,
+                                   size_t* workspace_bytes) {
+  if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  size_t most = 0;  // with and without an lse
+  for (bool lse : {false, true}) {
+    MaskShape shape;
+    if (kvq_status s = masked_shape(&eff_, params, lse, &shape)) return s;
+    size_t head = 0, need = 0;
+    if (kvq_status s = masked_workspace(&eff_, params, shape, tree, &head, &need)) return s;
+    most = need > most ? need : most;
+  }
+  *workspace_bytes = most;
+  return KVQ_OK;
+}
+
+kvq_status attend_groups(const kvq_cache* cache, const kvq_decode_params* params, const kvq_score_mask* mask,
+                         const kvq_tree* tree, const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                         const float* head_sink, void* out, float* lse_out, void* workspace, size_t workspace_bytes,
+                         kvq_stream_t stream) {
+  kvq_cache eff_;
+  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
+  cache = &eff_;
+  MaskShape shape;
+  if (kvq_status s = masked_shape(cache, params, lse_out != nullptr, &shape)) return s;
+  {
+    const kvq_decode_params v = masked_params(params, shape, shape.groups < kMaxBatch ? shape.groups : kMaxBatch);
+    if (kvq_status s = check_params(cache, &v, shape.qt)) return s;
+  }
+  if (params->flags & ~(KVQ_DECODE_EARLY_INPUTS | KVQ_DECODE_NO_TCGEN05 | KVQ_DECODE_EARLY_CACHE))
+    return KVQ_ERR_INVALID_ARG;
+  if (kvq_status s = check_mask(mask)) return s;
+  if (tree) {
+    if (kvq_status s = check_tree(params, tree)) return s;
+  }
+  if (params->batch == 0) return KVQ_OK;
+  if (!q || !block_table || !seq_lens || !workspace || !out) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256) ||
+      !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)) || (head_sink && !aligned(head_sink, 4)))
+    return KVQ_ERR_INVALID_ARG;
+  {
+    // some rows are finished while others' queries are still to be read
+    const uint64_t rows = (uint64_t)params->batch * params->q_tokens * params->num_q_heads;
+    const uint64_t q0 = reinterpret_cast<uint64_t>(q), o0 = reinterpret_cast<uint64_t>(out);
+    if (q0 < o0 + rows * cache->v_head_size * 2 && o0 < q0 + rows * cache->head_dim * 2) return KVQ_ERR_INVALID_ARG;
+  }
+  size_t head = 0, need = 0;
+  if (kvq_status s = masked_workspace(cache, params, shape, tree != nullptr, &head, &need)) return s;
+  if (workspace_bytes < need) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  VSeq* table = static_cast<VSeq*>(workspace);
+  MaskCall mc{};
+  mc.split = shape.split;
+  mc.out = out;
+  mc.lse_out = lse_out;
+  mc.head_sink = head_sink;
+  kvq_decode_params tree_params;  // (the window is in the nodes' intervals and bits)
+  if (tree) {
+    const size_t nodes = align256(4 * (size_t)params->batch * params->q_tokens);
+    char* rows = static_cast<char*>(workspace) + align256((size_t)shape.groups * sizeof(VSeq));
+    TreeArgs t{};
+    t.parents = tree->parents;
+    t.num_nodes = tree->num_nodes;
+    t.seq_lens = seq_lens;
+    t.out = table;
+    t.begin = reinterpret_cast<int32_t*>(rows);
+    t.end = reinterpret_cast<int32_t*>(rows + nodes);
+    t.bits = reinterpret_cast<uint32_t*>(rows + 2 * nodes);
+    t.batch = params->batch;
+    t.C = params->q_tokens;
+    t.T = shape.T;
+    t.n = shape.n;
+    t.words = tree_words(params);
+    t.window = params->window;
+    t.cap = params->max_blocks_per_seq * cache->block_size;
+    t.max_seq_len = params->max_seq_len;
+    t.err = dev->err;
+    if (cudaError_t e = launch_tree_rows(t, reinterpret_cast<cudaStream_t>(stream))) return from_cuda(e);
+    mc.key_begin = t.begin;
+    mc.key_end = t.end;
+    mc.tree_bits = t.bits;
+    mc.tree_words = t.words;
+    tree_params = *params;
+    tree_params.window = 0;
+    params = &tree_params;
+  } else {
+    if (kvq_status s = prepare_groups(cache, params, mask, seq_lens, shape.T, shape.n, table, dev->err,
+                                      reinterpret_cast<cudaStream_t>(stream)))
+      return s;
+    mc.slopes = mask ? mask->slopes : nullptr;
+    mc.key_begin = mask ? mask->key_begin : nullptr;
+    mc.key_end = mask ? mask->key_end : nullptr;
+  }
+  char* ws = static_cast<char*>(workspace) + head;
+  for (long long v0 = 0; v0 < shape.groups; v0 += kMaxBatch) {
+    const long long left = shape.groups - v0;
+    const kvq_decode_params v = masked_params(params, shape, left < kMaxBatch ? left : kMaxBatch);
+    mc.vseq = table + v0;
+    if (kvq_status s = decode_impl(cache, &v, q, block_table, seq_lens, 1, 0, shape.qt, ws, workspace_bytes - head,
+                                   stream, &mc))
+      return s;
+    if (kvq_status s = combine_impl(cache, &v, shape.qt, ws, workspace_bytes - head, head_sink, out, lse_out, stream,
+                                    shape.n > 1, &mc))
+      return s;
+  }
+  return KVQ_OK;
 }
 
 // Launch shape of kvq_evict_compact: units of up to 128 rows and kUnitBytes,
@@ -1193,72 +1383,221 @@ KVQ_API kvq_status kvq_prefill(const kvq_cache* cache, const kvq_decode_params* 
 
 KVQ_API kvq_status kvq_attend_masked_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
                                                     size_t* workspace_bytes) {
-  if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
-  kvq_cache eff_;
-  if (kvq_status s = resolve_cache(cache, &eff_)) return s;
-  size_t most = 0;  // with and without an lse
-  for (bool lse : {false, true}) {
-    MaskShape shape;
-    if (kvq_status s = masked_shape(&eff_, params, lse, &shape)) return s;
-    size_t head = 0, need = 0;
-    if (kvq_status s = masked_workspace(&eff_, params, shape, &head, &need)) return s;
-    most = need > most ? need : most;
-  }
-  *workspace_bytes = most;
-  return KVQ_OK;
+  return attend_groups_workspace(cache, params, false, workspace_bytes);
 }
 
 KVQ_API kvq_status kvq_attend_masked(const kvq_cache* cache, const kvq_decode_params* params,
                                      const kvq_score_mask* mask, const void* q, const int32_t* block_table,
                                      const int32_t* seq_lens, const float* head_sink, void* out, float* lse_out,
                                      void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  return attend_groups(cache, params, mask, nullptr, q, block_table, seq_lens, head_sink, out, lse_out, workspace,
+                       workspace_bytes, stream);
+}
+
+KVQ_API kvq_status kvq_attend_tree_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
+                                                  size_t* workspace_bytes) {
+  if (!params || params->q_tokens < 1) return KVQ_ERR_INVALID_ARG;
+  if (params->q_tokens > KVQ_MAX_TREE_NODES) return KVQ_ERR_UNSUPPORTED;
+  return attend_groups_workspace(cache, params, true, workspace_bytes);
+}
+
+KVQ_API kvq_status kvq_attend_tree(const kvq_cache* cache, const kvq_decode_params* params, const kvq_tree* tree,
+                                   const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                                   const float* head_sink, void* out, float* lse_out, void* workspace,
+                                   size_t workspace_bytes, kvq_stream_t stream) {
+  if (!tree) return KVQ_ERR_INVALID_ARG;
+  return attend_groups(cache, params, nullptr, tree, q, block_table, seq_lens, head_sink, out, lse_out, workspace,
+                       workspace_bytes, stream);
+}
+
+KVQ_API kvq_status kvq_tree_accept(const kvq_cache* cache, const kvq_decode_params* params, const kvq_tree* tree,
+                                   const int64_t* drafts, const int64_t* chosen, const int32_t* block_table,
+                                   const int32_t* seq_lens, int32_t* path, int32_t* accepted, int32_t* new_lens,
+                                   int64_t* next_tokens, float* mass, kvq_stream_t stream) {
   kvq_cache eff_;
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
-  MaskShape shape;
-  if (kvq_status s = masked_shape(cache, params, lse_out != nullptr, &shape)) return s;
-  {
-    const kvq_decode_params v = masked_params(params, shape, shape.groups < kMaxBatch ? shape.groups : kMaxBatch);
-    if (kvq_status s = check_params(cache, &v, shape.qt)) return s;
-  }
-  if (params->flags & ~(KVQ_DECODE_EARLY_INPUTS | KVQ_DECODE_NO_TCGEN05 | KVQ_DECODE_EARLY_CACHE))
+  if (!params || params->batch < 0 || params->q_tokens < 1 || params->max_blocks_per_seq <= 0 || params->max_seq_len < 0)
     return KVQ_ERR_INVALID_ARG;
-  if (kvq_status s = check_mask(mask)) return s;
+  const long long cap = (long long)params->max_blocks_per_seq * cache->block_size;
+  if (cap > (1LL << 30)) return KVQ_ERR_INVALID_ARG;
+  if (params->batch > kMaxBatch || cache->num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (kvq_status s = check_tree(params, tree)) return s;
   if (params->batch == 0) return KVQ_OK;
-  if (!q || !block_table || !seq_lens || !workspace || !out) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256) ||
-      !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)) || (head_sink && !aligned(head_sink, 4)))
+  if (!drafts || !chosen || !block_table || !seq_lens || !path || !accepted || !new_lens || !next_tokens)
     return KVQ_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)drafts, (const void*)chosen, (const void*)next_tokens})
+    if (!aligned(p, 8)) return KVQ_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)block_table, (const void*)seq_lens, (const void*)path, (const void*)accepted,
+                        (const void*)new_lens, (const void*)mass})
+    if (!aligned(p, 4)) return KVQ_ERR_INVALID_ARG;
   {
-    // some rows are finished while others' queries are still to be read
-    const uint64_t rows = (uint64_t)params->batch * params->q_tokens * params->num_q_heads;
-    const uint64_t q0 = reinterpret_cast<uint64_t>(q), o0 = reinterpret_cast<uint64_t>(out);
-    if (q0 < o0 + rows * cache->v_head_size * 2 && o0 < q0 + rows * cache->head_dim * 2) return KVQ_ERR_INVALID_ARG;
+    // the CTAs of a sequence's heads each read its tree, length and pages
+    const uint64_t lens = 4ull * params->batch, nodes = lens * params->q_tokens;
+    const uint64_t cells = (uint64_t)cache->num_blocks * cache->num_kv_heads * cache->block_size;
+    const bool two = cache->layout != KVQ_LAYOUT_LATENT;
+    const std::pair<const void*, uint64_t> in[] = {
+        {tree->parents, nodes}, {tree->num_nodes, tree->num_nodes ? lens : 0}, {drafts, 2 * nodes}, {chosen, 2 * nodes},
+        {block_table, lens * params->max_blocks_per_seq}, {seq_lens, lens}};
+    const std::pair<const void*, uint64_t> out[] = {
+        {path, nodes}, {accepted, lens}, {new_lens, lens}, {next_tokens, 2 * lens},
+        {cache->k_codes, cells * row_bytes(cache)}, {cache->v_codes, two ? cells * row_bytes(cache) : 0},
+        {cache->k_scale, 4 * cells * scales_per_row(cache, cache->k_mode)},
+        {cache->v_scale, two ? 4 * cells * scales_per_row(cache, cache->v_mode) : 0}, {mass, mass ? 4 * cells : 0}};
+    if (!disjoint(in, out)) return KVQ_ERR_INVALID_ARG;
   }
-  size_t head = 0, need = 0;
-  if (kvq_status s = masked_workspace(cache, params, shape, &head, &need)) return s;
-  if (workspace_bytes < need) return KVQ_ERR_WORKSPACE_TOO_SMALL;
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
-  VSeq* table = static_cast<VSeq*>(workspace);
-  if (kvq_status s = prepare_groups(cache, params, mask, seq_lens, shape.T, shape.n, table, dev->err,
-                                    reinterpret_cast<cudaStream_t>(stream)))
-    return s;
-  char* ws = static_cast<char*>(workspace) + head;
-  MaskCall mc{table, mask ? mask->slopes : nullptr, mask ? mask->key_begin : nullptr, mask ? mask->key_end : nullptr,
-              shape.split, out, lse_out, head_sink};
-  for (long long v0 = 0; v0 < shape.groups; v0 += kMaxBatch) {
-    const long long left = shape.groups - v0;
-    const kvq_decode_params v = masked_params(params, shape, left < kMaxBatch ? left : kMaxBatch);
-    mc.vseq = table + v0;
-    if (kvq_status s = decode_impl(cache, &v, q, block_table, seq_lens, 1, 0, shape.qt, ws, workspace_bytes - head,
-                                   stream, &mc))
-      return s;
-    if (kvq_status s = combine_impl(cache, &v, shape.qt, ws, workspace_bytes - head, head_sink, out, lse_out, stream,
-                                    shape.n > 1, &mc))
-      return s;
+  AcceptArgs a{};
+  a.parents = tree->parents;
+  a.num_nodes = tree->num_nodes;
+  a.drafts = drafts;
+  a.chosen = chosen;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.path = path;
+  a.accepted = accepted;
+  a.new_lens = new_lens;
+  a.next_tokens = next_tokens;
+  a.sides = cache->layout == KVQ_LAYOUT_LATENT ? 1 : 2;
+  a.codes[0] = static_cast<uint8_t*>(cache->k_codes);
+  a.codes[1] = static_cast<uint8_t*>(cache->v_codes);
+  a.scale[0] = cache->k_scale;
+  a.scale[1] = cache->v_scale;
+  a.n_scale[0] = scales_per_row(cache, cache->k_mode);
+  a.n_scale[1] = a.sides == 2 ? scales_per_row(cache, cache->v_mode) : 0;
+  a.mass = mass;
+  a.row_bytes = row_bytes(cache);
+  a.batch = params->batch;
+  a.T = params->q_tokens;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.max_blocks_per_seq = params->max_blocks_per_seq;
+  a.num_blocks = cache->num_blocks;
+  a.block_size = cache->block_size;
+  a.log2_bs = ilog2(cache->block_size);
+  a.lim = (int)((params->max_seq_len > 0 && params->max_seq_len < cap) ? params->max_seq_len : cap);
+  a.err = dev->err;
+  return from_cuda(launch_tree_accept(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+KVQ_API kvq_status kvq_pages_step(const kvq_pages_params* params, const int32_t* held_lens,
+                                  const int32_t* start_lens, const int32_t* new_tokens, const int32_t* parents,
+                                  int32_t* block_table, int32_t* free_blocks, const int32_t* free_count,
+                                  int32_t* seq_lens, int32_t* free_left, int32_t* cu_seqlens,
+                                  int64_t* slot_mapping, int64_t* positions, kvq_stream_t stream) {
+  const kvq_pages_params* p = params;
+  if (!p || p->batch < 0 || p->max_blocks_per_seq <= 0 || p->num_blocks <= 0 || p->max_tokens < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (!pow2(p->block_size) || p->block_size < 16 || p->block_size > (1 << 20)) return KVQ_ERR_INVALID_ARG;
+  if ((long long)p->num_blocks * p->block_size > (1LL << 31) - 1) return KVQ_ERR_INVALID_ARG;
+  if ((long long)p->max_blocks_per_seq * p->block_size > (1LL << 30)) return KVQ_ERR_INVALID_ARG;
+  if (parents && p->tree_nodes < 1) return KVQ_ERR_INVALID_ARG;
+  if (p->batch > kMaxBatch || p->max_tokens > (1 << 30) || (parents && p->tree_nodes > KVQ_MAX_TREE_NODES))
+    return KVQ_ERR_UNSUPPORTED;
+  if (p->batch == 0 && p->max_tokens == 0) return KVQ_OK;
+  if (!held_lens || !new_tokens || !block_table || !free_blocks || !free_count || !seq_lens || !free_left ||
+      !cu_seqlens || (p->max_tokens > 0 && (!slot_mapping || !positions)))
+    return KVQ_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)held_lens, (const void*)start_lens, (const void*)new_tokens, (const void*)parents,
+                        (const void*)block_table, (const void*)free_blocks, (const void*)free_count,
+                        (const void*)seq_lens, (const void*)free_left, (const void*)cu_seqlens})
+    if (!aligned(x, 4)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(slot_mapping, 8) || !aligned(positions, 8)) return KVQ_ERR_INVALID_ARG;
+  {
+    // lengths and count may be written in place (after every CTA has read them)
+    const uint64_t lens = 4ull * p->batch, tokens = 8ull * p->max_tokens;
+    const std::pair<const void*, uint64_t> in[] = {
+        {held_lens, held_lens == seq_lens ? 0 : lens},
+        {start_lens, start_lens && start_lens != seq_lens ? lens : 0},
+        {new_tokens, lens},
+        {parents, parents ? lens * p->tree_nodes : 0},
+        {free_count, free_count == free_left ? 0 : 4}};
+    const std::pair<const void*, uint64_t> out[] = {
+        {block_table, lens * p->max_blocks_per_seq}, {free_blocks, 4ull * p->num_blocks}, {seq_lens, lens},
+        {free_left, 4}, {cu_seqlens, lens + 4}, {slot_mapping, tokens}, {positions, tokens}};
+    if (!disjoint(in, out)) return KVQ_ERR_INVALID_ARG;
   }
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  PagesArgs a{};
+  a.held_lens = held_lens;
+  a.start_lens = start_lens;
+  a.new_tokens = new_tokens;
+  a.parents = parents;
+  a.block_table = block_table;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.seq_lens = seq_lens;
+  a.free_left = free_left;
+  a.cu_seqlens = cu_seqlens;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.batch = p->batch;
+  a.max_blocks_per_seq = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  a.block_size = p->block_size;
+  a.log2_bs = ilog2(p->block_size);
+  a.max_tokens = p->max_tokens;
+  a.tree_nodes = p->tree_nodes;
+  a.err = dev->err;
+  return from_cuda(launch_pages_step(a, dev->sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+KVQ_API kvq_status kvq_attend_prompt_workspace_size(const kvq_prompt_params* params, size_t* workspace_bytes) {
+  if (!workspace_bytes) return KVQ_ERR_INVALID_ARG;
+  if (kvq_status s = check_prompt(params)) return s;
+  *workspace_bytes = prompt_workspace(params);
   return KVQ_OK;
+}
+
+KVQ_API kvq_status kvq_attend_prompt(const kvq_prompt_params* params, const void* q, const void* k, const void* v,
+                                     const int32_t* cu_seqlens, const float* head_sink, void* out, float* lse_out,
+                                     void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  const kvq_prompt_params* p = params;
+  if (kvq_status s = check_prompt(p)) return s;
+  if (p->batch == 0 || p->total_tokens == 0) return KVQ_OK;
+  if (!q || !k || !v || !cu_seqlens || !out || !workspace) return KVQ_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, (const void*)out})
+    if (!aligned(x, 16)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(cu_seqlens, 4) || !aligned(head_sink, 4) || !aligned(lse_out, 4) || !aligned(workspace, 256))
+    return KVQ_ERR_INVALID_ARG;
+  if (workspace_bytes < prompt_workspace(p)) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  PromptArgs a{};
+  const int D = p->head_dim;
+  a.q_stride = p->q_stride ? p->q_stride : (long long)p->num_q_heads * D;
+  a.k_stride = p->k_stride ? p->k_stride : (long long)p->num_kv_heads * D;
+  a.v_stride = p->v_stride ? p->v_stride : (long long)p->num_kv_heads * D;
+  {
+    const uint64_t n = p->total_tokens, last = n - 1, qw = (uint64_t)p->num_q_heads * D, kw = (uint64_t)p->num_kv_heads * D;
+    const std::pair<const void*, uint64_t> in[] = {{q, 2 * (last * a.q_stride + qw)}, {k, 2 * (last * a.k_stride + kw)},
+                                                   {v, 2 * (last * a.v_stride + kw)}, {cu_seqlens, 4ull * p->batch + 4},
+                                                   {head_sink, head_sink ? 4ull * p->num_q_heads : 0}};
+    const std::pair<const void*, uint64_t> outs[] = {{out, 2 * n * qw}, {lse_out, lse_out ? 4 * n * p->num_q_heads : 0},
+                                                     {workspace, prompt_workspace(p)}};
+    if (!disjoint(in, outs)) return KVQ_ERR_INVALID_ARG;
+  }
+  DeviceInfo* dev;
+  if (kvq_status s = current_device(&dev)) return s;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.cu_seqlens = cu_seqlens;
+  a.head_sink = head_sink;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse_out = lse_out;
+  a.plan = static_cast<int*>(workspace);
+  a.batch = p->batch;
+  a.total_tokens = p->total_tokens;
+  a.num_q_heads = p->num_q_heads;
+  a.num_kv_heads = p->num_kv_heads;
+  a.head_dim = D;
+  a.group = p->num_q_heads / p->num_kv_heads;
+  a.max_seq_len = p->max_seq_len > 0 && p->max_seq_len < p->total_tokens ? p->max_seq_len : p->total_tokens;
+  a.sm_scale = p->sm_scale > 0.0f ? p->sm_scale : 1.0f / std::sqrt((float)D);
+  a.softcap = p->softcap;
+  a.window = p->window;
+  a.err = dev->err;
+  return from_cuda(launch_attend_prompt(a, dev->sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 KVQ_API kvq_status kvq_key_mass_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,

@@ -331,13 +331,14 @@ __host__ __device__ constexpr int wide_scratch_floats() {
 // and an lse that is asked for): the Q operand in two f16 parts, the second
 // one in shared memory.  An f16 query with the scale folded in is 2^-12 off,
 // which the bf16 output hides but the fp32 lse shows (3e-5 of it under a
-// steep bias; 1e-7 with the second part).
+// steep bias; 1e-7 with the second part).  RULE 3 and 4: the same two with the bits of
+// draft trees in place of the distance bias.
 template <int DT, int D, int MINB, int NT, int GS, int RULE>
 __global__ void __launch_bounds__(288, MINB)
     decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const DecodeArgs a) {
   using Gm = Geo<DT, D>;
-  constexpr bool MASK = RULE > 0, SPLIT = RULE == 2;
+  constexpr bool MASK = RULE > 0, SPLIT = RULE == 2 || RULE == 4, TREE = RULE > 2;
   constexpr float kLog2e = 1.4426950408889634f;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(288, MINB)
             // (the four key quarters write the same; lane group 0 of each does,
             // behind the barriers that ended the previous piece)
             const int rr = r < rows ? r : 0, t = dev::div_small(rr, inv_g);
-            if (g == 0) s_rule[r] = dev::row_rule(a, tok0 + t, a.vseq[b].pos0 + t, h * G + rr - t * G, L);
+            if (g == 0) s_rule[r] = dev::row_rule<TREE>(a, tok0 + t, a.vseq[b].pos0 + t, h * G + rr - t * G, L);
             pos[nt][i] = 0;
           } else {
             pos[nt][i] = r < rows ? L - T + dev::div_small(r, inv_g) : -1;
@@ -710,8 +711,8 @@ __global__ void __launch_bounds__(288, MINB)
               const int key = e < 2 ? key_a : key_b, p = pos[nt][e & 1];
               if constexpr (MASK) {
                 bool seen;
-                x[nt][e] = dev::rule_score(s_rule[rh * RW + nt * 8 + 2 * c + (e & 1)], x[nt][e], key,
-                                           a.slopes != nullptr, seen);
+                  x[nt][e] = dev::row_score<TREE>(a, s_rule[rh * RW + nt * 8 + 2 * c + (e & 1)], x[nt][e], key,
+                                                a.slopes != nullptr, seen);
                 if (e < 2) see_a = see_a || seen;
                 else see_b = see_b || seen;
               } else {
@@ -1028,8 +1029,8 @@ __global__ void __launch_bounds__(288, MINB)
     if constexpr (MASK) {
       const int q0 = r0 < rows ? r0 : 0, q1 = r1 < rows ? r1 : 0;
       const int t0 = dev::div_small(q0, inv_g), t1 = dev::div_small(q1, inv_g);
-      const dev::RowRule ru0 = dev::row_rule(a, tok0 + t0, a.vseq[b].pos0 + t0, h * G + q0 - t0 * G, L);
-      const dev::RowRule ru1 = dev::row_rule(a, tok0 + t1, a.vseq[b].pos0 + t1, h * G + q1 - t1 * G, L);
+      const dev::RowRule ru0 = dev::row_rule<TREE>(a, tok0 + t0, a.vseq[b].pos0 + t0, h * G + q0 - t0 * G, L);
+      const dev::RowRule ru1 = dev::row_rule<TREE>(a, tok0 + t1, a.vseq[b].pos0 + t1, h * G + q1 - t1 * G, L);
       if (g == 0) {
         rules[2 * c] = ru0;
         rules[2 * c + 1] = ru1;
@@ -1037,7 +1038,7 @@ __global__ void __launch_bounds__(288, MINB)
       }
       f_lo = max(ru0.begin, ru1.begin);
       f_hi = min(ru0.end, ru1.end);
-      if (a.slopes) f_hi = min(f_hi, min(ru0.pos, ru1.pos) + 1);
+      if (!TREE && a.slopes) f_hi = min(f_hi, min(ru0.pos, ru1.pos) + 1);
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         f_lo = max(f_lo, __shfl_xor_sync(0xffffffffu, f_lo, o));
@@ -1157,7 +1158,7 @@ __global__ void __launch_bounds__(288, MINB)
         if constexpr (MASK) {
           full = kb >= f_lo && kb + kSub <= f_hi;  // the same in every lane
           if (full) {
-            if (a.slopes) {
+            if (!TREE && a.slopes) {
               const float4 ln = lines[c];
               const float ka = (float)(key_a - k0), kb8 = ka + 8.0f;
               x[0] = fmaf(ln.y, ln.x - ka, x[0]);
@@ -1169,10 +1170,10 @@ __global__ void __launch_bounds__(288, MINB)
             const dev::RowRule ru0 = rules[2 * c], ru1 = rules[2 * c + 1];
             const bool bias = a.slopes != nullptr;
             bool va0, va1, vb0, vb1;
-            x[0] = dev::rule_score(ru0, x[0], key_a, bias, va0);
-            x[1] = dev::rule_score(ru1, x[1], key_a, bias, va1);
-            x[2] = dev::rule_score(ru0, x[2], key_b, bias, vb0);
-            x[3] = dev::rule_score(ru1, x[3], key_b, bias, vb1);
+            x[0] = dev::row_score<TREE>(a, ru0, x[0], key_a, bias, va0);
+            x[1] = dev::row_score<TREE>(a, ru1, x[1], key_a, bias, va1);
+            x[2] = dev::row_score<TREE>(a, ru0, x[2], key_b, bias, vb0);
+            x[3] = dev::row_score<TREE>(a, ru1, x[3], key_b, bias, vb1);
             // the V row of a key that neither of this lane's query rows sees
             // may hold anything: its scales are not used
             use_a = va0 || va1;

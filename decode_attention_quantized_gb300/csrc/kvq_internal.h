@@ -104,6 +104,9 @@ struct DecodeArgs {
   const float* slopes;        // [Hq] or null
   const int32_t* key_begin;   // [tokens] or null
   const int32_t* key_end;     // [tokens] or null
+  // draft trees: which of the `q_nodes` rows from a token's key_end on it sees
+  const uint32_t* tree_bits;  // [tokens, tree_words]
+  int tree_words;
   // masked query-tile kernel: a unit that one CTA attends whole is finished
   // there, and the combine leaves its rows alone
   uint16_t* out;              // bf16 bits [tokens, Hq, out_dim]
@@ -111,6 +114,81 @@ struct DecodeArgs {
   const float* head_sink;     // [Hq] or null
   int out_dim;
 };
+
+// kvq_pages_step.
+struct PagesArgs {
+  const int32_t* held_lens;   // [B]
+  const int32_t* start_lens;  // [B] or null: held_lens
+  const int32_t* new_tokens;  // [B]
+  const int32_t* parents;     // [B, tree_nodes] or null
+  int32_t* block_table;       // [B, max_blocks_per_seq]
+  int32_t* free_blocks;       // [num_blocks]
+  const int32_t* free_count;
+  int32_t* seq_lens;          // [B]
+  int32_t* free_left;
+  int32_t* cu_seqlens;        // [B + 1]
+  int64_t* slot_mapping;      // [max_tokens]
+  int64_t* positions;         // [max_tokens]
+  int batch, max_blocks_per_seq, num_blocks, block_size, log2_bs, max_tokens, tree_nodes;
+  unsigned int* err;
+};
+constexpr int kPagesThreads = 256;
+cudaError_t launch_pages_step(const PagesArgs& a, int sms, cudaStream_t stream);
+
+// The rows of a call's trees (kvq_attend_tree): the groups of T nodes, as
+// VSeqArgs's, and per node the prefix interval and the bits of the nodes it sees.
+struct TreeArgs {
+  const int32_t* parents;    // [B, C]
+  const int32_t* num_nodes;  // [B] or null
+  const int32_t* seq_lens;   // [B]
+  VSeq* out;                 // [B * n]
+  int32_t* begin;            // [B, C]
+  int32_t* end;              // [B, C]
+  uint32_t* bits;            // [B, C, words]
+  int batch, C, T, n, words, window, cap, max_seq_len;
+  unsigned int* err;
+};
+cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t stream);
+
+// kvq_tree_accept.
+struct AcceptArgs {
+  const int32_t* parents;     // [B, T]
+  const int32_t* num_nodes;   // [B] or null
+  const int64_t* drafts;      // [B, T]
+  const int64_t* chosen;      // [B, T]
+  const int32_t* block_table; // [B, max_blocks_per_seq]
+  const int32_t* seq_lens;    // [B]
+  int32_t* path;              // [B, T]
+  int32_t* accepted;          // [B]
+  int32_t* new_lens;          // [B]
+  int64_t* next_tokens;       // [B]
+  uint8_t* codes[2];          // K, V
+  float* scale[2];
+  float* mass;                // or null
+  int n_scale[2];             // fp32 scales per row of a side
+  int sides, row_bytes;
+  int batch, T, num_kv_heads, max_blocks_per_seq, num_blocks, block_size, log2_bs, lim;
+  unsigned int* err;
+};
+cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
+
+// kvq_attend_prompt.
+struct PromptArgs {
+  const uint16_t* q;          // bf16 bits [N, Hq, D], tokens q_stride elements apart
+  const uint16_t* k;          // [N, Hkv, D]
+  const uint16_t* v;
+  const int32_t* cu_seqlens;  // [B + 1]
+  const float* head_sink;     // [Hq] or null
+  uint16_t* out;              // bf16 bits [N, Hq, D]
+  float* lse_out;             // [N, Hq] or null
+  int* plan;                  // workspace
+  long long q_stride, k_stride, v_stride;
+  int batch, total_tokens, num_q_heads, num_kv_heads, head_dim, group, max_seq_len;
+  float sm_scale, softcap;
+  int window;
+  unsigned int* err;
+};
+cudaError_t launch_attend_prompt(const PromptArgs& a, int sms, cudaStream_t stream);
 
 struct CombineArgs {
   const int* plan;
@@ -407,6 +485,32 @@ cudaError_t launch_qt_mask_fp8(int head_dim, bool split, const CUtensorMap& tk, 
                                int grid, size_t smem, cudaStream_t stream);
 cudaError_t launch_qt_mask_int4(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                                 int grid, size_t smem, cudaStream_t stream);
+
+// The same with the bits of draft trees (kvq_attend_tree).
+cudaError_t dispatch_decode_tree_int8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                     int* blocks_per_sm);
+cudaError_t dispatch_decode_tree_split_int8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                     int* blocks_per_sm);
+cudaError_t launch_qt_tree_int8(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t dispatch_decode_tree_fp8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                     int* blocks_per_sm);
+cudaError_t dispatch_decode_tree_split_fp8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                     int* blocks_per_sm);
+cudaError_t launch_qt_tree_fp8(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t dispatch_decode_tree_int4(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                     int* blocks_per_sm);
+cudaError_t dispatch_decode_tree_split_int4(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
+                                     int* blocks_per_sm);
+cudaError_t launch_qt_tree_int4(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
 
 cudaError_t occupancy_decode_int8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
 cudaError_t occupancy_decode_fp8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);

@@ -20,7 +20,8 @@ namespace dev {
 struct __align__(16) RowRule {
   int begin, end, pos, d0;
   float ns;
-  int pad[3];
+  int bits;  // draft trees: where the row's bits begin in DecodeArgs::tree_bits (-1: none)
+  int pad[2];
 };
 
 // The score x of `key` under a row's rule, key by key: the slow form, for
@@ -28,6 +29,34 @@ struct __align__(16) RowRule {
 __device__ __forceinline__ float rule_score(const RowRule& r, float x, int key, bool bias, bool& seen) {
   if (bias) x = fmaf(r.ns, (float)(abs(r.pos - key) - r.d0), x);
   seen = key >= r.begin && key < r.end;
+  return seen ? x : -INFINITY;
+}
+
+// Draft trees: the row of a node sees the prefix keys [begin, end) and, of the
+// nodes' keys from `end` on, those whose bit is set.
+__device__ __forceinline__ bool tree_sees(const DecodeArgs& a, const RowRule& r, int key) {
+  const int d = key - r.end;
+  if (r.bits < 0 || (unsigned)d >= 32u * (unsigned)a.tree_words) return false;
+  return (a.tree_bits[r.bits + (d >> 5)] >> (d & 31)) & 1u;
+}
+
+// The same for the 64 keys from key0 on, as bits.
+__device__ __forceinline__ void tree_sees_64(const DecodeArgs& a, const RowRule& r, int key0, uint32_t (&m)[2]) {
+  const int d = key0 - r.end, w0 = d >> 5;
+  uint32_t w[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    w[j] = r.bits >= 0 && (unsigned)(w0 + j) < (unsigned)a.tree_words ? a.tree_bits[r.bits + w0 + j] : 0u;
+  m[0] = __funnelshift_r(w[0], w[1], (unsigned)d & 31u);
+  m[1] = __funnelshift_r(w[1], w[2], (unsigned)d & 31u);
+}
+
+// rule_score for the instances of draft trees.
+template <bool TREE>
+__device__ __forceinline__ float row_score(const DecodeArgs& a, const RowRule& r, float x, int key, bool bias,
+                                           bool& seen) {
+  if constexpr (!TREE) return rule_score(r, x, key, bias, seen);
+  seen = (key >= r.begin && key < r.end) || tree_sees(a, r, key);
   return seen ? x : -INFINITY;
 }
 
@@ -48,6 +77,7 @@ __device__ __forceinline__ int row_anchor(float slope, int pos, int begin, int e
   return pos < begin ? begin - pos : (pos >= end ? pos - (end - 1) : 0);
 }
 
+template <bool TREE = false>
 __device__ __forceinline__ RowRule row_rule(const DecodeArgs& a, size_t tok, int pos, int hq, int hi) {
   RowRule r{};
   r.pos = pos;
@@ -57,6 +87,10 @@ __device__ __forceinline__ RowRule row_rule(const DecodeArgs& a, size_t tok, int
   r.end = max(0, r.end);
   r.ns = 0.0f;
   r.d0 = 0;
+  if constexpr (TREE) {
+    r.bits = (int)tok * a.tree_words;  // (at most 2^18 tokens of 8 words)
+    return r;
+  }
   if (a.slopes) {
     const float s = a.slopes[hq];
     r.ns = -s * 1.4426950408889634f;

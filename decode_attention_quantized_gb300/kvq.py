@@ -22,7 +22,8 @@ LAYOUT_SEPARATE, LAYOUT_LATENT = 0, 1
 PER_ROW, PER_TENSOR, PER_CHANNEL, PER_GROUP = 1, 2, 3, 4
 DECODE_EARLY_INPUTS, DECODE_NO_TCGEN05, DECODE_EARLY_CACHE = 0x1, 0x2, 0x4  # kvq_decode_params.flags
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_POSITION = 0x1, 0x2, 0x4, 0x8, 0x10
-DEVERR_KEEP_INDEX = 0x20
+DEVERR_KEEP_INDEX, DEVERR_NO_BLOCKS = 0x20, 0x40
+MAX_TREE_NODES = 256
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
           5: "device timeout"}
 
@@ -66,6 +67,22 @@ class EvictParams(ctypes.Structure):
                 ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32)]
 
 
+class PromptParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
+                ("q_stride", ctypes.c_int32), ("k_stride", ctypes.c_int32), ("v_stride", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32)]
+
+
+class TreeDesc(ctypes.Structure):
+    _fields_ = [("parents", ctypes.c_void_p), ("num_nodes", ctypes.c_void_p)]
+
+
+class PagesParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("tree_nodes", ctypes.c_int32)]
+
+
 # every exported entry point of include/kvq.h with its ctypes signature
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 SIGNATURES = {
@@ -98,6 +115,16 @@ SIGNATURES = {
                                                 ctypes.POINTER(_SZ)]),
     "kvq_evict_compact": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(EvictParams), _VP, _VP, _VP, _VP, _VP,
                                  _VP, _SZ, _VP]),
+    "kvq_attend_prompt_workspace_size": (_I32, [ctypes.POINTER(PromptParams), ctypes.POINTER(_SZ)]),
+    "kvq_attend_prompt": (_I32, [ctypes.POINTER(PromptParams), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "kvq_attend_tree_workspace_size": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams),
+                                              ctypes.POINTER(_SZ)]),
+    "kvq_attend_tree": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams), ctypes.POINTER(TreeDesc),
+                               _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "kvq_tree_accept": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams), ctypes.POINTER(TreeDesc),
+                               _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "kvq_pages_step": (_I32, [ctypes.POINTER(PagesParams), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                              _VP]),
     "kvq_attend_noalloc": (_I32, [ctypes.POINTER(CacheDesc), ctypes.POINTER(DecodeParams), _VP, _VP, _VP, _VP, _VP,
                                   _VP, _VP]),
 }
@@ -535,3 +562,141 @@ def evict_step(cache: QuantizedPagedCache, params: EvictParams, block_table: tor
     kvq_evict_select(params, mass, block_table, seq_lens, bufs.keep, kept, stream)
     kvq_evict_compact(cache, params, block_table, dst_table, bufs.keep, kept, mass, bufs.workspace, stream)
     return kept
+
+
+# ---------------------------------------------------------------------------
+# whole prompts, draft trees and the bookkeeping of pages
+# ---------------------------------------------------------------------------
+
+def make_prompt_params(batch, total_tokens, num_q_heads, num_kv_heads, head_dim, *, max_seq_len=0, sm_scale=0.0,
+                       softcap=0.0, window=0) -> PromptParams:
+    """`batch` prompts of `total_tokens` tokens in all, one after another."""
+    return PromptParams(int(batch), int(total_tokens), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                        int(max_seq_len), 0, 0, 0, float(sm_scale), float(softcap), int(window))
+
+
+def _rows(name: str, t: torch.Tensor, shape: tuple, dev: int):
+    """Device pointer and token stride of bf16 rows [N, H, D] whose heads are
+    dense (a slice of a wider projection)."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    N, H, D = shape
+    st = t.stride()
+    if (t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or st[2] != 1 or
+            (H > 1 and st[1] != D) or (N > 1 and st[0] < H * D)):
+        raise ValueError(f"{name}: needs torch.bfloat16 rows of shape {shape} on cuda:{dev}, each token's heads "
+                         f"contiguous, got {t.dtype} {tuple(t.shape)} of strides {st} on {t.device}")
+    return t.data_ptr(), st[0] if N > 1 else 0
+
+
+def kvq_attend_prompt_workspace_size(params: PromptParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check("kvq_attend_prompt_workspace_size",
+           load().kvq_attend_prompt_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def kvq_attend_prompt(params: PromptParams, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      cu_seqlens: torch.Tensor, head_sink: Optional[torch.Tensor], out: torch.Tensor,
+                      lse_out: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
+    """q bf16 [N, Hq, D], k, v bf16 [N, Hkv, D] (strided tokens are fine), out
+    bf16 [N, Hq, D]; cu_seqlens int32 [B + 1]; lse_out fp32 [N, Hq] or None."""
+    dev = _current(q)
+    N, Hq, Hkv, D = params.total_tokens, params.num_q_heads, params.num_kv_heads, params.head_dim
+    qp, qs = _rows("q", q, (N, Hq, D), dev)
+    kp, ks = _rows("k", k, (N, Hkv, D), dev)
+    vp, vs = _rows("v", v, (N, Hkv, D), dev)
+    p = PromptParams(params.batch, N, Hq, Hkv, D, params.max_seq_len, qs, ks, vs, params.sm_scale, params.softcap,
+                     params.window)
+    ws, nbytes = _workspace(workspace, dev)
+    _check("kvq_attend_prompt", load().kvq_attend_prompt(
+        ctypes.byref(p), qp, kp, vp, _need("cu_seqlens", cu_seqlens, torch.int32, (params.batch + 1,), dev),
+        _need("head_sink", head_sink, torch.float32, (Hq,), dev, True),
+        _need("out", out, torch.bfloat16, (N, Hq, D), dev), _need("lse_out", lse_out, torch.float32, (N, Hq), dev, True),
+        ws, nbytes, _raw_stream(stream, dev)))
+
+
+@dataclass
+class DraftTree:
+    """The drafted tokens of each sequence as trees (kvq_tree in kvq.h); tensors
+    on the device.  parents int32 [B, T]: the node that a node follows (outside
+    [0, i): the prefix); num_nodes int32 [B] or None: T nodes each."""
+    parents: torch.Tensor
+    num_nodes: Optional[torch.Tensor] = None
+
+    def desc(self, params: DecodeParams, dev: int) -> TreeDesc:
+        return TreeDesc(_need("parents", self.parents, torch.int32, (params.batch, params.q_tokens), dev),
+                        _need("num_nodes", self.num_nodes, torch.int32, (params.batch,), dev, True))
+
+
+def kvq_attend_tree_workspace_size(cache: QuantizedPagedCache, params: DecodeParams) -> int:
+    d, n = cache.desc(), ctypes.c_size_t(0)
+    _check("kvq_attend_tree_workspace_size",
+           load().kvq_attend_tree_workspace_size(ctypes.byref(d), ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def kvq_attend_tree(cache: QuantizedPagedCache, params: DecodeParams, tree: DraftTree, q: torch.Tensor,
+                    block_table: torch.Tensor, seq_lens: torch.Tensor, head_sink: Optional[torch.Tensor],
+                    out: torch.Tensor, lse_out: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
+    """q bf16 [B, T, Hq, D], out bf16 [B, T, Hq, out_dim] with T = params.q_tokens
+    nodes; lse_out fp32 [B, T, Hq] or None; seq_lens count the nodes."""
+    dev, B, T, Hq = _current(cache.k_codes), params.batch, params.q_tokens, params.num_q_heads
+    d, t = cache.desc(), tree.desc(params, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    _check("kvq_attend_tree", load().kvq_attend_tree(
+        ctypes.byref(d), ctypes.byref(params), ctypes.byref(t),
+        _need("q", q, torch.bfloat16, (B, T, Hq, cache.head_dim), dev),
+        _need("block_table", block_table, torch.int32, (B, params.max_blocks_per_seq), dev),
+        _need("seq_lens", seq_lens, torch.int32, (B,), dev),
+        _need("head_sink", head_sink, torch.float32, (Hq,), dev, True),
+        _need("out", out, torch.bfloat16, (B, T, Hq, cache.out_dim), dev),
+        _need("lse_out", lse_out, torch.float32, (B, T, Hq), dev, True), ws, nbytes, _raw_stream(stream, dev)))
+
+
+def kvq_tree_accept(cache: QuantizedPagedCache, params: DecodeParams, tree: DraftTree, drafts: torch.Tensor,
+                    chosen: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, path: torch.Tensor,
+                    accepted: torch.Tensor, new_lens: torch.Tensor, next_tokens: torch.Tensor,
+                    mass: Optional[torch.Tensor] = None, stream=None):
+    """drafts, chosen int64 [B, T]; path int32 [B, T], accepted, new_lens int32
+    [B], next_tokens int64 [B] (outputs); the accepted rows of the cache (and of
+    mass) move together behind the prefix."""
+    dev, B, T = _current(cache.k_codes), params.batch, params.q_tokens
+    d, t = cache.desc(), tree.desc(params, dev)
+    _check("kvq_tree_accept", load().kvq_tree_accept(
+        ctypes.byref(d), ctypes.byref(params), ctypes.byref(t), _need("drafts", drafts, torch.int64, (B, T), dev),
+        _need("chosen", chosen, torch.int64, (B, T), dev),
+        _need("block_table", block_table, torch.int32, (B, params.max_blocks_per_seq), dev),
+        _need("seq_lens", seq_lens, torch.int32, (B,), dev), _need("path", path, torch.int32, (B, T), dev),
+        _need("accepted", accepted, torch.int32, (B,), dev), _need("new_lens", new_lens, torch.int32, (B,), dev),
+        _need("next_tokens", next_tokens, torch.int64, (B,), dev),
+        _need("mass", mass, torch.float32, (cache.num_blocks, cache.num_kv_heads, cache.block_size), dev, True),
+        _raw_stream(stream, dev)))
+
+
+def make_pages_params(batch, max_blocks_per_seq, *, num_blocks, block_size, max_tokens, tree_nodes=0) -> PagesParams:
+    """max_tokens: entries of the slot map; tree_nodes: row length of parents."""
+    return PagesParams(int(batch), int(max_blocks_per_seq), int(num_blocks), int(block_size), int(max_tokens),
+                       int(tree_nodes))
+
+
+def kvq_pages_step(params: PagesParams, held_lens: torch.Tensor, start_lens: Optional[torch.Tensor],
+                   new_tokens: torch.Tensor, parents: Optional[torch.Tensor], block_table: torch.Tensor,
+                   free_blocks: torch.Tensor, free_count: torch.Tensor, seq_lens: torch.Tensor,
+                   free_left: torch.Tensor, cu_seqlens: torch.Tensor, slot_mapping: torch.Tensor,
+                   positions: torch.Tensor, stream=None):
+    """held_lens, start_lens, new_tokens, seq_lens int32 [B]; parents int32
+    [B, tree_nodes] or None; free_blocks int32 [num_blocks]; free_count,
+    free_left int32 [1]; cu_seqlens int32 [B + 1]; slot_mapping, positions int64
+    [max_tokens].  seq_lens may be held_lens or start_lens, free_left free_count."""
+    dev, B, i32 = _current(block_table), params.batch, torch.int32
+    _check("kvq_pages_step", load().kvq_pages_step(
+        ctypes.byref(params), _need("held_lens", held_lens, i32, (B,), dev),
+        _need("start_lens", start_lens, i32, (B,), dev, True), _need("new_tokens", new_tokens, i32, (B,), dev),
+        _need("parents", parents, i32, (B, params.tree_nodes), dev, True),
+        _need("block_table", block_table, i32, (B, params.max_blocks_per_seq), dev),
+        _need("free_blocks", free_blocks, i32, (params.num_blocks,), dev),
+        _need("free_count", free_count, i32, (1,), dev), _need("seq_lens", seq_lens, i32, (B,), dev),
+        _need("free_left", free_left, i32, (1,), dev), _need("cu_seqlens", cu_seqlens, i32, (B + 1,), dev),
+        _need("slot_mapping", slot_mapping, torch.int64, (params.max_tokens,), dev),
+        _need("positions", positions, torch.int64, (params.max_tokens,), dev), _raw_stream(stream, dev)))

@@ -104,6 +104,7 @@ typedef enum {
 #define KVQ_DEVERR_POSITION 0x10u /* norm/RoPE prologue: position outside [0, max_position) */
 #define KVQ_DEVERR_KEEP_INDEX 0x20u /* kvq_evict_compact: a kept row outside [0, capacity), or in
                                        * place before its destination */
+#define KVQ_DEVERR_NO_BLOCKS 0x40u  /* kvq_pages_step: a sequence got no pages (the pool is short) */
 
 /* Cache layouts (PR #29912, kv_cache_layout and v_head_size): SEPARATE K and V
  * caches, or LATENT (absorbed MLA): one cache whose rows serve as K, and whose
@@ -486,6 +487,158 @@ KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_par
                                      const int32_t* block_table, const int32_t* dst_table, const int32_t* keep,
                                      const int32_t* kept_lens, float* mass, void* workspace,
                                      size_t workspace_bytes, kvq_stream_t stream);
+
+/* kvq_attend_prompt -- attention of whole prompts over the bf16 K and V at
+ * hand, before (or without) a cache: N = total_tokens rows hold the tokens of
+ * B sequences one after another, sequence b in rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1.  Token i of a sequence sees its tokens j <= i (with
+ * window > 0: j > i - window), so it is what kvq_prefill of the whole sequence
+ * gives without the cache's rounding.  Logits, softcap, window, head_sink,
+ * lse_out and the order of heads are those of kvq_decode_params.
+ *   q    bf16 [N, Hq, D]    out bf16 [N, Hq, D] (dense)
+ *   k, v bf16 [N, Hkv, D]   lse_out fp32 [N, Hq] (dense) or NULL
+ *   cu_seqlens int32 [B + 1], ascending (device)
+ * head_dim in {64, 128, 256}; Hq a multiple of Hkv, at most 8 times it.
+ * q, k and v may be slices of a wider projection: q_stride, k_stride and
+ * v_stride are the elements from one token to the next (a multiple of 8; 0:
+ * dense); the heads of a token are dense.  Lengths are on the device: rows of
+ * out and lse_out that belong to no sequence (before cu_seqlens[0], behind
+ * cu_seqlens[B], an empty sequence) are left as they were, and what q, k and v
+ * hold there, NaN included, changes nothing.  A sequence whose bounds descend,
+ * leave [0, N] or exceed max_seq_len sets KVQ_DEVERR_SEQ_LEN and is skipped.
+ * Inf or NaN in a token's own K or V row may spread to earlier tokens of the
+ * same sequence that share a tile of 128 keys with it.
+ * Weights enter the product with V as bf16; sums, maxima and lse are fp32.
+ * Repeated calls give the same bits.  out must not overlap q, k or v.
+ * batch <= 1024.  workspace: at least kvq_attend_prompt_workspace_size bytes,
+ * 256-byte aligned; it belongs to this call until the call's kernels have
+ * run. */
+typedef struct {
+  int32_t batch;        /* B (<= 1024) */
+  int32_t total_tokens; /* N: rows of q, k, v and out */
+  int32_t num_q_heads;  /* Hq */
+  int32_t num_kv_heads; /* Hkv */
+  int32_t head_dim;     /* D */
+  int32_t max_seq_len;  /* host upper bound on a sequence's tokens; 0 = total_tokens */
+  int32_t q_stride;     /* elements between tokens of q; 0 = Hq * D */
+  int32_t k_stride;     /* 0 = Hkv * D */
+  int32_t v_stride;     /* 0 = Hkv * D */
+  float sm_scale;       /* <= 0 selects 1/sqrt(head_dim) */
+  float softcap;        /* > 0: logit s -> softcap * tanh(s / softcap); 0 = off */
+  int32_t window;       /* > 0: the `window` most recent tokens, the query's own among them; 0 = off */
+} kvq_prompt_params;
+
+KVQ_API kvq_status kvq_attend_prompt_workspace_size(const kvq_prompt_params* params, size_t* workspace_bytes);
+KVQ_API kvq_status kvq_attend_prompt(const kvq_prompt_params* params, const void* q, const void* k, const void* v,
+                                     const int32_t* cu_seqlens, const float* head_sink, void* out, float* lse_out,
+                                     void* workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/* A tree of drafted tokens per sequence (speculative decode with several
+ * candidates; the drafts of kvq_decode are its case of one chain).  The last
+ * num_nodes[b] rows of sequence b are the nodes, node i at row P + i with
+ * P = seq_lens[b] - num_nodes[b]; their K and V rows are appended first
+ * (kvq_append), like any tokens.  parents[b, i] is the node that node i
+ * follows; one outside [0, i) (-1, say) makes i a root, which follows the
+ * prefix alone.  Node i stands at position P + depth(i), a root's depth being
+ * 0: the position its rotary angle wants (kvq_pages_step gives it). */
+#define KVQ_MAX_TREE_NODES 256
+typedef struct {
+  const int32_t* parents;   /* int32 [B, T] (device), T = params->q_tokens <= KVQ_MAX_TREE_NODES */
+  const int32_t* num_nodes; /* int32 [B] (device), or NULL: T nodes each.  Outside [0, T], or more
+                               than seq_lens[b]: KVQ_DEVERR_SEQ_LEN, and cut to that range */
+} kvq_tree;
+
+/* kvq_attend_tree -- attention of the nodes of each sequence's tree over the
+ * quantized cache: node i sees the prefix rows j < P and, of the nodes, its
+ * ancestors and itself.  With params->window > 0 a key counts when its
+ * position (a prefix row's is its row, a node's P + depth) is above the
+ * node's own minus window.  q, out bf16 [B, T, Hq, D]; nodes i >= num_nodes[b]
+ * are padding: their output rows are zero and their lse -inf.  Everything
+ * else, the choice of kernels included, is as in kvq_attend_masked.
+ * batch <= 1024.  workspace: at least kvq_attend_tree_workspace_size bytes,
+ * 256-byte aligned; it belongs to this call until the call's kernels have
+ * run. */
+KVQ_API kvq_status kvq_attend_tree_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,
+                                                  size_t* workspace_bytes);
+KVQ_API kvq_status kvq_attend_tree(const kvq_cache* cache, const kvq_decode_params* params, const kvq_tree* tree,
+                                   const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                                   const float* head_sink, void* out, float* lse_out, void* workspace,
+                                   size_t workspace_bytes, kvq_stream_t stream);
+
+/* kvq_tree_accept -- the path through each tree that the model agrees with,
+ * and its rows moved together.  Node 0 is accepted (the step's own token);
+ * after an accepted node n the lowest child c of n with drafts[b, c] ==
+ * chosen[b, n] is, until there is none.  chosen[b, n] is what the model
+ * answers after node n (an argmax or a sample of its logits).
+ *   path [B, T] int32         the accepted nodes in order, then -1
+ *   accepted [B] int32        how many (0 for a sequence without nodes)
+ *   new_lens [B] int32        P + accepted: the lengths after the call
+ *   next_tokens [B] int64     chosen after the last accepted node (-1: no nodes)
+ * Row P + path[i] of the cache (K and V codes, per-row or per-group scales,
+ * and mass fp32 [num_blocks, Hkv, block_size] when it is given) moves to row
+ * P + i; the rows behind keep their contents.  The moves read block_table
+ * entries of the nodes' rows only; an unreadable block id sets
+ * KVQ_DEVERR_BLOCK_ID and its row is not moved.  A page that holds nodes must
+ * not be shared by two sequences.  Of params only batch, q_tokens (T),
+ * max_blocks_per_seq and max_seq_len are used.  drafts, chosen int64 [B, T].
+ * The outputs may overlap neither an input nor one another (refused). */
+KVQ_API kvq_status kvq_tree_accept(const kvq_cache* cache, const kvq_decode_params* params, const kvq_tree* tree,
+                                   const int64_t* drafts, const int64_t* chosen, const int32_t* block_table,
+                                   const int32_t* seq_lens, int32_t* path, int32_t* accepted, int32_t* new_lens,
+                                   int64_t* next_tokens, float* mass, kvq_stream_t stream);
+
+/* kvq_pages_step -- the bookkeeping of a step on the device: which pages each
+ * sequence gives back or gets, where its new rows lie, and at which positions.
+ * Sequence b holds the pages of held_lens[b] rows (ceil(held / block_size)
+ * entries of its block_table row); the first start_lens[b] <= held_lens[b]
+ * rows stay (start_lens NULL: all) and new_tokens[b] rows come behind them.
+ * With want = start + new it gives back the pages behind ceil(want /
+ * block_size) or gets those it lacks.  A finished sequence is start = new = 0,
+ * a fresh one held = 0, a step after kvq_tree_accept start = its new_lens.
+ * The pool is a stack: free_blocks[0 .. free_count) are free, the last on top.
+ * Given-back pages are pushed in order of sequence and page, then the pages
+ * that are asked for popped in that order; a call with the same inputs gives
+ * the same tables, and entries of free_blocks below free_count and of a table
+ * row below its held pages are never changed.
+ * A sequence is refused, and left as it was, when its rows would exceed its
+ * table row or the new tokens up to and with it max_tokens
+ * (KVQ_DEVERR_SEQ_LEN), or when it needs pages and the pages asked for up to
+ * and with it exceed the pool (KVQ_DEVERR_NO_BLOCKS); the sums count refused
+ * sequences too, the pool the pages that sequences not refused by the first
+ * two give back.  Its length stays held_lens[b] and it gets no tokens, so
+ * that the call can be made again with the same values.  held < 0 or above
+ * the table row, start outside [0, held] or new < 0: KVQ_DEVERR_SEQ_LEN,
+ * refused and not counted.
+ *   block_table [B, max_blocks_per_seq] int32  entries behind the held pages
+ *                are written for the pages that were got; others stay
+ *   seq_lens [B] int32        start + new (refused: held)
+ *   free_left [1] int32       free_count after the call
+ *   cu_seqlens [B + 1] int32  prefix sums of the tokens that were granted
+ *   slot_mapping [max_tokens] int64   slot of each new row, sequence after
+ *                sequence (kvq_append's); -1 behind the last
+ *   positions [max_tokens] int64      start + i for the i-th new row of a
+ *                sequence, or with parents [B, tree_nodes] (as in kvq_tree)
+ *                start + depth(i) for i < tree_nodes; 0 behind the last
+ * seq_lens may be held_lens or start_lens itself, free_left free_count itself
+ * (in place); otherwise outputs overlap neither an input nor one another
+ * (refused).  A page id outside [0, num_blocks) is passed on as it is, sets
+ * KVQ_DEVERR_BLOCK_ID, and its rows get slot -1; a free_count outside
+ * [0, num_blocks], or more pages given back than the pool has, sets it too.
+ * batch <= 1024; max_tokens <= 2^30. */
+typedef struct {
+  int32_t batch;              /* B (<= 1024) */
+  int32_t max_blocks_per_seq; /* block_table row length; capacity = it * block_size */
+  int32_t num_blocks;         /* pool size in blocks; entries of free_blocks */
+  int32_t block_size;         /* tokens per block (power of two >= 16) */
+  int32_t max_tokens;         /* entries of slot_mapping and positions */
+  int32_t tree_nodes;         /* row length of parents (<= KVQ_MAX_TREE_NODES); unused without parents */
+} kvq_pages_params;
+
+KVQ_API kvq_status kvq_pages_step(const kvq_pages_params* params, const int32_t* held_lens,
+                                  const int32_t* start_lens, const int32_t* new_tokens, const int32_t* parents,
+                                  int32_t* block_table, int32_t* free_blocks, const int32_t* free_count,
+                                  int32_t* seq_lens, int32_t* free_left, int32_t* cu_seqlens,
+                                  int64_t* slot_mapping, int64_t* positions, kvq_stream_t stream);
 
 /* kvq_attend_noalloc -- kvq_decode then kvq_combine, with the split-partial
  * scratch in a library-owned 16 MiB device array instead of a caller
