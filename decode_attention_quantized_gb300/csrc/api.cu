@@ -560,6 +560,23 @@ kvq_status encode_codes_map(const kvq_cache* c, void* base, CUtensorMap* tm) {
   return r == CUDA_SUCCESS ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+// bf16 rows [tokens, heads, D], tokens `stride` elements apart, in boxes of 64
+// channels x `heads_box` heads x `tokens_box` tokens; rows behind the last read
+// as zero.
+kvq_status encode_rows_map(const void* base, int D, int heads, int tokens, long long stride, int heads_box,
+                           int tokens_box, CUtensorMap* tm) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (kvq_status s = encoder(&enc)) return s;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)tokens_box};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
 kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 // Host checks of a norm/RoPE prologue for rows of head_dim channels; fills
@@ -1597,7 +1614,12 @@ KVQ_API kvq_status kvq_attend_prompt(const kvq_prompt_params* params, const void
   a.softcap = p->softcap;
   a.window = p->window;
   a.err = dev->err;
-  return from_cuda(launch_attend_prompt(a, dev->sms, reinterpret_cast<cudaStream_t>(stream)));
+  alignas(64) CUtensorMap tm[3];
+  const int tokens = 128 / a.group;
+  if (kvq_status s = encode_rows_map(q, D, p->num_q_heads, p->total_tokens, a.q_stride, a.group, tokens, &tm[0])) return s;
+  if (kvq_status s = encode_rows_map(k, D, p->num_kv_heads, p->total_tokens, a.k_stride, 1, 128, &tm[1])) return s;
+  if (kvq_status s = encode_rows_map(v, D, p->num_kv_heads, p->total_tokens, a.v_stride, 1, 128, &tm[2])) return s;
+  return from_cuda(launch_attend_prompt(tm, a, dev->sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 KVQ_API kvq_status kvq_key_mass_workspace_size(const kvq_cache* cache, const kvq_decode_params* params,

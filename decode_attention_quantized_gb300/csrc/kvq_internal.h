@@ -188,7 +188,9 @@ struct PromptArgs {
   int window;
   unsigned int* err;
 };
-cudaError_t launch_attend_prompt(const PromptArgs& a, int sms, cudaStream_t stream);
+// tm: tensor maps of q (boxes of 64 channels, G heads, 128 / G tokens), k and
+// v (64 channels, one head, 128 tokens).
+cudaError_t launch_attend_prompt(const CUtensorMap* tm, const PromptArgs& a, int sms, cudaStream_t stream);
 
 struct CombineArgs {
   const int* plan;
