@@ -169,6 +169,32 @@ __device__ __forceinline__ void cap_scores(float (&y)[N], float cap) {
   }
 }
 
+// The same by size: a thread whose N scores are all within 1/2 (logits within
+// half the cap, the usual ones) takes y P(y^2), P the minimax polynomial of
+// degree 4 to tanh(sqrt t) / sqrt t on [0, 1/4] (1.1e-7 relative in fp32), in
+// half the instructions and without the quotient.
+template <int N>
+__device__ __forceinline__ void cap_scores_by_size(float (&y)[N], float cap) {
+  float big = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) big = ptx::max3(big, fabsf(y[k]), fabsf(y[k + 1]));
+  if (big > 0.5f) {
+    cap_scores<N>(y, cap);
+    return;
+  }
+  const float c1 = -0.33333069f * cap, c2 = 0.13324779f * cap, c3 = -0.05298607f * cap, c4 = 0.01713501f * cap;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float t0, t1, p0, p1;
+    ptx::mul_x2(t0, t1, y[k], y[k + 1], y[k], y[k + 1]);
+    ptx::fma_x2(p0, p1, t0, t1, c4, c4, c3, c3);
+    ptx::fma_x2(p0, p1, p0, p1, t0, t1, c2, c2);
+    ptx::fma_x2(p0, p1, p0, p1, t0, t1, c1, c1);
+    ptx::fma_x2(p0, p1, p0, p1, t0, t1, cap, cap);
+    ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], p0, p1);
+  }
+}
+
 // Exact e4m3x2 -> f16x2 (hardware conversion; the low byte goes to the low
 // half).  Used for K only: a stale e4m3 NaN byte under a masked key can then
 // only poison that key's own score, which the mask replaces.

@@ -46,7 +46,7 @@ struct PromptCfg {
   static constexpr int QTILE = D / 64 * kSlab;
   static constexpr int STAGES = D == 64 ? 8 : 5;
   static constexpr int SOFTMAX = 4 * NQ;           // warps
-  static constexpr int THREADS = 32 * (SOFTMAX + 2);
+  static constexpr int THREADS = 32 * (SOFTMAX + 4);  // (a whole warpgroup beside the softmax: register shares)
   static constexpr int O_COL = 256;
   // shared memory behind the 1 KB alignment: Q, ring, barriers, units
   static constexpr int RING = NQ * QTILE;
@@ -238,7 +238,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   ptx::griddep_launch_dependents();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!ptx::mbar_try_wait(bar, parity)) dev::wait_or_abort(bar, parity, abort_flag, a.err);
+    if (ptx::mbar_try_wait(bar, parity) || *abort_flag) return;
+    if (!ptx::mbar_wait_bounded_inl(bar, parity)) {
+      *abort_flag = 1;
+      atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+    }
   };
   const int G = a.group, tpt = 128 / G, W = a.window;
   // The units of this CTA, one after another, as the producer writes them.
@@ -256,8 +260,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     return w < unit_tiles ? tile_range(u, w, tpt, W) : Range{0, 0};
   };
 
+  // 384 threads x 168 registers: the softmax holds a row of 128 scores
+  constexpr bool kShares = NQ > 1;
   if (warp == kProducer) {
     // ============================================================ producer
+    if constexpr (kShares) ptx::regs_down<88>();
     const int unit_tokens = unit_tiles * tpt;
     uint32_t slot = 0, phase = 0, issued = 0;
     int qn[NQ] = {};
@@ -332,13 +339,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     if (lane == 0) {
       const uint32_t last = issued < (uint32_t)C::STAGES ? issued : (uint32_t)C::STAGES;
       for (uint32_t i = issued - last; i < issued; ++i)
-        ptx::mbar_wait_bounded(&bar_full[i % C::STAGES], (i / C::STAGES) & 1);
+        ptx::mbar_wait_bounded_inl(&bar_full[i % C::STAGES], (i / C::STAGES) & 1);
       for (int w = 0; w < NQ; ++w)
-        if (qn[w] > 0) ptx::mbar_wait_bounded(&b_qfull[w], (qn[w] - 1) & 1);
+        if (qn[w] > 0) ptx::mbar_wait_bounded_inl(&b_qfull[w], (qn[w] - 1) & 1);
     }
     __syncwarp();
   } else if (warp == kMma) {
     // ================================================================ MMA
+    if constexpr (kShares) ptx::regs_down<88>();
     constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kKeys);
     constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, C::SD) | (1u << 16);  // B MN-major
     const uint64_t kd = ptx::smem_desc_sw128(ring);
@@ -472,10 +480,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     }
     // every MMA has completed before tensor memory can be released
     for (int w = 0; w < NQ; ++w)
-      if (np[w] > 0 && !ptx::mbar_wait_bounded(&b_o[w], (np[w] - 1) & 1) && lane == 0) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+      if (np[w] > 0 && !ptx::mbar_wait_bounded_inl(&b_o[w], (np[w] - 1) & 1) && lane == 0) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
     __syncwarp();
-  } else {
+  } else if (warp < C::SOFTMAX) {
     // ============================================================ softmax
+    if constexpr (kShares) ptx::regs_up<208>();
     const int w = warp >> 2, q = warp & 3, r = 32 * q + lane;  // tile, row
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t o_col = t_lane + C::O_COL + w * D;
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         if constexpr (CAP) {
 #pragma unroll
           for (int k = 0; k < kKeys; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
-          dev::cap_scores<kKeys>(y, a.softcap * kLog2e);
+          dev::cap_scores_by_size<kKeys>(y, a.softcap * kLog2e);
         }
         const int key0 = j * kKeys;
         if (!(key0 + kKeys - 1 <= pos && key0 >= begin)) {
@@ -609,6 +618,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       }
       ptx::tc_fence_before();
     }
+  } else {
+    if constexpr (kShares) ptx::regs_down<88>();
   }
 
   ptx::tc_fence_before();

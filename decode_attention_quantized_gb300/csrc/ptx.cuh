@@ -277,6 +277,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// A warpgroup's registers per thread from here on (a multiple of 8; every warp
+// of it calls this, and the sum over the block's warpgroups stays within what
+// the block was launched with).
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Programmatic dependent launch: wait until the preceding grid on the stream
 // has completed and its memory is visible; allow the next grid to launch.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
