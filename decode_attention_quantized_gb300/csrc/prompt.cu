@@ -51,7 +51,7 @@ struct PromptCfg {
   // shared memory behind the 1 KB alignment: Q, ring, barriers, units
   static constexpr int RING = NQ * QTILE;
   static constexpr int BARS = RING + STAGES * STAGE;
-  static constexpr int N_BARS = 2 * STAGES + 2 * NQ + 2 * NQ * SB + NQ + 4;
+  static constexpr int N_BARS = 2 * STAGES + 2 * NQ + 3 * NQ * SB + NQ + 4;
   static constexpr int UNITS = BARS + (N_BARS * 8 + 15) / 16 * 16;
   static constexpr int TOTAL = UNITS + 2 * 16 + 16;
   static constexpr int SMEM = TOTAL + 1024;
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   uint64_t* b_qfull = bar_empty + C::STAGES;                         // [NQ] the unit's Q landed
   uint64_t* b_qfree = b_qfull + NQ;                                  // [NQ] its last QK^T complete
   uint64_t* b_s = b_qfree + NQ;                                      // [NQ][SB] S written
-  uint64_t* b_p = b_s + NQ * SB;                                     // [NQ][SB] P written, O rescaled
-  uint64_t* b_o = b_p + NQ * SB;                                     // [NQ] a PV complete
+  uint64_t* b_p = b_s + NQ * SB;                                     // [NQ][SB][2] a half of P written, O rescaled
+  uint64_t* b_o = b_p + 2 * NQ * SB;                                    // [NQ] a PV complete
   uint64_t* b_unit = b_o + NQ;                                       // [2] unit written
   uint64_t* b_ufree = b_unit + 2;                                    // [2] unit read
   Unit* units = reinterpret_cast<Unit*>(base + C::UNITS);            // [2]
@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     }
     for (int i = 0; i < NQ * SB; ++i) {
       ptx::mbar_init(&b_s[i], 1);
-      ptx::mbar_init(&b_p[i], 4);
+      ptx::mbar_init(&b_p[2 * i], 4);
+      ptx::mbar_init(&b_p[2 * i + 1], 4);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&b_unit[i], 1);
@@ -376,16 +377,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     // PV of tile w with the V tile in stages i ..; the unit's first overwrites O
     auto pv = [&](int w, uint32_t i, bool first) {
       const uint32_t buf = np[w] % SB;
-      wait(&b_p[w * SB + buf], (np[w] / SB) & 1);
-      __syncwarp();
-      ptx::tc_fence_after();
       const uint32_t p = tmem + 128 * (w * SB + buf);
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const uint32_t v = v_lo + ((stage_of(i + h) * C::STAGE) >> 4);
-        const uint32_t o = tmem + C::O_COL + w * D + h * C::SD;
-        ptx::mma_f16_ts_x4_step(o, p, 8, v, (16 * 128) >> 4, hi, idesc_pv, first ? 0u : 1u);
-        ptx::mma_f16_ts_x4_step(o, p + 32, 8, v + ((64 * 128) >> 4), (16 * 128) >> 4, hi, idesc_pv, 1u);
+      for (int half = 0; half < 2; ++half) {
+        wait(&b_p[2 * (w * SB + buf) + half], (np[w] / SB) & 1);
+        __syncwarp();
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          ptx::mma_f16_ts_x4_step(tmem + C::O_COL + w * D + h * C::SD, p + 32 * half, 8,
+                                  v_lo + ((stage_of(i + h) * C::STAGE + half * 64 * 128) >> 4), (16 * 128) >> 4, hi, idesc_pv,
+                                  first && half == 0 ? 0u : 1u);
       }
       ptx::mma_commit(&b_o[w]);
       ++np[w];
@@ -491,6 +493,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     const int t_row = dev::div_small(r, __frcp_rn((float)G)), g = r - t_row * G;
     // (finite and above 0, so that alpha times -inf is -inf)
     const float alpha = fminf(fmaxf(CAP ? a.sm_scale / a.softcap : a.sm_scale * kLog2e, 1.17549435e-38f), 3.4028234e38f);
+    // tanh(x) = x P(x^2) for |x| <= kCapNear, P the minimax polynomial of degree
+    // 3 to tanh(sqrt t) / sqrt t there (1.5e-7 relative in fp32); x = alpha S.
+    constexpr float kCapNear = 0.35f;
+    const float cap2 = CAP ? a.softcap * kLog2e : 0.0f, al2 = alpha * alpha;
+    const float c0 = alpha * cap2, c1 = -0.33332422f * al2 * c0, c2 = 0.13295799f * al2 * al2 * c0,
+                c3 = -0.04895823f * al2 * al2 * al2 * c0;
+    const ptx::f32x2 cc0 = ptx::pack_x2(c0, c0), cc1 = ptx::pack_x2(c1, c1), cc2 = ptx::pack_x2(c2, c2),
+                     cc3 = ptx::pack_x2(c3, c3), aa = ptx::pack_x2(alpha, alpha);
+    // (coefficients far from fp32's ends, or not at all)
+    const float cap_near =
+        CAP && alpha > 6e-5f && alpha < 1.6e4f && cap2 > 1e-6f && cap2 < 1e6f ? kCapNear / alpha : -1.0f;
     uint32_t ns = 0;  // S tiles taken
     for (;;) {
       const Unit u = next_unit();
@@ -507,42 +520,65 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         const uint32_t s_col = t_lane + 128 * (w * SB + buf);
         wait(&b_s[w * SB + buf], (ns / SB) & 1);
         if (idle) {  // rows of no token: what they hold is read by nobody
-          if (lane == 0) ptx::mbar_arrive(&b_p[w * SB + buf]);
+          if (lane == 0) {
+            ptx::mbar_arrive(&b_p[2 * (w * SB + buf)]);
+            ptx::mbar_arrive(&b_p[2 * (w * SB + buf) + 1]);
+          }
           continue;
         }
         ptx::tc_fence_after();
-        float y[kKeys];
-        {
-          uint32_t v[kKeys];
+        const int key0 = j * kKeys;
+        const bool full = key0 + kKeys - 1 <= pos && key0 >= begin;
+        const int lo = begin - key0, hi = pos - key0;  // the tile's visible keys
+        // Scores of 128 keys in registers; under a cap, whose unrolled code would
+        // not stay in the instruction cache, 32 at a time, twice.
+        constexpr int CH = CAP ? 32 : kKeys;
+        float y[CH];
+        auto load_s = [&](int c0) {
+          uint32_t v[CH];
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(s_col + c, v + c);
+          for (int c = 0; c < CH; c += 32) ptx::tmem_ld32(s_col + c0 + c, v + c);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) {
+          for (int i = 0; i < CH; ++i) {
             asm volatile("" : "+r"(v[i]));
             y[i] = __uint_as_float(v[i]);
           }
+        };
+        auto hide = [&](int c0) {
+#pragma unroll
+          for (int k = 0; k < CH; ++k)
+            if (c0 + k < lo || c0 + k > hi) y[k] = -INFINITY;
+        };
+        float m = -INFINITY, least = INFINITY;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kKeys; c0 += CH) {
+          load_s(c0);
+          if (!full) hide(c0);
+          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {least, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+          for (int k = 0; k < CH; k += 2) {
+            mx[k / 2 % 4] = ptx::max3(mx[k / 2 % 4], y[k], y[k + 1]);
+            if constexpr (CAP) mn[k / 2 % 4] = ptx::min3(mn[k / 2 % 4], y[k], y[k + 1]);
+          }
+          m = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
+          if constexpr (CAP) least = fminf(ptx::min3(mn[0], mn[1], mn[2]), mn[3]);
         }
+        // Under a cap, tanh by the polynomial below where no score of the row
+        // passes kCapNear of it (the usual scores), else by the quotient.
+        const bool near = CAP && fmaxf(fabsf(m), fabsf(least)) <= cap_near;
         if constexpr (CAP) {
-#pragma unroll
-          for (int k = 0; k < kKeys; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
-          dev::cap_scores_by_size<kKeys>(y, a.softcap * kLog2e);
+          if (near) {
+            const float t = m * m;
+            m *= fmaf(fmaf(fmaf(c3, t, c2), t, c1), t, c0);
+          } else if (m != -INFINITY) {
+            float x[2] = {m * alpha, 0.0f};
+            dev::cap_scores<2>(x, cap2);
+            m = x[0];
+          }
+        } else {
+          m *= alpha;
         }
-        const int key0 = j * kKeys;
-        if (!(key0 + kKeys - 1 <= pos && key0 >= begin)) {
-          const int lo = begin - key0, hi = pos - key0;
-#pragma unroll
-          for (int k = 0; k < kKeys; ++k)
-            if (k < lo || k > hi) y[k] = -INFINITY;
-        }
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kKeys; k += 4) {
-          m0 = ptx::max3(m0, y[k], y[k + 1]);
-          m1 = ptx::max3(m1, y[k + 2], y[k + 3]);
-        }
-        float m = fmaxf(m0, m1);
-        if constexpr (!CAP) m *= alpha;
         // move the reference only when the tile's maximum exceeds it by more
         // than 8; a row with no key yet holds zeros in O
         float corr = 1.0f;
@@ -557,17 +593,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         l0 *= corr;
         l1 *= corr;
         const float nmu = mu == -INFINITY ? 0.0f : -mu;
-        uint32_t p[kKeys / 2];
-#pragma unroll
-        for (int k = 0; k < kKeys; k += 2) {
-          float z0, z1;
-          if constexpr (CAP) ptx::add_x2(z0, z1, y[k], y[k + 1], nmu, nmu);
-          else ptx::fma_x2(z0, z1, y[k], y[k + 1], alpha, alpha, nmu, nmu);
-          const float e0 = ptx::fast_exp2(z0), e1 = ptx::fast_exp2(z1);
-          ptx::add_x2(l0, l1, l0, l1, e0, e1);
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-          p[k / 2] = *reinterpret_cast<const uint32_t*>(&b2);
-        }
         if (__any_sync(0xffffffffu, resc)) {
           wait(&b_o[w], (ns - 1) & 1);  // the PV before (a rescale is never a unit's first tile)
           ptx::tc_fence_after();
@@ -580,12 +605,57 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             dev::tmem_st_cols<16>(o_col + c0, o);
           }
         }
-        ptx::tmem_st32(s_col, p);
-        ptx::tmem_st32(s_col + 32, p + 32);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&b_p[w * SB + buf]);
+        // P = 2^(y - mu), bf16 pairs; the sums take the fp32 weights.  P goes out
+        // in two halves: PV over the first runs while the second is computed.
+        const ptx::f32x2 nm = ptx::pack_x2(nmu, nmu);
+        ptx::f32x2 l = ptx::pack_x2(l0, l1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[kKeys / 4];
+          // the weights of y[at ..] into p[to ..]
+          auto weigh = [&](int at, int to, int n, auto&& score) {
+#pragma unroll
+            for (int i = 0; i < n; i += 2) {
+              float z0, z1;
+              ptx::unpack_x2(score(ptx::pack_x2(y[at + i], y[at + i + 1])), z0, z1);
+              const float e0 = ptx::fast_exp2(z0), e1 = ptx::fast_exp2(z1);
+              l = ptx::add_x2(l, ptx::pack_x2(e0, e1));
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+              p[to + i / 2] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+          };
+          if constexpr (!CAP) {
+            weigh(half * (kKeys / 2), 0, kKeys / 2, [&](ptx::f32x2 x) { return ptx::fma_x2(x, aa, nm); });
+            ptx::tmem_st32(s_col + 32 * half, p);
+          } else {
+#pragma unroll 1
+            for (int c0 = half * (kKeys / 2); c0 < (half + 1) * (kKeys / 2); c0 += CH) {
+              load_s(c0);
+              if (near) {
+                // y P(y^2) - mu, the factors of alpha in P's coefficients (a row
+                // with hidden keys, of score -inf, is not near)
+                weigh(0, 0, CH, [&](ptx::f32x2 x) {
+                  const ptx::f32x2 t = ptx::mul_x2(x, x);
+                  return ptx::fma_x2(x, ptx::fma_x2(ptx::fma_x2(ptx::fma_x2(t, cc3, cc2), t, cc1), t, cc0), nm);
+                });
+              } else {
+#pragma unroll
+                for (int k = 0; k < CH; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
+                dev::cap_scores<CH>(y, cap2);
+                if (!full) hide(c0);
+                weigh(0, 0, CH, [&](ptx::f32x2 x) { return ptx::add_x2(x, nm); });
+              }
+              // (the columns of S that P takes have been read: P is half as wide)
+              __syncwarp();
+              ptx::tmem_st16(s_col + c0 / 2, *reinterpret_cast<uint32_t(*)[16]>(p));
+            }
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&b_p[2 * (w * SB + buf) + half]);
+        }
+        ptx::unpack_x2(l, l0, l1);
       }
       // ---- O of the unit, normalised, to memory
       if (SB > 1 && kr.b - kr.a > 1) wait(&b_o[w], (ns - 2) & 1);  // (phases one at a time)
@@ -599,22 +669,43 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       float f = 1.0f / l;
       if (a.head_sink && valid) f /= 1.0f + expf(a.head_sink[hq] - lse);
       if (valid && a.lse_out) a.lse_out[row] = lse;
-      uint16_t* dst = a.out + row * D;
+      // The lanes of a quad hold 64 bytes of four rows each; transposed, a quad
+      // stores 64 bytes of one row at a time (a thread's own 16-byte pieces of
+      // 32 rows took the store path 4 times as long).
+      const unsigned long long dst = valid ? reinterpret_cast<unsigned long long>(a.out + row * D) : 0;
+      unsigned long long at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, dst, (lane & ~3) | i);
+      const bool odd = lane & 1, high = lane & 2;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
         dev::tmem_ld_cols<32>(o_col + c0, o);
-        if (!valid) continue;
+        uint32_t x[4][4];  // [16-byte piece][word]
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i + 2 * k] * f, o[i + 2 * k + 1] * f);
-            x[k] = *reinterpret_cast<const uint32_t*>(&b2);
-          }
-          *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(x[0], x[1], x[2], x[3]);
+        for (int i = 0; i < 16; ++i) {
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[2 * i] * f, o[2 * i + 1] * f);
+          x[i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(&b2);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // pieces 0 <-> 1 and 2 <-> 3 with the neighbour, then 0 <-> 2 and 1 <-> 3
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x[k][i] : x[k + 1][i], 1);
+            (odd ? x[k][i] : x[k + 1][i]) = got;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[k][i] : x[k + 2][i], 2);
+            (high ? x[k][i] : x[k + 2][i]) = got;
+          }
+        }
+        // piece k is now this lane's 16 bytes of the quad's row k
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at[k])
+            *reinterpret_cast<uint4*>(at[k] + 2 * c0 + 16 * (lane & 3)) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
       }
       ptx::tc_fence_before();
     }
