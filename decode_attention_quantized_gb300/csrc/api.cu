@@ -167,6 +167,8 @@ constexpr int kTcPieceCost = 3;
 // 3-4x slower than the rest; 3 stages measured balanced and fastest).
 constexpr int kQtPieceCost = 8;
 constexpr int kQtMaxStages = 3;
+constexpr int kTtMaxStages = 6;
+static_assert(kTtRows == kQtRows, "one limit for both");
 constexpr int kPieceCost = 3;
 
 // Launch shape of the decode kernel and the workspace it implies.
@@ -279,23 +281,28 @@ bool qt_ok(const kvq_cache* c, const kvq_decode_params* p) {
   return !(p->flags & KVQ_DECODE_NO_TCGEN05) && (c->head_dim == 128 || c->head_dim == 256) && !any_group(c);
 }
 
-// The query-tile kernel: one CTA per SM (it holds all of the SM's TMEM), the
-// mma.sync kernel's 64-key stages, as many of them as fit beside the two
-// double-buffered f16 tiles.
-kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool split, Plan* P) {
+// The query-tile kernels (prompts and masks, draft trees): one CTA per SM (it
+// holds all of the SM's TMEM), the mma.sync kernel's 64-key stages, as many of
+// them as fit beside the two double-buffered f16 tiles.
+kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool split, bool tree,
+                        Plan* P) {
   const bool exch = split && c->head_dim == 256;
   const int B = p->batch > 0 ? p->batch : 1;
   const size_t stride = stage_stride(c, false);
   constexpr size_t kMaxSmem = 227 * 1024;  // per CTA
+  auto total = [&](int s) -> size_t {
+    return 1024 + (size_t)(tree ? tt_smem_layout(c->head_dim, s, B, (int)stride, exch).total
+                                : qt_smem_layout(c->head_dim, s, B, (int)stride, exch).total);
+  };
   int stages = 0;
-  for (int s = kQtMaxStages; s >= 2 && stages == 0; --s)
-    if ((size_t)qt_smem_layout(c->head_dim, s, B, (int)stride, exch).total + 1024 <= kMaxSmem) stages = s;
+  for (int s = tree ? kTtMaxStages : kQtMaxStages; s >= 2 && stages == 0; --s)
+    if (total(s) <= kMaxSmem) stages = s;
   if (stages == 0) return KVQ_ERR_UNSUPPORTED;
   P->qt = 1;
   P->stages = stages;
   P->stride = stride;
-  P->smem = (size_t)qt_smem_layout(c->head_dim, stages, B, (int)stride, exch).total + 1024;
-  P->threads = kQtWarps * 32;
+  P->smem = total(stages);
+  P->threads = 32 * (tree ? kTtWarps : kQtWarps);
   const long long cap = (long long)p->max_blocks_per_seq * c->block_size;
   const long long maxlen = (p->max_seq_len > 0 && p->max_seq_len < cap) ? p->max_seq_len : cap;
   long long grid = dev.sms;
@@ -406,7 +413,7 @@ kvq_status make_plan_uncached(const kvq_cache* c, const kvq_decode_params* p, co
   P.rows = G * p->q_tokens;
   if (qt) {
     if (!qt_ok(c, p) || P.rows > kQtRows) return KVQ_ERR_UNSUPPORTED;
-    if (kvq_status s = make_plan_qt(c, p, dev, split, &P)) return s;
+    if (kvq_status s = make_plan_qt(c, p, dev, split, tree, &P)) return s;
     const int B = p->batch > 0 ? p->batch : 1;
     P.units_max = P.grid + B * c->num_kv_heads;
     P.ws_plan = align256((size_t)(4 + B + 1) * 4);
@@ -760,9 +767,9 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
   cudaError_t e;
   if (mask && mask->tree_bits && P.qt) {
     switch (cache->dtype) {
-      case KVQ_INT8: e = launch_qt_tree_int8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
-      case KVQ_FP8_E4M3: e = launch_qt_tree_fp8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
-      default: e = launch_qt_tree_int4(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_INT8: e = launch_tree_tile_int8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = launch_tree_tile_fp8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      default: e = launch_tree_tile_int4(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
     }
   } else if (mask && mask->tree_bits) {
     e = tree_kernel(cache, mask->split)(cache->head_dim, kernel_nt(cache, P), &tk, &tv, &a, P.grid, P.threads, P.smem, st,
@@ -930,7 +937,7 @@ struct MaskShape {
   long long groups;  // batch * n
 };
 
-kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse, MaskShape* out) {
+kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse, bool tree, MaskShape* out) {
   if (!p || p->q_tokens < 1 || p->batch < 0 || p->num_q_heads <= 0) return KVQ_ERR_INVALID_ARG;
   if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
   const int C = p->q_tokens, G = p->num_q_heads / c->num_kv_heads;
@@ -940,7 +947,7 @@ kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse
   s.split = lse && c->k_mode == KVQ_SCALE_PER_CHANNEL;
   const int tile = s.split && c->head_dim == 256 ? kQtRows / 2 : kQtRows;
   s.T = tile / G < C ? tile / G : C;
-  const int least = p->softcap > 0.0f ? (tile == kQtRows ? 64 : 56) : 17;
+  const int least = p->softcap > 0.0f && !tree ? (tile == kQtRows ? 64 : 56) : 17;
   s.qt = qt_ok(c, p) && s.T * G >= least;
   if (!s.qt) {
     const int most = c->head_dim == 576 && 48 / G < 8 ? 48 / G : 8;
@@ -1123,7 +1130,7 @@ kvq_status attend_groups_workspace(const kvq_cache* cache, const kvq_decode_para
   size_t most = 0;  // with and without an lse
   for (bool lse : {false, true}) {
     MaskShape shape;
-    if (kvq_status s = masked_shape(&eff_, params, lse, &shape)) return s;
+    if (kvq_status s = masked_shape(&eff_, params, lse, tree, &shape)) return s;
     size_t head = 0, need = 0;
     if (kvq_status s = masked_workspace(&eff_, params, shape, tree, &head, &need)) return s;
     most = need > most ? need : most;
@@ -1140,7 +1147,7 @@ kvq_status attend_groups(const kvq_cache* cache, const kvq_decode_params* params
   if (kvq_status s = resolve_cache(cache, &eff_)) return s;
   cache = &eff_;
   MaskShape shape;
-  if (kvq_status s = masked_shape(cache, params, lse_out != nullptr, &shape)) return s;
+  if (kvq_status s = masked_shape(cache, params, lse_out != nullptr, tree != nullptr, &shape)) return s;
   {
     const kvq_decode_params v = masked_params(params, shape, shape.groups < kMaxBatch ? shape.groups : kMaxBatch);
     if (kvq_status s = check_params(cache, &v, shape.qt)) return s;

@@ -93,7 +93,6 @@ __device__ __forceinline__ uint32_t qt_chunk(uint32_t tile, int kk, int c) {
 
 // RULE > 0: the score rule of a masked call over its virtual sequences, in
 // kernels of its own.  RULE == 2: the Q operand in two f16 parts (decode.cuh).
-// RULE 3 and 4: the same two with the bits of draft trees in place of a bias.
 // At head_dim 128 the second part has tensor-memory columns of its own and a
 // second pass of QK^T adds into the same S.  At head_dim 256 tensor memory is
 // full: a unit then has at most 64 rows, the second parts are the operand's
@@ -105,7 +104,7 @@ template <int DT, int D, int RULE, bool CAP>
 __global__ void __launch_bounds__(kQtWarps * 32, 1)
     decode_qt_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const DecodeArgs a) {
-  constexpr bool MASK = RULE > 0, SPLIT = RULE == 2 || RULE == 4, STACK = SPLIT && D == 256, TREE = RULE > 2;
+  constexpr bool MASK = RULE > 0, SPLIT = RULE == 2, STACK = SPLIT && D == 256;
   using C = QtCfg<DT, D, SPLIT && !STACK>;
   using Gm = typename C::Gm;
   constexpr int KT = C::KT;
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           float lse = -INFINITY;
           if (l > 0.0f) {
             lse = (mu + ptx::fast_log2(l)) * 0.69314718055994530942f;
-            if (!TREE && a.slopes && valid) lse -= a.slopes[hq] * (float)ru.d0;
+            if (a.slopes && valid) lse -= a.slopes[hq] * (float)ru.d0;
             if (a.head_sink && valid) inv /= 1.0f + expf(a.head_sink[hq] - lse);
           }
           if (a.v_mode == KVQ_SCALE_PER_TENSOR) inv *= a.v_scale[0];
@@ -604,8 +603,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           // scores that feed only its own unwritten output
           ru = dev::RowRule{};
           ru.end = L;
-          ru.bits = -1;
-          if (valid) ru = dev::row_rule<TREE>(a, tok0 + t_row, a.vseq[b].pos0 + t_row, h * G + (r - t_row * G), L);
+          if (valid) ru = dev::row_rule(a, tok0 + t_row, a.vseq[b].pos0 + t_row, h * G + (r - t_row * G), L);
         } else {
           pos = valid ? L - T + t_row : -1;
         }
@@ -695,7 +693,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
         float sg = 0.0f, b0 = 0.0f;
         bool folded = false;
         if constexpr (MASK) {
-          if (!TREE && a.slopes && (key0 + KT - 1 <= ru.pos || key0 >= ru.pos)) {
+          if (a.slopes && (key0 + KT - 1 <= ru.pos || key0 >= ru.pos)) {
             sg = key0 >= ru.pos ? ru.ns : -ru.ns;
             b0 = ru.ns * (float)(abs(ru.pos - key0) - ru.d0);
             folded = !CAP;
@@ -758,7 +756,7 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           }
         }
         if constexpr (MASK) {
-          if (!TREE && a.slopes && !folded) {
+          if (a.slopes && !folded) {
             // after a cap, or in the tile that holds pos (distances fold at it)
             if (key0 + KT - 1 <= ru.pos || key0 >= ru.pos) {
 #pragma unroll
@@ -771,17 +769,9 @@ __global__ void __launch_bounds__(kQtWarps * 32, 1)
           }
           if (!(key0 >= ru.begin && key0 + KT <= ru.end)) {
             const int lo = min(KT, max(0, ru.begin - key0)), hi = min(KT, max(0, ru.end - key0));
-            if constexpr (TREE) {
-              uint32_t m[KT / 32];
-              dev::tree_sees_64(a, ru, key0, m);
 #pragma unroll
-              for (int k = 0; k < KT; ++k)
-                if (!(k >= lo && k < hi) && !((m[k / 32] >> (k % 32)) & 1u)) y[k] = -INFINITY;
-            } else {
-#pragma unroll
-              for (int k = 0; k < KT; ++k)
-                if (!(k >= lo && k < hi)) y[k] = -INFINITY;
-            }
+            for (int k = 0; k < KT; ++k)
+              if (!(k >= lo && k < hi)) y[k] = -INFINITY;
           }
         } else {
           const bool full = key0 + KT - 1 <= pos && (W == 0 || key0 > pos - W);
@@ -893,16 +883,16 @@ cudaError_t dispatch_decode_qt(int head_dim, const CUtensorMap& tk, const CUtens
 }
 
 // A masked call's instances: a one-part or a two-part Q operand, with or
-// without a softcap; RULE 1, or 3 for draft trees.
-template <int DT, int RULE = 1>
+// without a softcap.
+template <int DT>
 cudaError_t dispatch_qt_mask(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
                              const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream) {
   if (a.softcap > 0.0f) {
-    if (split) return dispatch_decode_qt<DT, RULE + 1, true>(head_dim, tk, tv, a, grid, smem, stream);
-    return dispatch_decode_qt<DT, RULE, true>(head_dim, tk, tv, a, grid, smem, stream);
+    if (split) return dispatch_decode_qt<DT, 2, true>(head_dim, tk, tv, a, grid, smem, stream);
+    return dispatch_decode_qt<DT, 1, true>(head_dim, tk, tv, a, grid, smem, stream);
   }
-  if (split) return dispatch_decode_qt<DT, RULE + 1, false>(head_dim, tk, tv, a, grid, smem, stream);
-  return dispatch_decode_qt<DT, RULE, false>(head_dim, tk, tv, a, grid, smem, stream);
+  if (split) return dispatch_decode_qt<DT, 2, false>(head_dim, tk, tv, a, grid, smem, stream);
+  return dispatch_decode_qt<DT, 1, false>(head_dim, tk, tv, a, grid, smem, stream);
 }
 
 }  // namespace kvq

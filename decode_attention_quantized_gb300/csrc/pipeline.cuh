@@ -407,8 +407,9 @@ struct TileOrder {
 // ATTEND: the attention kernels, a piece's tiles from its last to its first
 // (TileOrder), and nothing from pages that end before the first key some token
 // sees (they may have left the table).  The key-mass kernels write to every
-// key's place and flag each unreadable id.
-template <class Gm, bool ATTEND = false>
+// key's place and flag each unreadable id.  INL: waits without a call (a kernel
+// whose warps share its registers unequally may not make any).
+template <class Gm, bool ATTEND = false, bool INL = false>
 __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& sp, const CUtensorMap* tmk,
                               const CUtensorMap* tmv, uint8_t* ring, uint64_t* bar_full, uint64_t* bar_empty,
                               const int* pl_pre, const int* pl_misc) {
@@ -450,7 +451,8 @@ __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& 
       const int key_next = key + Order::step;
       if (mine && key_next >= k0 && key_next < k1) id_next = bt[key_next >> a.log2_bs];
       if (lane == 0 && it >= S && ok) {
-        ok = ptx::mbar_wait_bounded(&bar_empty[stage], rp.phase ^ 1u) ? 1 : 0;
+        ok = (INL ? ptx::mbar_wait_bounded_inl(&bar_empty[stage], rp.phase ^ 1u)
+                  : ptx::mbar_wait_bounded(&bar_empty[stage], rp.phase ^ 1u)) ? 1 : 0;
         if (!ok) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -484,7 +486,9 @@ __device__ void produce_lanes(const DecodeArgs& a, const Slice<Gm::KEYS, true>& 
   if (lane == 0) {
     for (uint32_t s = 0; s < S && s < it; ++s) {
       const uint32_t last = it - 1 - ((it - 1 - s) % S);
-      if (!ptx::mbar_wait_bounded(&bar_full[s], (last / S) & 1)) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+      if (!(INL ? ptx::mbar_wait_bounded_inl(&bar_full[s], (last / S) & 1)
+                : ptx::mbar_wait_bounded(&bar_full[s], (last / S) & 1)))
+        atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
     }
   }
   __syncwarp();
