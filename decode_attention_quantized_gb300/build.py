@@ -31,8 +31,8 @@ SOURCES = ["api.cu", "append.cu", "combine.cu", "decode_int8.cu", "decode_fp8.cu
            "decode_mask_int4.cu", "decode_split_int8.cu", "decode_split_fp8.cu", "decode_split_int4.cu", "qt_mask_int8.cu", "qt_mask_fp8.cu", "qt_mask_int4.cu", "key_mass_int8.cu",
            "key_mass_fp8.cu", "key_mass_int4.cu", "key_mass_tc_int8.cu", "key_mass_tc_fp8.cu", "key_mass_tc_int4.cu", "evict.cu",
            "decode_tree_int8.cu", "decode_tree_fp8.cu", "decode_tree_int4.cu", "decode_tree_split_int8.cu",
-           "decode_tree_split_fp8.cu", "decode_tree_split_int4.cu", "tree_tile_int8.cu", "tree_tile_fp8.cu",
-           "tree_tile_int4.cu", "tree.cu", "pages.cu", "prompt.cu"]
+           "decode_tree_split_fp8.cu", "decode_tree_split_int4.cu", "tree_tile_int8_d128.cu", "tree_tile_int8_d256.cu",
+           "tree_tile_fp8_d128.cu", "tree_tile_fp8_d256.cu", "tree_tile_int4_d128.cu", "tree_tile_int4_d256.cu", "tree.cu", "pages.cu", "prompt.cu"]
 
 
 def _nvcc() -> str:

@@ -286,12 +286,12 @@ bool qt_ok(const kvq_cache* c, const kvq_decode_params* p) {
 // them as fit beside the two double-buffered f16 tiles.
 kvq_status make_plan_qt(const kvq_cache* c, const kvq_decode_params* p, const DeviceInfo& dev, bool split, bool tree,
                         Plan* P) {
-  const bool exch = split && c->head_dim == 256;
+  const bool exch = split && c->head_dim == 256, fold = tt_fold(c->head_dim, split, P->rows);
   const int B = p->batch > 0 ? p->batch : 1;
   const size_t stride = stage_stride(c, false);
   constexpr size_t kMaxSmem = 227 * 1024;  // per CTA
   auto total = [&](int s) -> size_t {
-    return 1024 + (size_t)(tree ? tt_smem_layout(c->head_dim, s, B, (int)stride, exch).total
+    return 1024 + (size_t)(tree ? tt_smem_layout(c->head_dim, s, B, (int)stride, tt_exchange(c->head_dim, split, fold)).total
                                 : qt_smem_layout(c->head_dim, s, B, (int)stride, exch).total);
   };
   int stages = 0;
@@ -766,10 +766,11 @@ kvq_status decode_impl(const kvq_cache* cache, const kvq_decode_params* params, 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (mask && mask->tree_bits && P.qt) {
+    const bool d128 = cache->head_dim == 128, fold = tt_fold(cache->head_dim, mask->split, P.rows);  // (qt_ok: 128 or 256)
     switch (cache->dtype) {
-      case KVQ_INT8: e = launch_tree_tile_int8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
-      case KVQ_FP8_E4M3: e = launch_tree_tile_fp8(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
-      default: e = launch_tree_tile_int4(cache->head_dim, mask->split, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_INT8: e = (d128 ? launch_tree_tile_int8_d128 : launch_tree_tile_int8_d256)(mask->split, fold, tk, tv, a, P.grid, P.smem, st); break;
+      case KVQ_FP8_E4M3: e = (d128 ? launch_tree_tile_fp8_d128 : launch_tree_tile_fp8_d256)(mask->split, fold, tk, tv, a, P.grid, P.smem, st); break;
+      default: e = (d128 ? launch_tree_tile_int4_d128 : launch_tree_tile_int4_d256)(mask->split, fold, tk, tv, a, P.grid, P.smem, st); break;
     }
   } else if (mask && mask->tree_bits) {
     e = tree_kernel(cache, mask->split)(cache->head_dim, kernel_nt(cache, P), &tk, &tv, &a, P.grid, P.threads, P.smem, st,

@@ -292,28 +292,39 @@ __host__ __device__ constexpr QtSmem qt_smem_layout(int head_dim, int stages, in
   return s;
 }
 
-// The tcgen05 draft-tree kernel (tree_tile.cuh): the same rows and stages, 16
+// The tcgen05 draft-tree kernel (tree_tile.cuh): the same rows and stages, 20
 // warps.  ring: stages x stage stride; kf, vf: two [D/64 slabs][kTile keys]
-// [128 B] f16 tiles each; sc: four [kTile] K scales, four [kTile] V scales over
-// 2^F and four F; exch (two-part Q at head_dim 256 only): two [64 rows][kTile
-// keys] f16 blocks; pre: split plan; bars: mbarriers; slot: TMEM address +
-// abort flag.
-constexpr int kTtWarps = 16;
+// [128 B] f16 tiles each; sc: eight [kTile] K scales, eight [kTile] V scales over
+// 2^F and eight F; exch: two-part Q at head_dim 256: two [64 rows][kTile
+// keys] f16 blocks; folded rows: their references and sums and 16 columns of O
+// at a time; pair: the rows' references and sums; pre:
+// split plan; bars: mbarriers; slot: TMEM address + abort flag.
+constexpr int kTtWarps = 20;
 constexpr int kTtRows = 128;
 
+// Units of at most 64 rows (without a two-part Q at head_dim 256, which takes
+// the other 64 itself) stand in the tile twice.
+__host__ __device__ constexpr bool tt_fold(int head_dim, bool split, int rows) {
+  return rows <= kTtRows / 2 && !(split && head_dim == 256);
+}
+__host__ __device__ constexpr int tt_exchange(int head_dim, bool split, bool fold) {
+  return split && head_dim == 256 ? 2 * 64 * kTile * 2 : fold ? 512 * 4 + 4 * 256 * 16 : 0;
+}
+
 struct TtSmem {
-  int ring, kf, vf, sc, exch, pre, bars, slot, total;
+  int ring, kf, vf, sc, exch, pair, pre, bars, slot, total;
 };
-__host__ __device__ constexpr TtSmem tt_smem_layout(int head_dim, int stages, int batch, int stage_stride, bool exchange) {
+__host__ __device__ constexpr TtSmem tt_smem_layout(int head_dim, int stages, int batch, int stage_stride, int exchange) {
   TtSmem s{};
   s.ring = 0;
   s.kf = stages * stage_stride;
   s.vf = s.kf + 2 * (head_dim / 64) * kTile * 128;
   s.sc = s.vf + 2 * (head_dim / 64) * kTile * 128;
-  s.exch = s.sc + 8 * kTile * 4 + 4 * 4;
-  s.pre = s.exch + (exchange ? 2 * 64 * kTile * 2 : 0);
+  s.exch = s.sc + 16 * kTile * 4 + 8 * 4;
+  s.pair = s.exch + exchange;
+  s.pre = s.pair + 5 * kTtRows * 4;
   s.bars = (s.pre + (batch + 5) * 4 + 7) / 8 * 8;
-  s.slot = s.bars + (2 * stages + 19) * 8;
+  s.slot = s.bars + (2 * stages + 33) * 8;
   s.total = s.slot + 16;
   return s;
 }
@@ -521,24 +532,30 @@ cudaError_t dispatch_decode_tree_int8(int head_dim, int nt, const CUtensorMap* t
 cudaError_t dispatch_decode_tree_split_int8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
                                      const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
                                      int* blocks_per_sm);
-cudaError_t launch_tree_tile_int8(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_tree_tile_int8_d128(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_tree_tile_int8_d256(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
 cudaError_t dispatch_decode_tree_fp8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
                                      const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
                                      int* blocks_per_sm);
 cudaError_t dispatch_decode_tree_split_fp8(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
                                      const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
                                      int* blocks_per_sm);
-cudaError_t launch_tree_tile_fp8(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_tree_tile_fp8_d128(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_tree_tile_fp8_d256(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
 cudaError_t dispatch_decode_tree_int4(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
                                      const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
                                      int* blocks_per_sm);
 cudaError_t dispatch_decode_tree_split_int4(int head_dim, int nt, const CUtensorMap* tk, const CUtensorMap* tv,
                                      const DecodeArgs* a, int grid, int threads, size_t smem, cudaStream_t stream,
                                      int* blocks_per_sm);
-cudaError_t launch_tree_tile_int4(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_tree_tile_int4_d128(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_tree_tile_int4_d256(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream);
 
 cudaError_t occupancy_decode_int8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);
 cudaError_t occupancy_decode_fp8(int head_dim, int nt, int threads, size_t smem, int* blocks_per_sm);

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeArgs a) {
     for (int j = 0; j < KVQ_MAX_TREE_NODES / 32; ++j)
       if (j < a.words) a.bits[tok * a.words + j] = w[j];
     const int begin = i < n && a.window > 0 ? max(0, P + depth - a.window + 1) : 0;
-    a.begin[tok] = begin;
+    a.begin[tok] = i < n ? begin : 0x7FFFFFFF;  // (no key; the attention kernel knows absent nodes by it)
     a.end[tok] = i < n ? P : 0;
     low[i] = min(begin, P);
   }

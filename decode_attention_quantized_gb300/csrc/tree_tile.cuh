@@ -12,16 +12,24 @@
 // Each key tile's codes are dequantized once into f16 tiles in shared memory
 // (two of each), exactly: per-row scales go into the scores (K) and, under a
 // power-of-two normaliser 2^F, into the weights (V), per-channel ones into Q
-// and the output.  P overwrites its own S, so that head_dim 256 has two S
-// buffers too (Q 128 + O 256 + S 2 x 64 columns) and QK^T of the next tile runs
-// during the softmax; one warp issues both products, whose order in the tensor
-// pipe is what keeps S, P and Q apart.
+// and the output.  P overwrites its own S: head_dim 256 has two S buffers (Q 128 + O 256 + S 2 x
+// 64 columns), head_dim 128 four.  One warp issues both products; their order
+// in the tensor pipe is what keeps S, P and Q apart.
 //
-// Warp roles (16 warps): 0-3 softmax, one thread a row (Q of a piece into
-// TMEM, S -> P with lazy row maxima, the epilogue); 4-7 K dequant, key
-// 32 (w & 1) + lane, channel half w >> 1; 8-11 V dequant, the same; 12 TMA
-// producer of the code stages; 13 the MMAs.
+// Warp roles (20 warps, 18 and 19 for the even share of registers): 0-3 and 4-7 softmax of the even and of the odd tiles,
+// one thread a row (S -> P with lazy row maxima; together Q of a piece into
+// TMEM and the epilogue, half of the channels each); 8-11 K dequant, two warps for the even
+// tiles and two for the odd ones, one key a thread; 12-15 V dequant, the same; 16 TMA
+// producer of the code stages; 17 the MMAs.
+//
+// A tile's softmax is a chain of latencies (tensor memory, row maximum,
+// reference, weights) about twice as long as its work, so two groups of warps
+// walk alternate tiles.  They share O and with it the reference maximum of a
+// row, which goes from tile to tile through shared memory; each keeps its own
+// sum, under the reference it last saw.
 #pragma once
+
+#include <type_traits>
 
 #include "decode_tc.cuh"
 
@@ -34,22 +42,6 @@ namespace dev {
 template <int SLAB>
 __device__ __forceinline__ uint32_t tt_chunk(uint32_t tile, int kk, int c) {
   return tile + (uint32_t)(c >> 3) * SLAB + (uint32_t)kk * 128u + ((((uint32_t)c & 7u) ^ ((uint32_t)kk & 7u)) << 4);
-}
-
-// One 16-byte chunk of a V code row in k_cols's order; e4m3 by the hardware
-// conversion with NaN codes (a key no row sees may hold one) made finite.
-template <int DT>
-__device__ __forceinline__ void tt_v_cols(const uint4 w4, uint32_t* v) {
-  if constexpr (DT == KVQ_FP8_E4M3) {
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = f8cvt(w[i], 0x4410u);
-      v[2 * i + 1] = f8cvt(w[i], 0x4432u);
-    }
-  } else {
-    k_cols<DT>(w4, v);
-  }
 }
 
 // Transposes the 4 x 4 16-byte pieces of a quad of lanes: x[k] of lane i
@@ -78,8 +70,13 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][4]) {
 // its own and a second pass of QK^T adds into the same S; at head_dim 256 a
 // unit then has at most 64 rows, the second parts are the operand's rows
 // 64..127, and warps 2 and 3 hand their rows of S to warps 0 and 1 through
-// shared memory (as f16: 2^-11 of a 2^-12 correction).  CAP: a softcap.
-template <int DT, int D, bool SPLIT, bool CAP>
+// shared memory (as f16: 2^-11 of a 2^-12 correction).
+// FOLD (not with that): units of at most 64 rows stand in the tile twice, and
+// each copy takes 32 keys of every tile as a row of its own (P is 0 at the
+// others), so that all four warps of a group have half a tile's softmax each;
+// the epilogue adds the copies up.
+// CAP: a softcap.
+template <int DT, int D, bool SPLIT, bool CAP, bool FOLD>
 __global__ void __launch_bounds__(kTtWarps * 32, 1)
     tree_tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const DecodeArgs a) {
@@ -90,28 +87,34 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
   constexpr int Q_COL = 0, QL_COL = D / 2, O_COL = D / 2 * (SPLIT && !STACK ? 2 : 1), S_COL = O_COL + D;
   static_assert(S_COL + 2 * KT <= 512, "TMEM columns");
   using Order = TileOrder<KT, true>;
-  constexpr int kDqK = 4, kDqV = 8, kProducer = 12, kMma = 13;
+  constexpr int kDqK = 8, kDqV = 12, kProducer = 16, kMma = 17;
+  constexpr int NSB = S_COL + 4 * KT <= 512 ? 4 : 2;  // S buffers
+  constexpr int LA = NSB - 1;                          // tiles of QK^T ahead of PV
+  constexpr int CH = KT / 2;                           // keys of a softmax thread in a tile
+  static_assert(!(FOLD && STACK), "one use of the second 64 rows");
   constexpr float kLog2e = 1.4426950408889634f;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  const TtSmem lay = tt_smem_layout(D, a.stages, a.batch, a.stage_stride, STACK);
+  const TtSmem lay = tt_smem_layout(D, a.stages, a.batch, a.stage_stride, tt_exchange(D, SPLIT, FOLD));
   uint8_t* ring = base + lay.ring;
   const uint32_t kf = ptx::smem_u32(base + lay.kf), vf = ptx::smem_u32(base + lay.vf);
-  float* ksb = reinterpret_cast<float*>(base + lay.sc);  // [4][KT] K scales of tile it, at it & 3
-  float* vsb = ksb + 4 * KT;                              // [4][KT] its V scales over 2^F
-  int* fexp = reinterpret_cast<int*>(vsb + 4 * KT);       // [4] its F
+  float* ksb = reinterpret_cast<float*>(base + lay.sc);  // [8][KT] K scales of tile it, at it & 7
+  float* vsb = ksb + 8 * KT;                              // [8][KT] its V scales over 2^F
+  int* fexp = reinterpret_cast<int*>(vsb + 8 * KT);       // [8] its F (of the piece's tiles so far)
+  float* ref = reinterpret_cast<float*>(base + lay.pair);  // [128] the rows' reference maxima
+  float* part = ref + kTtRows;                             // [2 groups][128] their last references and sums
   int* pl_pre = reinterpret_cast<int*>(base + lay.pre);
   int* pl_misc = pl_pre + a.batch + 1;
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(base + lay.bars);
   uint64_t* bar_empty = bar_full + a.stages;
-  uint64_t* b_s = bar_empty + a.stages;  // [2] QK^T of tile it complete: S buffer and K tile it & 1
-  uint64_t* b_kfull = b_s + 2;           // [2] K f16 tile written
-  uint64_t* b_vfull = b_s + 4;           // [2] V f16 tile written
-  uint64_t* b_p = b_s + 6;               // [2] P of tile it written (and O rescaled)
-  uint64_t* b_pv = b_s + 8;              // [2] PV of tile it complete: V tile it & 1 free
-  uint64_t* b_q = b_s + 10;              // Q of a piece in TMEM
-  uint64_t* b_ksc = b_s + 11;            // [4] K scales of tile it (per-row K)
-  uint64_t* b_vsc = b_s + 15;            // [4] V scales of tile it (per-row V)
+  uint64_t* b_s = bar_empty + a.stages;  // [NSB] QK^T of tile it complete: S buffer it % NSB, K tile it & 1
+  uint64_t* b_pv = b_s + 4;              // [NSB] PV of tile it complete: V tile it & 1 free
+  uint64_t* b_kfull = b_s + 8;           // [2] K f16 tile written
+  uint64_t* b_vfull = b_s + 10;          // [2] V f16 tile written
+  uint64_t* b_p = b_s + 12;              // [NSB] P of tile it written (and O rescaled)
+  uint64_t* b_q = b_s + 16;              // Q of a piece in TMEM
+  uint64_t* b_ksc = b_s + 17;            // [8] K scales of tile it (per-row K)
+  uint64_t* b_vsc = b_s + 25;            // [8] V scales of tile it (per-row V)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + lay.slot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -122,15 +125,17 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       ptx::mbar_init(&bar_empty[s], 8);  // K and V dequant warps
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&b_s[i], 1);
       ptx::mbar_init(&b_kfull[i], 4);
       ptx::mbar_init(&b_vfull[i], 4);
-      ptx::mbar_init(&b_p[i], 4);
-      ptx::mbar_init(&b_pv[i], 1);
     }
-    ptx::mbar_init(b_q, 4);
+    ptx::mbar_init(b_q, 8);
     for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(&b_ksc[i], 2);  // the two warps of channel half 0
+      ptx::mbar_init(&b_s[i], 1);
+      ptx::mbar_init(&b_pv[i], 1);
+      ptx::mbar_init(&b_p[i], FOLD ? 4 : 8);  // the softmax warps of a tile
+    }
+    for (int i = 0; i < 8; ++i) {
+      ptx::mbar_init(&b_ksc[i], 2);
       ptx::mbar_init(&b_vsc[i], 2);
     }
     *abort_flag = 0;
@@ -156,27 +161,27 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
   };
   const bool k_row = a.k_mode == KVQ_SCALE_PER_ROW, v_row = a.v_mode == KVQ_SCALE_PER_ROW;
 
+  if (warp >= kProducer) ptx::regs_down<64>();
   if (warp == kProducer) {
     // ============================================================ producer
-    ptx::regs_down<96>();
     produce_lanes<Gm, true, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
   } else if (warp >= kDqK && warp < kDqV + 4) {
     // ==================================================== K and V dequant
-    // A stage's codes are converted 64 bytes of a row at a time; the wait for
-    // the MMA that frees the f16 tile comes before the first store.
-    ptx::regs_down<104>();
+    // A stage's codes are converted 64 of a row at a time; the wait for the MMA
+    // that frees the f16 tile comes before the first store.
+    ptx::regs_down<88>();
     const bool is_v = warp >= kDqV;
     const int q = warp - (is_v ? kDqV : kDqK);
     const int kk = 32 * (q & 1) + lane, hf = q >> 1;
-    constexpr int HB = Gm::DP / 2;                       // code bytes of a channel half
-    constexpr int PB = HB < 64 ? HB : 64;                // of a piece
-    constexpr int NC = PB / 16;                          // its 16-byte chunks
-    constexpr int CW = DT == KVQ_INT4 ? 16 : 8;          // f16 pairs per chunk
-    const uint32_t f16_base = is_v ? vf : kf;
+    constexpr int HB = Gm::DP / 2;                // code bytes of a channel half
+    constexpr int PB = DT == KVQ_INT4 ? 32 : 64;  // of a piece
+    constexpr int PC = PB / 16;                   // its 16-byte chunks
+    constexpr int CW = DT == KVQ_INT4 ? 16 : 8;   // f16 pairs of a chunk
     uint64_t* b_free = is_v ? b_pv : b_s;
     uint64_t* b_full = is_v ? b_vfull : b_kfull;
+    const uint32_t f16_base = is_v ? vf : kf;
     const uint32_t code_off = is_v ? (uint32_t)Gm::CODE_BYTES : 0u;
-    const bool scaled = is_v ? v_row : k_row;
+    const bool scaled = (is_v ? v_row : k_row) && hf == 0;
     uint32_t it = 0;
     RingPos rp;
     for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
@@ -185,15 +190,13 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       int F = -126;  // V-scale normaliser exponent of the piece
       const int first_key = a.vseq[b].lo;  // (a row below it may hold anything)
       for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it, rp.next(a.stages)) {
-        const uint32_t buf = it & 1;
         wait(&bar_full[rp.stage], rp.phase);
         const uint8_t* st = ring + (size_t)rp.stage * a.stage_stride;
-        if (scaled && hf == 0) {
-          // K: slot it & 3 was last read by the softmax of tile it - 4, done
-          // before PV of that tile was issued, which was before QK^T of it - 2;
-          // this warp waited for QK^T of it - 3 and waits here for it - 2.
-          // V: the softmax of it - 4 was done before PV of it - 3 completed,
-          // which this warp waited for on its previous tile.
+        if (scaled) {
+          // Slot it & 7 was last read by the softmax of it - 8 (its own) and of
+          // it - 7 (which reads the F before its own).  K: this warp has waited
+          // for QK^T of it - 3, issued after PV of it - 3 - NSB, whose softmax was
+          // done; V: for PV of it - 3.
           const float* scp = reinterpret_cast<const float*>(st + 2 * Gm::CODE_BYTES + (is_v ? KT * 4 : 0));
           float sc = scp[kk];
           if (is_v) {
@@ -202,21 +205,20 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
             if (seen(key0 + 32 + lane)) vm = fmaxf(vm, scp[32 + lane]);
             vm = ptx::redux_max(vm);
             if (vm > 0.0f) F = max(F, min(126, max(-126, dev::ceil_log2(vm))));
-            vsb[(it & 3) * KT + kk] = seen(key0 + kk) ? sc * dev::pow2i(-F) : 0.0f;
-            if (q == 0 && lane == 0) fexp[it & 3] = F;
+            vsb[(it & 7) * KT + kk] = seen(key0 + kk) ? sc * dev::pow2i(-F) : 0.0f;
+            if (q == 0 && lane == 0) fexp[it & 7] = F;
           } else {
-            if (it >= 2) wait(&b_free[buf], ((it - 2) >> 1) & 1);
-            ksb[(it & 3) * KT + kk] = sc;
+            ksb[(it & 7) * KT + kk] = sc;
           }
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(is_v ? &b_vsc[it & 3] : &b_ksc[it & 3]);
+          if (lane == 0) ptx::mbar_arrive(is_v ? &b_vsc[it & 7] : &b_ksc[it & 7]);
         }
-        const uint32_t tile = f16_base + buf * TILE;
+        const uint32_t buf = it & 1, tile = f16_base + buf * TILE;
 #pragma unroll
         for (int pc = 0; pc < HB / PB; ++pc) {
-          uint4 w[NC];
+          uint4 w[PC];
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
+          for (int j = 0; j < PC; ++j) {
             const uint32_t byte = (uint32_t)(hf * HB + pc * PB + 16 * j);
             w[j] = *reinterpret_cast<const uint4*>(st + code_off + (byte / Gm::SPAN) * (KT * Gm::SPAN) +
                                                    dev::swz<Gm::SPAN>((uint32_t)kk * Gm::SPAN + byte % Gm::SPAN));
@@ -225,16 +227,18 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bar_empty[rp.stage]);
           }
-          uint32_t v[NC * CW];
+          uint32_t v[PC * CW];
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            if (is_v) dev::tt_v_cols<DT>(w[j], v + CW * j);
-            else dev::k_cols<DT>(w[j], v + CW * j);
+          for (int j = 0; j < PC; ++j) dev::k_cols<DT>(w[j], v + CW * j);
+          if (DT == KVQ_FP8_E4M3 && is_v) {  // (a key no row sees may hold NaN codes: they lose against -448)
+#pragma unroll
+            for (int j = 0; j < PC * CW; ++j) v[j] = ptx::max_f16x2(v[j], 0xDF00DF00u);
           }
-          if (pc == 0 && it >= 2) wait(&b_free[buf], ((it - 2) >> 1) & 1);  // the MMA two tiles back has read this tile
+          // the MMA two tiles back has read this f16 tile
+          if (pc == 0 && it >= 2) wait(&b_free[(it - 2) % NSB], ((it - 2) / NSB) & 1);
 #pragma unroll
-          for (int c = 0; c < NC * CW / 4; ++c) {
-            const uint32_t addr = dev::tt_chunk<SLAB>(tile, kk, hf * (D / 16) + pc * (NC * CW / 4) + c);
+          for (int c = 0; c < PC * CW / 4; ++c) {
+            const uint32_t addr = dev::tt_chunk<SLAB>(tile, kk, hf * (D / 16) + pc * (PC * CW / 4) + c);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[4 * c]), "r"(v[4 * c + 1]),
                          "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
                          : "memory");
@@ -247,16 +251,15 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
     }
   } else if (warp == kMma) {
     // ================================================================ MMA
-    // QK^T(it + 1), PV(it), QK^T(it + 2), ...: executed in this order, so the
-    // S buffer of it + 2 is written after PV(it) has read its P there.
-    ptx::regs_down<96>();
+    // QK^T(it + LA), PV(it), QK^T(it + LA + 1), ...: executed in this order, and
+    // LA < NSB, so an S buffer is written again after PV has read its P there.
     constexpr uint32_t idesc_qk = ptx::idesc_f16_f32(128, KT);
     constexpr uint32_t idesc_pv = ptx::idesc_f16_f32(128, D) | (1u << 16);  // B MN-major
     const uint64_t kd = ptx::smem_desc_sw128(kf);
     const uint32_t k_lo = (uint32_t)kd, d_hi = (uint32_t)(kd >> 32);
     const uint32_t v_lo = (uint32_t)ptx::smem_desc_sw128_mn(vf, SLAB);
     auto issue_qk = [&](uint32_t j) {
-      const uint32_t buf = j & 1;
+      const uint32_t buf = j & 1, s_col = tmem + S_COL + KT * (j % NSB);
       wait(&b_kfull[buf], (j >> 1) & 1);
       __syncwarp();
       ptx::tc_fence_after();
@@ -264,25 +267,25 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         // the small part first: less is rounded
 #pragma unroll
         for (int sl = 0; sl < D / 64; ++sl)
-          ptx::mma_f16_ts_x4(tmem + S_COL + KT * buf, tmem + QL_COL + 32 * sl, 8, k_lo + ((buf * TILE + sl * SLAB) >> 4),
+          ptx::mma_f16_ts_x4(s_col, tmem + QL_COL + 32 * sl, 8, k_lo + ((buf * TILE + sl * SLAB) >> 4),
                              d_hi, idesc_qk, sl > 0 ? 1u : 0u);
       }
 #pragma unroll
       for (int sl = 0; sl < D / 64; ++sl)
-        ptx::mma_f16_ts_x4(tmem + S_COL + KT * buf, tmem + Q_COL + 32 * sl, 8, k_lo + ((buf * TILE + sl * SLAB) >> 4),
+        ptx::mma_f16_ts_x4(s_col, tmem + Q_COL + 32 * sl, 8, k_lo + ((buf * TILE + sl * SLAB) >> 4),
                            d_hi, idesc_qk, sl > 0 || (SPLIT && !STACK) ? 1u : 0u);
-      ptx::mma_commit(&b_s[buf]);
+      ptx::mma_commit(&b_s[j % NSB]);
     };
     // a piece's first PV overwrites O
     auto issue_pv = [&](uint32_t j, bool first) {
       const uint32_t buf = j & 1;
       wait(&b_vfull[buf], (j >> 1) & 1);
-      wait(&b_p[buf], (j >> 1) & 1);
+      wait(&b_p[j % NSB], (j / NSB) & 1);
       __syncwarp();
       ptx::tc_fence_after();
-      ptx::mma_f16_ts_x4_step(tmem + O_COL, tmem + S_COL + KT * buf, 8, v_lo + buf * (TILE >> 4), (16 * 128) >> 4, d_hi,
+      ptx::mma_f16_ts_x4_step(tmem + O_COL, tmem + S_COL + KT * (j % NSB), 8, v_lo + buf * (TILE >> 4), (16 * 128) >> 4, d_hi,
                               idesc_pv, first ? 0u : 1u);
-      ptx::mma_commit(&b_pv[buf]);
+      ptx::mma_commit(&b_pv[j % NSB]);
     };
     uint32_t it = 0;
     int pc = 0;
@@ -290,30 +293,35 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       int b, h, k0, k1, L, u;
       sp.piece(a, gt, b, h, k0, k1, L, u, next);
       wait(b_q, pc & 1);
-      issue_qk(it);
-      for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it) {
-        if (Order::more(key0 + Order::step, k0, k1)) issue_qk(it + 1);
-        issue_pv(it, key0 == Order::first(k0, k1));
+      const uint32_t n = (uint32_t)((k1 - k0 + KT - 1) / KT);
+      for (uint32_t i = 0; i < n && i < LA; ++i) issue_qk(it + i);
+      for (uint32_t i = 0; i < n; ++i, ++it) {
+        if (i + LA < n) issue_qk(it + LA);
+        issue_pv(it, i == 0);
       }
     }
     // every MMA has completed before TMEM can be released
-    if (it > 0 && !ptx::mbar_wait_bounded_inl(&b_pv[(it - 1) & 1], ((it - 1) >> 1) & 1) && lane == 0)
+    if (it > 0 && !ptx::mbar_wait_bounded_inl(&b_pv[(it - 1) % NSB], ((it - 1) / NSB) & 1) && lane == 0)
       atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
     __syncwarp();
   } else if (warp < kDqK) {
     // ============================================================ softmax
-    ptx::regs_up<208>();
-    const int q = warp;
-    // query row = TMEM lane (STACK: lanes 64..127 hold the second parts of rows 0..63)
-    const int r = STACK ? (32 * q + lane) & 63 : 32 * q + lane;
+    ptx::regs_up<120>();
+    const int q = warp & 3, grp = warp >> 2;  // TMEM lane quarter; even or odd tiles
+    // query row = TMEM lane (STACK: lanes 64..127 hold the second parts of rows 0..63,
+    // FOLD: rows 0..63 again)
+    const int r = STACK || FOLD ? (32 * q + lane) & 63 : 32 * q + lane;
     const bool second = STACK && q >= 2;
+    const int part0 = CH * (FOLD ? q >> 1 : grp);  // first key of this thread in a tile
     const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16);
     const int G = a.group, Hq = a.num_q_heads, rows = a.rows;
     const uint32_t exch = ptx::smem_u32(base + lay.exch);
-    // S of the second parts, [2][64 rows][KT keys] f16, 16-byte chunks XOR (row & 7)
-    auto exch_at = [&](uint32_t buf, int chunk) -> uint32_t {
-      return exch + buf * (64 * KT * 2) + (uint32_t)r * (KT * 2) + (((uint32_t)chunk ^ ((uint32_t)r & 7u)) << 4);
+    // S of the second parts, [2 tiles][2 groups][64 rows][CH keys] f16, 16-byte chunks XOR (row >> 1 & 3)
+    auto exch_at = [&](uint32_t it, int chunk) -> uint32_t {
+      return exch + ((it & 1) * 2 + grp) * (64 * CH * 2) + (uint32_t)r * (CH * 2) + (((uint32_t)chunk ^ ((uint32_t)r >> 1 & 3u)) << 4);
     };
+    const int bar_mine = 1 + q + 4 * grp, bar_other = 1 + q + 4 * (grp ^ 1);  // "the other group's reference is there"
+    const int bar_exch = 9 + (q & 1) + 2 * grp;
     const int t_row = dev::div_small(r, __frcp_rn((float)G));
     uint32_t it = 0;
     int pc = 0;
@@ -326,11 +334,13 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       const size_t tok = (size_t)vs.tok0 + t_row;
       const int hq = h * G + (r - t_row * G);
       dev::RowRule ru{};
+      bool blind = !valid;
       float alpha = 1.0f;
       // ---- Q of this piece (every QK^T of the previous one has completed: this
       // thread waited for its last S): the per-channel K scale folded in under a
       // power-of-two normaliser, the row normalised by the power of two at or
-      // above its maximum, f16 pairs in the K order of the K tile.
+      // above its maximum, f16 pairs in the K order of the K
+      // tile (each of the row's two threads writes half of the channels).
       if (!idle) {
         const bool kc = a.k_mode == KVQ_SCALE_PER_CHANNEL;
         const uint16_t* src = a.q + (tok * Hq + hq) * D;
@@ -361,7 +371,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
             qv[4] *= s1.x * sk; qv[5] *= s1.y * sk; qv[6] *= s1.z * sk; qv[7] *= s1.w * sk;
           }
         };
-        constexpr int NCH8 = D / 8, BAT = 16;
+        constexpr int NCH8 = D / 8, BAT = 8;
         float qm = 0.0f;
 #pragma unroll 1
         for (int c0 = 0; c0 < NCH8; c0 += BAT) {
@@ -379,7 +389,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         const int eq = qm > 0.0f ? min(126, max(-126, dev::ceil_log2(qm))) : 0;
         const float sq = dev::pow2i(-eq);
 #pragma unroll 1
-        for (int c32 = 0; c32 < D / 32; ++c32) {
+        for (int c32 = grp * (D / 64); c32 < (grp + 1) * (D / 64); ++c32) {
           uint4 raw[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) raw[i] = valid ? ptx::ldg_nc_v4(src + 8 * (4 * c32 + i)) : make_uint4(0, 0, 0, 0);
@@ -414,11 +424,16 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         // that alpha * -inf stays -inf)
         const int e = ek + eq, e1 = e / 2;
         alpha = valid ? fmaxf(fminf(base_f * dev::pow2i(e1) * dev::pow2i(e - e1), 3.4028234e38f), 1.17549435e-38f) : 1.0f;
-        // (a row with no node sees the piece's keys: finite scores that feed
-        // only its own unwritten output)
+        // Rows that see none of the piece's keys (of no node, or all of them
+        // outside a window) are scored like any other and count for nothing
+        // at the end: hiding every key of every tile would take longer.
         ru.end = L;
         ru.bits = -1;
-        if (valid) ru = dev::row_rule<true>(a, tok, vs.pos0 + t_row, hq, L);
+        if (valid) {
+          const dev::RowRule rr = dev::row_rule<true>(a, tok, vs.pos0 + t_row, hq, L);
+          blind = rr.begin == 0x7FFFFFFF || (max(rr.begin, k0) >= min(rr.end, k1) && k1 <= rr.end);
+          if (!blind) ru = rr;
+        }
         ptx::tc_fence_before();
         __syncwarp();
       }
@@ -427,84 +442,92 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       // tanh(x) = x P(x^2) for |x| <= kCapNear, P the minimax polynomial of
       // degree 3 to tanh(sqrt t) / sqrt t there (1.5e-7 relative); x = alpha S
       constexpr float kCapNear = 0.35f;
-      const float cap2 = CAP ? a.softcap * kLog2e : 0.0f, al2 = alpha * alpha;
-      const float c0f = alpha * cap2, c1f = -0.33332422f * al2 * c0f, c2f = 0.13295799f * al2 * al2 * c0f,
-                  c3f = -0.04895823f * al2 * al2 * al2 * c0f;
-      const float cap_near =
-          CAP && alpha > 6e-5f && alpha < 1.6e4f && cap2 > 1e-6f && cap2 < 1e6f ? kCapNear / alpha : -1.0f;
+      const float cap2 = CAP ? a.softcap * kLog2e : 0.0f;
+      const float c0f = cap2, c1f = -0.33332422f * cap2, c2f = 0.13295799f * cap2, c3f = -0.04895823f * cap2;
       const ptx::f32x2 aa = ptx::pack_x2(alpha, alpha);
 
-      float mu = -INFINITY;         // reference maximum of this row (log2 units)
-      ptx::f32x2 l2 = ptx::pack_x2(0.0f, 0.0f);  // its weight sum, in two halves (even and odd keys)
-      int F = -126;                 // V-scale normaliser exponent
+      float mu = -INFINITY;                      // this row's reference (log2 units) as of this group's last tile
+      ptx::f32x2 l2 = ptx::pack_x2(0.0f, 0.0f), l3 = l2;  // its weight sum there, in four parts
       for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it) {
-        const bool first = key0 == Order::first(k0, k1);
-        const uint32_t buf = it & 1;
-        const uint32_t s_col = t_lane + S_COL + KT * buf;
-        wait(&b_s[buf], (it >> 1) & 1);
+        if (FOLD && (int)(it & 1) != grp) continue;
+        const bool first = key0 == Order::first(k0, k1), last = !Order::more(key0 + Order::step, k0, k1);
+        const uint32_t s_col = t_lane + S_COL + KT * (it % NSB);
+        wait(&b_s[it % NSB], (it / NSB) & 1);
         if (idle) {
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&b_p[buf]);
+          if (lane == 0) ptx::mbar_arrive(&b_p[it % NSB]);
           continue;
         }
         ptx::tc_fence_after();
         if constexpr (STACK) {
-          // one barrier a tile between a row's two warps (q & 1 and 2 + (q & 1)):
-          // a buffer is written again two tiles on, after the other side has
-          // passed the barrier of the tile between
+          // (a place is written again two tiles on, past the barrier of the tile between)
           if (second) {
-            float y[KT];
-            dev::tmem_ld_cols<KT>(s_col, y);
+            float y[CH];
+            dev::tmem_ld_cols<CH>(s_col + part0, y);
 #pragma unroll
-            for (int c8 = 0; c8 < KT / 8; ++c8)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(exch_at(buf, c8)),
+            for (int c8 = 0; c8 < CH / 8; ++c8)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(exch_at(it, c8)),
                            "r"(dev::pack_h2(y[8 * c8], y[8 * c8 + 1])), "r"(dev::pack_h2(y[8 * c8 + 2], y[8 * c8 + 3])),
                            "r"(dev::pack_h2(y[8 * c8 + 4], y[8 * c8 + 5])), "r"(dev::pack_h2(y[8 * c8 + 6], y[8 * c8 + 7]))
                            : "memory");
-            ptx::named_bar_sync(1 + (q & 1), 64);
+            __syncwarp();
+            ptx::named_bar_sync(bar_exch, 64);
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&b_p[buf]);
+            if (lane == 0) ptx::mbar_arrive(&b_p[it % NSB]);
             continue;
           }
-          ptx::named_bar_sync(1 + (q & 1), 64);
         }
-        if (k_row) wait(&b_ksc[it & 3], (it >> 2) & 1);
-        const float* ksc = ksb + (it & 3) * KT;
-        const float* vsc = vsb + (it & 3) * KT;
+        if (k_row) wait(&b_ksc[it & 7], (it >> 3) & 1);
+        const float* ksc = ksb + (it & 7) * KT;
+        const float* vsc = vsb + (it & 7) * KT;
         const bool full = key0 >= ru.begin && key0 + KT <= ru.end;
         uint32_t bits[2] = {0u, 0u};  // visible keys of a tile that is not whole
         if (!full) {
-          dev::tree_sees_64(a, ru, key0, bits);
+          if (key0 + KT > ru.end) dev::tree_sees_64(a, ru, key0, bits);
           const int lo = min(KT, max(0, ru.begin - key0)), hi = min(KT, max(0, ru.end - key0));
           if (lo < hi) {
             const uint64_t in = (hi == 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
             bits[0] |= (uint32_t)in;
             bits[1] |= (uint32_t)(in >> 32);
           }
+          if (part0) bits[0] = bits[1];
         }
-        // Scores (with a per-row K scale in): 64 keys in registers; under a cap,
-        // whose unrolled code would not stay in the instruction cache, 32 at a
-        // time, twice.
-        constexpr int CH = CAP ? 32 : KT;
+        // scores, with a per-row K scale (and 1 / softcap) in
         float y[CH];
-        auto load_s = [&](int c0) {
+        {
           uint32_t v[CH];
+          ptx::tmem_ld32(s_col + part0, v);
+          auto scores = [&]() {
+            ptx::tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < CH; c += 32) ptx::tmem_ld32(s_col + c0 + c, v + c);
-          ptx::tmem_wait_ld();
+            for (int k = 0; k < CH; ++k) {
+              asm volatile("" : "+r"(v[k]));
+              y[k] = __uint_as_float(v[k]);
+            }
+          };
+          if (!STACK && k_row) {
+            float4 s4[CH / 4];  // (on their way before the scores are there)
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            asm volatile("" : "+r"(v[i]));
-            y[i] = __uint_as_float(v[i]);
+            for (int k = 0; k < CH / 4; ++k) s4[k] = *reinterpret_cast<const float4*>(ksc + part0 + 4 * k);
+            scores();
+#pragma unroll
+            for (int k = 0; k < CH; k += 4) {
+              ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], s4[k / 4].x, s4[k / 4].y);
+              ptx::mul_x2(y[k + 2], y[k + 3], y[k + 2], y[k + 3], s4[k / 4].z, s4[k / 4].w);
+            }
+          } else {
+            scores();
           }
           if constexpr (STACK) {
+            __syncwarp();
+            ptx::named_bar_sync(bar_exch, 64);
 #pragma unroll
             for (int c8 = 0; c8 < CH / 8; ++c8) {
               uint32_t w[4];
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(exch_at(buf, c0 / 8 + c8))
+                           : "r"(exch_at(it, c8))
                            : "memory");
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -514,26 +537,19 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
               }
             }
           }
-          if (k_row) {
+        }
+        if constexpr (CAP) {
 #pragma unroll
-            for (int k = 0; k < CH; k += 4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(ksc + c0 + k);
-              ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], s4.x, s4.y);
-              ptx::mul_x2(y[k + 2], y[k + 3], y[k + 2], y[k + 3], s4.z, s4.w);
-            }
-          }
-        };
-        auto hide = [&](int c0) {
+          for (int k = 0; k < CH; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
+        }
+        if (!full) {  // keys that this row does not see
 #pragma unroll
           for (int k = 0; k < CH; ++k)
-            if (!((bits[CAP ? c0 / 32 : k / 32] >> (k % 32)) & 1u)) y[k] = -INFINITY;
-        };
-        float m = -INFINITY, least = INFINITY;
-#pragma unroll 1
-        for (int c0 = 0; c0 < KT; c0 += CH) {
-          load_s(c0);
-          if (!full) hide(c0);
-          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {least, INFINITY, INFINITY, INFINITY};
+            if (!((bits[0] >> k) & 1u)) y[k] = -INFINITY;
+        }
+        float m, least = INFINITY;
+        {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
 #pragma unroll
           for (int k = 0; k < CH; k += 2) {
             mx[k / 2 % 4] = ptx::max3(mx[k / 2 % 4], y[k], y[k + 1]);
@@ -542,49 +558,71 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           m = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
           if constexpr (CAP) least = fminf(ptx::min3(mn[0], mn[1], mn[2]), mn[3]);
         }
-        const bool near = CAP && fmaxf(fabsf(m), fabsf(least)) <= cap_near;
+        // (rows that count for nothing may hold anything)
+        const bool near = CAP && __all_sync(0xffffffffu, blind || fmaxf(fabsf(m), fabsf(least)) <= kCapNear);
+        if constexpr (!FOLD) {
+          // the row's other half (a place is written again two tiles on, past the
+          // barrier of the tile between); both have S in registers before either
+          // writes its part of P over it
+          float* place = part + 256 * (it & 1) + 32 * q + lane;
+          place[128 * grp] = m;
+          ptx::tc_fence_before();
+          __syncwarp();
+          ptx::named_bar_sync(1 + q, 64);
+          ptx::tc_fence_after();
+          m = fmaxf(m, place[128 * (grp ^ 1)]);
+        }
         if constexpr (CAP) {
-          if (near) {
+          if (fabsf(m) <= kCapNear) {
             const float t = m * m;
             m *= fmaf(fmaf(fmaf(c3f, t, c2f), t, c1f), t, c0f);
           } else if (m != -INFINITY) {
-            float x[2] = {m * alpha, 0.0f};
+            float x[2] = {m, 0.0f};
             dev::cap_scores<2>(x, cap2);
             m = x[0];
           }
         } else {
           m *= alpha;
         }
-        float fs = 1.0f;  // growth of the V-scale normaliser
+        float fs = 1.0f;  // the V-scale normaliser's growth since the last tile
         if (v_row) {
-          wait(&b_vsc[it & 3], (it >> 2) & 1);
-          const int fn = fexp[it & 3];
-          if (fn > F) {
-            fs = (F - fn < -126) ? 0.0f : dev::pow2i(F - fn);
-            F = fn;
+          wait(&b_vsc[it & 7], (it >> 3) & 1);
+          if (!first) {
+            const int f0 = fexp[(it - 1) & 7], f1 = fexp[it & 7];
+            if (f1 > f0) fs = (f0 - f1 < -126) ? 0.0f : dev::pow2i(f0 - f1);
           }
         }
-        // move the reference only when the tile's maximum exceeds it by more
-        // than 8 (P <= 2^8 in f16); a row with no key yet holds zeros in O
-        float corr = 1.0f;
-        bool resc = false;
-        if (m > mu + 8.0f) {
-          if (mu != -INFINITY) {
-            corr = ptx::fast_exp2(mu - m);
-            resc = !first;
-          }
-          mu = m;
+        // The reference (FOLD: that the other group left at the tile before) moves
+        // only when this tile's maximum exceeds it by more than 8 (P <= 2^8 in
+        // f16); a row with no key yet holds zeros in O.
+        float was = mu;
+        if (FOLD && !first) {
+          __syncwarp();
+          ptx::named_bar_sync(bar_mine, 64);
+          was = ref[32 * q + lane];
         }
-        l2 = ptx::mul_x2(l2, ptx::pack_x2(corr, corr));
-        resc = resc || (fs != 1.0f && !first);
+        const float now = m > was + 8.0f ? m : was;
+        if (FOLD && !last) {
+          ref[32 * q + lane] = now;
+          __syncwarp();
+          ptx::named_bar_arrive(bar_other, 64);
+        }
+        const float corr = now != was && was != -INFINITY ? ptx::fast_exp2(was - now) : 1.0f;
+        if (now != mu) {
+          const float c = mu != -INFINITY ? ptx::fast_exp2(mu - now) : 1.0f;
+          l2 = ptx::mul_x2(l2, ptx::pack_x2(c, c));
+          l3 = ptx::mul_x2(l3, ptx::pack_x2(c, c));
+          mu = now;
+        }
+        const bool resc = !first && (corr != 1.0f || fs != 1.0f);
         if (__any_sync(0xffffffffu, resc)) {
-          // bring this warp's rows of O to the new reference and normaliser
-          // (after the previous PV has landed)
-          wait(&b_pv[(it - 1) & 1], ((it - 1) >> 1) & 1);
+          // bring O (a row's two threads half of the channels each, FOLD: all) to the
+          // new reference and normaliser, after the previous PV has landed
+          wait(&b_pv[(it - 1) % NSB], ((it - 1) / NSB) & 1);
           ptx::tc_fence_after();
           const float f = resc ? corr * fs : 1.0f;
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
+          for (int c0 = FOLD ? 0 : grp * (D / 2); c0 < (FOLD ? D : (grp + 1) * (D / 2)); c0 += 16) {
             float o[16];
             dev::tmem_ld_cols<16>(t_lane + O_COL + c0, o);
 #pragma unroll
@@ -596,55 +634,66 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         // weights
         const float nmu = mu == -INFINITY ? 0.0f : -mu;
         const ptx::f32x2 nm = ptx::pack_x2(nmu, nmu);
-        auto weigh = [&](int c0, auto&& score) {
+        if constexpr (FOLD) {
+          const uint32_t none[16] = {};
+          __syncwarp();
+          ptx::tmem_st16(s_col + (CH - part0) / 2, none);
+        }
+        auto weigh_as = [&](auto&& score, auto rows) {  // rows: per-row V scales
+          constexpr bool VR = decltype(rows)::value;
           uint32_t p[CH / 2];
 #pragma unroll
-          for (int k = 0; k < CH; k += 2) {
-            float z0, z1;
-            ptx::unpack_x2(score(ptx::pack_x2(y[k], y[k + 1])), z0, z1);
-            const ptx::f32x2 e = ptx::pack_x2(ptx::fast_exp2(z0), ptx::fast_exp2(z1));
-            l2 = ptx::add_x2(l2, e);
-            float e0, e1;
-            ptx::unpack_x2(e, e0, e1);
-            if (v_row) {
-              const float2 s2 = *reinterpret_cast<const float2*>(vsc + c0 + k);
-              ptx::mul_x2(e0, e1, e0, e1, s2.x, s2.y);
+          for (int k = 0; k < CH; k += 4) {
+            float4 s4;
+            if constexpr (VR) s4 = *reinterpret_cast<const float4*>(vsc + part0 + k);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float z0, z1;
+              ptx::unpack_x2(score(ptx::pack_x2(y[k + 2 * j], y[k + 2 * j + 1])), z0, z1);
+              const ptx::f32x2 e = ptx::pack_x2(ptx::fast_exp2(z0), ptx::fast_exp2(z1));
+              if (j) l3 = ptx::add_x2(l3, e);
+              else l2 = ptx::add_x2(l2, e);
+              float e0, e1;
+              ptx::unpack_x2(e, e0, e1);
+              if constexpr (VR) ptx::mul_x2(e0, e1, e0, e1, j ? s4.z : s4.x, j ? s4.w : s4.y);
+              p[k / 2 + j] = dev::pack_h2(e0, e1);
             }
-            p[k / 2] = dev::pack_h2(e0, e1);
           }
-          // (the columns of S that P takes have been read: P is half as wide)
           __syncwarp();
-          if constexpr (CH == 32) ptx::tmem_st16(s_col + c0 / 2, *reinterpret_cast<uint32_t(*)[16]>(p));
-          else ptx::tmem_st32(s_col, p);
+          ptx::tmem_st16(s_col + part0 / 2, p);
+        };
+        // (one branch here: one at each key would keep the keys apart)
+        auto weigh = [&](auto&& score) {
+          if (v_row) weigh_as(score, std::true_type{});
+          else weigh_as(score, std::false_type{});
         };
         if constexpr (!CAP) {
-          weigh(0, [&](ptx::f32x2 x) { return ptx::fma_x2(x, aa, nm); });
-        } else {
+          weigh([&](ptx::f32x2 x) { return ptx::fma_x2(x, aa, nm); });
+        } else if (near) {
+          // x P(x^2) - mu (of a tile with hidden keys, of score -inf, not all rows are near)
           const ptx::f32x2 cc0 = ptx::pack_x2(c0f, c0f), cc1 = ptx::pack_x2(c1f, c1f), cc2 = ptx::pack_x2(c2f, c2f),
                            cc3 = ptx::pack_x2(c3f, c3f);
-#pragma unroll 1
-          for (int c0 = 0; c0 < KT; c0 += CH) {
-            load_s(c0);
-            if (!near) {
+          weigh([&](ptx::f32x2 x) {
+            const ptx::f32x2 t = ptx::mul_x2(x, x);
+            return ptx::fma_x2(x, ptx::fma_x2(ptx::fma_x2(ptx::fma_x2(t, cc3, cc2), t, cc1), t, cc0), nm);
+          });
+        } else {
 #pragma unroll
-              for (int k = 0; k < CH; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
-              dev::cap_scores<CH>(y, cap2);
-              if (!full) hide(c0);
-            }
-            // near: y P(y^2) - mu, the factors of alpha in P's coefficients (a
-            // row with hidden keys, of score -inf, is not near); else y - mu
-            const bool nr = near;
-            weigh(c0, [&](ptx::f32x2 x) {
-              if (!nr) return ptx::add_x2(x, nm);
-              const ptx::f32x2 t = ptx::mul_x2(x, x);
-              return ptx::fma_x2(x, ptx::fma_x2(ptx::fma_x2(ptx::fma_x2(t, cc3, cc2), t, cc1), t, cc0), nm);
-            });
+          for (int c = 0; c < CH; c += 16) {
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = y[c + k];
+            dev::cap_scores<16>(x, cap2);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (y[c + k] != -INFINITY) y[c + k] = x[k];  // (a hidden key stays -inf)
           }
+          weigh([&](ptx::f32x2 x) { return ptx::add_x2(x, nm); });
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&b_p[buf]);
+        if (lane == 0) ptx::mbar_arrive(&b_p[it % NSB]);
       }
 
       // ---- epilogue: O out of TMEM, normalised.  The workspace and the output
@@ -652,19 +701,87 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       // the first tile's codes).  A unit of one piece (`whole`) is finished here:
       // head sink, static V scale and bf16, as in the combine; otherwise the
       // partial with its base-2 log-sum-exp.
-      if (it > 1) wait(&b_pv[it & 1], ((it - 2) >> 1) & 1);
-      wait(&b_pv[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      if (it > 1) wait(&b_pv[(it - 2) % NSB], ((it - 2) / NSB) & 1);
+      wait(&b_pv[(it - 1) % NSB], ((it - 1) / NSB) & 1);
       if (idle || second) continue;
       ptx::tc_fence_after();
-      float l, lb;
-      ptx::unpack_x2(l2, l, lb);
-      l += lb;
-      float inv = l > 0.0f ? (v_row ? dev::pow2i(F) : 1.0f) / l : 0.0f;
+      // both groups' sums under the last reference
+      float l, mu_o;
+      {
+        float lb;
+        ptx::unpack_x2(ptx::add_x2(l2, l3), l, lb);
+        l += lb;
+        part[256 * grp + 32 * q + lane] = mu;
+        part[256 * grp + 128 + 32 * q + lane] = l;
+        __syncwarp();
+        ptx::named_bar_sync(1 + q, 64);
+        mu_o = part[256 * (grp ^ 1) + 32 * q + lane];
+        lb = part[256 * (grp ^ 1) + 128 + 32 * q + lane];
+        const float top = fmaxf(mu, mu_o);
+        if (mu != top) l *= ptx::fast_exp2(mu - top);
+        if (mu_o != top) lb *= ptx::fast_exp2(mu_o - top);
+        mu = top;
+        l = blind ? 0.0f : l + lb;
+      }
+      // FOLD: both copies of a row under one reference; the second sends its O,
+      // 16 columns at a time (a place is written again two steps on, past the
+      // barrier of the step between)
+      float copy = 1.0f;
+      float* fold = reinterpret_cast<float*>(base + lay.exch);
+      float4* fold_o = reinterpret_cast<float4*>(fold + 512) + (2 * grp + (q & 1)) * 256;  // [2 steps][4][32 rows]
+      if constexpr (FOLD) {
+        float* f = fold + 256 * grp + 32 * q + lane;
+        f[0] = mu;
+        f[128] = l;
+        __syncwarp();
+        ptx::named_bar_sync(bar_exch, 64);
+        f = fold + 256 * grp + 32 * (q ^ 2) + lane;
+        const float top = fmaxf(mu, f[0]);
+        if (mu != top) copy = ptx::fast_exp2(mu - top);
+        l = l * copy + f[128] * (f[0] != top ? ptx::fast_exp2(f[0] - top) : 1.0f);
+        mu = top;
+        if (q >= 2) {
+          if (!(l > 0.0f)) copy = 0.0f;
+#pragma unroll 1
+          for (int c0 = grp * (D / 2); c0 < (grp + 1) * (D / 2); c0 += 16) {
+            float o[16];
+            dev::tmem_ld_cols<16>(t_lane + O_COL + c0, o);
+            float4* to = fold_o + (c0 / 16 & 1) * 128 + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              to[32 * j] = make_float4(o[4 * j] * copy, o[4 * j + 1] * copy, o[4 * j + 2] * copy, o[4 * j + 3] * copy);
+            __syncwarp();
+            ptx::named_bar_sync(bar_exch, 64);
+          }
+          ptx::tc_fence_before();
+          continue;
+        }
+      }
+      const int F = v_row ? fexp[(it - 1) & 7] : 0;
+      const bool some = l > 0.0f;
+      float inv = some ? (v_row ? dev::pow2i(F) : 1.0f) / l : 0.0f;
       const bool whole = k0 == (vs.lo & ~(KT - 1)) && k1 == L;
       // channels c0 .. c0 + 15 of this thread's row, in channel order
       auto channels = [&](int c0, float (&x)[16]) {
         float o[16];
         dev::tmem_ld_cols<16>(t_lane + O_COL + c0, o);
+        if constexpr (FOLD) {
+          __syncwarp();
+          ptx::named_bar_sync(bar_exch, 64);
+          const float4* from = fold_o + (c0 / 16 & 1) * 128 + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 x4 = from[32 * j];
+            o[4 * j] = o[4 * j] * copy + x4.x;
+            o[4 * j + 1] = o[4 * j + 1] * copy + x4.y;
+            o[4 * j + 2] = o[4 * j + 2] * copy + x4.z;
+            o[4 * j + 3] = o[4 * j + 3] * copy + x4.w;
+          }
+        }
+        if (!some) {  // (O may hold anything)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+        }
         if constexpr (DT == KVQ_INT4) {
           // N index 8 i + 2 m + e holds channel 8 i + m + 4 e, odd m times 16
 #pragma unroll
@@ -683,15 +800,15 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       unsigned long long dst;
       if (whole) {
         float lse = -INFINITY;
-        if (l > 0.0f) {
+        if (some) {
           lse = (mu + ptx::fast_log2(l)) * 0.69314718055994530942f;
           if (a.head_sink && valid) inv /= 1.0f + expf(a.head_sink[hq] - lse);
         }
         if (a.v_mode == KVQ_SCALE_PER_TENSOR) inv *= a.v_scale[0];
-        if (valid && a.lse_out) a.lse_out[tok * Hq + hq] = lse;
+        if (valid && grp == 0 && a.lse_out) a.lse_out[tok * Hq + hq] = lse;
         dst = reinterpret_cast<unsigned long long>(a.out + (tok * Hq + hq) * a.out_dim);
       } else {
-        if (valid) a.part_lse[(size_t)u * rows + r] = l > 0.0f ? mu + ptx::fast_log2(l) : -INFINITY;
+        if (valid && grp == 0) a.part_lse[(size_t)u * rows + r] = some ? mu + ptx::fast_log2(l) : -INFINITY;
         dst = reinterpret_cast<unsigned long long>(a.part_o + ((size_t)u * rows + r) * D);
       }
       // quads of lanes store 64 bytes of a row at a time
@@ -701,7 +818,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, dst, (lane & ~3) | i);
       const float* vs_ch = whole && a.v_mode == KVQ_SCALE_PER_CHANNEL ? a.v_scale + (size_t)h * D : nullptr;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += whole ? 32 : 16) {
+      for (int c0 = grp * (D / 2); c0 < (grp + 1) * (D / 2); c0 += whole ? 32 : 16) {
         uint32_t w[4][4];
         if (whole) {
 #pragma unroll
@@ -732,8 +849,6 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       }
       ptx::tc_fence_before();
     }
-  } else {
-    ptx::regs_down<96>();
   }
 
   // every role ends here; TMEM is released once no warp can touch it
@@ -745,28 +860,33 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
   }
 }
 
-template <int DT, int D, bool SPLIT, bool CAP>
+template <int DT, int D, bool SPLIT, bool CAP, bool FOLD>
 cudaError_t launch_tree_tile(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid, size_t smem,
                              cudaStream_t stream) {
   static std::atomic<int> smem_set[64];
-  const void* kernel = reinterpret_cast<const void*>(tree_tile_kernel<DT, D, SPLIT, CAP>);
+  const void* kernel = reinterpret_cast<const void*>(tree_tile_kernel<DT, D, SPLIT, CAP, FOLD>);
   if (cudaError_t e = raise_smem_limit(kernel, smem_set, smem)) return e;
-  return launch_pdl(tree_tile_kernel<DT, D, SPLIT, CAP>, grid, kTtWarps * 32, smem, stream, tk, tv, a);
+  return launch_pdl(tree_tile_kernel<DT, D, SPLIT, CAP, FOLD>, grid, kTtWarps * 32, smem, stream, tk, tv, a);
 }
 
-template <int DT>
-cudaError_t dispatch_tree_tile(int head_dim, bool split, const CUtensorMap& tk, const CUtensorMap& tv,
+template <int DT, int D, bool CAP>
+cudaError_t dispatch_tree_tile(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
                                const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream) {
-  const bool cap = a.softcap > 0.0f;
-  if (head_dim == 128) {
-    if (split) return cap ? launch_tree_tile<DT, 128, true, true>(tk, tv, a, grid, smem, stream) : launch_tree_tile<DT, 128, true, false>(tk, tv, a, grid, smem, stream);
-    return cap ? launch_tree_tile<DT, 128, false, true>(tk, tv, a, grid, smem, stream) : launch_tree_tile<DT, 128, false, false>(tk, tv, a, grid, smem, stream);
+  if constexpr (D == 256) {
+    if (split) return launch_tree_tile<DT, D, true, CAP, false>(tk, tv, a, grid, smem, stream);
+  } else {
+    if (split && fold) return launch_tree_tile<DT, D, true, CAP, true>(tk, tv, a, grid, smem, stream);
+    if (split) return launch_tree_tile<DT, D, true, CAP, false>(tk, tv, a, grid, smem, stream);
   }
-  if (head_dim == 256) {
-    if (split) return cap ? launch_tree_tile<DT, 256, true, true>(tk, tv, a, grid, smem, stream) : launch_tree_tile<DT, 256, true, false>(tk, tv, a, grid, smem, stream);
-    return cap ? launch_tree_tile<DT, 256, false, true>(tk, tv, a, grid, smem, stream) : launch_tree_tile<DT, 256, false, false>(tk, tv, a, grid, smem, stream);
-  }
-  return cudaErrorInvalidValue;
+  if (fold) return launch_tree_tile<DT, D, false, CAP, true>(tk, tv, a, grid, smem, stream);
+  return launch_tree_tile<DT, D, false, CAP, false>(tk, tv, a, grid, smem, stream);
+}
+
+template <int DT, int D>
+cudaError_t dispatch_tree_tile(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream) {
+  return a.softcap > 0.0f ? dispatch_tree_tile<DT, D, true>(split, fold, tk, tv, a, grid, smem, stream)
+                          : dispatch_tree_tile<DT, D, false>(split, fold, tk, tv, a, grid, smem, stream);
 }
 
 }  // namespace kvq

@@ -1,0 +1,13 @@
+// tree_tile_fp8_d256.cu -- the tcgen05 draft-tree kernel's fp8 instances for
+// head_dim 256: a one-part or a two-part Q operand, rows once or folded, with
+// and without a softcap.
+#include "tree_tile.cuh"
+
+namespace kvq {
+
+cudaError_t launch_tree_tile_fp8_d256(bool split, bool fold, const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const DecodeArgs& a, int grid, size_t smem, cudaStream_t stream) {
+  return dispatch_tree_tile<KVQ_FP8_E4M3, 256>(split, fold, tk, tv, a, grid, smem, stream);
+}
+
+}  // namespace kvq
