@@ -95,6 +95,15 @@ __device__ __forceinline__ uint32_t f8pair(uint32_t w, uint32_t sel) {
   return (y & 0x80008000u) | ((y >> 1) & 0x3F803F80u);
 }
 
+// Draft trees: a node's row that holds infinities or NaN (a per-row scale that
+// is not finite) must not reach the nodes that do not see it.  It takes no part
+// in the V-scale normaliser, which all rows share, and a weight of 0 stays 0.
+__device__ __forceinline__ float finite_or_0(float s) { return s < INFINITY ? s : 0.0f; }
+template <bool TREE>
+__device__ __forceinline__ float scaled(float p, float s) {
+  return TREE && p == 0.0f ? 0.0f : p * s;
+}
+
 // e4m3 pair (bytes selected by sel into a 16-bit word) -> exact f16x2 by the
 // hardware conversion.  kClamp: then max with -448 so that a NaN code (a
 // stale byte past the sequence end, under a masked key) becomes finite.
@@ -769,7 +778,7 @@ __global__ void __launch_bounds__(288, MINB)
           }
         }
         if (v_row) {
-          float vm = fmaxf(vpa, vpb);
+          float vm = TREE ? fmaxf(dev::finite_or_0(vpa), dev::finite_or_0(vpb)) : fmaxf(vpa, vpb);
 #pragma unroll
           for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
           // (unmasked: the same in both halves; masked: each half has its rows')
@@ -815,8 +824,8 @@ __global__ void __launch_bounds__(288, MINB)
           if (active) {
             const float va = v_row ? vpa * inv : 1.0f, vb = v_row ? vpb * inv : 1.0f;
             // (keys x rows) -> (row g; keys 2c, 2c+1) of each 8-key half
-            const uint32_t y0 = ptx::movmatrix_trans(dev::pack_h2(p0 * va, p1 * va));
-            const uint32_t y1 = ptx::movmatrix_trans(dev::pack_h2(p2 * vb, p3 * vb));
+            const uint32_t y0 = ptx::movmatrix_trans(dev::pack_h2(dev::scaled<TREE>(p0, va), dev::scaled<TREE>(p1, va)));
+            const uint32_t y1 = ptx::movmatrix_trans(dev::pack_h2(dev::scaled<TREE>(p2, vb), dev::scaled<TREE>(p3, vb)));
             const int row = rh * RW + nt * 8 + g;
             ptx::st_shared_u32(p_base + p_off(row, kq * kSub + 2 * c), y0);
             ptx::st_shared_u32(p_base + p_off(row, kq * kSub + 8 + 2 * c), y1);
@@ -1257,7 +1266,7 @@ __global__ void __launch_bounds__(288, MINB)
             ua = use_a ? vs_row[sub * kSub + g] : 0.0f;
             ub = use_b ? vs_row[sub * kSub + g + 8] : 0.0f;
           }
-          float vm = fmaxf(ua, ub);
+          float vm = TREE ? fmaxf(dev::finite_or_0(ua), dev::finite_or_0(ub)) : fmaxf(ua, ub);
 #pragma unroll
           for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
           if (vm > 0.0f) {
@@ -1282,8 +1291,8 @@ __global__ void __launch_bounds__(288, MINB)
           }
         }
         // P (keys x rows) -> PV operand (rows x keys) by an 8x8 transpose
-        const uint32_t pb0 = ptx::movmatrix_trans(v_sc ? dev::pack_h2(p0 * vsa, p1 * vsa) : dev::pack_h2(p0, p1));
-        const uint32_t pb1 = ptx::movmatrix_trans(v_sc ? dev::pack_h2(p2 * vsb, p3 * vsb) : dev::pack_h2(p2, p3));
+        const uint32_t pb0 = ptx::movmatrix_trans(v_sc ? dev::pack_h2(dev::scaled<TREE>(p0, vsa), dev::scaled<TREE>(p1, vsa)) : dev::pack_h2(p0, p1));
+        const uint32_t pb1 = ptx::movmatrix_trans(v_sc ? dev::pack_h2(dev::scaled<TREE>(p2, vsb), dev::scaled<TREE>(p3, vsb)) : dev::pack_h2(p2, p3));
 
         // ---- O += V^T P^T for all channels (channels are MMA-M).  Every key
         // below the sequence end holds a code the quantizer wrote (never NaN);

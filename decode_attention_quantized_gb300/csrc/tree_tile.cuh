@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           float sc = scp[kk];
           if (is_v) {
             auto seen = [&](int key) { return key >= first_key && key < L; };
-            float vm = seen(key0 + lane) ? scp[lane] : 0.0f;
-            if (seen(key0 + 32 + lane)) vm = fmaxf(vm, scp[32 + lane]);
+            float vm = seen(key0 + lane) ? dev::finite_or_0(scp[lane]) : 0.0f;
+            if (seen(key0 + 32 + lane)) vm = fmaxf(vm, dev::finite_or_0(scp[32 + lane]));
             vm = ptx::redux_max(vm);
             if (vm > 0.0f) F = max(F, min(126, max(-126, dev::ceil_log2(vm))));
             vsb[(it & 7) * KT + kk] = seen(key0 + kk) ? sc * dev::pow2i(-F) : 0.0f;
@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           __syncwarp();
           ptx::tmem_st16(s_col + (CH - part0) / 2, none);
         }
-        auto weigh_as = [&](auto&& score, auto rows) {  // rows: per-row V scales
-          constexpr bool VR = decltype(rows)::value;
+        // rows: per-row V scales, some: of a tile that is not whole (the scales of
+        // hidden keys may be anything)
+        auto weigh_as = [&](auto&& score, auto rows, auto some) {
+          constexpr bool VR = decltype(rows)::value, SOME = decltype(some)::value;
           uint32_t p[CH / 2];
 #pragma unroll
           for (int k = 0; k < CH; k += 4) {
@@ -655,17 +657,24 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
               else l2 = ptx::add_x2(l2, e);
               float e0, e1;
               ptx::unpack_x2(e, e0, e1);
-              if constexpr (VR) ptx::mul_x2(e0, e1, e0, e1, j ? s4.z : s4.x, j ? s4.w : s4.y);
+              if constexpr (SOME) {
+                e0 = dev::scaled<true>(e0, j ? s4.z : s4.x);
+                e1 = dev::scaled<true>(e1, j ? s4.w : s4.y);
+              } else if constexpr (VR) {
+                ptx::mul_x2(e0, e1, e0, e1, j ? s4.z : s4.x, j ? s4.w : s4.y);
+              }
               p[k / 2 + j] = dev::pack_h2(e0, e1);
             }
           }
           __syncwarp();
           ptx::tmem_st16(s_col + part0 / 2, p);
         };
-        // (one branch here: one at each key would keep the keys apart)
+        // (one branch here, the same for a warp: one at each key would keep the keys apart)
+        const bool whole_tile = __all_sync(0xffffffffu, full);
         auto weigh = [&](auto&& score) {
-          if (v_row) weigh_as(score, std::true_type{});
-          else weigh_as(score, std::false_type{});
+          if (!v_row) weigh_as(score, std::false_type{}, std::false_type{});
+          else if (whole_tile) weigh_as(score, std::true_type{}, std::false_type{});
+          else weigh_as(score, std::true_type{}, std::true_type{});
         };
         if constexpr (!CAP) {
           weigh([&](ptx::f32x2 x) { return ptx::fma_x2(x, aa, nm); });
@@ -741,7 +750,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         l = l * copy + f[128] * (f[0] != top ? ptx::fast_exp2(f[0] - top) : 1.0f);
         mu = top;
         if (q >= 2) {
-          if (!(l > 0.0f)) copy = 0.0f;
+          if (l == 0.0f) copy = 0.0f;
 #pragma unroll 1
           for (int c0 = grp * (D / 2); c0 < (grp + 1) * (D / 2); c0 += 16) {
             float o[16];
@@ -758,7 +767,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         }
       }
       const int F = v_row ? fexp[(it - 1) & 7] : 0;
-      const bool some = l > 0.0f;
+      const bool some = l != 0.0f;  // (or NaN)
       float inv = some ? (v_row ? dev::pow2i(F) : 1.0f) / l : 0.0f;
       const bool whole = k0 == (vs.lo & ~(KT - 1)) && k1 == L;
       // channels c0 .. c0 + 15 of this thread's row, in channel order

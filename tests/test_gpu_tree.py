@@ -105,6 +105,38 @@ def test_trees_over_no_prefix_and_empty_sequences(kvq, name, T):
     check(cache, run(kvq, cache, parents, nodes), parents, nodes)
 
 
+@pytest.mark.parametrize("name", ["int8 row d128", "fp8 tensor cap", "int8 row d256 g6", "int4 channel d256"])
+@pytest.mark.parametrize("T", [3, 13])
+def test_trees_over_long_prefixes(kvq, name, T):
+    """Many tiles of many CTAs, one sequence beside it that is shorter than a tile."""
+    base = CASES[name]
+    case = dataclasses.replace(base, c=T, seed=T, lens=(8009, 63 + T))
+    cache = ref.Cache(case)
+    parents = step_ref.random_parents(np.random.default_rng(T), 2, T)
+    nodes = np.array([T, (T + 1) // 2])
+    check(cache, run(kvq, cache, parents, nodes), parents, nodes)
+
+
+@pytest.mark.parametrize("name,T", [("int8 row d128", 2), ("int8 row d128", 5), ("int8 row d128", 40),
+                                    ("int8 row d256 g6", 16), ("fp8 row", 20), ("int4 row", 3), ("int4 row", 33)])
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+def test_a_node_that_is_not_finite_reaches_its_descendants_only(kvq, name, T, bad):
+    cache, parents, nodes = make(name, T, ragged=False)
+    parents[:, -1] = -1  # the last node: a root without children, seen by itself alone
+    g = gpu_cache(kvq, cache)
+    for b, L in enumerate(cache.case.lens):
+        page, row = cache.table[b, (L - 1) // g.block_size], (L - 1) % g.block_size
+        g.k_scale[int(page), :, row] = bad
+        g.v_scale[int(page), :, row] = bad
+    out, lse = run(kvq, cache, parents, gcache=g)
+    r_out, r_lse, absv, f16, size = step_ref.attend_tree(cache, parents, nodes, None)
+    seen, ds = slice(0, T - 1), 2.0 ** -15
+    assert np.isfinite(out[:, seen]).all() and np.isfinite(lse[:, seen]).all()
+    tol = 2.0 ** -8 * np.abs(r_out) + f16 + 2 * ds * absv + 1e-30
+    assert (np.abs(out - r_out) / tol)[:, seen].max() <= 1.0
+    assert (np.abs(lse - r_lse) <= ds + 2.0 ** -20 * (1 + np.abs(r_lse)))[:, seen].all()
+
+
 @pytest.mark.parametrize("name,T", [("int8 row d128", 256), ("fp8 tensor cap", 200)])
 def test_the_largest_trees(kvq, name, T):
     """A tree of 256 nodes, among them a chain of all of them."""
