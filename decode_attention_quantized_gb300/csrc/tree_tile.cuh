@@ -1,6 +1,11 @@
 // tree_tile.cuh -- attention of many drafted nodes per kv head over the
 // quantized paged cache on the tcgen05 tensor cores: kvq_attend_tree from 17
-// query rows on at head_dim 128 and 256.
+// query rows on (9 over long caches) at head_dim 128 and 256.
+//
+// Mathematics: for the row of a node, S_j = sm_scale <q, k_j> (capped) over the
+// prefix keys j (of its window), its ancestors and itself; with a running
+// reference mu and P_j = 2^(S_j log2 e - mu): o = sum P_j v_j / sum P_j, lse =
+// ln 2 (mu + log2 sum P_j).
 //
 // A work unit is one (sequence, kv head) of up to 128 query rows, row r =
 // node t * G + head g of the GQA group, with the split plan, producer, 64-key
@@ -12,21 +17,29 @@
 // Each key tile's codes are dequantized once into f16 tiles in shared memory
 // (two of each), exactly: per-row scales go into the scores (K) and, under a
 // power-of-two normaliser 2^F, into the weights (V), per-channel ones into Q
-// and the output.  P overwrites its own S: head_dim 256 has two S buffers (Q 128 + O 256 + S 2 x
-// 64 columns), head_dim 128 four.  One warp issues both products; their order
-// in the tensor pipe is what keeps S, P and Q apart.
+// and the output.  P overwrites its own S: head_dim 256 has two S buffers (Q
+// 128 + O 256 + S 2 x 64 columns), head_dim 128 four.  One warp issues both
+// products; their order in the tensor pipe is what keeps S, P and Q apart.
 //
-// Warp roles (20 warps, 18 and 19 for the even share of registers): 0-3 and 4-7 softmax of the even and of the odd tiles,
-// one thread a row (S -> P with lazy row maxima; together Q of a piece into
-// TMEM and the epilogue, half of the channels each); 8-11 K dequant, two warps for the even
-// tiles and two for the odd ones, one key a thread; 12-15 V dequant, the same; 16 TMA
+// Warp roles (20 warps, 18 and 19 for the even share of registers): 0-7 softmax
+// (S -> P with lazy row maxima, 32 keys a thread; together Q of a piece into
+// TMEM and the epilogue, half of the channels each); 8-11 K dequant, key
+// 32 (w & 1) + lane, channel half w >> 1; 12-15 V dequant, the same; 16 TMA
 // producer of the code stages; 17 the MMAs.
 //
 // A tile's softmax is a chain of latencies (tensor memory, row maximum,
-// reference, weights) about twice as long as its work, so two groups of warps
-// walk alternate tiles.  They share O and with it the reference maximum of a
-// row, which goes from tile to tile through shared memory; each keeps its own
-// sum, under the reference it last saw.
+// reference, weights) longer than its work, so a row's 64 keys go to two
+// threads.  Rows past 64: warps 0-3 and 4-7 take the halves of the keys of every
+// tile and agree on its maximum.  Up to 64 rows (FOLD): warps 0-3 take the even
+// tiles and 4-7 the odd ones, and the halves are two copies of the row; the
+// groups share O and with it a row's reference, which goes from tile to tile
+// through shared memory; each keeps its own sum, under the reference it last saw.
+//
+// Bound: cache bytes for few rows of 8-bit codes, else the chain of a tile
+// (conversion, QK^T, softmax, PV) and instruction issue, 0.45 of the slots.
+// 131,072 int8 keys of head_dim 256, 16 nodes of 6 heads: 93 us, 2.9 TB/s; 4 x
+// 32,768 int4 keys, 32 nodes: 271 us; 16 sequences to 32,768 fp8 keys, capped,
+// 13 nodes of 4 heads: 248 us, 2.8 TB/s.
 #pragma once
 
 #include <type_traits>
