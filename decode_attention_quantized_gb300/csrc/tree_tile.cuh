@@ -37,8 +37,8 @@
 //
 // Bound: cache bytes for few rows of 8-bit codes, else the chain of a tile
 // (conversion, QK^T, softmax, PV) and instruction issue, 0.45 of the slots.
-// 131,072 int8 keys of head_dim 256, 16 nodes of 6 heads: 93 us, 2.9 TB/s; 4 x
-// 32,768 int4 keys, 32 nodes: 271 us; 16 sequences to 32,768 fp8 keys, capped,
+// 131,072 int8 keys of head_dim 256, 16 nodes of 6 heads: 92 us, 3.0 TB/s; 4 x
+// 32,768 int4 keys, 32 nodes: 274 us; 16 sequences to 32,768 fp8 keys, capped,
 // 13 nodes of 4 heads: 248 us, 2.8 TB/s.
 #pragma once
 
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
     produce_lanes<Gm, true, true>(a, sp, &tmk, &tmv, ring, bar_full, bar_empty, pl_pre, pl_misc);
   } else if (warp >= kDqK && warp < kDqV + 4) {
     // ==================================================== K and V dequant
-    // A stage's codes are converted 64 of a row at a time; the wait for the MMA
-    // that frees the f16 tile comes before the first store.
+    // A stage's codes are read at once and converted 64 of a row at a time; the
+    // wait for the MMA that frees the f16 tile comes before the first store.
     ptx::regs_down<88>();
     const bool is_v = warp >= kDqV;
     const int q = warp - (is_v ? kDqV : kDqK);
@@ -227,22 +227,22 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           if (lane == 0) ptx::mbar_arrive(is_v ? &b_vsc[it & 7] : &b_ksc[it & 7]);
         }
         const uint32_t buf = it & 1, tile = f16_base + buf * TILE;
+        // (all of the codes first: the sooner the stage is free, the more of the
+        // cache is on its way)
+        uint4 w[HB / 16];
+#pragma unroll
+        for (int j = 0; j < HB / 16; ++j) {
+          const uint32_t byte = (uint32_t)(hf * HB + 16 * j);
+          w[j] = *reinterpret_cast<const uint4*>(st + code_off + (byte / Gm::SPAN) * (KT * Gm::SPAN) +
+                                                 dev::swz<Gm::SPAN>((uint32_t)kk * Gm::SPAN + byte % Gm::SPAN));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar_empty[rp.stage]);
 #pragma unroll
         for (int pc = 0; pc < HB / PB; ++pc) {
-          uint4 w[PC];
-#pragma unroll
-          for (int j = 0; j < PC; ++j) {
-            const uint32_t byte = (uint32_t)(hf * HB + pc * PB + 16 * j);
-            w[j] = *reinterpret_cast<const uint4*>(st + code_off + (byte / Gm::SPAN) * (KT * Gm::SPAN) +
-                                                   dev::swz<Gm::SPAN>((uint32_t)kk * Gm::SPAN + byte % Gm::SPAN));
-          }
-          if (pc == HB / PB - 1) {
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bar_empty[rp.stage]);
-          }
           uint32_t v[PC * CW];
 #pragma unroll
-          for (int j = 0; j < PC; ++j) dev::k_cols<DT>(w[j], v + CW * j);
+          for (int j = 0; j < PC; ++j) dev::k_cols<DT>(w[pc * PC + j], v + CW * j);
           if (DT == KVQ_FP8_E4M3 && is_v) {  // (a key no row sees may hold NaN codes: they lose against -448)
 #pragma unroll
             for (int j = 0; j < PC * CW; ++j) v[j] = ptx::max_f16x2(v[j], 0xDF00DF00u);

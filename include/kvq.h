@@ -553,8 +553,9 @@ typedef struct {
  * ancestors and itself.  With params->window > 0 a key counts when its
  * position (a prefix row's is its row, a node's P + depth) is above the
  * node's own minus window.  q, out bf16 [B, T, Hq, D]; nodes i >= num_nodes[b]
- * are padding: their output rows are zero and their lse -inf.  Everything
- * else, the choice of kernels included, is as in kvq_attend_masked.
+ * are padding: their output rows are zero and their lse -inf.  A node whose
+ * cached row has a scale of inf or NaN reaches its descendants only.
+ * Everything else is as in kvq_attend_masked.
  * batch <= 1024.  workspace: at least kvq_attend_tree_workspace_size bytes,
  * 256-byte aligned; it belongs to this call until the call's kernels have
  * run. */
