@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
   float* vsb = ksb + 8 * KT;                              // [8][KT] its V scales over 2^F
   int* fexp = reinterpret_cast<int*>(vsb + 8 * KT);       // [8] its F (of the piece's tiles so far)
   float* ref = reinterpret_cast<float*>(base + lay.pair);  // [128] the rows' reference maxima
-  float* part = ref + kTtRows;                             // [2 groups][128] their last references and sums
+  float* part = ref + kTtRows;                             // [2][2 groups][128] a tile's maxima; last references and sums
   int* pl_pre = reinterpret_cast<int*>(base + lay.pre);
   int* pl_misc = pl_pre + a.batch + 1;
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(base + lay.bars);
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       bool blind = !valid;
       float alpha = 1.0f;
       // ---- Q of this piece (every QK^T of the previous one has completed: this
-      // thread waited for its last S): the per-channel K scale folded in under a
+      // thread waited for its last PV): the per-channel K scale folded in under a
       // power-of-two normaliser, the row normalised by the power of two at or
       // above its maximum, f16 pairs in the K order of the K
       // tile (each of the row's two threads writes half of the channels).
