@@ -95,10 +95,36 @@ __device__ __forceinline__ uint32_t f8pair(uint32_t w, uint32_t sel) {
   return (y & 0x80008000u) | ((y >> 1) & 0x3F803F80u);
 }
 
-// Draft trees: a node's row that holds infinities or NaN (a per-row scale that
-// is not finite) must not reach the nodes that do not see it.  It takes no part
-// in the V-scale normaliser, which all rows share, and a weight of 0 stays 0.
+// Draft trees: a node's row must not reach the nodes that do not see it, whatever
+// its V scale (one normaliser 2^F above all of them flushed the others' f16
+// weights to 0).  Infinities and NaN take no part in F, and a weight of 0 stays 0.
 __device__ __forceinline__ float finite_or_0(float s) { return s < INFINITY ? s : 0.0f; }
+__device__ __forceinline__ int scale_exponent(float s) { return s > 0.0f ? min(126, max(-126, ceil_log2(s))) : -126; }
+// How far above 2^F the scales up to s are (from 2^-112 on, so that weights stay within fp32).
+__device__ __forceinline__ float scale_lift(float s, int F) { return (float)max(scale_exponent(s) - F, -112); }
+
+// The normaliser 2^F of a row group's V scales in draft trees, tile by tile.  A
+// weight is 2^(y - mu) s / 2^F, O is over 2^(mu + F), and a row's reference mu is
+// kept where its largest weight is at most 2^8: at its maximum plus the `lift`,
+// by which the scales that the row itself sees are above 2^F (below it, if
+// negative).  When F moves, mu moves against it and O stays as it is.  F follows
+// the scales of the tiles whose keys all rows see (lift 0).  A scale that only
+// some rows see counts to 2^-46 of it, to 2^-94 in the tiles that all see: then
+// no lift leaves [-112, 94], and a row's sum, over 2^mu, stays within fp32.
+struct ScaleUnit {
+  // mu follows a growth of F up to here (above, O counts for nothing in the new unit)
+  static constexpr int kMost = 100;
+  int all = -126, some = -126;
+  // F of a tile of scales up to 2^f; common: all rows see all of its keys.
+  __device__ __forceinline__ int next(int f, bool common) {
+    if (common) {
+      all = max(all, f);
+      return max(all, some - 48);
+    }
+    some = max(some, f - 46);
+    return max(all, some);
+  }
+};
 template <bool TREE>
 __device__ __forceinline__ float scaled(float p, float s) {
   return TREE && p == 0.0f ? 0.0f : p * s;
@@ -449,6 +475,7 @@ __global__ void __launch_bounds__(288, MINB)
     float* s_max = scr + ROWS * 32;                      // [4][ROWS]
     float* s_l = s_max + 4 * ROWS;                       // [4][ROWS]
     float* s_vmax = s_l + 4 * ROWS;                      // [4]
+    float* s_vrow = s_l;  // draft trees: [4][ROWS] the rows' largest V scales of a tile (s_l is the piece's end's)
     const uint32_t p_base = ptx::smem_u32(scr);          // P: [ROWS][64 keys] f16, 128-byte rows
     float* s_q = s_vmax + 32;                            // Q: [ROWS][D] f16 in MMA k-slot order
     const uint32_t q_base = ptx::smem_u32(s_q);
@@ -615,6 +642,8 @@ __global__ void __launch_bounds__(288, MINB)
       }
       if constexpr (MASK) __syncwarp();
       int F = v_row ? -126 : 0;  // V-scale normaliser exponent, the same in every warp
+      dev::ScaleUnit unit;       // draft trees
+      const int c_lo = TREE ? a.vseq[b].gaps : 0, c_hi = TREE ? a.key_end[tok0] : 0;  // the keys that all rows see
       float acc[MTW][NT][4];
 #pragma unroll
       for (int mt = 0; mt < MTW; ++mt)
@@ -637,6 +666,7 @@ __global__ void __launch_bounds__(288, MINB)
         // ---- phase A: scores of this warp's 16 keys x NT n-tiles of rows
         const int kb = key0 + kq * kSub;
         const bool active = ok && kb < k1 && !idle;
+        const bool common = !TREE || (key0 >= c_lo && key0 + kTile <= c_hi);
         const int key_a = kb + g, key_b = key_a + 8;
         float x[NT][4];
         float vpa = 0.0f, vpb = 0.0f;
@@ -746,7 +776,7 @@ __global__ void __launch_bounds__(288, MINB)
               const int key = e < 2 ? key_a : key_b, p = pos[nt][e & 1];
               if constexpr (MASK) {
                 bool seen;
-                  x[nt][e] = dev::row_score<TREE>(a, s_rule[rh * RW + nt * 8 + 2 * c + (e & 1)], x[nt][e], key,
+                x[nt][e] = dev::row_score<TREE>(a, s_rule[rh * RW + nt * 8 + 2 * c + (e & 1)], x[nt][e], key,
                                                 a.slopes != nullptr, seen);
                 if (e < 2) see_a = see_a || seen;
                 else see_b = see_b || seen;
@@ -777,16 +807,48 @@ __global__ void __launch_bounds__(288, MINB)
             if (g == 0) s_max[kq * ROWS + rh * RW + nt * 8 + 2 * c + i] = t;
           }
         }
+        if (TREE && v_row && !common) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // (a weight of 0 needs no room)
+              float t = fmaxf(x[nt][i] != -INFINITY ? dev::finite_or_0(vpa) : 0.0f,
+                              x[nt][i + 2] != -INFINITY ? dev::finite_or_0(vpb) : 0.0f);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+              if (g == 0) s_vrow[kq * ROWS + rh * RW + nt * 8 + 2 * c + i] = t;
+            }
+        }
         if (v_row) {
           float vm = TREE ? fmaxf(dev::finite_or_0(vpa), dev::finite_or_0(vpb)) : fmaxf(vpa, vpb);
+          if constexpr (TREE) vm = ptx::redux_max(vm);
 #pragma unroll
-          for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          for (int o = TREE ? 32 : MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
           // (unmasked: the same in both halves; masked: each half has its rows')
           if ((MASK || rh == 0) && lane == 0) s_vmax[MASK ? warp : kq] = vm;
         }
         ptx::named_bar_sync(1, 8 * 32);
 
         // ---- phase B: the running maximum of every row over the 4 quarters
+        float fs = 1.0f, inv = 1.0f;
+        bool lifted = false;
+        if (TREE && v_row) {
+          float vm = fmaxf(fmaxf(s_vmax[0], s_vmax[1]), fmaxf(s_vmax[2], s_vmax[3]));
+          vm = fmaxf(vm, fmaxf(fmaxf(s_vmax[4], s_vmax[5]), fmaxf(s_vmax[6], s_vmax[7])));
+          const int f = dev::scale_exponent(vm);
+          lifted = !common || f > F || F != unit.all;
+          if (lifted) {
+            const int to = unit.next(f, common), grown = min(to - F, dev::ScaleUnit::kMost);
+            F = to;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                m[nt][i] -= (float)grown;
+                l[nt][i] *= dev::pow2i(grown);
+              }
+          }
+        }
         float mu[NT][2], corr[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -796,14 +858,19 @@ __global__ void __launch_bounds__(288, MINB)
             float tm = s_max[row];
 #pragma unroll
             for (int q = 1; q < 4; ++q) tm = fmaxf(tm, s_max[q * ROWS + row]);
+            if (TREE && lifted)
+              tm += common ? (float)(unit.all - F)
+                           : dev::scale_lift(fmaxf(fmaxf(s_vrow[row], s_vrow[ROWS + row]),
+                                                   fmaxf(s_vrow[2 * ROWS + row], s_vrow[3 * ROWS + row])), F);
             const float mn = fmaxf(m[nt][i], tm);
             mu[nt][i] = mn == -INFINITY ? 0.0f : mn;
             corr[nt][i] = ptx::fast_exp2(m[nt][i] - mu[nt][i]);
             m[nt][i] = mn;
           }
         }
-        float fs = 1.0f, inv = 1.0f;
-        if (v_row) {
+        if (TREE && v_row) {
+          inv = dev::pow2i(-F);
+        } else if (v_row) {
           float vm = fmaxf(fmaxf(s_vmax[0], s_vmax[1]), fmaxf(s_vmax[2], s_vmax[3]));
           if constexpr (MASK) vm = fmaxf(vm, fmaxf(fmaxf(s_vmax[4], s_vmax[5]), fmaxf(s_vmax[6], s_vmax[7])));
           if (vm > 0.0f) {
@@ -1084,6 +1151,7 @@ __global__ void __launch_bounds__(288, MINB)
 
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     int F = v_sc ? -126 : 0;  // V-scale normaliser exponent (warp uniform)
+    dev::ScaleUnit unit;      // draft trees
     float acc[Gm::NMT][4];
 #pragma unroll
     for (int mt = 0; mt < Gm::NMT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.0f;
@@ -1231,6 +1299,45 @@ __global__ void __launch_bounds__(288, MINB)
         // in f16 and most sub-tiles skip the reduction and the rescale
         float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
         float c0 = 1.0f, c1 = 1.0f;
+        float ua = 0.0f, ub = 0.0f;  // the keys' V scales (per-group: the largest)
+        if (v_sc) {
+          if (GRP && v_grp) {
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) {
+              if (use_a) ua = fmaxf(ua, vs_row[(sub * kSub + g) * NG + gi]);
+              if (use_b) ub = fmaxf(ub, vs_row[(sub * kSub + g + 8) * NG + gi]);
+            }
+          } else {
+            ua = use_a ? vs_row[sub * kSub + g] : 0.0f;
+            ub = use_b ? vs_row[sub * kSub + g + 8] : 0.0f;
+          }
+        }
+        if (TREE && v_sc) {
+          const float fa = dev::finite_or_0(ua), fb = dev::finite_or_0(ub);
+          const int f = dev::scale_exponent(ptx::redux_max(fmaxf(fa, fb)));
+          if (!full || f > F || F != unit.all) {
+            const int to = unit.next(f, full), grown = min(to - F, dev::ScaleUnit::kMost);
+            F = to;
+            m0 -= (float)grown;
+            m1 -= (float)grown;
+            l0 *= dev::pow2i(grown);
+            l1 *= dev::pow2i(grown);
+            float w0 = (float)(unit.all - F), w1 = w0;
+            if (!full) {  // (a weight of 0 needs no room)
+              w0 = fmaxf(x[0] != -INFINITY ? fa : 0.0f, x[2] != -INFINITY ? fb : 0.0f);
+              w1 = fmaxf(x[1] != -INFINITY ? fa : 0.0f, x[3] != -INFINITY ? fb : 0.0f);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                w0 = fmaxf(w0, __shfl_xor_sync(0xffffffffu, w0, o));
+                w1 = fmaxf(w1, __shfl_xor_sync(0xffffffffu, w1, o));
+              }
+              w0 = dev::scale_lift(w0, F);
+              w1 = dev::scale_lift(w1, F);
+            }
+            t0 += w0;
+            t1 += w1;
+          }
+        }
         if (__any_sync(0xffffffffu, t0 > m0 + 8.0f || t1 > m1 + 8.0f)) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
@@ -1255,25 +1362,16 @@ __global__ void __launch_bounds__(288, MINB)
         // scale 0 (their scale slots may hold anything)
         float vsa = 1.0f, vsb = 1.0f, fs = 1.0f, vinv = 1.0f;
         if (v_sc) {
-          float ua = 0.0f, ub = 0.0f;
-          if (GRP && v_grp) {
+          if constexpr (!TREE) {
+            float vm = fmaxf(ua, ub);
 #pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-              if (use_a) ua = fmaxf(ua, vs_row[(sub * kSub + g) * NG + gi]);
-              if (use_b) ub = fmaxf(ub, vs_row[(sub * kSub + g + 8) * NG + gi]);
-            }
-          } else {
-            ua = use_a ? vs_row[sub * kSub + g] : 0.0f;
-            ub = use_b ? vs_row[sub * kSub + g + 8] : 0.0f;
-          }
-          float vm = TREE ? fmaxf(dev::finite_or_0(ua), dev::finite_or_0(ub)) : fmaxf(ua, ub);
-#pragma unroll
-          for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-          if (vm > 0.0f) {
-            const int fn = min(126, max(-126, dev::ceil_log2(vm)));
-            if (fn > F) {
-              fs = (F - fn < -126) ? 0.0f : dev::pow2i(F - fn);
-              F = fn;
+            for (int o = MASK ? 1 : 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+            if (vm > 0.0f) {
+              const int fn = min(126, max(-126, dev::ceil_log2(vm)));
+              if (fn > F) {
+                fs = (F - fn < -126) ? 0.0f : dev::pow2i(F - fn);
+                F = fn;
+              }
             }
           }
           vinv = dev::pow2i(-F);

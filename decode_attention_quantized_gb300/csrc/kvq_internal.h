@@ -69,7 +69,8 @@ struct VSeq {
   int pos0, tok0, ntok;
   int brow;  // row of the block table
   int gaps;  // 1: some key of [lo, hi) may be seen by no token of the group, and
-             // its cache row may then hold anything (0: every key is seen)
+             // its cache row may then hold anything (0: every key is seen).  Draft
+             // trees: the prefix keys from here on are seen by every node of the group
 };
 
 struct DecodeArgs {
@@ -295,7 +296,7 @@ __host__ __device__ constexpr QtSmem qt_smem_layout(int head_dim, int stages, in
 // The tcgen05 draft-tree kernel (tree_tile.cuh): the same rows and stages, 20
 // warps.  ring: stages x stage stride; kf, vf: two [D/64 slabs][kTile keys]
 // [128 B] f16 tiles each; sc: eight [kTile] K scales, eight [kTile] V scales over
-// 2^F and eight F; exch: two-part Q at head_dim 256: two [64 rows][kTile
+// 2^F and four values of each F; exch: two-part Q at head_dim 256: two [64 rows][kTile
 // keys] f16 blocks; folded rows: their references and sums and 16 columns of O
 // at a time; pair: the rows' references and sums; pre:
 // split plan; bars: mbarriers; slot: TMEM address + abort flag.
@@ -320,7 +321,7 @@ __host__ __device__ constexpr TtSmem tt_smem_layout(int head_dim, int stages, in
   s.kf = stages * stage_stride;
   s.vf = s.kf + 2 * (head_dim / 64) * kTile * 128;
   s.sc = s.vf + 2 * (head_dim / 64) * kTile * 128;
-  s.exch = s.sc + 16 * kTile * 4 + 8 * 4;
+  s.exch = s.sc + 16 * kTile * 4 + 8 * 16;
   s.pair = s.exch + exchange;
   s.pre = s.pair + 5 * kTtRows * 4;
   s.bars = (s.pre + (batch + 5) * 4 + 7) / 8 * 8;

@@ -69,10 +69,13 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeArgs a) {
     s.ntok = min(a.T, C - j * a.T);
     s.pos0 = P + j * a.T;
     s.brow = b;
-    s.gaps = 0;  // the nodes' rows are all there, and of the prefix each needs the end
     const int real = min(s.ntok, n - j * a.T);
-    int lo = P;
-    for (int i = 0; i < real; ++i) lo = min(lo, low[j * a.T + i]);
+    int lo = P, all = 0;
+    for (int i = 0; i < real; ++i) {
+      lo = min(lo, low[j * a.T + i]);
+      all = max(all, low[j * a.T + i]);
+    }
+    s.gaps = all;
     s.lo = real > 0 ? lo : 0;
     s.hi = real > 0 ? P + j * a.T + real : 0;
     a.out[b * a.n + j] = s;

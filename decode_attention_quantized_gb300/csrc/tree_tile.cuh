@@ -17,9 +17,11 @@
 // Each key tile's codes are dequantized once into f16 tiles in shared memory
 // (two of each), exactly: per-row scales go into the scores (K) and, under a
 // power-of-two normaliser 2^F, into the weights (V), per-channel ones into Q
-// and the output.  P overwrites its own S: head_dim 256 has two S buffers (Q
-// 128 + O 256 + S 2 x 64 columns), head_dim 128 four.  One warp issues both
-// products; their order in the tensor pipe is what keeps S, P and Q apart.
+// and the output.  F is dev::ScaleUnit's: a node takes nothing of the precision
+// of those that do not see it.  P overwrites its own S: head_dim 256 has two S
+// buffers (Q 128 + O 256 + S 2 x 64 columns), head_dim 128 four.  One warp
+// issues both products; their order in the tensor pipe is what keeps S, P and Q
+// apart.
 //
 // Warp roles (20 warps, 18 and 19 for the even share of registers): 0-7 softmax
 // (S -> P with lazy row maxima, 32 keys a thread; together Q of a piece into
@@ -113,7 +115,9 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
   const uint32_t kf = ptx::smem_u32(base + lay.kf), vf = ptx::smem_u32(base + lay.vf);
   float* ksb = reinterpret_cast<float*>(base + lay.sc);  // [8][KT] K scales of tile it, at it & 7
   float* vsb = ksb + 8 * KT;                              // [8][KT] its V scales over 2^F
-  int* fexp = reinterpret_cast<int*>(vsb + 8 * KT);       // [8] its F (of the piece's tiles so far)
+  // [8] F, how far it has grown since the tile before, how far the scales (of the
+  // tile; where all rows see them, of those so far) are above 2^F
+  float4* funit = reinterpret_cast<float4*>(vsb + 8 * KT);
   float* ref = reinterpret_cast<float*>(base + lay.pair);  // [128] the rows' reference maxima
   float* part = ref + kTtRows;                             // [2][2 groups][128] a tile's maxima; last references and sums
   int* pl_pre = reinterpret_cast<int*>(base + lay.pre);
@@ -200,16 +204,18 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
     for (int gt = sp.t_begin, next; gt < sp.t_end; gt = next) {
       int b, h, k0, k1, L, u;
       sp.piece(a, gt, b, h, k0, k1, L, u, next);
-      int F = -126;  // V-scale normaliser exponent of the piece
-      const int first_key = a.vseq[b].lo;  // (a row below it may hold anything)
+      dev::ScaleUnit unit;  // of the piece's V scales
+      int F_last = 0;
+      const VSeq vs = a.vseq[b];
+      const int first_key = vs.lo;  // (a row below it may hold anything)
+      const int c_lo = vs.gaps, c_hi = a.key_end[vs.tok0];  // the keys that all rows see
       for (int key0 = Order::first(k0, k1); Order::more(key0, k0, k1); key0 += Order::step, ++it, rp.next(a.stages)) {
         wait(&bar_full[rp.stage], rp.phase);
         const uint8_t* st = ring + (size_t)rp.stage * a.stage_stride;
         if (scaled) {
-          // Slot it & 7 was last read by the softmax of it - 8 (its own) and of
-          // it - 7 (which reads the F before its own).  K: this warp has waited
-          // for QK^T of it - 3, issued after PV of it - 3 - NSB, whose softmax was
-          // done; V: for PV of it - 3.
+          // Slot it & 7 was last read by the softmax of it - 8.  K: this warp has
+          // waited for QK^T of it - 3, issued after PV of it - 3 - NSB, whose softmax
+          // was done; V: for PV of it - 3.
           const float* scp = reinterpret_cast<const float*>(st + 2 * Gm::CODE_BYTES + (is_v ? KT * 4 : 0));
           float sc = scp[kk];
           if (is_v) {
@@ -217,9 +223,15 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
             float vm = seen(key0 + lane) ? dev::finite_or_0(scp[lane]) : 0.0f;
             if (seen(key0 + 32 + lane)) vm = fmaxf(vm, dev::finite_or_0(scp[32 + lane]));
             vm = ptx::redux_max(vm);
-            if (vm > 0.0f) F = max(F, min(126, max(-126, dev::ceil_log2(vm))));
+            const bool common = key0 >= c_lo && key0 + KT <= c_hi;
+            const int f = dev::scale_exponent(vm), F = unit.next(f, common);
             vsb[(it & 7) * KT + kk] = seen(key0 + kk) ? sc * dev::pow2i(-F) : 0.0f;
-            if (q == 0 && lane == 0) fexp[it & 7] = F;
+            if (q == 0 && lane == 0) {
+              const bool first = key0 == Order::first(k0, k1);
+              funit[it & 7] = make_float4(__int_as_float(F), first ? 0.0f : (float)min(F - F_last, dev::ScaleUnit::kMost),
+                                          (float)((common ? unit.all : f) - F), 0.0f);
+            }
+            F_last = F;
           } else {
             ksb[(it & 7) * KT + kk] = sc;
           }
@@ -496,6 +508,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         const float* vsc = vsb + (it & 7) * KT;
         const bool full = key0 >= ru.begin && key0 + KT <= ru.end;
         uint32_t bits[2] = {0u, 0u};  // visible keys of a tile that is not whole
+        float lift = 0.0f;            // how far the V scales that the row sees of it are above 2^F
         if (!full) {
           if (key0 + KT > ru.end) dev::tree_sees_64(a, ru, key0, bits);
           const int lo = min(KT, max(0, ru.begin - key0)), hi = min(KT, max(0, ru.end - key0));
@@ -503,6 +516,20 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
             const uint64_t in = (hi == 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
             bits[0] |= (uint32_t)in;
             bits[1] |= (uint32_t)(in >> 32);
+          }
+          if (v_row) {
+            // (a row's two threads find the same; FOLD: each copy for its own keys)
+            wait(&b_vsc[it & 7], (it >> 3) & 1);
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KT; k += 4) {
+              if (FOLD && (k < 32) != (part0 == 0)) continue;
+              const float4 s4 = *reinterpret_cast<const float4*>(vsc + k);
+              const uint32_t b4 = (k < 32 ? bits[0] : bits[1]) >> (k & 31);
+              top = fmaxf(top, fmaxf(fmaxf(b4 & 1u ? dev::finite_or_0(s4.x) : 0.0f, b4 & 2u ? dev::finite_or_0(s4.y) : 0.0f),
+                                     fmaxf(b4 & 4u ? dev::finite_or_0(s4.z) : 0.0f, b4 & 8u ? dev::finite_or_0(s4.w) : 0.0f)));
+            }
+            lift = dev::scale_lift(top, 0);
           }
           if (part0) bits[0] = bits[1];
         }
@@ -597,23 +624,24 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         } else {
           m *= alpha;
         }
-        float fs = 1.0f;  // the V-scale normaliser's growth since the last tile
+        float grown = 0.0f;  // F since the last tile
         if (v_row) {
           wait(&b_vsc[it & 7], (it >> 3) & 1);
-          if (!first) {
-            const int f0 = fexp[(it - 1) & 7], f1 = fexp[it & 7];
-            if (f1 > f0) fs = (f0 - f1 < -126) ? 0.0f : dev::pow2i(f0 - f1);
-          }
+          const float4 fu = funit[it & 7];
+          m += full ? fu.z : lift;
+          grown = fu.y;
         }
         // The reference (FOLD: that the other group left at the tile before) moves
         // only when this tile's maximum exceeds it by more than 8 (P <= 2^8 in
-        // f16); a row with no key yet holds zeros in O.
+        // f16), and against F, which leaves O as it is; a row with no key yet holds
+        // zeros in O.
         float was = mu;
         if (FOLD && !first) {
           __syncwarp();
           ptx::named_bar_sync(bar_mine, 64);
           was = ref[32 * q + lane];
         }
+        was -= grown;
         const float now = m > was + 8.0f ? m : was;
         if (FOLD && !last) {
           ref[32 * q + lane] = now;
@@ -627,19 +655,17 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           l3 = ptx::mul_x2(l3, ptx::pack_x2(c, c));
           mu = now;
         }
-        const bool resc = !first && (corr != 1.0f || fs != 1.0f);
-        if (__any_sync(0xffffffffu, resc)) {
+        if (__any_sync(0xffffffffu, !first && corr != 1.0f)) {
           // bring O (a row's two threads half of the channels each, FOLD: all) to the
-          // new reference and normaliser, after the previous PV has landed
+          // new reference, after the previous PV has landed
           wait(&b_pv[(it - 1) % NSB], ((it - 1) / NSB) & 1);
           ptx::tc_fence_after();
-          const float f = resc ? corr * fs : 1.0f;
 #pragma unroll 1
           for (int c0 = FOLD ? 0 : grp * (D / 2); c0 < (FOLD ? D : (grp + 1) * (D / 2)); c0 += 16) {
             float o[16];
             dev::tmem_ld_cols<16>(t_lane + O_COL + c0, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= f;
+            for (int i = 0; i < 16; ++i) o[i] *= corr;
             dev::tmem_st_cols<16>(t_lane + O_COL + c0, o);
           }
         }
@@ -727,7 +753,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       wait(&b_pv[(it - 1) % NSB], ((it - 1) / NSB) & 1);
       if (idle || second) continue;
       ptx::tc_fence_after();
-      // both groups' sums under the last reference
+      // both groups' sums under the last reference (FOLD: the last tile's group has it)
       float l, mu_o;
       {
         float lb;
@@ -739,7 +765,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         ptx::named_bar_sync(1 + q, 64);
         mu_o = part[256 * (grp ^ 1) + 32 * q + lane];
         lb = part[256 * (grp ^ 1) + 128 + 32 * q + lane];
-        const float top = fmaxf(mu, mu_o);
+        const float top = !FOLD || (int)((it - 1) & 1) == grp ? mu : mu_o;
         if (mu != top) l *= ptx::fast_exp2(mu - top);
         if (mu_o != top) lb *= ptx::fast_exp2(mu_o - top);
         mu = top;
@@ -779,7 +805,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           continue;
         }
       }
-      const int F = v_row ? fexp[(it - 1) & 7] : 0;
+      const int F = v_row ? __float_as_int(funit[(it - 1) & 7].x) : 0;
       const bool some = l != 0.0f;  // (or NaN)
       float inv = some ? (v_row ? dev::pow2i(F) : 1.0f) / l : 0.0f;
       const bool whole = k0 == (vs.lo & ~(KT - 1)) && k1 == L;
