@@ -1413,8 +1413,8 @@ __global__ void __launch_bounds__(288, MINB)
                 const int grp = j * CH / (GRP ? GS : 1);
                 const float ga = use_a ? vs_row[(sub * kSub + g) * NG + grp] * vinv : 0.0f;
                 const float gb = use_b ? vs_row[(sub * kSub + g + 8) * NG + grp] * vinv : 0.0f;
-                qb0 = ptx::movmatrix_trans(dev::pack_h2(p0 * ga, p1 * ga));
-                qb1 = ptx::movmatrix_trans(dev::pack_h2(p2 * gb, p3 * gb));
+                qb0 = ptx::movmatrix_trans(dev::pack_h2(dev::scaled<TREE>(p0, ga), dev::scaled<TREE>(p1, ga)));
+                qb1 = ptx::movmatrix_trans(dev::pack_h2(dev::scaled<TREE>(p2, gb), dev::scaled<TREE>(p3, gb)));
               }
               if constexpr (DT == KVQ_INT4) {
                 const uint32_t xl = wl ^ 0x88888888u, xh = wh ^ 0x88888888u;

@@ -111,3 +111,21 @@ def test_a_large_row_behind_the_window(kvq, name, T):
     for b, L in enumerate(case.lens):
         enlarge(cache, b, L - T - 17, 2.0 ** 30)  # nodes 0 .. 2 see it
     check(cache, run(kvq, cache, parents), parents, nodes)
+
+
+@pytest.mark.parametrize("name,T,hq", [("int4 group", 4, 8), ("int4 group", 5, 2), ("int4 group", 20, 6),
+                                       ("fp8 group v", 8, 2), ("fp8 group v", 9, 6), ("int8 group k, row v", 7, 6),
+                                       ("latent d256", 5, 3), ("latent d576", 6, 8), ("latent d576", 4, 1)])
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+def test_a_node_of_group_scales_that_is_not_finite_reaches_its_descendants_only(kvq, name, T, hq, bad):
+    """(An odd number of heads a group: two nodes share a lane's pair of rows.)"""
+    cache, parents, nodes = make(name, T, ragged=False, hq=hq)
+    parents[:, -1] = -1
+    g = gpu_cache(kvq, cache)
+    for b, L in enumerate(cache.case.lens):
+        page, row = int(cache.table[b, (L - 1) // g.block_size]), (L - 1) % g.block_size
+        if cache.case.km in (ref.ROW, ref.GROUP):
+            g.k_scale[page, :, row] = bad
+        if cache.case.vm in (ref.ROW, ref.GROUP) and not cache.case.latent:
+            g.v_scale[page, :, row] = bad
+    check(cache, run(kvq, cache, parents, gcache=g), parents, nodes, slice(0, T - 1))
