@@ -24,6 +24,13 @@
 // memory, mask, lazy reference maxima -- O is rescaled only when a row's
 // maximum grows by more than 2^8 --, P back; at the end O, normalised, to
 // memory); then one producer (work units, TMA) and one MMA warp.
+//
+// A weight of 0 times infinity or NaN is NaN, so a V row may spoil the rows of a
+// tile that do not see it.  A unit whose results hold NaN therefore runs again
+// with care: in key tiles that some row does not see whole, elements of V that
+// are not finite are set to 0 before the product, and rows that see them get
+// them added at the end.  (Looking through those tiles every time instead, by
+// two warps of their own, cost 5% with a window of 512 or prompts of 200 tokens.)
 #include <cuda_bf16.h>
 
 #include "decode_tc.cuh"
@@ -53,15 +60,16 @@ struct PromptCfg {
   static constexpr int BARS = RING + STAGES * STAGE;
   static constexpr int N_BARS = 2 * STAGES + 2 * NQ + 3 * NQ * SB + NQ + 4;
   static constexpr int UNITS = BARS + (N_BARS * 8 + 15) / 16 * 16;
-  static constexpr int TOTAL = UNITS + 2 * 16 + 16;
+  static constexpr int TOTAL = UNITS + 2 * 16 + 16 + 8 * 4;
   static constexpr int SMEM = TOTAL + 1024;
 };
 
 // One unit's rows and keys.  Token 0 of the unit is token q0 of the sequence,
 // whose rows begin at row0.
 struct __align__(16) Unit {
-  int row0, len, q0, head;  // len 0: no more units
+  int row0, len, q0, head;  // len 0: the last units are done; -1: nothing to do
 };
+constexpr int kCare = 1 << 30;  // in head: the unit runs again, with care for V
 
 // The key tiles [a, b) that tile w of a unit needs.
 struct Range {
@@ -71,6 +79,13 @@ __device__ __forceinline__ Range tile_range(const Unit& u, int w, int tpt, int w
   const int t0 = u.q0 + w * tpt, t1 = min(t0 + tpt, u.len);
   if (t0 >= t1) return {0, 0};
   return {window > 0 ? max(0, t0 - window + 1) / kKeys : 0, (t1 - 1) / kKeys + 1};
+}
+
+// Every row of a unit of `tokens` tokens sees all of the key tiles [a, b) that it
+// multiplies; of the others some row may not see some key.
+__device__ __forceinline__ Range whole_range(const Unit& u, int tokens, int window) {
+  const int last = min(u.q0 + tokens, u.len) - 1;
+  return {window > 0 ? (max(0, last - window + 1) + kKeys - 1) / kKeys : 0, (u.q0 + 1) / kKeys};
 }
 
 __device__ __forceinline__ bool bad_bounds(const PromptArgs& a, int s0, int s1) {
@@ -204,6 +219,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   Unit* units = reinterpret_cast<Unit*>(base + C::UNITS);            // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* total = abort_flag + 1;  // number of the unit behind the last one
+  volatile int* spoilt = reinterpret_cast<volatile int*>(tmem_slot + 4);  // [8] at unit n & 7: n + 1, if it is to run again
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -225,6 +242,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       ptx::mbar_init(&b_unit[i], 1);
       ptx::mbar_init(&b_ufree[i], C::SOFTMAX + 1);
     }
+    for (int i = 0; i < 8; ++i) spoilt[i] = 0;
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -257,6 +275,15 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     ++un;
     return u;
   };
+  // Whether units follow behind one of len 0: the last two may have to run again.
+  // (The same for every warp, whatever else has happened: nothing writes these
+  // between the barrier and the next unit's results.)
+  auto go_on = [&]() -> bool {
+    __syncwarp();
+    ptx::named_bar_sync(1, (C::SOFTMAX + 2) * 32);
+    const int n = *total;
+    return (n > 0 && spoilt[(n - 1) & 7] == n) || (n > 1 && spoilt[(n - 2) & 7] == n - 1);
+  };
   auto range = [&](const Unit& u, int w) -> Range {
     return w < unit_tiles ? tile_range(u, w, tpt, W) : Range{0, 0};
   };
@@ -284,11 +311,38 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       }
     };
     int u = blockIdx.x;
+    Unit ahead{}, before[3] = {};  // the next unit; the last three written
+    bool have = false;
+    int late = 0;  // units that are looked after behind the list's end
     for (int n = 0;; ++n) {
-      const Unit x = planned ? planned_unit(a, u, unit_tokens) : (n == 0 ? small_unit(a, u, unit_tokens) : Unit{});
+      if (!have) {
+        ahead = planned ? planned_unit(a, u, unit_tokens) : (u >= 0 ? small_unit(a, u, unit_tokens) : Unit{});
+        have = true;
+      }
+      // Once unit n - 2 has been taken, unit n - 3 is finished: it may have to run
+      // again.  The last two are looked after behind the end of the list.
+      int again = 0;
+      if (lane == 0 && n >= 2) {
+        wait(&b_ufree[n & 1], ((n - 2) >> 1) & 1);
+        again = n >= 3 && spoilt[(n - 3) & 7] == n - 2;
+      }
+      again = __shfl_sync(0xffffffffu, again, 0);
+      Unit x = ahead;
+      if (again) {
+        x = before[2];
+        x.head |= kCare;
+      } else if (late > 0) {
+        x.len = -1;
+      } else {
+        have = x.len == 0;
+      }
+      late = max(0, late - 1);
+      before[2] = before[1];
+      before[1] = before[0];
+      before[0] = x;
       if (lane == 0) {
-        if (n >= 2) wait(&b_ufree[n & 1], ((n - 2) >> 1) & 1);
         units[n & 1] = x;
+        x.head &= ~kCare;
         ptx::mbar_arrive(&b_unit[n & 1]);
         if (x.len > 0) {
           const Range r0 = range(x, 0), r1 = NQ > 1 ? range(x, NQ - 1) : Range{0, 0};
@@ -329,22 +383,23 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           units[(n + 1) & 1] = Unit{};
           ptx::mbar_arrive(&b_unit[(n + 1) & 1]);
         }
-        break;
+        // every copy has landed before the CTA may end
+        if (lane == 0) {
+          *total = n;
+          const uint32_t last = issued < (uint32_t)C::STAGES ? issued : (uint32_t)C::STAGES;
+          for (uint32_t i = issued - last; i < issued; ++i)
+            ptx::mbar_wait_bounded_inl(&bar_full[i % C::STAGES], (i / C::STAGES) & 1);
+          for (int w = 0; w < NQ; ++w)
+            if (qn[w] > 0) ptx::mbar_wait_bounded_inl(&b_qfull[w], (qn[w] - 1) & 1);
+        }
+        if (!go_on()) break;
+        late = 2;
       }
-      if (planned) {
-        if (lane == 0) u = atomicAdd(&a.plan[0], 1);
+      if (!have) {
+        if (lane == 0) u = planned ? atomicAdd(&a.plan[0], 1) : -1;
         u = __shfl_sync(0xffffffffu, u, 0);
       }
     }
-    // every copy has landed before the CTA may end
-    if (lane == 0) {
-      const uint32_t last = issued < (uint32_t)C::STAGES ? issued : (uint32_t)C::STAGES;
-      for (uint32_t i = issued - last; i < issued; ++i)
-        ptx::mbar_wait_bounded_inl(&bar_full[i % C::STAGES], (i / C::STAGES) & 1);
-      for (int w = 0; w < NQ; ++w)
-        if (qn[w] > 0) ptx::mbar_wait_bounded_inl(&b_qfull[w], (qn[w] - 1) & 1);
-    }
-    __syncwarp();
   } else if (warp == kMma) {
     // ================================================================ MMA
     if constexpr (kShares) ptx::regs_down<88>();
@@ -401,22 +456,45 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       for (int h = 0; h < NH; ++h) landed(i + h);
     };
     // Rows of V behind the sequence hold anything (NaN times a weight of 0 is
-    // NaN): they are set to 0.
-    auto clear_tail = [&](uint32_t i, int rows) {
+    // NaN): they are set to 0.  With care, elements before them that are not
+    // finite are, too.
+    auto clear = [&](uint32_t i, int rows, bool care) {
       for (int h = 0; h < NH; ++h) {
         const uint32_t st = ring + stage_of(i + h) * C::STAGE;
-        const int n = (kKeys - rows) * 8;
         for (int c = 0; c < C::SD / 64; ++c)
-          for (int k = lane; k < n; k += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(st + c * kSlab + rows * 128 + 16 * k), "r"(0)
+          for (int k = lane + (care ? 0 : 8 * rows); k < 8 * kKeys; k += 32) {
+            const uint32_t at = st + c * kSlab + 16 * k;
+            uint32_t x[4] = {0u, 0u, 0u, 0u};
+            if (k < 8 * rows) {
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u;
+                if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0xFFFFu;
+              }
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
                          : "memory");
+          }
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
     };
     for (;;) {
       const Unit u = next_unit();
-      if (u.len == 0) break;
+      if (u.len == 0) {
+        // every MMA has completed before tensor memory can be released
+        for (int w = 0; w < NQ; ++w)
+          if (np[w] > 0 && !ptx::mbar_wait_bounded_inl(&b_o[w], (np[w] - 1) & 1) && lane == 0) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
+        if (!go_on()) break;
+      }
+      if (u.len <= 0) continue;
+      const Range whole = whole_range(u, unit_tiles * tpt, W);
+      auto prepare = [&](uint32_t i, int j) {
+        const bool care = (u.head & kCare) && (j < whole.a || j >= whole.b);
+        if (care || (j + 1) * kKeys > u.len) clear(i, min(kKeys, u.len - j * kKeys), care);
+      };
       const Range r0 = range(u, 0), r1 = NQ > 1 ? range(u, NQ - 1) : Range{0, 0};
       const int end = max(r0.b, r1.b);
       auto q_ready = [&](int w) {
@@ -442,7 +520,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           v_at = k_at + NH;
           k_at = v_at + NH;
           land(v_at);
-          if ((j + 1) * kKeys > u.len) clear_tail(v_at, u.len - j * kKeys);
+          prepare(v_at, j);
           if (j < r0.b) pv(0, v_at, j == r0.a);
           if (more) {
             land(k_at);
@@ -473,17 +551,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             v_at = k_at + (j > r0.a ? 2 * NH : NH);
           }
           land(v_at);
-          if ((j + 1) * kKeys > u.len) clear_tail(v_at, u.len - j * kKeys);
+          prepare(v_at, j);
           pv(0, v_at, j == r0.a);
           release(v_at);
           it = v_at + NH;
         }
       }
     }
-    // every MMA has completed before tensor memory can be released
-    for (int w = 0; w < NQ; ++w)
-      if (np[w] > 0 && !ptx::mbar_wait_bounded_inl(&b_o[w], (np[w] - 1) & 1) && lane == 0) atomicOr(a.err, KVQ_DEVERR_TIMEOUT);
-    __syncwarp();
   } else if (warp < C::SOFTMAX) {
     // ============================================================ softmax
     if constexpr (kShares) ptx::regs_up<208>();
@@ -506,9 +580,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         CAP && alpha > 6e-5f && alpha < 1.6e4f && cap2 > 1e-6f && cap2 < 1e6f ? kCapNear / alpha : -1.0f;
     uint32_t ns = 0;  // S tiles taken
     for (;;) {
-      const Unit u = next_unit();
-      if (u.len == 0) break;
-      const Range kr = range(u, w);
+      Unit u = next_unit();
+      if (u.len == 0 && !go_on()) break;
+      const bool care = u.head & kCare;
+      u.head &= ~kCare;
+      const Range kr = u.len > 0 ? range(u, w) : Range{0, 0};
       if (kr.a >= kr.b) continue;
       const int tok = u.q0 + w * tpt + t_row;
       const bool valid = t_row < tpt && tok < u.len;
@@ -677,6 +753,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, dst, (lane & ~3) | i);
       const bool odd = lane & 1, high = lane & 2;
+      __nv_bfloat162 sum = __floats2bfloat162_rn(0.0f, 0.0f);  // not finite if a result is not
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
@@ -686,6 +763,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int i = 0; i < 16; ++i) {
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[2 * i] * f, o[2 * i + 1] * f);
           x[i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        {
+          auto pair = [&](int i) { return *reinterpret_cast<const __nv_bfloat162*>(&x[i / 4][i % 4]); };
+          __nv_bfloat162 t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = __hfma2(pair(i), pair(4 + i), __hmul2(pair(8 + i), pair(12 + i)));
+          sum = __hadd2(sum, __hadd2(__hadd2(t[0], t[1]), __hadd2(t[2], t[3])));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -706,6 +790,23 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         for (int k = 0; k < 4; ++k)
           if (at[k])
             *reinterpret_cast<uint4*>(at[k] + 2 * c0 + 16 * (lane & 3)) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
+      }
+      const float2 s2 = __bfloat1622float2(sum);
+      if (valid && !(fabsf(s2.x + s2.y) < INFINITY) && !care) spoilt[(un - 1) & 7] = un;
+      if (care) {
+        // the elements of V that were set to 0, to the rows that see them
+        __syncwarp();
+        const Range whole = whole_range(u, unit_tiles * tpt, W);
+        for (int key = max(0, begin); valid && key <= pos; ++key) {
+          if (key / kKeys >= whole.a && key / kKeys < whole.b) key = whole.b * kKeys;
+          if (key > pos) break;
+          const uint16_t* src = a.v + (size_t)(u.row0 + key) * a.v_stride + (size_t)u.head * D;
+          for (int c = 0; c < D; ++c)
+            if ((src[c] & 0x7F80u) == 0x7F80u) {
+              __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + row * D + c;
+              *o = __float2bfloat16(__bfloat162float(*o) + __uint_as_float((uint32_t)src[c] << 16));
+            }
+        }
       }
       ptx::tc_fence_before();
     }

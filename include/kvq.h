@@ -506,8 +506,8 @@ KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_par
  * cu_seqlens[B], an empty sequence) are left as they were, and what q, k and v
  * hold there, NaN included, changes nothing.  A sequence whose bounds descend,
  * leave [0, N] or exceed max_seq_len sets KVQ_DEVERR_SEQ_LEN and is skipped.
- * Inf or NaN in a token's own K or V row may spread to earlier tokens of the
- * same sequence that share a tile of 128 keys with it.
+ * Inf or NaN in a token's K or V row reaches the tokens that see it, and no
+ * other (tiles of rows whose results hold NaN are computed twice).
  * Weights enter the product with V as bf16; sums, maxima and lse are fp32.
  * Repeated calls give the same bits.  out must not overlap q, k or v.
  * batch <= 1024.  workspace: at least kvq_attend_prompt_workspace_size bytes,
