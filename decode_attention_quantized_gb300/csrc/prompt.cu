@@ -93,6 +93,9 @@ __device__ __forceinline__ Range whole_range(const Unit& u, int tokens, int wind
 __device__ __forceinline__ bool bad_bounds(const PromptArgs& a, int s0, int s1) {
   return s0 < 0 || s1 < s0 || s1 > a.total_tokens || s1 - s0 > a.max_seq_len;
 }
+// Where bounds descend, a sequence may also begin before the end of an earlier
+// one; it is skipped, so that no row is written for two sequences and the work is
+// that of at most total_tokens.  (One that descends is among the flagged.)
 
 // The plan of many units: [0] the next unit, [1] blocks of tokens in all, then
 // for the sequences in order of length, longest first, the prefix sums of
@@ -103,14 +106,24 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a, i
   ptx::griddep_launch_dependents();
   const int b = threadIdx.x, lane = b & 31, warp = b >> 5, B = a.batch;
   int s0 = 0, n = 0;
+  bool descends = false;
   if (b < B) {
     s0 = a.cu_seqlens[b];
     const int s1 = a.cu_seqlens[b + 1];
-    if (bad_bounds(a, s0, s1)) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
+    descends = s1 < s0;
+    const bool bad = bad_bounds(a, s0, s1);
+    if (bad) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
     else n = s1 - s0;
     len[b] = n;
+    sorted[b] = bad ? 0 : s1;
   }
-  __syncthreads();
+  if (__syncthreads_or(descends)) {
+    for (int i = 0; i < b && b < B; ++i)
+      if (s0 < sorted[i]) n = 0;
+    __syncthreads();
+    if (b < B) len[b] = n;
+    __syncthreads();
+  }
   if (b < B) {
     int rank = 0;
     for (int i = 0; i < B; ++i) rank += len[i] > n || (len[i] == n && i < b);
@@ -162,13 +175,26 @@ __device__ __forceinline__ Unit small_unit(const PromptArgs& a, int u, int unit_
   const int lane = threadIdx.x & 31;
   int blk = u / a.num_kv_heads;
   const int head = u - blk * a.num_kv_heads;
+  int ends = 0;  // the furthest end so far
+  bool descends = false;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int s0 = 0, n = 0;
+    int s0 = 0, s1 = 0, n = 0;
     if (b0 + lane < a.batch) {
       s0 = a.cu_seqlens[b0 + lane];
-      const int s1 = a.cu_seqlens[b0 + lane + 1];
+      s1 = a.cu_seqlens[b0 + lane + 1];
       if (!bad_bounds(a, s0, s1)) n = s1 - s0;
       else if (u == 0) atomicOr(a.err, KVQ_DEVERR_SEQ_LEN);
+    }
+    int end = bad_bounds(a, s0, s1) ? 0 : s1;
+    descends = __any_sync(0xffffffffu, descends || s1 < s0);
+    if (descends || b0 > 0) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+      const int up = __shfl_up_sync(0xffffffffu, end, 1);
+      if (s0 < max(ends, lane > 0 ? up : 0)) n = 0;
+      ends = max(ends, __shfl_sync(0xffffffffu, end, 31));
+    } else if (b0 + 32 < a.batch) {
+      ends = __reduce_max_sync(0xffffffffu, end);
     }
     const int own = (n + unit_tokens - 1) / unit_tokens;
     int x = own;

@@ -505,7 +505,9 @@ KVQ_API kvq_status kvq_evict_compact(const kvq_cache* cache, const kvq_evict_par
  * out and lse_out that belong to no sequence (before cu_seqlens[0], behind
  * cu_seqlens[B], an empty sequence) are left as they were, and what q, k and v
  * hold there, NaN included, changes nothing.  A sequence whose bounds descend,
- * leave [0, N] or exceed max_seq_len sets KVQ_DEVERR_SEQ_LEN and is skipped.
+ * leave [0, N] or exceed max_seq_len sets KVQ_DEVERR_SEQ_LEN and is skipped; so
+ * is, behind such bounds, a sequence that begins before the end of an earlier
+ * one whose own bounds are right (no row belongs to two sequences).
  * Inf or NaN in a token's K or V row reaches the tokens that see it, and no
  * other (tiles of rows whose results hold NaN are computed twice).
  * Weights enter the product with V as bf16; sums, maxima and lse are fp32.
