@@ -1528,9 +1528,9 @@ KVQ_API kvq_status kvq_pages_step(const kvq_pages_params* params, const int32_t*
   if (p->batch > kMaxBatch || p->max_tokens > (1 << 30) || (parents && p->tree_nodes > KVQ_MAX_TREE_NODES))
     return KVQ_ERR_UNSUPPORTED;
   if (p->batch == 0 && p->max_tokens == 0) return KVQ_OK;
-  if (!held_lens || !new_tokens || !block_table || !free_blocks || !free_count || !seq_lens || !free_left ||
-      !cu_seqlens || (p->max_tokens > 0 && (!slot_mapping || !positions)))
+  if (!free_blocks || !free_count || !free_left || !cu_seqlens || (p->max_tokens > 0 && (!slot_mapping || !positions)))
     return KVQ_ERR_INVALID_ARG;
+  if (p->batch > 0 && (!held_lens || !new_tokens || !block_table || !seq_lens)) return KVQ_ERR_INVALID_ARG;
   for (const void* x : {(const void*)held_lens, (const void*)start_lens, (const void*)new_tokens, (const void*)parents,
                         (const void*)block_table, (const void*)free_blocks, (const void*)free_count,
                         (const void*)seq_lens, (const void*)free_left, (const void*)cu_seqlens})

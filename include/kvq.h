@@ -629,7 +629,8 @@ KVQ_API kvq_status kvq_tree_accept(const kvq_cache* cache, const kvq_decode_para
  * (refused).  A page id outside [0, num_blocks) is passed on as it is, sets
  * KVQ_DEVERR_BLOCK_ID, and its rows get slot -1; a free_count outside
  * [0, num_blocks], or more pages given back than the pool has, sets it too.
- * batch <= 1024; max_tokens <= 2^30. */
+ * With batch 0 the [B] arrays may be NULL; with batch 0 and max_tokens 0 the
+ * call does nothing.  batch <= 1024; max_tokens <= 2^30. */
 typedef struct {
   int32_t batch;              /* B (<= 1024) */
   int32_t max_blocks_per_seq; /* block_table row length; capacity = it * block_size */
