@@ -1122,9 +1122,8 @@ kvq_status check_prompt(const kvq_prompt_params* p) {
 // (the table of work units)
 size_t prompt_workspace(const kvq_prompt_params* p) { return align256((size_t)(4 * p->batch + 8) * 4); }
 
-// (a NULL parents array is a host-side mistake whatever the batch)
 kvq_status check_tree(const kvq_decode_params* p, const kvq_tree* t) {
-  if (!t || !t->parents || !aligned(t->parents, 4) || (t->num_nodes && !aligned(t->num_nodes, 4)))
+  if (!t || (!t->parents && p->batch > 0) || !aligned(t->parents, 4) || (t->num_nodes && !aligned(t->num_nodes, 4)))
     return KVQ_ERR_INVALID_ARG;
   return p->q_tokens > KVQ_MAX_TREE_NODES ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
 }
