@@ -583,7 +583,7 @@ def _rows(name: str, t: torch.Tensor, shape: tuple, dev: int):
     N, H, D = shape
     st = t.stride()
     if (t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or st[2] != 1 or
-            (H > 1 and st[1] != D) or (N > 1 and st[0] < H * D)):
+            (H > 1 and st[1] != D) or (N > 1 and not H * D <= st[0] < 2 ** 31)):
         raise ValueError(f"{name}: needs torch.bfloat16 rows of shape {shape} on cuda:{dev}, each token's heads "
                          f"contiguous, got {t.dtype} {tuple(t.shape)} of strides {st} on {t.device}")
     return t.data_ptr(), st[0] if N > 1 else 0
