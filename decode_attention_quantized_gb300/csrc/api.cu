@@ -1596,12 +1596,12 @@ KVQ_API kvq_status kvq_attend_prompt(const kvq_prompt_params* params, const void
   if (workspace_bytes < prompt_workspace(p)) return KVQ_ERR_WORKSPACE_TOO_SMALL;
   PromptArgs a{};
   const int D = p->head_dim;
-  a.q_stride = p->q_stride ? p->q_stride : (long long)p->num_q_heads * D;
-  a.k_stride = p->k_stride ? p->k_stride : (long long)p->num_kv_heads * D;
+  const long long q_stride = p->q_stride ? p->q_stride : (long long)p->num_q_heads * D;
+  const long long k_stride = p->k_stride ? p->k_stride : (long long)p->num_kv_heads * D;
   a.v_stride = p->v_stride ? p->v_stride : (long long)p->num_kv_heads * D;
   {
     const uint64_t n = p->total_tokens, last = n - 1, qw = (uint64_t)p->num_q_heads * D, kw = (uint64_t)p->num_kv_heads * D;
-    const std::pair<const void*, uint64_t> in[] = {{q, 2 * (last * a.q_stride + qw)}, {k, 2 * (last * a.k_stride + kw)},
+    const std::pair<const void*, uint64_t> in[] = {{q, 2 * (last * q_stride + qw)}, {k, 2 * (last * k_stride + kw)},
                                                    {v, 2 * (last * a.v_stride + kw)}, {cu_seqlens, 4ull * p->batch + 4},
                                                    {head_sink, head_sink ? 4ull * p->num_q_heads : 0}};
     const std::pair<const void*, uint64_t> outs[] = {{out, 2 * n * qw}, {lse_out, lse_out ? 4 * n * p->num_q_heads : 0},
@@ -1610,8 +1610,6 @@ KVQ_API kvq_status kvq_attend_prompt(const kvq_prompt_params* params, const void
   }
   DeviceInfo* dev;
   if (kvq_status s = current_device(&dev)) return s;
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
   a.cu_seqlens = cu_seqlens;
   a.head_sink = head_sink;
@@ -1631,8 +1629,8 @@ KVQ_API kvq_status kvq_attend_prompt(const kvq_prompt_params* params, const void
   a.err = dev->err;
   alignas(64) CUtensorMap tm[3];
   const int tokens = 128 / a.group;
-  if (kvq_status s = encode_rows_map(q, D, p->num_q_heads, p->total_tokens, a.q_stride, a.group, tokens, &tm[0])) return s;
-  if (kvq_status s = encode_rows_map(k, D, p->num_kv_heads, p->total_tokens, a.k_stride, 1, 128, &tm[1])) return s;
+  if (kvq_status s = encode_rows_map(q, D, p->num_q_heads, p->total_tokens, q_stride, a.group, tokens, &tm[0])) return s;
+  if (kvq_status s = encode_rows_map(k, D, p->num_kv_heads, p->total_tokens, k_stride, 1, 128, &tm[1])) return s;
   if (kvq_status s = encode_rows_map(v, D, p->num_kv_heads, p->total_tokens, a.v_stride, 1, 128, &tm[2])) return s;
   return from_cuda(launch_attend_prompt(tm, a, dev->sms, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -204,29 +204,47 @@ __device__ __forceinline__ void cap_scores(float (&y)[N], float cap) {
   }
 }
 
-// The same by size: a thread whose N scores are all within 1/2 (logits within
-// half the cap, the usual ones) takes y P(y^2), P the minimax polynomial of
-// degree 4 to tanh(sqrt t) / sqrt t on [0, 1/4] (1.1e-7 relative in fp32), in
-// half the instructions and without the quotient.
-template <int N>
-__device__ __forceinline__ void cap_scores_by_size(float (&y)[N], float cap) {
-  float big = 0.0f;
-#pragma unroll
-  for (int k = 0; k < N; k += 2) big = ptx::max3(big, fabsf(y[k]), fabsf(y[k + 1]));
-  if (big > 0.5f) {
-    cap_scores<N>(y, cap);
-    return;
+// cap tanh(alpha S) = S P(S^2) for |alpha S| <= kReach (the usual scores), P the
+// minimax polynomial of degree 3 to tanh(sqrt t) / sqrt t there (1.5e-7 relative
+// in fp32): half the instructions of the quotient.
+struct CapNear {
+  static constexpr float kReach = 0.35f;
+  float c0, c1, c2, c3;
+  __device__ __forceinline__ CapNear(float cap, float alpha) {
+    const float a2 = alpha * alpha;
+    c0 = alpha * cap;
+    c1 = -0.33332422f * a2 * c0;
+    c2 = 0.13295799f * a2 * a2 * c0;
+    c3 = -0.04895823f * a2 * a2 * a2 * c0;
   }
-  const float c1 = -0.33333069f * cap, c2 = 0.13324779f * cap, c3 = -0.05298607f * cap, c4 = 0.01713501f * cap;
+  __device__ __forceinline__ float score(float s) const {
+    const float t = s * s;
+    return s * fmaf(fmaf(fmaf(c3, t, c2), t, c1), t, c0);
+  }
+  // two scores, plus b
+  __device__ __forceinline__ ptx::f32x2 scores(ptx::f32x2 s, ptx::f32x2 b) const {
+    const ptx::f32x2 t = ptx::mul_x2(s, s);
+    return ptx::fma_x2(s, ptx::fma_x2(ptx::fma_x2(ptx::fma_x2(t, ptx::pack_x2(c3, c3), ptx::pack_x2(c2, c2)), t, ptx::pack_x2(c1, c1)),
+                                      t, ptx::pack_x2(c0, c0)), b);
+  }
+};
+
+// Transposes the 4 x 4 16-byte pieces of a quad of lanes: x[k] of lane i
+// becomes what x[i] of lane k was (i, k within the quad).
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][4]) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    float t0, t1, p0, p1;
-    ptx::mul_x2(t0, t1, y[k], y[k + 1], y[k], y[k + 1]);
-    ptx::fma_x2(p0, p1, t0, t1, c4, c4, c3, c3);
-    ptx::fma_x2(p0, p1, p0, p1, t0, t1, c2, c2);
-    ptx::fma_x2(p0, p1, p0, p1, t0, t1, c1, c1);
-    ptx::fma_x2(p0, p1, p0, p1, t0, t1, cap, cap);
-    ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], p0, p1);
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x[k][i] : x[k + 1][i], 1);
+      (odd ? x[k][i] : x[k + 1][i]) = got;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[k][i] : x[k + 2][i], 2);
+      (high ? x[k][i] : x[k + 2][i]) = got;
+    }
   }
 }
 

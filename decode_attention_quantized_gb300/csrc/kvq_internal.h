@@ -175,15 +175,13 @@ cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
 
 // kvq_attend_prompt.
 struct PromptArgs {
-  const uint16_t* q;          // bf16 bits [N, Hq, D], tokens q_stride elements apart
-  const uint16_t* k;          // [N, Hkv, D]
-  const uint16_t* v;
+  const uint16_t* v;          // bf16 bits [N, Hkv, D], tokens v_stride elements apart (q, k: by tensor map)
   const int32_t* cu_seqlens;  // [B + 1]
   const float* head_sink;     // [Hq] or null
   uint16_t* out;              // bf16 bits [N, Hq, D]
   float* lse_out;             // [N, Hq] or null
   int* plan;                  // workspace
-  long long q_stride, k_stride, v_stride;
+  long long v_stride;
   int batch, total_tokens, num_q_heads, num_kv_heads, head_dim, group, max_seq_len;
   float sm_scale, softcap;
   int window;

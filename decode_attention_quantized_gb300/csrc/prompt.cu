@@ -595,17 +595,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     const int t_row = dev::div_small(r, __frcp_rn((float)G)), g = r - t_row * G;
     // (finite and above 0, so that alpha times -inf is -inf)
     const float alpha = fminf(fmaxf(CAP ? a.sm_scale / a.softcap : a.sm_scale * kLog2e, 1.17549435e-38f), 3.4028234e38f);
-    // tanh(x) = x P(x^2) for |x| <= kCapNear, P the minimax polynomial of degree
-    // 3 to tanh(sqrt t) / sqrt t there (1.5e-7 relative in fp32); x = alpha S.
-    constexpr float kCapNear = 0.35f;
-    const float cap2 = CAP ? a.softcap * kLog2e : 0.0f, al2 = alpha * alpha;
-    const float c0 = alpha * cap2, c1 = -0.33332422f * al2 * c0, c2 = 0.13295799f * al2 * al2 * c0,
-                c3 = -0.04895823f * al2 * al2 * al2 * c0;
-    const ptx::f32x2 cc0 = ptx::pack_x2(c0, c0), cc1 = ptx::pack_x2(c1, c1), cc2 = ptx::pack_x2(c2, c2),
-                     cc3 = ptx::pack_x2(c3, c3), aa = ptx::pack_x2(alpha, alpha);
+    const float cap2 = CAP ? a.softcap * kLog2e : 0.0f;
+    const dev::CapNear cap_near(cap2, alpha);
+    const ptx::f32x2 aa = ptx::pack_x2(alpha, alpha);
     // (coefficients far from fp32's ends, or not at all)
-    const float cap_near =
-        CAP && alpha > 6e-5f && alpha < 1.6e4f && cap2 > 1e-6f && cap2 < 1e6f ? kCapNear / alpha : -1.0f;
+    const float reach =
+        CAP && alpha > 6e-5f && alpha < 1.6e4f && cap2 > 1e-6f && cap2 < 1e6f ? dev::CapNear::kReach / alpha : -1.0f;
     uint32_t ns = 0;  // S tiles taken
     for (;;) {
       Unit u = next_unit();
@@ -669,12 +664,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           if constexpr (CAP) least = fminf(ptx::min3(mn[0], mn[1], mn[2]), mn[3]);
         }
         // Under a cap, tanh by the polynomial below where no score of the row
-        // passes kCapNear of it (the usual scores), else by the quotient.
-        const bool near = CAP && fmaxf(fabsf(m), fabsf(least)) <= cap_near;
+        // passes its reach (the usual scores), else by the quotient.
+        const bool near = CAP && fmaxf(fabsf(m), fabsf(least)) <= reach;
         if constexpr (CAP) {
           if (near) {
-            const float t = m * m;
-            m *= fmaf(fmaf(fmaf(c3, t, c2), t, c1), t, c0);
+            m = cap_near.score(m);
           } else if (m != -INFINITY) {
             float x[2] = {m * alpha, 0.0f};
             dev::cap_scores<2>(x, cap2);
@@ -736,12 +730,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             for (int c0 = half * (kKeys / 2); c0 < (half + 1) * (kKeys / 2); c0 += CH) {
               load_s(c0);
               if (near) {
-                // y P(y^2) - mu, the factors of alpha in P's coefficients (a row
-                // with hidden keys, of score -inf, is not near)
-                weigh(0, 0, CH, [&](ptx::f32x2 x) {
-                  const ptx::f32x2 t = ptx::mul_x2(x, x);
-                  return ptx::fma_x2(x, ptx::fma_x2(ptx::fma_x2(ptx::fma_x2(t, cc3, cc2), t, cc1), t, cc0), nm);
-                });
+                // (a row with hidden keys, of score -inf, is not near)
+                weigh(0, 0, CH, [&](ptx::f32x2 x) { return cap_near.scores(x, nm); });
               } else {
 #pragma unroll
                 for (int k = 0; k < CH; k += 2) ptx::mul_x2(y[k], y[k + 1], y[k], y[k + 1], alpha, alpha);
@@ -780,7 +770,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       unsigned long long at[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, dst, (lane & ~3) | i);
-      const bool odd = lane & 1, high = lane & 2;
       __nv_bfloat162 sum = __floats2bfloat162_rn(0.0f, 0.0f);  // not finite if a result is not
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -799,20 +788,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           for (int i = 0; i < 4; ++i) t[i] = __hfma2(pair(i), pair(4 + i), __hmul2(pair(8 + i), pair(12 + i)));
           sum = __hadd2(sum, __hadd2(__hadd2(t[0], t[1]), __hadd2(t[2], t[3])));
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // pieces 0 <-> 1 and 2 <-> 3 with the neighbour, then 0 <-> 2 and 1 <-> 3
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x[k][i] : x[k + 1][i], 1);
-            (odd ? x[k][i] : x[k + 1][i]) = got;
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[k][i] : x[k + 2][i], 2);
-            (high ? x[k][i] : x[k + 2][i]) = got;
-          }
-        }
+        dev::quad_transpose(x);
         // piece k is now this lane's 16 bytes of the quad's row k
 #pragma unroll
         for (int k = 0; k < 4; ++k)

@@ -59,25 +59,6 @@ __device__ __forceinline__ uint32_t tt_chunk(uint32_t tile, int kk, int c) {
   return tile + (uint32_t)(c >> 3) * SLAB + (uint32_t)kk * 128u + ((((uint32_t)c & 7u) ^ ((uint32_t)kk & 7u)) << 4);
 }
 
-// Transposes the 4 x 4 16-byte pieces of a quad of lanes: x[k] of lane i
-// becomes what x[i] of lane k was (i, k within the quad).
-__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][4]) {
-  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x[k][i] : x[k + 1][i], 1);
-      (odd ? x[k][i] : x[k + 1][i]) = got;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[k][i] : x[k + 2][i], 2);
-      (high ? x[k][i] : x[k + 2][i]) = got;
-    }
-  }
-}
-
 }  // namespace dev
 
 // SPLIT: the Q operand in two f16 parts (a per-channel K scale and an lse that
@@ -464,11 +445,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
       }
       if (lane == 0) ptx::mbar_arrive(b_q);
 
-      // tanh(x) = x P(x^2) for |x| <= kCapNear, P the minimax polynomial of
-      // degree 3 to tanh(sqrt t) / sqrt t there (1.5e-7 relative); x = alpha S
-      constexpr float kCapNear = 0.35f;
       const float cap2 = CAP ? a.softcap * kLog2e : 0.0f;
-      const float c0f = cap2, c1f = -0.33332422f * cap2, c2f = 0.13295799f * cap2, c3f = -0.04895823f * cap2;
       const ptx::f32x2 aa = ptx::pack_x2(alpha, alpha);
 
       float mu = -INFINITY;                      // this row's reference (log2 units) as of this group's last tile
@@ -599,7 +576,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           if constexpr (CAP) least = fminf(ptx::min3(mn[0], mn[1], mn[2]), mn[3]);
         }
         // (rows that count for nothing may hold anything)
-        const bool near = CAP && __all_sync(0xffffffffu, blind || fmaxf(fabsf(m), fabsf(least)) <= kCapNear);
+        const bool near = CAP && __all_sync(0xffffffffu, blind || fmaxf(fabsf(m), fabsf(least)) <= dev::CapNear::kReach);
         if constexpr (!FOLD) {
           // the row's other half (a place is written again two tiles on, past the
           // barrier of the tile between); both have S in registers before either
@@ -613,9 +590,8 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
           m = fmaxf(m, place[128 * (grp ^ 1)]);
         }
         if constexpr (CAP) {
-          if (fabsf(m) <= kCapNear) {
-            const float t = m * m;
-            m *= fmaf(fmaf(fmaf(c3f, t, c2f), t, c1f), t, c0f);
+          if (fabsf(m) <= dev::CapNear::kReach) {
+            m = dev::CapNear(cap2, 1.0f).score(m);
           } else if (m != -INFINITY) {
             float x[2] = {m, 0.0f};
             dev::cap_scores<2>(x, cap2);
@@ -718,13 +694,9 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         if constexpr (!CAP) {
           weigh([&](ptx::f32x2 x) { return ptx::fma_x2(x, aa, nm); });
         } else if (near) {
-          // x P(x^2) - mu (of a tile with hidden keys, of score -inf, not all rows are near)
-          const ptx::f32x2 cc0 = ptx::pack_x2(c0f, c0f), cc1 = ptx::pack_x2(c1f, c1f), cc2 = ptx::pack_x2(c2f, c2f),
-                           cc3 = ptx::pack_x2(c3f, c3f);
-          weigh([&](ptx::f32x2 x) {
-            const ptx::f32x2 t = ptx::mul_x2(x, x);
-            return ptx::fma_x2(x, ptx::fma_x2(ptx::fma_x2(ptx::fma_x2(t, cc3, cc2), t, cc1), t, cc0), nm);
-          });
+          // (of a tile with hidden keys, of score -inf, not all rows are near)
+          const dev::CapNear cap_near(cap2, 1.0f);
+          weigh([&](ptx::f32x2 x) { return cap_near.scores(x, nm); });
         } else {
 #pragma unroll
           for (int c = 0; c < CH; c += 16) {
