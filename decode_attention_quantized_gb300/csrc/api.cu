@@ -950,9 +950,10 @@ kvq_status masked_shape(const kvq_cache* c, const kvq_decode_params* p, bool lse
   s.T = tile / G < C ? tile / G : C;
   int least = p->softcap > 0.0f ? (tile == kQtRows ? 64 : 56) : 17;
   if (tree) {
-    // the tree kernel against the mma.sync one: 4 x 32,768 keys of head_dim 256
-    // int4 12 rows 82 / 102 us, head_dim 128 int8 16 rows 85 / 105 (fp8 under a
-    // cap 103 / 102); 4 x 2,048: 26 / 22, 22 / 20
+    // the tree kernel against the mma.sync one: 4 x 32,768 keys of 4 kv heads of
+    // head_dim 256, int4, 12 rows 80 / 102 us; 8 of head_dim 128, int8, 16 rows
+    // 96 / 109 (fp8 under a cap 103 / 102); one of head_dim 128 26 / 24; 4 x 2,048
+    // keys 26 / 20, 22 / 19
     const long long cap = (long long)p->max_blocks_per_seq * c->block_size;
     const long long keys = p->batch * (p->max_seq_len > 0 && p->max_seq_len < cap ? p->max_seq_len : cap);
     least = keys > 65536 && !(p->softcap > 0.0f) ? 9 : 17;

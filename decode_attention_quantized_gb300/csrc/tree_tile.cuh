@@ -39,9 +39,9 @@
 //
 // Bound: cache bytes for few rows of 8-bit codes, else the chain of a tile
 // (conversion, QK^T, softmax, PV) and instruction issue, 0.45 of the slots.
-// 131,072 int8 keys of head_dim 256, 16 nodes of 6 heads: 92 us, 3.0 TB/s; 4 x
-// 32,768 int4 keys, 32 nodes: 277 us; 16 sequences to 32,768 fp8 keys, capped,
-// 13 nodes of 4 heads: 248 us, 2.8 TB/s.
+// 131,072 int8 keys of head_dim 256, 16 nodes of 6 heads: 93 us, 2.9 TB/s; 4 x
+// 32,768 int4 keys, 32 nodes: 276 us; 16 sequences to 32,768 fp8 keys, capped,
+// 13 nodes of 4 heads: 246 us, 2.8 TB/s.
 #pragma once
 
 #include <type_traits>
