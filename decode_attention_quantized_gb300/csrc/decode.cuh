@@ -112,8 +112,9 @@ __device__ __forceinline__ float scale_lift(float s, int F) { return (float)max(
 // some rows see counts to 2^-46 of it, to 2^-94 in the tiles that all see: then
 // no lift leaves [-112, 94], and a row's sum, over 2^mu, stays within fp32.
 struct ScaleUnit {
-  // mu follows a growth of F up to here (above, O counts for nothing in the new unit)
-  static constexpr int kMost = 100;
+  // mu follows a growth of F up to here: scales may lie 2^126 apart (those of bf16
+  // rows of size one and of its largest do)
+  static constexpr int kMost = 126;
   int all = -126, some = -126;
   // F of a tile of scales up to 2^f; common: all rows see all of its keys.
   __device__ __forceinline__ int next(int f, bool common) {

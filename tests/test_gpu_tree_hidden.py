@@ -99,6 +99,21 @@ def test_branches_of_different_size(kvq, name, T, by):
     check(cache, run(kvq, cache, parents, flags=kvq.DECODE_NO_TCGEN05), parents, nodes, others)
 
 
+@pytest.mark.parametrize("name", ["int8 row d128", "int8 row d256 g6", "fp8 row", "int4 row", "int4 group"])
+@pytest.mark.parametrize("T", [65, 100])
+@pytest.mark.parametrize("at", [2, 63, 64])
+@pytest.mark.parametrize("by", [2.0 ** 30, 2.0 ** 118])
+def test_a_large_node_among_tiles_of_nodes(kvq, name, T, at, by):
+    """No prefix, or a short one: no tile is seen whole by all nodes."""
+    case = dataclasses.replace(CASES[name], c=T, seed=T, lens=(T, T + 70))
+    cache = ref.Cache(case)
+    parents = step_ref.random_parents(np.random.default_rng(at), 2, T, wide=50)
+    nodes = np.full(2, T)
+    for b, L in enumerate(case.lens):
+        enlarge(cache, b, L - T + at, by)
+    check(cache, run(kvq, cache, parents), parents, nodes)
+
+
 @pytest.mark.parametrize("name,T", [("int8 row d128", 6), ("int8 row d128", 33), ("int8 row d256 g6", 12), ("int4 row", 9),
                                     ("int4 group", 8)])
 def test_a_large_row_behind_the_window(kvq, name, T):
