@@ -897,6 +897,7 @@ kvq_status combine_impl(const kvq_cache* cache, const kvq_decode_params* params,
     a.slopes = mask->slopes;
     a.key_begin = mask->key_begin;
     a.key_end = mask->key_end;
+    a.tree = mask->tree_bits != nullptr;
     a.window = params->window;
     a.direct = qt ? 1 : 0;
     return from_cuda(launch_combine_masked(a, reinterpret_cast<cudaStream_t>(stream), warp_rows));

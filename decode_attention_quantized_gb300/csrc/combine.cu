@@ -76,7 +76,7 @@ __device__ __forceinline__ void combine_finish(const CombineArgs& a, const Combi
   const int hq = c.hq, h = c.h;
   constexpr int E = D / 32;
   float lse_nat = -INFINITY;
-  if (wsum > 0.0f) {
+  if (wsum > 0.0f || (MASK && a.tree && wsum != wsum)) {
     const float inv = 1.0f / wsum;
     const float lse2 = m + ptx::fast_log2(wsum);
     lse_nat = lse2 * 0.69314718055994530942f;

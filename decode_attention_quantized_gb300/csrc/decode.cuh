@@ -95,6 +95,19 @@ __device__ __forceinline__ uint32_t f8pair(uint32_t w, uint32_t sel) {
   return (y & 0x80008000u) | ((y >> 1) & 0x3F803F80u);
 }
 
+// What the combine gets of a row whose weights sum to l over 2^m: the factor of its
+// O, and its log-sum-exp (-inf: no key).  Draft trees: +inf for a sum of NaN, so
+// that the combine, whose maximum drops NaN, gives NaN and not what is left.
+template <bool TREE>
+__device__ __forceinline__ float part_factor(float l, float unit) {
+  return (TREE ? l != 0.0f : l > 0.0f) ? unit / l : 0.0f;
+}
+template <bool TREE>
+__device__ __forceinline__ float part_lse(float m, float l) {
+  if (TREE && l != l) return INFINITY;
+  return l > 0.0f ? m + ptx::fast_log2(l) : -INFINITY;
+}
+
 // Draft trees: a node's row must not reach the nodes that do not see it, whatever
 // its V scale (one normaliser 2^F above all of them flushed the others' f16
 // weights to 0).  Infinities and NaN take no part in F, and a weight of 0 stays 0.
@@ -1058,7 +1071,7 @@ __global__ void __launch_bounds__(288, MINB)
           lt[i] += s_l[2 * ROWS + row];
           lt[i] += s_l[3 * ROWS + row];
         }
-        const float f0 = lt[0] > 0.0f ? to_true / lt[0] : 0.0f, f1 = lt[1] > 0.0f ? to_true / lt[1] : 0.0f;
+        const float f0 = dev::part_factor<TREE>(lt[0], to_true), f1 = dev::part_factor<TREE>(lt[1], to_true);
         float* o0 = a.part_o + ((size_t)u * a.rows + r0) * D;
         float* o1 = o0 + D;
 #pragma unroll
@@ -1069,8 +1082,8 @@ __global__ void __launch_bounds__(288, MINB)
           if (r1 < a.rows) *reinterpret_cast<float2*>(o1 + ch) = make_float2(acc[mt][nt][1] * f1, acc[mt][nt][3] * f1);
         }
         if (kq == 0 && g == 0) {
-          if (r0 < a.rows) a.part_lse[(size_t)u * a.rows + r0] = lt[0] > 0.0f ? m[nt][0] + ptx::fast_log2(lt[0]) : -INFINITY;
-          if (r1 < a.rows) a.part_lse[(size_t)u * a.rows + r1] = lt[1] > 0.0f ? m[nt][1] + ptx::fast_log2(lt[1]) : -INFINITY;
+          if (r0 < a.rows) a.part_lse[(size_t)u * a.rows + r0] = dev::part_lse<TREE>(m[nt][0], lt[0]);
+          if (r1 < a.rows) a.part_lse[(size_t)u * a.rows + r1] = dev::part_lse<TREE>(m[nt][1], lt[1]);
         }
       }
       ptx::named_bar_sync(1, 8 * 32);
@@ -1523,7 +1536,7 @@ __global__ void __launch_bounds__(288, MINB)
       // the tiles above may run while the preceding grid finishes; the
       // workspace is written only after it (no-op after the first)
       ptx::griddep_wait();
-      const float f0 = l0 > 0.0f ? to_true / l0 : 0.0f, f1 = l1 > 0.0f ? to_true / l1 : 0.0f;
+      const float f0 = dev::part_factor<TREE>(l0, to_true), f1 = dev::part_factor<TREE>(l1, to_true);
       const int rr0 = rg * 8 + 2 * c, rr1 = rr0 + 1;
       float* o0 = a.part_o + ((size_t)u * a.rows + rr0) * D;
       float* o1 = o0 + D;
@@ -1534,8 +1547,8 @@ __global__ void __launch_bounds__(288, MINB)
         if (rr1 < a.rows) *reinterpret_cast<float2*>(o1 + ch) = make_float2(acc[mt][1] * f1, acc[mt][3] * f1);
       }
       if (g == 0) {
-        if (rr0 < a.rows) a.part_lse[(size_t)u * a.rows + rr0] = l0 > 0.0f ? m0 + ptx::fast_log2(l0) : -INFINITY;
-        if (rr1 < a.rows) a.part_lse[(size_t)u * a.rows + rr1] = l1 > 0.0f ? m1 + ptx::fast_log2(l1) : -INFINITY;
+        if (rr0 < a.rows) a.part_lse[(size_t)u * a.rows + rr0] = dev::part_lse<TREE>(m0, l0);
+        if (rr1 < a.rows) a.part_lse[(size_t)u * a.rows + rr1] = dev::part_lse<TREE>(m1, l1);
       }
     }
   }

@@ -209,6 +209,7 @@ struct CombineArgs {
   const int32_t* key_end;
   int window;
   int direct;  // 1: rows of one piece were finished by the attention kernel
+  int tree;    // 1: draft trees, a sum of NaN gives NaN
 };
 
 // Writes the virtual sequences of a masked call: sequence b's tokens in groups

@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kTtWarps * 32, 1)
         if (valid && grp == 0 && a.lse_out) a.lse_out[tok * Hq + hq] = lse;
         dst = reinterpret_cast<unsigned long long>(a.out + (tok * Hq + hq) * a.out_dim);
       } else {
-        if (valid && grp == 0) a.part_lse[(size_t)u * rows + r] = some ? mu + ptx::fast_log2(l) : -INFINITY;
+        if (valid && grp == 0) a.part_lse[(size_t)u * rows + r] = dev::part_lse<true>(mu, l);
         dst = reinterpret_cast<unsigned long long>(a.part_o + ((size_t)u * rows + r) * D);
       }
       // quads of lanes store 64 bytes of a row at a time

@@ -556,9 +556,10 @@ typedef struct {
  * position (a prefix row's is its row, a node's P + depth) is above the
  * node's own minus window.  q, out bf16 [B, T, Hq, D]; nodes i >= num_nodes[b]
  * are padding: their output rows are zero and their lse -inf.  A node whose
- * cached row has a scale of inf or NaN reaches its descendants only, and a
- * finite one, however large, takes nothing of the others' precision: weights
- * are relative to the largest V scale of the rows that a node itself sees.
+ * cached row has a scale of inf or NaN reaches its descendants only (their
+ * results are NaN, as those of a query that holds NaN), and a finite one,
+ * however large, takes nothing of the others' precision: weights are relative
+ * to the largest V scale of the rows that a node itself sees.
  * Everything else is as in kvq_attend_masked.
  * batch <= 1024.  workspace: at least kvq_attend_tree_workspace_size bytes,
  * 256-byte aligned; it belongs to this call until the call's kernels have
