@@ -99,6 +99,17 @@ def test_branches_of_different_size(kvq, name, T, by):
     check(cache, run(kvq, cache, parents, flags=kvq.DECODE_NO_TCGEN05), parents, nodes, others)
 
 
+@pytest.mark.parametrize("name,T", [("int8 row d128", 5), ("int8 row d128", 40), ("int8 row d256 g6", 16), ("fp8 row", 20),
+                                    ("int4 row", 9), ("int4 group", 8)])
+@pytest.mark.parametrize("cap", [2.0, 50.0])
+def test_a_large_node_under_a_cap(kvq, name, T, cap):
+    cache, parents, nodes = make(name, T, ragged=False, softcap=cap, amp=4.0)
+    parents[:, -1] = -1
+    for b, L in enumerate(cache.case.lens):
+        enlarge(cache, b, L - 1, 2.0 ** 30)
+    check(cache, run(kvq, cache, parents), parents, nodes)
+
+
 @pytest.mark.parametrize("name", ["int8 row d128", "int8 row d256 g6", "fp8 row", "int4 row", "int4 group"])
 @pytest.mark.parametrize("T", [65, 100])
 @pytest.mark.parametrize("at", [2, 63, 64])
