@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   Unit* units = reinterpret_cast<Unit*>(base + C::UNITS);            // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* total = abort_flag + 1;  // [2] number of the unit behind the last one, in turn
+  volatile int* total = abort_flag + 1;  // number of the unit behind the last one
   volatile int* spoilt = reinterpret_cast<volatile int*>(tmem_slot + 4);  // [8] at unit n & 7: n + 1, if it is to run again
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -304,14 +304,19 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     return u;
   };
   // Whether units follow behind one of len 0: the last two may have to run again.
-  // (The same for every warp, whatever else has happened: what one reads here is
-  // not written again before all have come to the next such barrier.)
-  int ends = 0;
+  // (The same for every warp, whatever else has happened: nothing of it is written
+  // again before all have read it.)
   auto go_on = [&]() -> bool {
+    constexpr uint32_t kThreads = (C::SOFTMAX + 2) * 32;
     __syncwarp();
-    ptx::named_bar_sync(1, (C::SOFTMAX + 2) * 32);
-    const int n = total[ends++ & 1];
-    return (n > 0 && spoilt[(n - 1) & 7] == n) || (n > 1 && spoilt[(n - 2) & 7] == n - 1);
+    ptx::named_bar_sync(1, kThreads);
+    const int n = *total;
+    const bool more = (n > 0 && spoilt[(n - 1) & 7] == n) || (n > 1 && spoilt[(n - 2) & 7] == n - 1);
+    if (more) {
+      __syncwarp();
+      ptx::named_bar_sync(1, kThreads);
+    }
+    return more;
   };
   auto range = [&](const Unit& u, int w) -> Range {
     return w < unit_tiles ? tile_range(u, w, tpt, W) : Range{0, 0};
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         }
         // every copy has landed before the CTA may end
         if (lane == 0) {
-          total[ends & 1] = n;
+          *total = n;
           const uint32_t last = issued < (uint32_t)C::STAGES ? issued : (uint32_t)C::STAGES;
           for (uint32_t i = issued - last; i < issued; ++i)
             ptx::mbar_wait_bounded_inl(&bar_full[i % C::STAGES], (i / C::STAGES) & 1);
