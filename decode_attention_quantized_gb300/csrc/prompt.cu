@@ -29,9 +29,9 @@
 // tile that do not see it.  A unit whose results hold NaN therefore runs again
 // with care: in key tiles that some row does not see whole, elements of V that
 // are not finite are set to 0 before the product, and rows that see them get
-// them added at the end.  It costs a barrier and a look at the results: one
-// prompt of 77 tokens 5.4 -> 5.6 us, 64 of 200 tokens 78 -> 82, 16,384 tokens the
-// same.  (Two warps that look through those tiles every time: 5.7, 85 and the
+// them added at the end.  It costs a barrier, a look at the results and longer
+// code: one prompt of 77 tokens 5.4 -> 5.8 us, 64 of 200 tokens 77 -> 83, 16,384
+// tokens 1%.  (Two warps that look through those tiles every time: 5.7, 85 and the
 // same, but 185 -> 200 us with a window of 1024 at head_dim 256.)
 #include <cuda_bf16.h>
 
